@@ -22,6 +22,7 @@
 
 #include "../../include/tpmlp.h"
 #include "common.h"
+#include "host.h"
 
 #include <algorithm>
 #include <mutex>
@@ -31,6 +32,12 @@
 namespace tpmlp {
 
 thread_local LaunchEvents g_launch_events;
+thread_local std::string g_last_error;
+
+tpmlp_status fail(tpmlp_status s, const std::string& what) {
+  g_last_error = what;
+  return s;
+}
 
 namespace {
 
@@ -46,13 +53,6 @@ __device__ __align__(256) unsigned char scratch[TPMLP_NOALLOC_SCRATCH_BYTES];
 constexpr int64_t MAX_DIM = int64_t(1) << 23;
 constexpr int NUM_CU = 256;  // MI355X compute units, used to size split-K
 constexpr size_t WS_ALIGN = 256;
-
-thread_local std::string g_last_error;
-
-tpmlp_status fail(tpmlp_status s, const std::string& what) {
-  g_last_error = what;
-  return s;
-}
 
 size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 
@@ -301,6 +301,8 @@ size_t batch_area_bytes(int t, int64_t M, int64_t H, int64_t F) {
 std::mutex g_dev_mu;
 std::vector<int> g_dev_ok;  // -1 unknown, 0 no, 1 yes
 
+}  // namespace
+
 tpmlp_status check_device() {
   int dev = -1;
   hipError_t e = hipGetDevice(&dev);
@@ -320,6 +322,8 @@ tpmlp_status check_device() {
   if (!g_dev_ok[dev]) return fail(TPMLP_ERR_UNSUPPORTED, "current device is not gfx950");
   return TPMLP_OK;
 }
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // Kernel timing: while enabled, an event pair bound to each timed call's first
@@ -411,9 +415,13 @@ tpmlp_status check_ptrs(std::initializer_list<std::pair<const void*, const char*
   return TPMLP_OK;
 }
 
+}  // namespace
+
 tpmlp_status hip_fail(hipError_t e, const char* what) {
   return fail(TPMLP_ERR_HIP, std::string(what) + ": " + hipGetErrorString(e));
 }
+
+namespace {
 
 // ---------------------------------------------------------------------------
 // GEMM launch helpers
