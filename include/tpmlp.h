@@ -334,6 +334,154 @@ tpmlp_status tpmlp_fwd_noalloc(const tpmlp_bf16* X, const tpmlp_bf16* A_i, const
                                int64_t M, int64_t H, int64_t F_i, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Block operators: what stands around one MLP                               */
+/* ------------------------------------------------------------------------ */
+/* The conventions above hold, with these differences.  Sizes are any that each
+ * call names, zero rows included (tensors without elements may be NULL).  Rows
+ * may be strided: ld_* is the distance between rows in elements, at least the
+ * row's length, 0 for dense rows; columns are contiguous.  Pointers need only
+ * their element's alignment (TPMLP_ERR_ALIGN); rows whose addresses are multiples
+ * of 16 bytes are fastest.  Values are float32 or bf16 as a tpmlp_dtype says;
+ * sums and statistics are float32 or wider, and each output is rounded once, to
+ * nearest even.  No result depends on the timing of the launch.  These calls are
+ * not among the kernel kinds that timing records. */
+
+typedef enum { TPMLP_F32 = 0, TPMLP_BF16 = 1 } tpmlp_dtype;
+
+typedef enum {
+  TPMLP_NORM_NONE = 0,
+  TPMLP_NORM_RMS = 1,  /* v / sqrt(mean(v^2) + eps) * w */
+  TPMLP_NORM_LAYER = 2 /* (v - mean(v)) / sqrt(var(v) + eps) * w + b */
+} tpmlp_norm;
+
+/* Largest hidden size of the edge, which holds a row in registers. */
+#define TPMLP_EDGE_MAX_H 32768
+
+/* The edge between two blocks: from the output y of one block and the residual
+ * stream r to the stream r' after it and the input x of the next block,
+ *   r' = alpha r + g (.) N_post(y),   x = N_pre(r')
+ * (residual additions and norms around the MLP: QLM page §2.1.2.2 and §2.1.3).
+ * N_post and N_pre are one of tpmlp_norm; the gate g has one row of H values for
+ * each gate_rows consecutive tokens (gate_rows >= M: one row for all; the rows of
+ * one sequence: a gate per sequence; 1: a gate per token).  Without a block before
+ * it (y NULL: no norm after it, no gate) the edge is x = N_pre(alpha r). */
+typedef struct {
+  int64_t M, H;            /* tokens (0 .. 2^31 - 1), hidden size (8 .. TPMLP_EDGE_MAX_H) */
+  int32_t post, pre;       /* tpmlp_norm of y and of r' */
+  int32_t y_type;          /* tpmlp_dtype of y */
+  int32_t r_type;          /* tpmlp_dtype of r, r', and their gradients */
+  int32_t param_type;      /* tpmlp_dtype of the norms' vectors and the gate */
+  float alpha, eps;        /* residual scale (finite); the norms' eps (finite, >= 0) */
+  const void *w_post, *b_post; /* [H]; w with a norm, b (nullable) with a LayerNorm */
+  const void *w_pre, *b_pre;   /* [H], likewise */
+  const void* gate;        /* [ceil(M / gate_rows)][H] or NULL (1) */
+  int64_t gate_rows, ld_gate;
+} tpmlp_edge;
+
+/* Forward.  x (bf16) is required with a norm before the next block and NULL
+ * without; r_out is nullable if x is written, and may be r itself (same address
+ * and stride). */
+tpmlp_status tpmlp_edge_fwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r, int64_t ld_r,
+                            void* r_out, int64_t ld_r_out, tpmlp_bf16* x, int64_t ld_x, void* stream);
+
+/* Workspace bytes of tpmlp_edge_bwd (the workgroups' float32 column sums): a
+ * function of M, H, gate_rows (if there is a gate) and whether a norm is a
+ * LayerNorm.  0 if the description is invalid or M is 0. */
+size_t tpmlp_edge_bwd_workspace_bytes(const tpmlp_edge* e);
+
+/* Backward.  r_out is the stream that the forward wrote (the norms' statistics are
+ * recomputed from it and from y); dr_out (nullable: zeros) the gradient that
+ * reaches it from later blocks; dx[M,H] (dx_type) the gradient of x.  dx and r_out
+ * are required with a norm before the next block and unused (NULL) without, where
+ * dr_out is required.  Writes dr[M,H], the stream's gradient before the edge (may
+ * be dr_out itself), dy[M,H] in bf16 (the dZ of the MLP's backward; NULL without
+ * y), and the float32 gradients dw_post, db_post, dw_pre, db_pre [H] and dgate
+ * [ceil(M / gate_rows)][H], each nullable and only where its parameter exists.
+ * ws is required if any of these five is. */
+tpmlp_status tpmlp_edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r_out, int64_t ld_r_out,
+                            const void* dr_out, int64_t ld_dr_out, const void* dx, int dx_type, int64_t ld_dx,
+                            void* dr, int64_t ld_dr, tpmlp_bf16* dy, int64_t ld_dy, float* dw_post, float* db_post,
+                            float* dw_pre, float* db_pre, float* dgate, void* ws, size_t ws_bytes, void* stream);
+
+/* Expert route: each of T tokens chooses K of E experts, whose MLPs take their
+ * tokens as contiguous rows.  Pair p = t K + k is token t's choice k.  The sorted
+ * buffers have `rows` rows; expert e's segment starts at row offsets[e], holds its
+ * counts[e] pairs in the order of p, and is padded to a multiple of `align` rows
+ * (8 gives segments that tpmlp_fwd takes).  With capacity 0 the segments follow
+ * one another; with a capacity (a multiple of align) every segment is that long
+ * and an expert's pairs beyond it are dropped, so all sizes are known beforehand.
+ * A pair whose id is outside 0 .. E-1 is dropped. */
+#define TPMLP_ROUTE_MAX_EXPERTS 512
+#define TPMLP_ROUTE_MAX_CHOICES 64
+
+/* Rows of the sorted buffers: E * capacity, or, with capacity 0, enough for any
+ * choice, T K + min(E, T K) (align - 1) rounded down to a multiple of align.  -1 if
+ * an argument is invalid (T >= 0, 1 <= K <= TPMLP_ROUTE_MAX_CHOICES, 1 <= E <=
+ * TPMLP_ROUTE_MAX_EXPERTS, align >= 1, T K and the rows at most 2^31 - 1). */
+int64_t tpmlp_route_rows(int64_t T, int K, int E, int align, int capacity);
+
+/* Workspace bytes of tpmlp_route_sort; 0 if none is needed or T K is invalid. */
+size_t tpmlp_route_workspace_bytes(int64_t T, int K, int E);
+
+/* Sorts the pairs by expert.  ids [T,K], int32 (id_bits 32) or int64 (64).  Writes
+ * counts[E], offsets[E+1], row_of[T,K] (the pair's sorted row, -1 if dropped) and
+ * src_of[rows] (the row's pair, -1 for padding), all int32, where rows is
+ * tpmlp_route_rows of the same arguments. */
+tpmlp_status tpmlp_route_sort(const void* ids, int id_bits, int64_t T, int K, int E, int align, int capacity,
+                              int32_t* counts, int32_t* offsets, int32_t* row_of, int32_t* src_of, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* Xs[row_of[t,k]] = X[t] for every k, zeros where src_of is -1.  X[T,H], Xs[rows,H]
+ * bf16, H from 8 to 2^23.  row_of and src_of are tpmlp_route_sort's; entries of
+ * row_of outside 0 .. rows-1 count as dropped. */
+tpmlp_status tpmlp_route_dispatch(const tpmlp_bf16* X, int64_t ld_x, const int32_t* row_of, const int32_t* src_of,
+                                  int64_t T, int K, int64_t H, int64_t rows, tpmlp_bf16* Xs, int64_t ld_xs,
+                                  void* stream);
+
+/* Y[t] = sum over k of w[t,k] Zs[row_of[t,k]], dropped pairs left out (zeros if all
+ * of a token's are), added in the order of k.  Zs[rows,H] z_type, w[T,K] float32
+ * (NULL: ones, which is the gradient of tpmlp_route_dispatch), Y[T,H] y_type. */
+tpmlp_status tpmlp_route_combine(const void* Zs, int z_type, int64_t ld_zs, const int32_t* row_of, const float* w,
+                                 int64_t T, int K, int64_t H, int64_t rows, void* Y, int y_type, int64_t ld_y,
+                                 void* stream);
+
+/* Gradients of tpmlp_route_combine: dZs[row_of[t,k]] = w[t,k] dY[t] in bf16 (the dZ
+ * of the experts' backward), zeros where src_of is -1, and dw[t,k] = <dY[t],
+ * Zs[row_of[t,k]]>, 0 where dropped.  dw and Zs are NULL together, dZs and src_of
+ * are NULL together; one of the outputs is written.  w NULL: ones. */
+tpmlp_status tpmlp_route_combine_bwd(const void* dY, int dy_type, int64_t ld_dy, const void* Zs, int z_type,
+                                     int64_t ld_zs, const int32_t* row_of, const int32_t* src_of, const float* w,
+                                     int64_t T, int K, int64_t H, int64_t rows, tpmlp_bf16* dZs, int64_t ld_dzs,
+                                     float* dw, void* stream);
+
+/* Global norm and clipping of n gradients (n >= 0; any sizes, 0 included):
+ *   norm = |scale| sqrt(sum of all g^2),   out = g * scale * c,
+ *   c = max_norm / norm if norm is finite and above max_norm, 1 otherwise.
+ * `scale` (finite) undoes a loss scale or averages over steps.  A norm that is not
+ * finite is reported and clips nothing, so the caller can skip the step.  grads,
+ * outs, sizes and types (tpmlp_dtype) are host arrays of n entries; outs NULL (or an
+ * entry equal to its gradient) scales in place, and a gradient in place that needs
+ * no change is not written.  Squares are summed in float64. */
+
+/* Workspace bytes of tpmlp_grad_sumsq and tpmlp_clip_grad_norm; 0 if invalid. */
+size_t tpmlp_grad_workspace_bytes(const int64_t* sizes, int n);
+
+/* *sumsq (device float64) = sum of squares of all values.  Ranks that hold
+ * different parameters add theirs before tpmlp_grad_clip. */
+tpmlp_status tpmlp_grad_sumsq(const void* const* grads, const int64_t* sizes, const int32_t* types, int n,
+                              double* sumsq, void* ws, size_t ws_bytes, void* stream);
+
+/* Scales by the norm that *sumsq (device) gives; norm (device float, nullable)
+ * receives it.  max_norm > 0 (+infinity: never clip). */
+tpmlp_status tpmlp_grad_clip(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types,
+                             int n, const double* sumsq, float scale, float max_norm, float* norm, void* stream);
+
+/* Both in one call, for gradients that one rank holds whole. */
+tpmlp_status tpmlp_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes,
+                                  const int32_t* types, int n, float scale, float max_norm, float* norm, void* ws,
+                                  size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Kernel timing (measurement aid; not needed to compute anything)           */
 /* ------------------------------------------------------------------------ */
 

@@ -40,6 +40,17 @@ _lib = None
 _vp, _sz, _i64, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.c_int
 _PP = ctypes.POINTER(ctypes.c_void_p)
 
+
+
+class EdgeDesc(ctypes.Structure):
+    """tpmlp_edge: the description of the edge between two blocks."""
+    _fields_ = [("M", _i64), ("H", _i64), ("post", ctypes.c_int32), ("pre", ctypes.c_int32),
+                ("y_type", ctypes.c_int32), ("r_type", ctypes.c_int32), ("param_type", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("eps", ctypes.c_float), ("w_post", _vp), ("b_post", _vp),
+                ("w_pre", _vp), ("b_pre", _vp), ("gate", _vp), ("gate_rows", _i64), ("ld_gate", _i64)]
+
+
+_EP = ctypes.POINTER(EdgeDesc)
 _SIGS = {
     "tpmlp_abi_version": ([], _int),
     "tpmlp_status_str": ([_int], ctypes.c_char_p),
@@ -65,6 +76,21 @@ _SIGS = {
     "tpmlp_fp8_tp_fwd": ([_vp, _PP, _PP, _PP, _vp, _int, _i64, _i64, _i64, _vp, _sz, _vp], _int),
     "tpmlp_fp8_tp_bwd": ([_vp, _vp, _PP, _PP, _PP, _PP, _PP, _vp, _int, _i64, _i64, _i64, _vp, _sz, _vp], _int),
     "tpmlp_fp8_quantize": ([_vp, _i64, _i64, _int, _int, _vp, _vp, _vp], _int),
+    "tpmlp_edge_fwd": ([_EP, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp], _int),
+    "tpmlp_edge_bwd_workspace_bytes": ([_EP], _sz),
+    "tpmlp_edge_bwd": ([_EP, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _int, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                        _vp, _vp, _vp, _sz, _vp], _int),
+    "tpmlp_route_rows": ([_i64, _int, _int, _int, _int], _i64),
+    "tpmlp_route_workspace_bytes": ([_i64, _int, _int], _sz),
+    "tpmlp_route_sort": ([_vp, _int, _i64, _int, _int, _int, _int, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
+    "tpmlp_route_dispatch": ([_vp, _i64, _vp, _vp, _i64, _int, _i64, _i64, _vp, _i64, _vp], _int),
+    "tpmlp_route_combine": ([_vp, _int, _i64, _vp, _vp, _i64, _int, _i64, _i64, _vp, _int, _i64, _vp], _int),
+    "tpmlp_route_combine_bwd": ([_vp, _int, _i64, _vp, _int, _i64, _vp, _vp, _vp, _i64, _int, _i64, _i64, _vp, _i64,
+                                 _vp, _vp], _int),
+    "tpmlp_grad_workspace_bytes": ([_vp, _int], _sz),
+    "tpmlp_grad_sumsq": ([_vp, _vp, _vp, _int, _vp, _vp, _sz, _vp], _int),
+    "tpmlp_grad_clip": ([_vp, _vp, _vp, _vp, _int, _vp, ctypes.c_float, ctypes.c_float, _vp, _vp], _int),
+    "tpmlp_clip_grad_norm": ([_vp, _vp, _vp, _vp, _int, ctypes.c_float, ctypes.c_float, _vp, _vp, _sz, _vp], _int),
     "tpmlp_timing_begin": ([_int], _int),
     "tpmlp_timing_begin_kinds": ([_int, ctypes.c_uint], _int),
     "tpmlp_timing_end": ([ctypes.POINTER(_int), ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_int)], _int),
@@ -432,6 +458,256 @@ def tpmlp_fp8_quantize(T, fmt: int, transpose: bool, codes, amax, stream=None):
     st = lib().tpmlp_fp8_quantize(_ptr(T), R, C, int(fmt), 1 if transpose else 0, _ptr(codes), _ptr(amax),
                                   _stream(stream))
     _check(st, "tpmlp_fp8_quantize")
+
+
+# --- block operators ----------------------------------------------------------------
+F32, BF16 = 0, 1                                       # tpmlp_dtype
+NORMS = {"none": 0, "rms": 1, "layer": 2}              # tpmlp_norm
+EDGE_MAX_H = 32768                                     # TPMLP_EDGE_MAX_H
+ROUTE_MAX_EXPERTS, ROUTE_MAX_CHOICES = 512, 64         # TPMLP_ROUTE_MAX_*
+
+
+def _dtype(t, name) -> int:
+    """tpmlp_dtype of a tensor (bf16 data may be uint16 or int16 bits)."""
+    import torch
+    if t.dtype == torch.float32:
+        return F32
+    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        return BF16
+    raise TypeError(f"{name} must be float32 or hold bf16 bits (bfloat16/uint16/int16), got {t.dtype}")
+
+
+def _rows(t, shape, name, kind=None):
+    """(pointer, row stride) of a [rows, columns] tensor with contiguous columns, after
+    checking its shape and, if given, its tpmlp_dtype."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if kind is not None and _dtype(t, name) != kind:
+        raise TypeError(f"{name} must be {'float32' if kind == F32 else 'bf16'}, got {t.dtype}")
+    row, col = t.stride()
+    if shape[1] > 1 and col != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    return t.data_ptr(), (row if shape[0] > 1 else 0)
+
+
+def _flat(t, n, dtype, name):
+    """Pointer of a contiguous tensor of n elements."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous {dtype} tensor")
+    if t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} elements, expected {n}")
+    return t.data_ptr()
+
+
+def _ws(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+
+
+def edge_desc(H: int, post="none", pre="none", w_post=None, b_post=None, w_pre=None, b_pre=None, gate=None,
+              gate_rows: int = 0, alpha: float = 1.0, eps: float = 1e-5) -> EdgeDesc:
+    """A tpmlp_edge with its parameters (all float32 or all bf16; the gate [G, H], or [H] for
+    one row); M, y_type and r_type are set by each call.  gate_rows 0: one row for all tokens."""
+    params = [(n, t) for n, t in (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre),
+                                  ("gate", gate)) if t is not None]
+    kinds = {_dtype(t, n) for n, t in params}
+    if len(kinds) > 1:
+        raise TypeError("the edge's parameters must have one type")
+    for n, t in params:
+        if n != "gate":
+            _flat(t, H, t.dtype, n)
+    d = EdgeDesc(M=0, H=H, post=NORMS[post], pre=NORMS[pre], param_type=kinds.pop() if kinds else F32, alpha=alpha,
+                 eps=eps, w_post=_ptr(w_post), b_post=_ptr(b_post), w_pre=_ptr(w_pre), b_pre=_ptr(b_pre))
+    if gate is not None:
+        g = gate if gate.dim() == 2 else gate.unsqueeze(0)
+        d.gate, d.ld_gate = _rows(g, (g.shape[0], H), "gate")
+        d.gate_rows = gate_rows if gate_rows > 0 else (1 << 31) - 1
+    elif gate_rows < 0:
+        raise ValueError("gate_rows must not be negative")
+    return d
+
+
+def _gate_groups(d: EdgeDesc, M: int) -> int:
+    return -(-M // d.gate_rows) if d.gate else 0
+
+
+def tpmlp_edge_fwd(d: EdgeDesc, y, r, r_out, x, stream=None):
+    """r_out = alpha r + gate * N_post(y), x = N_pre(r_out); y None: no block before the edge."""
+    M, H = r.shape[0], d.H
+    d.M, d.r_type = M, _dtype(r, "r")
+    pr, lr = _rows(r, (M, H), "r")
+    py = ly = None
+    if y is not None:
+        d.y_type = _dtype(y, "y")
+        py, ly = _rows(y, (M, H), "y")
+    po, lo = _rows(r_out, (M, H), "r_out", d.r_type)
+    px, lx = _rows(x, (M, H), "x", BF16)
+    st = lib().tpmlp_edge_fwd(ctypes.byref(d), py, ly or 0, pr, lr, po, lo, px, lx, _stream(stream))
+    if st:
+        _check(st, "tpmlp_edge_fwd")
+
+
+def tpmlp_edge_bwd_workspace_bytes(d: EdgeDesc, M: int) -> int:
+    d.M = M
+    return lib().tpmlp_edge_bwd_workspace_bytes(ctypes.byref(d))
+
+
+def tpmlp_edge_bwd(d: EdgeDesc, y, r_out, dr_out, dx, dr, dy, dw_post=None, db_post=None, dw_pre=None, db_pre=None,
+                   dgate=None, ws=None, stream=None):
+    """Backward of the edge; r_out is the stream the forward wrote, dr and dy are written."""
+    import torch
+    M, H = dr.shape[0], d.H
+    d.M, d.r_type = M, _dtype(dr, "dr")
+    pr, lr = _rows(r_out, (M, H), "r_out", d.r_type)
+    po, lo = _rows(dr_out, (M, H), "dr_out", d.r_type)
+    px, lx = _rows(dx, (M, H), "dx")
+    pd, ld = _rows(dr, (M, H), "dr")
+    py, ly = _rows(y, (M, H), "y")
+    if y is not None:
+        d.y_type = _dtype(y, "y")
+    pg, lg = _rows(dy, (M, H), "dy", BF16)
+    f32 = torch.float32
+    grads = [_flat(dw_post, H, f32, "dw_post"), _flat(db_post, H, f32, "db_post"), _flat(dw_pre, H, f32, "dw_pre"),
+             _flat(db_pre, H, f32, "db_pre"),
+             _flat(dgate, _gate_groups(d, M) * H, f32, "dgate") if dgate is not None else None]
+    pw, nw = _ws(ws)
+    st = lib().tpmlp_edge_bwd(ctypes.byref(d), py, ly, pr, lr, po, lo, px, _dtype(dx, "dx") if dx is not None else F32,
+                              lx, pd, ld, pg, lg, *grads, pw, nw, _stream(stream))
+    if st:
+        _check(st, "tpmlp_edge_bwd")
+
+
+def tpmlp_route_rows(T: int, K: int, E: int, align: int = 8, capacity: int = 0) -> int:
+    return lib().tpmlp_route_rows(T, K, E, align, capacity)
+
+
+def tpmlp_route_workspace_bytes(T: int, K: int, E: int) -> int:
+    return lib().tpmlp_route_workspace_bytes(T, K, E)
+
+
+def tpmlp_route_sort(ids, E: int, align: int, capacity: int, counts, offsets, row_of, src_of, ws=None, stream=None):
+    """Pairs sorted by expert; ids [T,K] int32 or int64, the outputs int32."""
+    import torch
+    T, K = ids.shape
+    if ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise TypeError("ids must be a contiguous int32 or int64 tensor")
+    i32, rows = torch.int32, max(0, tpmlp_route_rows(T, K, E, align, capacity))
+    pw, nw = _ws(ws)
+    st = lib().tpmlp_route_sort(ids.data_ptr(), 32 if ids.dtype == i32 else 64, T, K, E, align, capacity,
+                                _flat(counts, E, i32, "counts"), _flat(offsets, E + 1, i32, "offsets"),
+                                _flat(row_of, T * K, i32, "row_of"), _flat(src_of, rows, i32, "src_of"), pw, nw,
+                                _stream(stream))
+    if st:
+        _check(st, "tpmlp_route_sort")
+
+
+def tpmlp_route_dispatch(X, row_of, src_of, Xs, stream=None):
+    """Xs[row_of[t,k]] = X[t], zeros on padding rows; bf16."""
+    import torch
+    (T, K), (rows, H) = row_of.shape, Xs.shape
+    px, lx = _rows(X, (T, H), "X", BF16)
+    ps, ls = _rows(Xs, (rows, H), "Xs", BF16)
+    st = lib().tpmlp_route_dispatch(px, lx, _flat(row_of, T * K, torch.int32, "row_of"),
+                                    _flat(src_of, rows, torch.int32, "src_of"), T, K, H, rows, ps, ls, _stream(stream))
+    if st:
+        _check(st, "tpmlp_route_dispatch")
+
+
+def tpmlp_route_combine(Zs, row_of, w, Y, stream=None):
+    """Y[t] = sum over k of w[t,k] Zs[row_of[t,k]]; w None: ones."""
+    import torch
+    (T, K), (rows, H) = row_of.shape, Zs.shape
+    pz, lz = _rows(Zs, (rows, H), "Zs")
+    py, ly = _rows(Y, (T, H), "Y")
+    st = lib().tpmlp_route_combine(pz, _dtype(Zs, "Zs"), lz, _flat(row_of, T * K, torch.int32, "row_of"),
+                                   _flat(w, T * K, torch.float32, "w"), T, K, H, rows, py, _dtype(Y, "Y"), ly,
+                                   _stream(stream))
+    if st:
+        _check(st, "tpmlp_route_combine")
+
+
+def tpmlp_route_combine_bwd(dY, Zs, row_of, src_of, w, dZs, dw, stream=None):
+    """dZs[row_of[t,k]] = w[t,k] dY[t] (bf16) and dw[t,k] = <dY[t], Zs[row_of[t,k]]>; dZs (with
+    src_of) or dw (with Zs) may be None."""
+    import torch
+    T, K = row_of.shape
+    H = dY.shape[1]
+    rows = (dZs if dZs is not None else Zs).shape[0]
+    pd, ld = _rows(dY, (T, H), "dY")
+    pz, lz = _rows(Zs, (rows, H), "Zs")
+    po, lo = _rows(dZs, (rows, H), "dZs", BF16)
+    st = lib().tpmlp_route_combine_bwd(pd, _dtype(dY, "dY"), ld, pz, _dtype(Zs, "Zs") if Zs is not None else F32, lz,
+                                       _flat(row_of, T * K, torch.int32, "row_of"),
+                                       _flat(src_of, rows, torch.int32, "src_of"), _flat(w, T * K, torch.float32, "w"),
+                                       T, K, H, rows, po, lo, _flat(dw, T * K, torch.float32, "dw"), _stream(stream))
+    if st:
+        _check(st, "tpmlp_route_combine_bwd")
+
+
+class GradTable:
+    """The host arrays that the gradient calls take: addresses, sizes and types of float32 or
+    bf16 tensors, and of the tensors that receive the scaled values (None: in place).  Keeps
+    the tensors alive; their storage must stay where it is."""
+
+    def __init__(self, grads, outs=None):
+        self.grads, self.outs, n = list(grads), None if outs is None else list(outs), len(grads)
+        if self.outs is not None and len(self.outs) != n:
+            raise ValueError(f"outs has {len(self.outs)} entries, expected {n}")
+        self.n = n
+        self.ptrs, self.out_ptrs = (_vp * max(n, 1))(), (_vp * max(n, 1))()
+        self.sizes, self.types = (_i64 * max(n, 1))(), (ctypes.c_int32 * max(n, 1))()
+        for i, g in enumerate(self.grads):
+            o = g if self.outs is None else self.outs[i]
+            if not g.is_contiguous() or not o.is_contiguous():
+                raise ValueError(f"gradient {i} and its output must be contiguous")
+            if o.dtype != g.dtype or o.numel() != g.numel():
+                raise ValueError(f"outs[{i}] differs from its gradient in type or size")
+            self.ptrs[i], self.out_ptrs[i] = g.data_ptr(), o.data_ptr()
+            self.sizes[i], self.types[i] = g.numel(), _dtype(g, f"grads[{i}]")
+
+
+def tpmlp_grad_workspace_bytes(table: GradTable) -> int:
+    return lib().tpmlp_grad_workspace_bytes(table.sizes, table.n)
+
+
+def _one(t, dtype, name):
+    if t.dtype != dtype or t.numel() != 1:
+        raise TypeError(f"{name} must be one {dtype}")
+    return t.data_ptr()
+
+
+def tpmlp_grad_sumsq(table: GradTable, sumsq, ws, stream=None):
+    """sumsq (one float64) = sum of squares of all gradients."""
+    import torch
+    pw, nw = _ws(ws)
+    st = lib().tpmlp_grad_sumsq(table.ptrs, table.sizes, table.types, table.n, _one(sumsq, torch.float64, "sumsq"),
+                                pw, nw, _stream(stream))
+    if st:
+        _check(st, "tpmlp_grad_sumsq")
+
+
+def tpmlp_grad_clip(table: GradTable, sumsq, max_norm: float, norm=None, scale: float = 1.0, stream=None):
+    """Scales the gradients by scale * min(1, max_norm / norm), norm = |scale| sqrt(sumsq)."""
+    import torch
+    st = lib().tpmlp_grad_clip(table.ptrs, table.out_ptrs, table.sizes, table.types, table.n,
+                               _one(sumsq, torch.float64, "sumsq"), scale, max_norm,
+                               None if norm is None else _one(norm, torch.float32, "norm"), _stream(stream))
+    if st:
+        _check(st, "tpmlp_grad_clip")
+
+
+def tpmlp_clip_grad_norm(table: GradTable, max_norm: float, norm, ws, scale: float = 1.0, stream=None):
+    """tpmlp_grad_sumsq and tpmlp_grad_clip in one call."""
+    import torch
+    pw, nw = _ws(ws)
+    st = lib().tpmlp_clip_grad_norm(table.ptrs, table.out_ptrs, table.sizes, table.types, table.n, scale, max_norm,
+                                    None if norm is None else _one(norm, torch.float32, "norm"), pw, nw,
+                                    _stream(stream))
+    if st:
+        _check(st, "tpmlp_clip_grad_norm")
 
 
 def tpmlp_timing_begin(capacity: int):

@@ -18,7 +18,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtpmlp.so")
-SOURCES = ["gemm.hip", "reduce.hip", "ffn.hip", "fp8.hip", "tpmlp.hip"]
+SOURCES = ["gemm.hip", "reduce.hip", "ffn.hip", "fp8.hip", "tpmlp.hip", "block_edge.hip", "block_edge_bwd.hip",
+           "block_edge_bwd_layer.hip", "block_route.hip", "block_clip.hip", "block.hip"]
 
 ARCH = "gfx950"
 CFLAGS = [

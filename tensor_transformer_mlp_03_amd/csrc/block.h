@@ -1,0 +1,144 @@
+// Internal declarations of the block operators: what stands around one MLP in a
+// training or serving step (the block's edge, the expert route, gradient clipping).
+// All of them move each value once and compute a few operations on it, so HBM
+// bandwidth bounds the large calls and launch latency the small ones.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/tpmlp.h"
+#include "common.h"
+
+namespace tpmlp {
+
+// ---------------------------------------------------------------------------
+// The edge between two blocks (block_edge.hip, block_edge_bwd.hip)
+// ---------------------------------------------------------------------------
+struct EdgeFwdArgs {
+  const void *y, *r;
+  void* r_out;   // nullable
+  uint16_t* x;   // nullable
+  const void *w_post, *b_post, *gate, *w_pre, *b_pre;  // nullable
+  int64_t ld_y, ld_r, ld_r_out, ld_x, ld_gate;
+  int64_t M, gate_rows;
+  int H, post, pre, p_bf16;
+  float alpha, eps;
+};
+
+struct EdgeBwdArgs {
+  const void *y, *r, *dr_out, *dx;  // dr_out, dx nullable
+  void* dr;
+  uint16_t* dy;
+  const void *w_post, *gate, *w_pre;
+  float* part;  // [groups * chunks][acc][H] column sums of each workgroup's rows
+  int64_t ld_y, ld_r, ld_dr_out, ld_dx, ld_dr, ld_dy, ld_gate;
+  int64_t M, gate_rows;
+  int64_t chunk_rows;  // rows of one workgroup, all in one gate group
+  int chunks;          // workgroups per gate group
+  int H, post, pre, p_bf16, dx_bf16;
+  float alpha, eps;
+};
+
+struct EdgeFinishArgs {
+  const float* part;
+  const void *w_post, *b_post, *gate;
+  float *dw_post, *db_post, *dgate, *dw_pre, *db_pre;  // nullable
+  int64_t groups, ld_gate;
+  int chunks, n_acc, H, p_bf16;
+};
+
+// The edge's column sums: which of them a workgroup keeps, in this order.
+//   S1 = sum d yh, T1 = sum dx xh; with a LayerNorm also S0 = sum d, T0 = sum dx.
+constexpr int EDGE_ACC_RMS = 2, EDGE_ACC_LAYER = 4;
+
+// How the backward's rows are cut: a function of the sizes alone, so the
+// workspace query and the launch agree.
+struct EdgeBwdPlan {
+  int64_t groups, chunk_rows;
+  int chunks, n_acc;
+  size_t ws_bytes;
+};
+EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer);
+
+hipError_t launch_edge_fwd(const EdgeFwdArgs& a, int y_type, int r_type, hipStream_t s);  // y_type -1: no y
+hipError_t launch_edge_bwd(const EdgeBwdArgs& a, const EdgeBwdPlan& p, int y_type, int r_type, hipStream_t s);
+hipError_t launch_edge_finish(const EdgeFinishArgs& a, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// The expert route (block_route.hip)
+// ---------------------------------------------------------------------------
+struct RouteSortArgs {
+  const void* ids;
+  int ids64;
+  int64_t pairs, rows;
+  int E, align, capacity;
+  int32_t *counts, *offsets, *row_of, *src_of;
+  int32_t* hist;     // [blocks][E], unused by the one-workgroup form
+  int blocks;
+  int64_t per_block;  // pairs of one workgroup
+};
+hipError_t launch_route_sort(const RouteSortArgs& a, hipStream_t s);
+// Pairs of one workgroup of the sort and the workgroups that cover `pairs`.
+int64_t route_sort_blocks(int64_t pairs, int64_t* per_block);
+
+struct RouteDispatchArgs {
+  const uint16_t* x;
+  uint16_t* xs;
+  const int32_t *row_of, *src_of;
+  int64_t T, rows, ld_x, ld_xs;
+  int K, H;
+  int token_blocks, segments;
+};
+hipError_t launch_route_dispatch(RouteDispatchArgs a, hipStream_t s);
+
+struct RouteCombineArgs {
+  const void* zs;
+  void* y;
+  const float* w;  // nullable: 1
+  const int32_t* row_of;
+  int64_t T, rows, ld_zs, ld_y;
+  int K, H, segments;
+};
+hipError_t launch_route_combine(RouteCombineArgs a, int z_type, int y_type, hipStream_t s);
+
+struct RouteCombineBwdArgs {
+  const void *dy, *zs;  // zs nullable with dw
+  uint16_t* dzs;
+  float* dw;
+  const float* w;
+  const int32_t *row_of, *src_of;
+  int64_t T, rows, ld_dy, ld_zs, ld_dzs;
+  int K, H;
+  int token_blocks;
+};
+hipError_t launch_route_combine_bwd(RouteCombineBwdArgs a, int dy_type, int z_type, hipStream_t s);
+
+// ---------------------------------------------------------------------------
+// Gradient norm and clipping (block_clip.hip)
+// ---------------------------------------------------------------------------
+// Tensors of one launch: the table travels in the kernel's arguments, which
+// keeps a call free of host-to-device copies (and so capturable); 28 bytes a
+// tensor stay below the 4 KiB that every launch path takes.
+constexpr int CLIP_TENSORS = 128;
+constexpr int64_t CLIP_CHUNK = 16384;  // elements of one unit of work
+constexpr int CLIP_BLOCKS = 2048;      // most workgroups (and partial sums) of one launch
+
+struct ClipArgs {
+  const void* in[CLIP_TENSORS];
+  void* out[CLIP_TENSORS];
+  int64_t size[CLIP_TENSORS];       // elements; bit 62 set: bf16
+  uint32_t first[CLIP_TENSORS + 1]; // first chunk of each tensor; [n] = all chunks
+  int n;
+  double* part;       // sumsq launches: one partial per workgroup; clip launches: n_part partials
+  int n_part;
+  float scale, max_norm;
+  float* norm;        // nullable
+};
+static_assert(sizeof(ClipArgs) <= 4096, "kernel arguments stay below 4 KiB");
+
+hipError_t launch_clip_sumsq(const ClipArgs& a, int blocks, hipStream_t s);
+hipError_t launch_clip_total(const double* part, int n, double* total, hipStream_t s);
+hipError_t launch_clip_scale(const ClipArgs& a, int blocks, hipStream_t s);
+
+}  // namespace tpmlp

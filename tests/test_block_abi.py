@@ -1,0 +1,275 @@
+"""Argument checks of the block operators: every refusal happens on the host, before any
+HIP call, and names its argument.  Runs where no GPU is visible, so that even a check that
+failed could not send a made-up address to a kernel."""
+import ctypes
+import os
+
+import pytest
+
+from tensor_transformer_mlp_03_amd import _lib as L
+
+
+def _gpu_visible():
+    try:
+        import torch
+        return torch.cuda.device_count() > 0
+    except Exception:
+        return False
+
+
+pytestmark = [
+    pytest.mark.skipif(not os.path.exists(L.LIB_PATH), reason="libtpmlp.so not built"),
+    pytest.mark.skipif(_gpu_visible(), reason="made-up device addresses are only passed where no GPU is visible"),
+]
+
+OK, NULL, SHAPE, ALIGN, WS, SHARDS, HIP, UNSUP, ALIAS, NO_FORWARD = range(10)
+PASSED = (HIP, UNSUP)  # every check passed: the next step is the device's
+
+
+def _p(i, off=0):
+    return (1 << 40) + i * (1 << 34) + off
+
+
+def _err():
+    return L.lib().tpmlp_last_error().decode()
+
+
+# --- edge -------------------------------------------------------------------------------------------------------
+def _desc(**kw):
+    a = dict(M=16, H=64, post=1, pre=1, y_type=0, r_type=0, param_type=1, alpha=1.0, eps=1e-5, w_post=_p(10),
+             b_post=None, w_pre=_p(11), b_pre=None, gate=None, gate_rows=0, ld_gate=0)
+    a.update(kw)
+    return L.EdgeDesc(**a)
+
+
+def _fwd(d=None, **kw):
+    a = dict(y=_p(0), ly=0, r=_p(1), lr=0, ro=_p(2), lo=0, x=_p(3), lx=0)
+    a.update(kw)
+    d = _desc() if d is None else d
+    st = L.lib().tpmlp_edge_fwd(ctypes.byref(d), a["y"], a["ly"], a["r"], a["lr"], a["ro"], a["lo"], a["x"], a["lx"], None)
+    return st, _err()
+
+
+def _bwd(d=None, **kw):
+    a = dict(y=_p(0), ly=0, r=_p(1), lr=0, do=_p(2), lo=0, dx=_p(3), t=0, lx=0, dr=_p(4), ld=0, dy=_p(5), lg=0,
+             dwp=_p(6), dbp=None, dwn=_p(7), dbn=None, dg=None, ws=_p(8), n=1 << 30)
+    a.update(kw)
+    d = _desc() if d is None else d
+    st = L.lib().tpmlp_edge_bwd(ctypes.byref(d), *a.values(), None)
+    return st, _err()
+
+
+def test_edge_accepts():
+    assert _fwd()[0] in PASSED and _bwd()[0] in PASSED
+    assert _fwd(ro=_p(1))[0] in PASSED                                   # the stream in place
+    assert _fwd(ro=None)[0] in PASSED                                    # only x wanted
+    assert _fwd(_desc(post=0, w_post=None), y=None, ro=None)[0] in PASSED  # the first block's entry
+    assert _fwd(_desc(pre=0, w_pre=None), x=None)[0] in PASSED
+    assert _fwd(_desc(H=65), ly=67, y=_p(0, 4))[0] in PASSED             # odd sizes, strides and addresses
+    assert _bwd(dr=_p(2))[0] in PASSED                                   # dr over dr_out
+    assert _bwd(do=None)[0] in PASSED
+    assert _bwd(dwp=None, dwn=None, ws=None, n=0)[0] in PASSED
+    assert _fwd(_desc(M=0), y=None, r=None, ro=None, x=None)[0] == OK    # no tokens
+    # column blocks of one buffer
+    assert _fwd(y=_p(0), ly=512, x=_p(0, 64 * 4), lx=1024)[0] in PASSED
+
+
+def test_edge_refuses():
+    assert L.lib().tpmlp_edge_fwd(None, *[None, 0] * 4, None) == NULL
+    for kw, text in ((dict(M=-1), "M outside"), (dict(H=7), "H outside"), (dict(H=32769), "H outside"),
+                     (dict(post=3), "tpmlp_norm"), (dict(r_type=2), "tpmlp_dtype"), (dict(param_type=-1), "tpmlp_dtype"),
+                     (dict(alpha=float("nan")), "alpha"), (dict(eps=-1.0), "eps"), (dict(eps=float("inf")), "eps"),
+                     (dict(post=0), "w_post"), (dict(b_post=_p(12)), "b_post"), (dict(b_pre=_p(12)), "b_pre"),
+                     (dict(gate=_p(13), gate_rows=0), "gate_rows"),
+                     (dict(gate=_p(13), gate_rows=4, ld_gate=63), "gate")):
+        for call in (_fwd, _bwd):
+            st, msg = call(_desc(**kw))
+            assert st == SHAPE and text in msg, (kw, st, msg)
+    for kw, text in ((dict(w_post=None), "w_post"), (dict(w_pre=None), "w_pre")):
+        st, msg = _fwd(_desc(**kw))
+        assert st == NULL and text in msg
+    assert _fwd(_desc(w_pre=_p(11, 1)))[0] == ALIGN
+    for kw, text in ((dict(r=None), "r is"), (dict(x=None), "x"), (dict(y=None), "y")):
+        st, msg = _fwd(**kw)
+        assert st == NULL and text in msg, (kw, msg)
+    assert _fwd(_desc(pre=0, w_pre=None))[0] == SHAPE                     # x without a norm
+    assert _fwd(_desc(pre=0, w_pre=None), x=None, ro=None)[0] == NULL    # nothing to write
+    assert _fwd(ly=63)[0] == SHAPE
+    assert _fwd(y=_p(0, 2))[0] == ALIGN and _fwd(x=_p(3, 1))[0] == ALIGN
+    for kw in (dict(x=_p(1)), dict(ro=_p(0)), dict(ro=_p(1, 4)), dict(ro=_p(1), lo=128), dict(x=_p(2, 512)),
+               dict(x=_p(10)), dict(y=_p(0), ly=512, x=_p(0, 64 * 4 - 2), lx=1024)):
+        st, msg = _fwd(**kw)
+        assert st == ALIAS, (kw, st, msg)
+
+
+def test_edge_backward_refuses():
+    for kw, text in ((dict(dx=None), "dx"), (dict(r=None), "r_out"), (dict(dr=None), "dr"), (dict(dy=None), "dy"),
+                     (dict(ws=None), "ws")):
+        st, msg = _bwd(**kw)
+        assert st == NULL and text in msg, (kw, st, msg)
+    assert _bwd(t=2)[0] == SHAPE
+    for kw in (dict(dbp=_p(9)), dict(dbn=_p(9)), dict(dg=_p(9))):
+        assert _bwd(**kw)[0] == SHAPE                                     # a gradient without its parameter
+    plain = dict(pre=0, w_pre=None)
+    assert _bwd(_desc(**plain), dwn=None)[0] == SHAPE                      # dx without a norm
+    assert _bwd(_desc(**plain), dwn=None, dx=None, r=None, do=None)[0] == NULL
+    assert _bwd(_desc(**plain), dwn=None, dx=None, r=None)[0] in PASSED
+    assert _bwd(_desc(post=0, w_post=None), y=None, dwp=None)[0] == SHAPE  # dy without y
+    d = _desc()
+    need = L.lib().tpmlp_edge_bwd_workspace_bytes(ctypes.byref(d))
+    assert need > 0 and _bwd(n=need)[0] in PASSED and _bwd(n=need - 1)[0] == WS
+    assert _bwd(ws=_p(8, 8))[0] == ALIGN and _bwd(dwp=_p(6, 2))[0] == ALIGN
+    for kw in (dict(dr=_p(1)), dict(dr=_p(2, 4)), dict(dy=_p(0)), dict(dwp=_p(7)), dict(dwp=_p(3)), dict(ws=_p(4)),
+               dict(dwn=_p(11))):
+        assert _bwd(**kw)[0] == ALIAS, kw
+
+
+def test_edge_workspace_query():
+    q = lambda **kw: L.lib().tpmlp_edge_bwd_workspace_bytes(ctypes.byref(_desc(**kw)))  # noqa: E731
+    assert q(M=0) == 0 and q(H=4) == 0 and q(gate=_p(1), gate_rows=0) == 0
+    assert q(M=4096, H=1024) >= 2 * 1024 * 4
+    assert q(M=4096, H=1024, post=2) == 2 * q(M=4096, H=1024)            # a LayerNorm keeps twice the sums
+    assert q(M=64, gate=_p(1), gate_rows=1) >= 64 * 64 * 4               # a slice a gate row
+
+
+# --- route ------------------------------------------------------------------------------------------------------
+def test_route_rows():
+    rows = lambda *a: L.lib().tpmlp_route_rows(*a)  # noqa: E731
+    assert rows(16, 2, 8, 8, 0) == 32 + 8 * 7
+    assert rows(1, 1, 8, 8, 0) == 8 and rows(0, 1, 8, 8, 0) == 0
+    assert rows(5, 3, 4, 1, 0) == 15 and rows(5, 3, 4, 8, 24) == 96
+    for bad in ((-1, 1, 8, 8, 0), (4, 0, 8, 8, 0), (4, 65, 8, 8, 0), (4, 1, 0, 8, 0), (4, 1, 513, 8, 0), (4, 1, 8, 0, 0),
+                (4, 1, 8, 8, 12), (4, 1, 8, 8, -8), (1 << 31, 1, 8, 8, 0), (1 << 30, 2, 8, 8, 0),
+                (4, 1, 512, 8, 1 << 23)):
+        assert rows(*bad) == -1, bad
+
+
+def _sort(**kw):
+    a = dict(ids=_p(0), bits=32, T=4096, K=4, E=16, align=8, capacity=0, counts=_p(1), offsets=_p(2), row_of=_p(3),
+             src_of=_p(4), ws=_p(5), n=1 << 24)
+    a.update(kw)
+    return L.lib().tpmlp_route_sort(*a.values(), None), _err()
+
+
+def test_route_sort_arguments():
+    assert _sort()[0] in PASSED and _sort(bits=64)[0] in PASSED
+    assert _sort(T=8, ws=None, n=0)[0] in PASSED                          # one workgroup needs no workspace
+    assert _sort(T=0, ids=None, row_of=None, src_of=None, ws=None, n=0)[0] in PASSED
+    for kw in (dict(bits=16), dict(K=0), dict(E=0), dict(E=513), dict(align=0), dict(capacity=4), dict(T=-1)):
+        assert _sort(**kw)[0] == SHAPE, kw
+    for k in ("ids", "counts", "offsets", "row_of", "src_of", "ws"):
+        assert _sort(**{k: None})[0] == NULL, k
+    need = L.lib().tpmlp_route_workspace_bytes(4096, 4, 16)
+    assert need > 0 and _sort(n=need)[0] in PASSED and _sort(n=need - 1)[0] == WS
+    assert _sort(ids=_p(0, 2))[0] == ALIGN and _sort(bits=64, ids=_p(0, 4))[0] == ALIGN
+    for kw in (dict(row_of=_p(0)), dict(counts=_p(2)), dict(ws=_p(4)), dict(ws=_p(0))):
+        assert _sort(**kw)[0] == ALIAS, kw
+
+
+def _dispatch(**kw):
+    a = dict(X=_p(0), lx=0, row_of=_p(1), src_of=_p(2), T=16, K=2, H=64, rows=64, Xs=_p(3), ls=0)
+    a.update(kw)
+    return L.lib().tpmlp_route_dispatch(*a.values(), None), _err()
+
+
+def _combine(**kw):
+    a = dict(Zs=_p(0), zt=0, lz=0, row_of=_p(1), w=_p(2), T=16, K=2, H=64, rows=64, Y=_p(3), yt=0, ly=0)
+    a.update(kw)
+    return L.lib().tpmlp_route_combine(*a.values(), None), _err()
+
+
+def _combine_bwd(**kw):
+    a = dict(dY=_p(0), dt=0, ld=0, Zs=_p(1), zt=0, lz=0, row_of=_p(2), src_of=_p(3), w=_p(4), T=16, K=2, H=64, rows=64,
+             dZs=_p(5), lo=0, dw=_p(6))
+    a.update(kw)
+    return L.lib().tpmlp_route_combine_bwd(*a.values(), None), _err()
+
+
+def test_route_moves_arguments():
+    for call, outs in ((_dispatch, ("Xs",)), (_combine, ("Y",)), (_combine_bwd, ("dZs", "dw"))):
+        assert call()[0] in PASSED
+        for kw in (dict(H=7), dict(H=(1 << 23) + 1), dict(K=0), dict(K=65), dict(T=-1), dict(rows=-1), dict(rows=1 << 31)):
+            assert call(**kw)[0] == SHAPE, (call, kw)
+        for o in outs:
+            assert call(**{o: _p(1 if call is not _combine_bwd else 2)})[0] == ALIAS  # on row_of
+            assert call(**{o: _p(9, 1)})[0] == ALIGN
+        assert call(row_of=None)[0] == NULL
+    assert _dispatch(X=None)[0] == NULL and _dispatch(src_of=None)[0] == NULL and _dispatch(Xs=None)[0] == NULL
+    assert _dispatch(lx=63)[0] == SHAPE and _dispatch(rows=0, src_of=None, Xs=None)[0] == OK
+    assert _combine(w=None)[0] in PASSED and _combine(zt=2)[0] == SHAPE and _combine(yt=-1)[0] == SHAPE
+    assert _combine(T=0, row_of=None, w=None, Y=None)[0] == OK
+    assert _combine_bwd(w=None)[0] in PASSED and _combine_bwd(dt=3)[0] == SHAPE
+    assert _combine_bwd(dw=None, Zs=None)[0] in PASSED and _combine_bwd(dZs=None, src_of=None)[0] in PASSED
+    for kw in (dict(dw=None), dict(Zs=None), dict(dZs=None), dict(src_of=None),
+               dict(dw=None, Zs=None, dZs=None, src_of=None)):
+        assert _combine_bwd(**kw)[0] == NULL, kw
+
+
+# --- clipping ---------------------------------------------------------------------------------------------------
+def _arrays(ptrs, outs, sizes, types):
+    n = len(ptrs)
+    v, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    return ((v * n)(*ptrs), None if outs is None else (v * n)(*outs), (i64 * n)(*sizes), (i32 * n)(*types), n)
+
+
+def _clip(ptrs=(_p(0), _p(1, 2)), outs=None, sizes=(100, 7), types=(0, 1), scale=1.0, max_norm=1.0, norm=_p(2), ws=_p(3),
+          n_ws=1 << 20):
+    g, o, s, t, n = _arrays(ptrs, outs, sizes, types)
+    return L.lib().tpmlp_clip_grad_norm(g, o, s, t, n, scale, max_norm, norm, ws, n_ws, None), _err()
+
+
+def test_clip_arguments():
+    assert _clip()[0] in PASSED and _clip(norm=None)[0] in PASSED
+    assert _clip(outs=(_p(4), _p(1, 2)))[0] in PASSED
+    assert _clip(ptrs=(None, _p(1)), sizes=(0, 7))[0] in PASSED            # a tensor without elements
+    assert _clip(max_norm=float("inf"))[0] in PASSED
+    for kw in (dict(sizes=(-1, 7)), dict(sizes=(1 << 60, 7)), dict(types=(0, 2)), dict(scale=float("inf")),
+               dict(max_norm=0.0), dict(max_norm=float("nan"))):
+        assert _clip(**kw)[0] == SHAPE, kw
+    assert _clip(ptrs=(None, _p(1)))[0] == NULL and _clip(outs=(None, _p(1)))[0] == NULL and _clip(ws=None)[0] == NULL
+    assert _clip(ptrs=(_p(0, 2), _p(1)))[0] == ALIGN and _clip(norm=_p(2, 1))[0] == ALIGN and _clip(ws=_p(3, 8))[0] == ALIGN
+    assert _clip(outs=(_p(0, 4), _p(5)))[0] == ALIAS
+    g, _, s, t, n = _arrays((_p(0), _p(1)), None, (100, 7), (0, 1))
+    need = L.lib().tpmlp_grad_workspace_bytes(s, n)
+    assert _clip(n_ws=need)[0] in PASSED and _clip(n_ws=need - 1)[0] == WS
+    lib = L.lib()
+    assert lib.tpmlp_grad_sumsq(g, s, t, n, None, _p(3), need, None) == NULL
+    assert lib.tpmlp_grad_sumsq(g, s, t, n, _p(4, 4), _p(3), need, None) == ALIGN
+    assert lib.tpmlp_grad_clip(g, None, s, t, n, None, 1.0, 1.0, None, None) == NULL
+    assert lib.tpmlp_grad_clip(g, None, s, t, -1, _p(4), 1.0, 1.0, None, None) == SHAPE
+    assert lib.tpmlp_grad_clip(None, None, s, t, n, _p(4), 1.0, 1.0, None, None) == NULL
+    assert lib.tpmlp_clip_grad_norm(None, None, None, None, 0, 1.0, 1.0, _p(2), _p(3), 1 << 20, None) in PASSED
+
+
+def test_python_checks():
+    """The binding refuses tensors of the wrong type, shape or layout before it calls the
+    library (CPU tensors; nothing reaches a kernel)."""
+    torch = pytest.importorskip("torch")
+    bf = torch.bfloat16
+    w = torch.ones(16)
+    d = L.edge_desc(16, pre="rms", w_pre=w)
+    r, x = torch.zeros(4, 16), torch.zeros(4, 16, dtype=bf)
+    with pytest.raises(TypeError, match="one type"):
+        L.edge_desc(16, post="rms", pre="rms", w_post=w, w_pre=w.to(bf))
+    with pytest.raises(ValueError, match="expected 16"):
+        L.edge_desc(16, pre="rms", w_pre=torch.ones(15))
+    with pytest.raises(TypeError, match="x must be bf16"):
+        L.tpmlp_edge_fwd(d, None, r, None, torch.zeros(4, 16), stream=0)
+    with pytest.raises(TypeError, match="r_out must be float32"):
+        L.tpmlp_edge_fwd(d, None, r, x, x, stream=0)
+    with pytest.raises(ValueError, match="contiguous columns"):
+        L.tpmlp_edge_fwd(d, None, torch.zeros(16, 4).t(), None, x, stream=0)
+    with pytest.raises(ValueError, match="shape"):
+        L.tpmlp_edge_fwd(d, torch.zeros(4, 8), r, None, x, stream=0)
+    with pytest.raises(TypeError, match="y must be float32 or"):
+        L.tpmlp_edge_fwd(d, torch.zeros(4, 16, dtype=torch.float16), r, None, x, stream=0)
+    with pytest.raises(TypeError, match="ids"):
+        L.tpmlp_route_sort(torch.zeros(4, 2), 4, 8, 0, None, None, None, None, stream=0)
+    with pytest.raises(ValueError, match="outs"):
+        L.GradTable([w], [])
+    with pytest.raises(ValueError, match="type or size"):
+        L.GradTable([w], [w.to(bf)])
+    with pytest.raises(ValueError, match="contiguous"):
+        L.GradTable([torch.zeros(4, 4).t()])
+    with pytest.raises(TypeError, match="float32 or hold"):
+        L.GradTable([torch.zeros(4, dtype=torch.float64)])

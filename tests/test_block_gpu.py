@@ -1,0 +1,628 @@
+"""The block operators' kernels against the float64 oracle (oracle/block.py).
+
+Tolerances.  An output's error is its last rounding, half a step of its type relative to the
+value, plus what float32 evaluation loses: at most a number of roundings, counted below, times
+2^-24 times the output's magnitude (the same expression with every term positive).
+
+* A row's sum of squares: at most 32 elements in a lane one after another, 4 part sums, 6
+  levels over the wave and 16 waves, under 64 roundings; half of that in 1 / deviation, 64 in
+  a mean, and under 16 element-wise: r' within 100, and x, whose row is r', within 200.
+* Backward: d within 200 and dy, which goes through the second norm, within 400.  A column
+  sum adds at most M rows: within 450 + M.
+* combine: K products and K sums, 2 K.  dw: H / 1024 steps of 4 in a lane, then 8 levels: H / 256 + 16.
+* clip: the norm in float64, rounded once; a factor rounded once and a product: 2 and 4.
+"""
+import sys
+
+import numpy as np
+import pytest
+
+from oracle import block as OB
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+F32, BF16 = torch.float32, torch.bfloat16
+U = OB.U
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from tensor_transformer_mlp_03_amd import _lib as L
+    L.lib()
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    print(f"[case] {request.node.name}", flush=True)
+    sys.stdout.flush()
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def close(name, got, want, mag, roundings, rows=None):
+    """|got - want| <= half a step of got's type at want + roundings * 2^-24 * mag."""
+    half = torch.finfo(got.dtype).eps / 2
+    g = f64(got)
+    assert g.shape == want.shape, (name, g.shape, want.shape)
+    tol = half * np.abs(want) + (1 + half) * roundings * U * np.abs(mag) + 1e-37
+    bad = ~(np.abs(g - want) <= tol)
+    if bad.any():
+        i = np.unravel_index(np.argmax(np.where(bad, np.abs(g - want) / tol, 0)), g.shape)
+        raise AssertionError(f"{name}: {bad.sum()} of {g.size} off; at {i}: {g[i]!r} want {want[i]!r} tol {tol[i]!r}")
+
+
+class Strided:
+    """A [M,H] view with row stride ld at an element offset, in a buffer whose other elements
+    hold a NaN that no call may change."""
+
+    def __init__(self, M, H, dtype, ld=None, offset=0, fill=None):
+        ld = H if ld is None else ld
+        self.flat = torch.full((offset + M * ld + 64,), float("nan"), dtype=dtype, device="cuda")
+        self.view = self.flat.as_strided((M, H), (ld, 1), offset)
+        if fill is not None:
+            self.view.copy_(fill)
+
+    def untouched(self):
+        rest = self.flat.clone()
+        M, H = self.view.shape
+        rest.as_strided((M, H), self.view.stride(), self.view.storage_offset()).fill_(float("nan"))
+        return bool(torch.isnan(rest).all())
+
+
+def normal(gen, *shape, dtype=F32, scale=1.0, mean=0.0):
+    return (torch.randn(*shape, generator=gen) * scale + mean).to(dtype)
+
+
+def edge_case(seed, M, H, post, pre, y, r, p, rows, **over):
+    gen = torch.Generator().manual_seed(seed)
+    c = dict(post=post, pre=pre, alpha=0.75, eps=1e-5)
+    c.update(over)
+    params = {}
+    for side in ("post", "pre"):
+        if c[side] != "none":
+            params["w_" + side] = normal(gen, H, dtype=p, scale=0.2, mean=1.0)
+        if c[side] == "layer":
+            params["b_" + side] = normal(gen, H, dtype=p, scale=0.2)
+    if rows:
+        params["gate"] = normal(gen, max(1, -(-M // rows)), H, dtype=p, scale=0.3, mean=0.5)
+    t = dict(y=normal(gen, M, H, dtype=y, mean=0.3) if y else None, r=normal(gen, M, H, dtype=r, scale=2.0, mean=-0.5),
+             dr=normal(gen, M, H, dtype=r), dx=normal(gen, M, H, dtype=F32 if seed % 2 else BF16))
+    return c, params, t
+
+
+def make_edge(c, params, H, rows):
+    from tensor_transformer_mlp_03_amd.block import Edge
+    return Edge(H, **c, **{k: v.cuda() for k, v in params.items()}, gate_rows=rows)
+
+
+def run_edge(seed, M, H, post, pre, y, r, p, rows, pad=0, offset=0, **over):
+    c, params, t = edge_case(seed, M, H, post, pre, y, r, p, rows, **over)
+    e = make_edge(c, params, H, rows)
+    P = {k: f64(v) for k, v in params.items()}
+    kw = dict(c, rows=rows or M, **P)
+    n64 = lambda v: None if v is None else f64(v)  # noqa: E731
+    ld = H + pad
+
+    def put(v):
+        return None if v is None else Strided(M, H, v.dtype, ld, offset, v).view
+
+    want = OB.edge_forward(n64(t["y"]), n64(t["r"]), **kw)
+    yd, rd = put(t["y"]), put(t["r"])
+    ro, x = Strided(M, H, r, ld, offset), Strided(M, H, BF16, ld, offset)
+    e.forward(yd, rd, ro.view, x.view if pre != "none" else None)
+    torch.cuda.synchronize()
+    close("r'", ro.view, want["r"], want["r_mag"], 100)
+    if pre != "none":
+        close("x", x.view, want["x"], want["x_mag"], 200)
+        assert x.untouched()
+    assert ro.untouched()
+
+    # backward, from the stream as it was stored
+    has_x = pre != "none"
+    back = OB.edge_backward(n64(t["y"]), f64(ro.view), n64(t["dr"]), n64(t["dx"]) if has_x else None, **kw)
+    dr, dy = Strided(M, H, r, ld, offset), Strided(M, H, BF16, ld, offset)
+    g = e.backward(yd, ro.view if has_x else None, put(t["dr"]), put(t["dx"]) if has_x else None, dr.view,
+                   dy.view if y else None)
+    torch.cuda.synchronize()
+    close("dr", dr.view, back["dr"], back["dr_mag"], 200)
+    if y:
+        close("dy", dy.view, back["dy"], back["dy_mag"], 400)
+    assert dr.untouched() and dy.untouched()
+    assert set(g) == set(params)
+    for k in params:
+        close("d" + k, g[k], back[k], back[k + "_mag"], 450 + M)
+
+
+SIZES = [(1, 8), (3, 9), (5, 13), (4, 64), (7, 257), (33, 511), (2, 512), (6, 513), (130, 1000), (9, 1024), (5, 1025),
+         (3, 2048), (4, 2050), (21, 3584), (3, 4096), (3, 4100), (2, 8192), (3, 8200), (2, 16384), (2, 16392), (3, 20480),
+         (2, 20483), (2, 32768)]
+
+
+@pytest.mark.parametrize("M,H", SIZES)
+def test_edge_sizes(M, H):
+    """Every row form of the kernels, whole and ragged, RMSNorm and LayerNorm."""
+    run_edge(1 + H, M, H, "rms", "rms", F32, BF16, BF16, M)
+    run_edge(2 + H, M, H, "layer", "layer", BF16, F32, F32, 2)
+
+
+KINDS = [("none", "rms"), ("none", "layer"), ("rms", "none"), ("layer", "none"), ("none", "none"), ("rms", "layer"),
+         ("layer", "rms")]
+
+
+@pytest.mark.parametrize("post,pre", KINDS)
+@pytest.mark.parametrize("rows", [0, 1, 3, 1000])
+def test_edge_norms_and_gates(post, pre, rows):
+    """Every pair of norms with no gate, one per token, per 3 tokens (the last group short), and one for all."""
+    run_edge(5, 10, 200, post, pre, F32, F32, BF16, rows)
+    run_edge(8, 10, 1400, post, pre, BF16, BF16, F32, rows)
+
+
+@pytest.mark.parametrize("y", [None, F32, BF16])
+@pytest.mark.parametrize("r", [F32, BF16])
+@pytest.mark.parametrize("p", [F32, BF16])
+def test_edge_types_and_strides(y, r, p):
+    """Every type, with odd strides and addresses that only their elements are aligned to."""
+    post = "rms" if y else "none"
+    run_edge(3, 6, 331, post, "rms", y, r, p, 2 if y else 0, pad=5, offset=1)
+    run_edge(4, 5, 1336, "layer" if y else "none", "layer", y, r, p, 0, pad=24, offset=8)
+
+
+@pytest.mark.parametrize("rows", [64, 100, 7])
+def test_edge_many_rows(rows):
+    """More rows than workgroups hold at once, many gate groups and uneven chunks."""
+    run_edge(6, 1500, 96, "rms", "rms", F32, F32, F32, rows)
+    run_edge(7, 700, 1100, "layer", "layer", F32, BF16, BF16, rows)
+
+
+def test_edge_no_tokens():
+    c, params, _ = edge_case(1, 0, 64, "layer", "rms", F32, F32, F32, 4)
+    e = make_edge(c, params, 64, 4)
+    z = lambda d: torch.empty(0, 64, dtype=d, device="cuda")  # noqa: E731
+    e.forward(z(F32), z(F32), z(F32), z(BF16))
+    g = e.backward(z(F32), z(F32), z(F32), z(F32), z(F32), z(BF16))
+    torch.cuda.synchronize()
+    assert g["gate"].shape == (0, 64)
+    for k in ("w_post", "b_post", "w_pre"):
+        assert float(g[k].abs().max()) == 0.0, k
+
+
+def test_edge_in_place():
+    """r_out over r and dr over dr_out give the bits of separate buffers."""
+    for H in (96, 2056):
+        c, params, t = edge_case(2, 9, H, "rms", "layer", F32, F32, F32, 9)
+        e = make_edge(c, params, H, 9)
+        y, r = t["y"].cuda(), t["r"].cuda()
+        ro, x, x2 = torch.empty_like(r), torch.empty(9, H, dtype=BF16, device="cuda"), torch.empty(9, H, dtype=BF16, device="cuda")
+        e.forward(y, r, ro, x)
+        e.forward(y, r, r, x2)
+        assert torch.equal(r, ro) and torch.equal(x, x2)
+        d, dx = t["dr"].cuda(), t["dx"].cuda()
+        dr, dy, dy2 = torch.empty_like(d), torch.empty_like(x), torch.empty_like(x)
+        g = {k: v.clone() for k, v in e.backward(y, ro, d, dx, dr, dy).items()}
+        g2 = e.backward(y, ro, d, dx, d, dy2)
+        assert torch.equal(d, dr) and torch.equal(dy, dy2)
+        assert all(torch.equal(g[k], g2[k]) for k in g)
+
+
+def test_edge_only_x_and_no_later_gradient():
+    """r_out is not wanted; dr_out None stands for zeros."""
+    c, params, t = edge_case(4, 6, 520, "rms", "rms", F32, BF16, BF16, 6)
+    e = make_edge(c, params, 520, 6)
+    y, r = t["y"].cuda(), t["r"].cuda()
+    ro, x, x2 = torch.empty_like(r), torch.empty(6, 520, dtype=BF16, device="cuda"), torch.empty(6, 520, dtype=BF16, device="cuda")
+    e.forward(y, r, ro, x)
+    e.forward(y, r, None, x2)
+    assert torch.equal(x, x2)
+    outs = [(torch.empty_like(r), torch.empty_like(x)) for _ in range(2)]
+    e.backward(y, ro, None, t["dx"].cuda(), *outs[0])
+    e.backward(y, ro, torch.zeros_like(r), t["dx"].cuda(), *outs[1])
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+def test_edge_bad_rows_stay_alone():
+    """A row of NaN, of infinities or of zeros changes no other row."""
+    for H in (200, 2050):
+        c, params, t = edge_case(3, 8, H, "rms", "layer", F32, F32, F32, 0)
+        e = make_edge(c, params, H, 0)
+        y, r = t["y"].cuda(), t["r"].cuda()
+        ro, x = torch.empty_like(r), torch.empty(8, H, dtype=BF16, device="cuda")
+        e.forward(y, r, ro, x)
+        y2, r2 = y.clone(), r.clone()
+        y2[1], y2[3], y2[5], r2[5], r2[6, 7] = float("nan"), float("inf"), 0.0, 0.0, float("inf")
+        ro2, x2 = torch.empty_like(ro), torch.empty_like(x)
+        e.forward(y2, r2, ro2, x2)
+        keep = [0, 2, 4, 7]
+        assert torch.equal(ro[keep], ro2[keep]) and torch.equal(x[keep], x2[keep])
+        assert bool(torch.isfinite(x2[5]).all()) and bool(torch.isnan(x2[1]).all())
+
+
+def test_edge_large_values():
+    """A LayerNorm of values far from zero keeps its variance."""
+    H = 1000
+    c, params, t = edge_case(9, 4, H, "none", "layer", F32, F32, F32, 0)
+    e = make_edge(c, params, H, 0)
+    r = t["r"] + 3000.0
+    want = OB.edge_forward(f64(t["y"]), f64(r), **c, rows=4, **{k: f64(v) for k, v in params.items()})
+    ro, x = torch.empty(4, H, device="cuda"), torch.empty(4, H, dtype=BF16, device="cuda")
+    e.forward(t["y"].cuda(), r.cuda(), ro, x)
+    close("x", x, want["x"], want["x_mag"], 200)
+
+
+def test_edge_gradient_is_a_difference():
+    """<dr', r'> + <dx, x> moves along a direction of y as <dy, direction> says: central
+    differences of the kernel's own forward in float32.  x is bf16, so its part is left out
+    (no norm before the next block); the step's error is the float32 rounding of r', at most
+    100 roundings of its magnitude, over the step, and the third-order term, of the order of
+    the step squared."""
+    M, H, h = 4, 256, 2.0 ** -6
+    c, params, t = edge_case(12, M, H, "layer", "none", F32, F32, F32, 2, alpha=0.0)
+    e = make_edge(c, params, H, 2)
+    gen = torch.Generator().manual_seed(1)
+    u = normal(gen, M, H).cuda()
+    y, r, d = t["y"].cuda(), t["r"].cuda(), t["dr"].cuda()
+    f = []
+    for s in (h, -h):
+        ro = torch.empty_like(r)
+        e.forward(y + s * u, r, ro, None)
+        f.append(float((ro.double() * d.double()).sum()))
+    dr, dy = torch.empty_like(d), torch.empty(M, H, dtype=BF16, device="cuda")
+    e.backward(y, None, d, None, dr, dy)
+    got = float((dy.double() * u.double()).sum())
+    mag = float((d.double().abs() * 2).sum())
+    tol = 100 * U * mag / h + 2.0 ** -8 * float((dy.double() * u.double()).abs().sum()) + 8 * h * h * mag / np.sqrt(M * H)
+    assert abs(got - (f[0] - f[1]) / (2 * h)) <= tol
+
+
+def test_edge_offsets_past_32_bits():
+    """Rows 2^31 elements apart."""
+    H, ld = 136, 1 << 31
+    c, params, t = edge_case(5, 3, H, "none", "rms", F32, BF16, F32, 0)
+    flat = torch.empty(2 * ld + H, dtype=BF16, device="cuda")
+    r = flat.as_strided((3, H), (ld, 1))
+    r.copy_(t["r"])
+    e = make_edge(c, params, H, 0)
+    y = t["y"].cuda()
+    x, x2 = torch.empty(3, H, dtype=BF16, device="cuda"), torch.empty(3, H, dtype=BF16, device="cuda")
+    ro = torch.empty(3, H, dtype=BF16, device="cuda")
+    e.forward(y, t["r"].cuda(), ro, x)
+    e.forward(y, r, r, x2)
+    assert torch.equal(x, x2) and torch.equal(r.clone(), ro)
+    d, dx = t["dr"].cuda(), t["dx"].cuda()
+    a, b = [(torch.empty_like(d), torch.empty_like(x)) for _ in range(2)]
+    e.backward(y, ro, d, dx, *a)
+    e.backward(y, r, d, dx, *b)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# --- route -----------------------------------------------------------------------------------------------------
+def route_ids(seed, T, K, E, drop=0.0, bad=False):
+    gen = torch.Generator().manual_seed(seed)
+    ids = torch.randint(0, E, (T, K), generator=gen)
+    off = torch.rand(T, K, generator=gen) < drop
+    ids[off] = -1
+    if bad and T:
+        ids[0, 0], ids[-1, -1] = E, -(1 << 30)
+    return ids
+
+
+def check_sort(ids, E, align, capacity, dtype):
+    from tensor_transformer_mlp_03_amd.block import Route
+    T, K = ids.shape
+    want = OB.route_sort(ids.numpy(), E, align, capacity)
+    h = Route(T, K, E, align, capacity)
+    assert h.rows == OB.route_rows(T, K, E, align, capacity)
+    for t in (h.counts, h.offsets, h.row_of, h.src_of):
+        t.fill_(-77)
+    h.sort(ids.to(dtype).cuda())
+    torch.cuda.synchronize()
+    for name, w in zip(("counts", "offsets", "row_of", "src_of"), want):
+        got = getattr(h, name).cpu().numpy()
+        assert np.array_equal(got, w), (name, np.argwhere(got != w)[:5].tolist())
+    return h
+
+
+@pytest.mark.parametrize("T,K", [(0, 1), (1, 1), (1, 8), (7, 3), (63, 1), (64, 2), (65, 5), (1000, 4), (4096, 1),
+                                 (4097, 1), (2500, 7), (70000, 2)])
+@pytest.mark.parametrize("E", [1, 3, 8, 64, 65, 512])
+def test_route_sort(T, K, E):
+    check_sort(route_ids(T + E, T, K, E, 0.1, bad=T > 4), E, 8, 0, torch.int32)
+    check_sort(route_ids(T + E, T, K, E), E, 1, 0, torch.int64)
+    cap = -(-T * K // (2 * E)) // 8 * 8 + 8
+    check_sort(route_ids(T + E, T, K, E, 0.1), E, 8, cap, torch.int64)
+
+
+def test_route_sort_one_sided():
+    """Every pair to one expert, no pair to any, and the smallest and the largest expert only."""
+    for T in (100, 9000):
+        for v in (0, 5, 31, -1, 32):
+            check_sort(torch.full((T, 2), v), 32, 16, 0, torch.int32)
+            check_sort(torch.full((T, 2), v), 32, 16, 48, torch.int32)
+
+
+def put(v, pad=0, offset=0):
+    return Strided(v.shape[0], v.shape[1], v.dtype, v.shape[1] + pad, offset, v).view
+
+
+@pytest.mark.parametrize("T,K,E,H,capacity", [(1, 1, 4, 8, 0), (5, 2, 8, 9, 0), (33, 3, 7, 331, 0), (8, 2, 8, 4096, 0),
+                                              (200, 8, 16, 512, 64), (77, 9, 60, 2049, 0), (300, 1, 1, 1032, 0),
+                                              (50, 20, 64, 136, 8), (10, 4, 512, 5000, 0)])
+@pytest.mark.parametrize("pad,offset", [(0, 0), (3, 1)])
+def test_route_moves(T, K, E, H, capacity, pad, offset):
+    """There and back, both gradients; dropped pairs and padding rows hold NaN where they are read."""
+    gen = torch.Generator().manual_seed(T * 7 + H)
+    h = check_sort(route_ids(T, T, K, E, 0.15), E, 8, capacity, torch.int32)
+    row_of, src_of = h.row_of.cpu().numpy(), h.src_of.cpu().numpy()
+    X = normal(gen, T, H, dtype=BF16)
+    Xs = Strided(h.rows, H, BF16, H + pad, offset)
+    h.dispatch(put(X, pad, offset), Xs.view)
+    assert np.array_equal(f64(Xs.view), OB.route_dispatch(f64(X), row_of, h.rows)) and Xs.untouched()
+    w = torch.rand(T, K, generator=gen)
+    w[torch.from_numpy(row_of) < 0] = float("nan")  # of a pair that takes no part
+    w64 = np.where(row_of >= 0, f64(w), 0.0)
+    for zt in (F32, BF16):
+        for yt in (F32, BF16):
+            Z = normal(gen, h.rows, H, dtype=zt)
+            Z64 = f64(Z)
+            Z[torch.from_numpy(src_of) < 0] = float("nan")
+            for ww, w_ in ((w, w64), (None, None)):
+                Y = Strided(T, H, yt, H + pad, offset)
+                h.combine(put(Z, pad, offset), None if ww is None else ww.cuda(), Y.view)
+                want, mag = OB.route_combine(Z64, row_of, w_)
+                close("Y", Y.view, want, mag, 2 * K)
+                assert Y.untouched()
+            dY = normal(gen, T, H, dtype=yt)
+            dZs, dw = Strided(h.rows, H, BF16, H + pad, offset), torch.full((T, K), float("nan"), device="cuda")
+            h.combine_backward(put(dY, pad, offset), put(Z, pad, offset), w.cuda(), dZs.view, dw)
+            wz, ww_, mag = OB.route_combine_backward(f64(dY), Z64, row_of, w64, h.rows)
+            close("dZs", dZs.view, wz, np.abs(wz), 1)
+            close("dw", dw, ww_, mag, H / 256 + 16)
+            assert dZs.untouched()
+            # one of the two alone
+            a, b = torch.empty(h.rows, H, dtype=BF16, device="cuda"), torch.empty(T, K, device="cuda")
+            h.combine_backward(dY.cuda(), None, w.cuda(), a, None)
+            from tensor_transformer_mlp_03_amd import _lib as L
+            L.tpmlp_route_combine_bwd(dY.cuda(), Z.cuda(), h.row_of, None, w.cuda(), None, b)
+            assert torch.equal(a, dZs.view) and torch.equal(b, dw)
+    dXs = normal(gen, h.rows, H)
+    dX = Strided(T, H, F32, H + pad, offset)
+    h.dispatch_backward(put(dXs, pad, offset), dX.view)
+    want, mag = OB.route_combine(f64(dXs), row_of, None)
+    close("dX", dX.view, want, mag, 2 * K)
+
+
+def test_route_no_tokens_and_all_dropped():
+    from tensor_transformer_mlp_03_amd.block import Route
+    h = Route(0, 2, 4, capacity=8)
+    h.sort(torch.empty(0, 2, dtype=torch.int32, device="cuda"))
+    Xs = torch.full((32, 64), 3.0, dtype=BF16, device="cuda")
+    h.dispatch(torch.empty(0, 64, dtype=BF16, device="cuda"), Xs)
+    assert float(Xs.abs().max()) == 0.0
+    h = Route(6, 2, 4)
+    h.sort(torch.full((6, 2), -1, dtype=torch.int64, device="cuda"))
+    Z, Y = torch.full((h.rows, 64), float("nan"), device="cuda"), torch.full((6, 64), 5.0, device="cuda")
+    h.combine(Z, torch.ones(6, 2, device="cuda"), Y)
+    assert float(Y.abs().max()) == 0.0
+    dZs, dw = torch.full((h.rows, 64), 2.0, dtype=BF16, device="cuda"), torch.full((6, 2), 2.0, device="cuda")
+    h.combine_backward(Y + 1, Z, torch.ones(6, 2, device="cuda"), dZs, dw)
+    assert float(dZs.abs().max()) == 0.0 and float(dw.abs().max()) == 0.0
+
+
+def test_route_rows_out_of_range_are_dropped():
+    """row_of entries outside the sorted buffer (not the sort's) are treated as dropped: no
+    access, zeros in their place."""
+    from tensor_transformer_mlp_03_amd import _lib as L
+    row_of = torch.tensor([[0, 99], [-5, 1], [2 ** 31 - 1, -(2 ** 31)]], dtype=torch.int32, device="cuda")
+    src_of = torch.tensor([0, 3, -1, -1], dtype=torch.int32, device="cuda")
+    X = torch.arange(3 * 64, device="cuda").reshape(3, 64).to(BF16)
+    Xs = torch.full((4, 64), 7.0, dtype=BF16, device="cuda")
+    L.tpmlp_route_dispatch(X, row_of, src_of, Xs)
+    assert torch.equal(Xs[0], X[0]) and torch.equal(Xs[1], X[1]) and float(Xs[2:].abs().max()) == 0.0
+    Y = torch.empty(3, 64, device="cuda")
+    L.tpmlp_route_combine(Xs, row_of, None, Y)
+    assert torch.equal(Y[:2], X[:2].float()) and float(Y[2].abs().max()) == 0.0
+
+
+def test_route_offsets_past_32_bits():
+    from tensor_transformer_mlp_03_amd.block import Route
+    H, ld = 72, 1 << 30
+    h = Route(3, 1, 1, align=1)
+    h.sort(torch.zeros(3, 1, dtype=torch.int32, device="cuda"))
+    Xs = torch.empty(2 * ld + H, dtype=BF16, device="cuda").as_strided((3, H), (ld, 1))
+    X = normal(torch.Generator().manual_seed(1), 3, H, dtype=BF16).cuda()
+    h.dispatch(X, Xs)
+    assert torch.equal(Xs.clone(), X)
+    Y = torch.empty(3, H, dtype=BF16, device="cuda")
+    h.combine(Xs, None, Y)
+    assert torch.equal(Y, X)
+
+
+# --- clipping ----------------------------------------------------------------------------------------------------
+def grads_of(seed, sizes, kinds, offset=0, scale=0.1):
+    gen = torch.Generator().manual_seed(seed)
+    out = []
+    for n, k in zip(sizes, kinds):
+        flat = torch.full((n + offset + 8,), float("nan"), dtype=k, device="cuda")
+        flat[offset:offset + n] = normal(gen, n, dtype=k, scale=scale).cuda()
+        out.append(flat)
+    return out, [f[offset:offset + n] for f, n in zip(out, sizes)]
+
+
+SIZE_SETS = {
+    "one": [1], "odd": [1, 2, 3, 5, 1023, 1025, 4097], "chunks": [16383, 16384, 16385, 32768, 40000],
+    "empty": [0, 7, 0, 0, 16384, 0], "many": [(37 * i) % 501 for i in range(300)], "long": [3000001, 17],
+    "table": [5] * 128, "table1": [5] * 129,
+}
+
+
+@pytest.mark.parametrize("sizes", SIZE_SETS)
+@pytest.mark.parametrize("offset", [0, 1, 3])
+@pytest.mark.parametrize("factor", [0.3, 4.0])
+def test_clip(sizes, offset, factor):
+    from tensor_transformer_mlp_03_amd.block import GradClip
+    n = SIZE_SETS[sizes]
+    kinds = [BF16 if i % 3 == 1 else F32 for i in range(len(n))]
+    flats, g = grads_of(7, n, kinds, offset)
+    g64 = [f64(t) for t in g]
+    for scale in (1.0, -0.5):
+        plain, _ = OB.clip(g64, np.inf, scale)
+        max_norm = float(np.float32(factor * plain))
+        norm, want = OB.clip(g64, max_norm, scale)
+        outs = [torch.full_like(t, 9.0) for t in g]
+        before = [f.clone() for f in flats]
+        got = GradClip(g, outs).clip(max_norm, scale)
+        close("norm", got, np.float64(norm), norm, 2)
+        for o, w in zip(outs, want):
+            close("out", o, w, w, 4)
+        assert all(torch.equal(torch.nan_to_num(a, 5.0), torch.nan_to_num(b, 5.0)) for a, b in zip(before, flats))
+        # in place, and through the two calls that ranks use
+        h = GradClip(g)
+        total = h.sumsq().clone()
+        assert abs(float(total) - sum((v ** 2).sum() for v in g64)) <= 1e-12 * float(total)
+        h.scale(max_norm, scale)
+        for t, o in zip(g, outs):
+            assert torch.equal(t, o)
+        for f, b, t in zip(flats, before, g):
+            f2, b2 = f.clone(), b.clone()
+            f2[offset:offset + t.numel()] = b2[offset:offset + t.numel()] = 0
+            assert torch.equal(torch.nan_to_num(f2, 5.0), torch.nan_to_num(b2, 5.0))
+            f.copy_(b)
+
+
+def test_clip_nothing():
+    from tensor_transformer_mlp_03_amd.block import GradClip
+    assert float(GradClip([]).clip(1.0)) == 0.0
+    z = torch.zeros(100, device="cuda")
+    assert float(GradClip([z]).clip(1.0)) == 0.0 and float(z.abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_clip_not_finite(bad):
+    """The norm says so and the gradients keep their values."""
+    from tensor_transformer_mlp_03_amd.block import GradClip
+    g = [torch.ones(5000, device="cuda"), torch.ones(9, dtype=BF16, device="cuda")]
+    g[0][4321] = bad
+    keep = [t.clone() for t in g]
+    norm = float(GradClip(g).clip(1.0))
+    assert np.isnan(norm) if np.isnan(bad) else np.isposinf(norm)
+    for t, k in zip(g, keep):
+        assert torch.equal(torch.nan_to_num(t, 3.0), torch.nan_to_num(k, 3.0))
+    h = GradClip(g)
+    h.clip(1.0, scale=0.5)
+    assert float(g[1][0]) == 0.5
+
+
+def test_clip_squares_past_float32():
+    from tensor_transformer_mlp_03_amd.block import GradClip
+    g = torch.full((1 << 16,), 2.0 ** 100, device="cuda")
+    h = GradClip([g])
+    assert float(h.clip(1.0)) == 2.0 ** 108
+    assert float(g[0]) == 2.0 ** -8
+    tiny = torch.full((1 << 16,), 2.0 ** -100, device="cuda")
+    assert float(GradClip([tiny]).clip(1.0)) == 2.0 ** -92 and float(tiny[0]) == 2.0 ** -100
+
+
+def test_clip_past_32_bits():
+    """A gradient of more than 2^31 elements."""
+    from tensor_transformer_mlp_03_amd.block import GradClip
+    n = (1 << 31) + 12345
+    g = torch.zeros(n, dtype=BF16, device="cuda")
+    g[-1], g[0], g[1 << 31] = 3.0, 4.0, 12.0
+    assert float(GradClip([g]).clip(6.5)) == 13.0
+    assert float(g[-1]) == 1.5 and float(g[0]) == 2.0 and float(g[1 << 31]) == 6.0
+
+
+# --- streams and graphs ------------------------------------------------------------------------------------------
+def test_on_another_stream():
+    """Every call runs on the stream it is given."""
+    from tensor_transformer_mlp_03_amd.block import GradClip, Route
+    c, params, t = edge_case(2, 40, 520, "rms", "rms", F32, F32, F32, 40)
+    e = make_edge(c, params, 520, 40)
+    y, r = t["y"].cuda(), t["r"].cuda()
+    want_r, want_x = torch.empty_like(r), torch.empty(40, 520, dtype=BF16, device="cuda")
+    e.forward(y, r, want_r, want_x)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    ro, x = torch.empty_like(want_r), torch.empty_like(want_x)
+    ids = route_ids(3, 40, 2, 8).to(torch.int32).cuda()
+    h = Route(40, 2, 8)
+    Xs, Y = torch.empty(h.rows, 520, dtype=BF16, device="cuda"), torch.empty(40, 520, device="cuda")
+    clip = GradClip([Y])
+    torch.cuda.synchronize()
+    e.forward(y, r, ro, x, stream=s)
+    h.sort(ids, stream=s)
+    h.dispatch(x, Xs, stream=s)
+    h.combine(Xs, None, Y, stream=s)
+    norm = clip.clip(1.0, stream=s)
+    s.synchronize()
+    assert torch.equal(ro, want_r) and torch.equal(x, want_x)
+    both = 2 * want_x.float()
+    assert abs(float(norm) - float(both.double().norm())) <= 1e-6 * float(norm)
+    close("clipped", Y, f64(both) / float(both.double().norm()), f64(both) / float(norm), 4)
+
+
+def test_in_a_graph():
+    """A whole step captured once, replayed on new inputs with eager work between the replays."""
+    from tensor_transformer_mlp_03_amd.block import GradClip, Route
+    M, H, E, K = 70, 264, 6, 3
+    c, params, t = edge_case(7, M, H, "layer", "rms", F32, F32, F32, 20)
+    e = make_edge(c, params, H, 20)
+    gen = torch.Generator().manual_seed(0)
+    y, r, ids, w = t["y"].cuda(), t["r"].cuda(), route_ids(1, M, K, E, 0.1).cuda(), torch.rand(M, K, generator=gen).cuda()
+    h = Route(M, K, E)
+    new = lambda *s, d=F32: torch.empty(*s, dtype=d, device="cuda")  # noqa: E731
+    b = dict(ro=new(M, H), x=new(M, H, d=BF16), Xs=new(h.rows, H, d=BF16), Y=new(M, H), dZs=new(h.rows, H, d=BF16),
+             dw=new(M, K), dX=new(M, H), dr=new(M, H), dy=new(M, H, d=BF16))
+    e._place(M, r.device)
+    outs = [torch.empty_like(g) for g in e.grads.values()]
+    clip = GradClip(list(e.grads.values()), outs)
+
+    def step():
+        e.forward(y, r, b["ro"], b["x"])
+        h.sort(ids)
+        h.dispatch(b["x"], b["Xs"])
+        h.combine(b["Xs"], w, b["Y"])
+        h.combine_backward(b["Y"], b["Xs"], w, b["dZs"], b["dw"])
+        h.dispatch_backward(b["dZs"], b["dX"])
+        e.backward(y, b["ro"], b["Y"], b["dX"], b["dr"], b["dy"])
+        clip.clip(0.5)
+
+    step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    for n in range(4):
+        y.copy_(normal(gen, M, H))
+        ids.copy_(route_ids(50 + n, M, K, E, 0.2))
+        step()
+        torch.cuda.synchronize()
+        want = [v.clone() for v in (*b.values(), *outs, clip.norm, h.counts, h.row_of)]
+        for v in (*b.values(), *outs):
+            v.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [*b.values(), *outs, clip.norm, h.counts, h.row_of]
+        assert all(torch.equal(a, g) for a, g in zip(want, got)), n
+
+
+def test_the_same_bits_twice():
+    """No result depends on timing."""
+    from tensor_transformer_mlp_03_amd.block import GradClip
+    c, params, t = edge_case(3, 3000, 640, "layer", "layer", F32, BF16, BF16, 700)
+    e = make_edge(c, params, 640, 700)
+    y, r, d, dx = (t[k].cuda() for k in ("y", "r", "dr", "dx"))
+    runs = []
+    for _ in range(3):
+        dr, dy = torch.empty_like(d), torch.empty(3000, 640, dtype=BF16, device="cuda")
+        g = e.backward(y, r, d, dx, dr, dy)
+        norm = GradClip([v.clone() for v in g.values()]).clip(1e-3)
+        runs.append([dr, dy, norm.clone(), *(v.clone() for v in g.values())])
+    assert all(torch.equal(a, b) for other in runs[1:] for a, b in zip(runs[0], other))
