@@ -52,6 +52,12 @@ struct EdgeFinishArgs {
 //   S1 = sum d yh, T1 = sum dx xh; with a LayerNorm also S0 = sum d, T0 = sum dx.
 constexpr int EDGE_ACC_RMS = 2, EDGE_ACC_LAYER = 4;
 
+// The backward's row forms, waves x chunks a lane; ANY: rows that are not FULL.
+enum EdgeShape : int {
+  EDGE_1x2, EDGE_4x1, EDGE_4x2, EDGE_8x2, EDGE_16x2, EDGE_16x4, EDGE_16x5, EDGE_16x8, EDGE_ANY_4x1, EDGE_ANY_8x2, EDGE_ANY_16x8
+};
+EdgeShape edge_bwd_shape(int H, bool full);
+
 // How the backward's rows are cut: a function of the sizes alone, so the
 // workspace query and the launch agree.
 struct EdgeBwdPlan {
@@ -61,8 +67,10 @@ struct EdgeBwdPlan {
 };
 EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer);
 
-hipError_t launch_edge_fwd(const EdgeFwdArgs& a, int y_type, int r_type, hipStream_t s);  // y_type -1: no y
-hipError_t launch_edge_bwd(const EdgeBwdArgs& a, const EdgeBwdPlan& p, int y_type, int r_type, hipStream_t s);
+// y_type -1: no y.  full: H is a multiple of 4 and every row of every matrix and
+// vector starts at a multiple of four elements.
+hipError_t launch_edge_fwd(const EdgeFwdArgs& a, int y_type, int r_type, bool full, hipStream_t s);
+hipError_t launch_edge_bwd(const EdgeBwdArgs& a, const EdgeBwdPlan& p, int y_type, int r_type, bool full, hipStream_t s);
 hipError_t launch_edge_finish(const EdgeFinishArgs& a, hipStream_t s);
 
 // ---------------------------------------------------------------------------

@@ -126,6 +126,15 @@ tpmlp_status check_edge(const tpmlp_edge* e, bool has_y) {
   return TPMLP_OK;
 }
 
+// Whether every row of the matrix starts at a multiple of four elements.
+bool quads(const Mat& m) {
+  return empty(m) || (reinterpret_cast<uintptr_t>(m.p) % (4 * m.elem) == 0 && (m.rows < 2 || m.ld % 4 == 0));
+}
+template <size_t NO, size_t NI>
+bool all_quads(int64_t H, const Mat (&outs)[NO], const Mat (&ins)[NI]) {
+  return H % 4 == 0 && std::all_of(outs, outs + NO, quads) && std::all_of(ins, ins + NI, quads);
+}
+
 // The edge's parameters as inputs of the overlap check.
 #define EDGE_PARAMS(e)                                                                                  \
   {(e).w_post, 1, (e).H, (e).H, size_of((e).param_type), "w_post"},                                     \
@@ -175,7 +184,7 @@ tpmlp_status edge_fwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
   a.p_bf16 = e->param_type == TPMLP_BF16;
   a.alpha = e->alpha;
   a.eps = e->eps;
-  return launched(launch_edge_fwd(a, y ? e->y_type : -1, e->r_type, stream_of(stream)), "tpmlp_edge_fwd launch");
+  return launched(launch_edge_fwd(a, y ? e->y_type : -1, e->r_type, all_quads(H, outs, ins), stream_of(stream)), "tpmlp_edge_fwd launch");
 }
 
 tpmlp_status edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r_out, int64_t ld_r_out,
@@ -225,8 +234,8 @@ tpmlp_status edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
     if (reinterpret_cast<uintptr_t>(ws) & 15) return fail(TPMLP_ERR_ALIGN, "ws is not 16-byte aligned");
     if (ws_bytes < plan.ws_bytes) return fail(TPMLP_ERR_WORKSPACE, "ws_bytes below tpmlp_edge_bwd_workspace_bytes");
   }
-  const int64_t ws_n = any ? (int64_t)plan.ws_bytes : 0;
-  const Mat outs[] = {mdr, mdy, g[0], g[1], g[2], g[3], g[4], {ws, 1, ws_n, ws_n, 1, "ws"}};
+  const int64_t ws_n = any ? (int64_t)(plan.ws_bytes / 4) : 0;
+  const Mat outs[] = {mdr, mdy, g[0], g[1], g[2], g[3], g[4], {ws, 1, ws_n, ws_n, 4, "ws"}};
   const Mat ins[] = {mdo, my, mr, mdx, EDGE_PARAMS(*e)};
   TRY(check_overlaps(outs, ins, 0, 0));
   if (M == 0 && !any) return TPMLP_OK;
@@ -262,7 +271,7 @@ tpmlp_status edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
     a.dx_bf16 = dx_type == TPMLP_BF16;
     a.alpha = e->alpha;
     a.eps = e->eps;
-    TRY(launched(launch_edge_bwd(a, plan, y ? e->y_type : -1, e->r_type, s), "tpmlp_edge_bwd launch"));
+    TRY(launched(launch_edge_bwd(a, plan, y ? e->y_type : -1, e->r_type, all_quads(H, outs, ins), s), "tpmlp_edge_bwd launch"));
   }
   if (!any) return TPMLP_OK;
   EdgeFinishArgs f{};

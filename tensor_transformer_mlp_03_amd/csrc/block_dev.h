@@ -32,6 +32,13 @@ __device__ __forceinline__ f32x4 widen(u16x4_u v) {
   return f32x4{bf16_to_f32(v[0]), bf16_to_f32(v[1]), bf16_to_f32(v[2]), bf16_to_f32(v[3])};
 }
 
+__device__ __forceinline__ void put(float* p, f32x4 v) { *reinterpret_cast<f32x4_u*>(p) = f32x4_u{v[0], v[1], v[2], v[3]}; }
+__device__ __forceinline__ void put(uint16_t* p, f32x4 v) {
+  *reinterpret_cast<u16x4_u*>(p) = u16x4_u{f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3])};
+}
+__device__ __forceinline__ void put1(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put1(uint16_t* p, float v) { *p = f32_to_bf16(v); }
+
 // Elements i .. i+3 of a row of n >= 4 elements, zeros past its end.  Every lane
 // reads four elements inside the row (the last four where i + 4 > n), so no lane
 // branches around the load; a lane on the ragged end shifts what it read.
@@ -50,13 +57,6 @@ __device__ __forceinline__ f32x4 load4(const typename T::elem* row, int i, int n
   return v;
 }
 
-__device__ __forceinline__ void put(float* p, f32x4 v) { *reinterpret_cast<f32x4_u*>(p) = f32x4_u{v[0], v[1], v[2], v[3]}; }
-__device__ __forceinline__ void put(uint16_t* p, f32x4 v) {
-  *reinterpret_cast<u16x4_u*>(p) = u16x4_u{f32_to_bf16(v[0]), f32_to_bf16(v[1]), f32_to_bf16(v[2]), f32_to_bf16(v[3])};
-}
-__device__ __forceinline__ void put1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void put1(uint16_t* p, float v) { *p = f32_to_bf16(v); }
-
 // Stores elements i .. i+3 of a row of n elements, those inside it.
 template <class T>
 __device__ __forceinline__ void store4(typename T::elem* row, int i, int n, f32x4 v) {
@@ -69,9 +69,66 @@ __device__ __forceinline__ void store4(typename T::elem* row, int i, int n, f32x
   }
 }
 
+// A row that a wave reads or writes four elements a lane.  FULL rows (n a multiple
+// of 4, every row at a multiple of four elements) go through a buffer descriptor
+// of the row's length: a chunk past the end reads zeros and writes nothing, without
+// a branch or an address select, and the address is one 32-bit offset a lane.  The
+// row's pointer has to be uniform over the wave.  Other rows take load4 and store4.
+template <class T, bool FULL>
+struct Row;
+
+template <class T>
+struct Row<T, false> {
+  typedef typename T::elem elem;
+  elem* p;
+  int n;
+  __device__ __forceinline__ Row(const void* base, int64_t at, int n_)
+      : p(const_cast<elem*>(static_cast<const elem*>(base)) + at), n(n_) {}
+  __device__ __forceinline__ f32x4 load(int i) const { return load4<T>(p, i, n); }
+  __device__ __forceinline__ void store(int i, f32x4 v) const { store4<T>(p, i, n, v); }
+};
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+#if defined(__HIP_DEVICE_COMPILE__)
+template <class T>
+struct Row<T, true> {
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ __forceinline__ Row(const void* base, int64_t at, int n)
+      : rs(__builtin_amdgcn_make_buffer_rsrc(
+            const_cast<typename T::elem*>(static_cast<const typename T::elem*>(base)) + at, (short)0,
+            (int)(n * sizeof(typename T::elem)), 0x00020000)) {}
+  __device__ __forceinline__ f32x4 load(int i) const {
+    if constexpr (sizeof(typename T::elem) == 4) {
+      return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, i * 4, 0, 0));
+    } else {
+      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, i * 2, 0, 0));
+      return f32x4{__builtin_bit_cast(float, v[0] << 16), __builtin_bit_cast(float, v[0] & 0xFFFF0000u),
+                   __builtin_bit_cast(float, v[1] << 16), __builtin_bit_cast(float, v[1] & 0xFFFF0000u)};
+    }
+  }
+  __device__ __forceinline__ void store(int i, f32x4 v) const {
+    if constexpr (sizeof(typename T::elem) == 4) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, i * 4, 0, 0);
+    } else {
+      const u32x2 o = {(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
+                       (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
+      __builtin_amdgcn_raw_buffer_store_b64(o, rs, i * 2, 0, 0);
+    }
+  }
+};
+#else
+template <class T>
+struct Row<T, true> : Row<T, false> {
+  using Row<T, false>::Row;
+};
+#endif
+
 // Parameter vectors are float32 or bf16 by a flag uniform over the launch.
-__device__ __forceinline__ f32x4 load4_param(const void* p, int bf16, int i, int n) {
-  return bf16 ? load4<BF16>(static_cast<const uint16_t*>(p), i, n) : load4<F32>(static_cast<const float*>(p), i, n);
+template <bool FULL>
+__device__ __forceinline__ f32x4 load_params(const void* p, int bf16, int64_t at, int i, int n) {
+  return bf16 ? Row<BF16, FULL>(p, at, n).load(i) : Row<F32, FULL>(p, at, n).load(i);
 }
 __device__ __forceinline__ float load_param(const void* p, int bf16, int64_t i) {
   return bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];

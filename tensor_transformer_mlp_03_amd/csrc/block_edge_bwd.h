@@ -27,13 +27,19 @@
 namespace tpmlp {
 namespace edge {
 
-template <class YT, class RT, bool HAS_Y, bool LAYER, int W, int NV>
+// Rows whose elements a workgroup holds W waves wide and NV chunks deep.  Up to two
+// chunks a lane, the two parameter products stay in registers over all rows; with
+// four or more (wider rows than 16 waves hold in two) they are read again for every
+// row, and T1, which one lane alone adds to, lives in LDS.
+template <class YT, class RT, bool HAS_Y, bool LAYER, int W, int NV, bool FULL>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) edge_bwd_kernel(EdgeBwdArgs a) {
   constexpr int NACC = LAYER ? EDGE_ACC_LAYER : EDGE_ACC_RMS;
+  constexpr bool KEEP = NV <= 2, T_LDS = W == 16 && NV >= 4;
   constexpr int SLOT = 8 * W;  // floats of one row's sums; two sets, used in turn
   __shared__ float slots[2 * SLOT];
+  __shared__ f32x4 t_lds[T_LDS ? NV * 64 * W : 1];
   const int lane = W == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const int wave = threadIdx.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int H = a.H;
   const float inv = 1.0f / (float)H;
   const int64_t group = blockIdx.x / a.chunks;
@@ -41,14 +47,32 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) edge_bwd_kernel(EdgeBwd
   const int64_t g_end = min((group + 1) * a.gate_rows, a.M);
   const int64_t row0 = min(group * a.gate_rows + chunk * a.chunk_rows, g_end);
   const int64_t row1 = min(row0 + a.chunk_rows, g_end);
-  const char* gp = static_cast<const char*>(a.gate) + group * a.ld_gate * (a.p_bf16 ? 2 : 4);
+  const int64_t gate_at = group * a.ld_gate;
+  const bool has_dx = a.dx != nullptr, post = HAS_Y && a.post != TPMLP_NORM_NONE;
   const bool pre_layer = LAYER && a.pre == TPMLP_NORM_LAYER, post_layer = LAYER && a.post == TPMLP_NORM_LAYER;
+  auto at = [&](int p) { return 4 * (p * 64 * W + lane); };
+  auto inside = [&](int i, int e) { return FULL ? i < H : i + e < H; };
+  // w_pre, and the product of w_post and the gate's row: what scales dx and d
+  auto pre_scale = [&](int p) { return load_params<FULL>(a.w_pre, a.p_bf16, 0, at(p), H); };
+  auto post_scale = [&](int p) {
+    f32x4 v = {1.0f, 1.0f, 1.0f, 1.0f};
+    if (post) v = load_params<FULL>(a.w_post, a.p_bf16, 0, at(p), H);
+    if (a.gate) v *= load_params<FULL>(a.gate, a.p_bf16, gate_at, at(p), H);
+    return v;
+  };
 
-  f32x4 S1[NV], T1[NV], S0[LAYER ? NV : 1], T0[LAYER ? NV : 1];
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 S1[NV], T1[T_LDS ? 1 : NV], S0[LAYER ? NV : 1], T0[LAYER ? NV : 1], wu[KEEP ? NV : 1], wv[KEEP ? NV : 1];
 #pragma unroll
   for (int p = 0; p < NV; ++p) {
-    S1[p] = T1[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (LAYER) S0[p] = T0[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    S1[p] = zero;
+    if (T_LDS) t_lds[p * 64 * W + lane] = zero;
+    else T1[p] = zero;
+    if (LAYER) S0[p] = T0[p] = zero;
+    if (KEEP) {
+      wu[p] = has_dx ? pre_scale(p) : zero;
+      if (HAS_Y) wv[p] = post_scale(p);
+    }
   }
 
   int turn = 0;
@@ -56,132 +80,133 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) edge_bwd_kernel(EdgeBwd
     float* slot = slots + turn * SLOT;
     f32x4 d[NV], y[NV];
     if (a.dr_out) {
-      const auto* p0 = static_cast<const typename RT::elem*>(a.dr_out) + row * a.ld_dr_out;
+      const Row<RT, FULL> m(a.dr_out, row * a.ld_dr_out, H);
 #pragma unroll
-      for (int p = 0; p < NV; ++p) d[p] = load4<RT>(p0, 4 * (p * 64 * W + lane), H);
+      for (int p = 0; p < NV; ++p) d[p] = m.load(at(p));
     } else {
 #pragma unroll
-      for (int p = 0; p < NV; ++p) d[p] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int p = 0; p < NV; ++p) d[p] = zero;
     }
     if (HAS_Y) {
-      const auto* p0 = static_cast<const typename YT::elem*>(a.y) + row * a.ld_y;
+      const Row<YT, FULL> m(a.y, row * a.ld_y, H);
 #pragma unroll
-      for (int p = 0; p < NV; ++p) y[p] = load4<YT>(p0, 4 * (p * 64 * W + lane), H);
+      for (int p = 0; p < NV; ++p) y[p] = m.load(at(p));
     }
-    if (a.dx) {
+    if (has_dx) {
       f32x4 r[NV], u[NV];
-      const auto* p0 = static_cast<const typename RT::elem*>(a.r) + row * a.ld_r;
+      const Row<RT, FULL> m(a.r, row * a.ld_r, H);
 #pragma unroll
-      for (int p = 0; p < NV; ++p) r[p] = load4<RT>(p0, 4 * (p * 64 * W + lane), H);
+      for (int p = 0; p < NV; ++p) r[p] = m.load(at(p));
+      if (a.dx_bf16) {
+        const Row<BF16, FULL> mu(a.dx, row * a.ld_dx, H);
 #pragma unroll
-      for (int p = 0; p < NV; ++p) {
-        const int i = 4 * (p * 64 * W + lane);
-        u[p] = a.dx_bf16 ? load4<BF16>(static_cast<const uint16_t*>(a.dx) + row * a.ld_dx, i, H)
-                         : load4<F32>(static_cast<const float*>(a.dx) + row * a.ld_dx, i, H);
+        for (int p = 0; p < NV; ++p) u[p] = mu.load(at(p));
+      } else {
+        const Row<F32, FULL> mu(a.dx, row * a.ld_dx, H);
+#pragma unroll
+        for (int p = 0; p < NV; ++p) u[p] = mu.load(at(p));
       }
-      float mean = 0.0f;
       if (pre_layer) {
         float t[1] = {0.0f};
 #pragma unroll
         for (int p = 0; p < NV; ++p) t[0] += (r[p][0] + r[p][1]) + (r[p][2] + r[p][3]);
         row_sum<W>(t, slot, wave);
-        mean = t[0] * inv;
+        const float mean = t[0] * inv;
+#pragma unroll
+        for (int p = 0; p < NV; ++p)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) r[p][e] = inside(at(p), e) ? r[p][e] - mean : 0.0f;
       }
-      // sum c^2, sum u w c, sum u w with c = r' - mean
-      float q[3] = {0.0f, 0.0f, 0.0f};
+      // sum c^2, sum u w c, and for a LayerNorm sum u w, with c = r' - mean
+      float q[LAYER ? 3 : 2] = {};
 #pragma unroll
       for (int p = 0; p < NV; ++p) {
-        const int i = 4 * (p * 64 * W + lane);
-        const f32x4 w = load4_param(a.w_pre, a.p_bf16, i, H);
+        const f32x4 w = KEEP ? wu[p] : pre_scale(p);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float c = i + e < H ? r[p][e] - mean : 0.0f;
-          r[p][e] = c;
-          q[0] = __builtin_fmaf(c, c, q[0]);
-          q[1] = __builtin_fmaf(u[p][e] * w[e], c, q[1]);
-          q[2] = __builtin_fmaf(u[p][e], w[e], q[2]);
+          const float t = u[p][e] * w[e];
+          q[0] = __builtin_fmaf(r[p][e], r[p][e], q[0]);
+          q[1] = __builtin_fmaf(t, r[p][e], q[1]);
+          if (LAYER) q[LAYER ? 2 : 0] += t;
         }
       }
       row_sum<W>(q, slot + W, wave);
       const float rstd = 1.0f / sqrtf(__builtin_fmaf(q[0], inv, a.eps));
-      const float dot = q[1] * rstd * inv, mu = pre_layer ? q[2] * inv : 0.0f;
+      const float dot = q[1] * rstd * inv, mu = pre_layer ? q[LAYER ? 2 : 0] * inv : 0.0f;
 #pragma unroll
       for (int p = 0; p < NV; ++p) {
-        const int i = 4 * (p * 64 * W + lane);
-        const f32x4 w = load4_param(a.w_pre, a.p_bf16, i, H);
-        const f32x4 xh = r[p] * rstd;
-        T1[p] += u[p] * xh;
+        const f32x4 w = KEEP ? wu[p] : pre_scale(p), xh = r[p] * rstd;
+        if (T_LDS) t_lds[p * 64 * W + lane] += u[p] * xh;
+        else T1[p] += u[p] * xh;
         if (LAYER) T0[p] += u[p];
-        d[p] += (u[p] * w - mu - xh * dot) * rstd;
+        f32x4 g = u[p] * w - xh * dot;
+        if (LAYER) g -= mu;
+        d[p] += g * rstd;
       }
     }
     {
-      auto* p0 = static_cast<typename RT::elem*>(a.dr) + row * a.ld_dr;
+      const Row<RT, FULL> m(a.dr, row * a.ld_dr, H);
 #pragma unroll
-      for (int p = 0; p < NV; ++p) store4<RT>(p0, 4 * (p * 64 * W + lane), H, d[p] * a.alpha);
+      for (int p = 0; p < NV; ++p) m.store(at(p), d[p] * a.alpha);
     }
     if (!HAS_Y) continue;
-    uint16_t* dyp = a.dy + row * a.ld_dy;
-    if (a.post == TPMLP_NORM_NONE) {
+    const Row<BF16, FULL> dyr(a.dy, row * a.ld_dy, H);
+    if (!post) {
 #pragma unroll
       for (int p = 0; p < NV; ++p) {
-        const int i = 4 * (p * 64 * W + lane);
         S1[p] += d[p] * y[p];
-        if (a.gate) d[p] *= load4_param(gp, a.p_bf16, i, H);
-        store4<BF16>(dyp, i, H, d[p]);
+        dyr.store(at(p), d[p] * (KEEP ? wv[p] : post_scale(p)));
       }
       continue;
     }
-    float mean = 0.0f;
     if (post_layer) {
       float t[1] = {0.0f};
 #pragma unroll
       for (int p = 0; p < NV; ++p) t[0] += (y[p][0] + y[p][1]) + (y[p][2] + y[p][3]);
       row_sum<W>(t, slot + 4 * W, wave);
-      mean = t[0] * inv;
+      const float mean = t[0] * inv;
+#pragma unroll
+      for (int p = 0; p < NV; ++p)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[p][e] = inside(at(p), e) ? y[p][e] - mean : 0.0f;
     }
-    float q[3] = {0.0f, 0.0f, 0.0f};
+    float q[LAYER ? 3 : 2] = {};
 #pragma unroll
     for (int p = 0; p < NV; ++p) {
-      const int i = 4 * (p * 64 * W + lane);
-      f32x4 v = load4_param(a.w_post, a.p_bf16, i, H);
-      if (a.gate) v *= load4_param(gp, a.p_bf16, i, H);
+      const f32x4 v = KEEP ? wv[p] : post_scale(p);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float c = i + e < H ? y[p][e] - mean : 0.0f, t = i + e < H ? d[p][e] * v[e] : 0.0f;
-        y[p][e] = c;
-        q[0] = __builtin_fmaf(c, c, q[0]);
-        q[1] = __builtin_fmaf(t, c, q[1]);
-        q[2] += t;
+        const float t = d[p][e] * v[e];  // v is 0 past the row's end
+        q[0] = __builtin_fmaf(y[p][e], y[p][e], q[0]);
+        q[1] = __builtin_fmaf(t, y[p][e], q[1]);
+        if (LAYER) q[LAYER ? 2 : 0] += t;
       }
     }
     row_sum<W>(q, slot + 5 * W, wave);
     const float rstd = 1.0f / sqrtf(__builtin_fmaf(q[0], inv, a.eps));
-    const float dot = q[1] * rstd * inv, mu = post_layer ? q[2] * inv : 0.0f;
+    const float dot = q[1] * rstd * inv, mu = post_layer ? q[LAYER ? 2 : 0] * inv : 0.0f;
 #pragma unroll
     for (int p = 0; p < NV; ++p) {
-      const int i = 4 * (p * 64 * W + lane);
-      f32x4 v = load4_param(a.w_post, a.p_bf16, i, H);
-      if (a.gate) v *= load4_param(gp, a.p_bf16, i, H);
-      const f32x4 yh = y[p] * rstd;
+      const f32x4 v = KEEP ? wv[p] : post_scale(p), yh = y[p] * rstd;
       S1[p] += d[p] * yh;
       if (LAYER) S0[p] += d[p];
-      store4<BF16>(dyp, i, H, (d[p] * v - mu - yh * dot) * rstd);
+      f32x4 g = d[p] * v - yh * dot;
+      if (LAYER) g -= mu;
+      dyr.store(at(p), g * rstd);
     }
   }
 
   if (!a.part) return;
-  float* part = a.part + (int64_t)blockIdx.x * NACC * H;
+  const int64_t part = (int64_t)blockIdx.x * NACC * H;
+  auto sum_of = [&](int k, int p) {
+    return k == 0 ? S1[p] : k == 1 ? (T_LDS ? t_lds[p * 64 * W + lane] : T1[T_LDS ? 0 : p]) : k == 2 ? S0[LAYER ? p : 0] : T0[LAYER ? p : 0];
+  };
   if (W > 1) {
 #pragma unroll
-    for (int p = 0; p < NV; ++p) {
-      const int i = 4 * (p * 64 * W + lane);
-      store4<F32>(part, i, H, S1[p]);
-      store4<F32>(part + H, i, H, T1[p]);
-      if (LAYER) {
-        store4<F32>(part + 2 * (int64_t)H, i, H, S0[p]);
-        store4<F32>(part + 3 * (int64_t)H, i, H, T0[p]);
-      }
+    for (int k = 0; k < NACC; ++k) {
+      const Row<F32, FULL> m(a.part, part + (int64_t)k * H, H);
+#pragma unroll
+      for (int p = 0; p < NV; ++p) m.store(at(p), sum_of(k, p));
     }
     return;
   }
@@ -191,48 +216,54 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) edge_bwd_kernel(EdgeBwd
   for (int k = 0; k < NACC; ++k) {
     __syncthreads();
 #pragma unroll
-    for (int p = 0; p < NV; ++p)
-      joint[wave * 64 * NV + p * 64 + lane] = k == 0 ? S1[p] : k == 1 ? T1[p] : k == 2 ? S0[LAYER ? p : 0] : T0[LAYER ? p : 0];
+    for (int p = 0; p < NV; ++p) joint[wave * 64 * NV + p * 64 + lane] = sum_of(k, p);
     __syncthreads();
-    if (wave == 0)
+    if (wave == 0) {
+      const Row<F32, FULL> m(a.part, part + (int64_t)k * H, H);
 #pragma unroll
       for (int p = 0; p < NV; ++p) {
         f32x4 t = joint[p * 64 + lane];
 #pragma unroll
         for (int w = 1; w < 4; ++w) t += joint[w * 64 * NV + p * 64 + lane];
-        store4<F32>(part + (int64_t)k * H, 4 * (p * 64 + lane), H, t);
+        m.store(at(p), t);
       }
+    }
   }
 }
 
 template <class YT, class RT, bool HAS_Y, bool LAYER>
-hipError_t launch_shape(const EdgeBwdArgs& a, int64_t blocks, hipStream_t s) {
+hipError_t launch_shape(const EdgeBwdArgs& a, int64_t blocks, bool full, hipStream_t s) {
   const dim3 grid((unsigned)blocks);
-  if (a.H <= 512) return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 1, 2>, grid, dim3(256), s, a);
-  if (a.H <= 1024) return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 1, 4>, grid, dim3(256), s, a);
-  if (a.H <= 2048) return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 4, 2>, grid, dim3(256), s, a);
-  if (a.H <= 4096) return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 4, 4>, grid, dim3(256), s, a);
-  if (a.H <= 8192) return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 8, 4>, grid, dim3(512), s, a);
-  if (a.H <= 16384) return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 4>, grid, dim3(1024), s, a);
-  if (a.H <= 20480) return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 5>, grid, dim3(1024), s, a);
-  if (a.H <= TPMLP_EDGE_MAX_H) return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 8>, grid, dim3(1024), s, a);
+  switch (edge_bwd_shape(a.H, full)) {
+    case EDGE_1x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 1, 2, true>, grid, dim3(256), s, a);
+    case EDGE_4x1: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 4, 1, true>, grid, dim3(256), s, a);
+    case EDGE_4x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 4, 2, true>, grid, dim3(256), s, a);
+    case EDGE_8x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 8, 2, true>, grid, dim3(512), s, a);
+    case EDGE_16x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 2, true>, grid, dim3(1024), s, a);
+    case EDGE_16x4: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 4, true>, grid, dim3(1024), s, a);
+    case EDGE_16x5: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 5, true>, grid, dim3(1024), s, a);
+    case EDGE_16x8: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 8, true>, grid, dim3(1024), s, a);
+    case EDGE_ANY_4x1: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 4, 1, false>, grid, dim3(256), s, a);
+    case EDGE_ANY_8x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 8, 2, false>, grid, dim3(512), s, a);
+    case EDGE_ANY_16x8: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 8, false>, grid, dim3(1024), s, a);
+  }
   return hipErrorInvalidValue;
 }
 
 template <bool LAYER>
-hipError_t launch_types(const EdgeBwdArgs& a, int64_t blocks, int y_type, int r_type, hipStream_t s) {
+hipError_t launch_types(const EdgeBwdArgs& a, int64_t blocks, int y_type, int r_type, bool full, hipStream_t s) {
   const bool rb = r_type == TPMLP_BF16;
   if (y_type < 0)
-    return rb ? launch_shape<F32, BF16, false, LAYER>(a, blocks, s) : launch_shape<F32, F32, false, LAYER>(a, blocks, s);
+    return rb ? launch_shape<F32, BF16, false, LAYER>(a, blocks, full, s) : launch_shape<F32, F32, false, LAYER>(a, blocks, full, s);
   if (y_type == TPMLP_BF16)
-    return rb ? launch_shape<BF16, BF16, true, LAYER>(a, blocks, s) : launch_shape<BF16, F32, true, LAYER>(a, blocks, s);
-  return rb ? launch_shape<F32, BF16, true, LAYER>(a, blocks, s) : launch_shape<F32, F32, true, LAYER>(a, blocks, s);
+    return rb ? launch_shape<BF16, BF16, true, LAYER>(a, blocks, full, s) : launch_shape<BF16, F32, true, LAYER>(a, blocks, full, s);
+  return rb ? launch_shape<F32, BF16, true, LAYER>(a, blocks, full, s) : launch_shape<F32, F32, true, LAYER>(a, blocks, full, s);
 }
 
 }  // namespace edge
 
 // Defined by the two instantiating files.
-hipError_t launch_edge_bwd_rms(const EdgeBwdArgs& a, int64_t blocks, int y_type, int r_type, hipStream_t s);
-hipError_t launch_edge_bwd_layer(const EdgeBwdArgs& a, int64_t blocks, int y_type, int r_type, hipStream_t s);
+hipError_t launch_edge_bwd_rms(const EdgeBwdArgs& a, int64_t blocks, int y_type, int r_type, bool full, hipStream_t s);
+hipError_t launch_edge_bwd_layer(const EdgeBwdArgs& a, int64_t blocks, int y_type, int r_type, bool full, hipStream_t s);
 
 }  // namespace tpmlp

@@ -8,85 +8,87 @@
 namespace tpmlp {
 namespace {
 
-// One workgroup finishes 32 columns: 32 lanes side by side on a row of the
-// partial sums, 32 of them down the slices.  For few gate rows the 32 go over the
-// slices of one gate row after another; for many (32 or more) each takes whole
-// gate rows, which then need no exchange between lanes.
-__global__ void __launch_bounds__(1024) edge_finish_kernel(EdgeFinishArgs a) {
-  __shared__ float sums[32][33];
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int col = (int)blockIdx.x * 32 + tx, H = a.H;
+// One workgroup finishes 16 columns: 16 lanes side by side on a row of the partial
+// sums, and 64 lines of them down the slices.  The largest power of two of lines that
+// lets the 64 work on different rows of the gate shares one row's slices.  A line
+// adds all four sums of its slices in one walk, eight slices' loads issued before
+// the first is added: the slices come from other XCDs' writes, through memory, and
+// the kernel is bound by the latency of these loads.
+constexpr int FIN_COLS = 16, FIN_LINES = 64, FIN_BATCH = 8;
+
+template <int NACC>
+__global__ void __launch_bounds__(FIN_COLS * FIN_LINES) edge_finish_kernel(EdgeFinishArgs a) {
+  __shared__ float sums[4][FIN_LINES][FIN_COLS + 1];
+  const int tx = threadIdx.x % FIN_COLS, ty = threadIdx.x / FIN_COLS;
+  const int H = a.H, col = (int)blockIdx.x * FIN_COLS + tx, c = min(col, H - 1);
   const bool in = col < H;
-  const int64_t blocks = a.groups * a.chunks, step = (int64_t)a.n_acc * H;
-  const float* base = a.part + col;
-  const bool layer = a.n_acc == EDGE_ACC_LAYER;
-
-  // Sum of v over the 32 lanes of a column, on every one of them.
-  auto column = [&](float v) {
-    __syncthreads();
-    sums[ty][tx] = v;
-    __syncthreads();
-    float t = 0.0f;
+  const int64_t step = (int64_t)NACC * H;
+  const float w = a.w_post ? load_param(a.w_post, a.p_bf16, c) : 1.0f;
+  const float b0 = a.b_post ? load_param(a.b_post, a.p_bf16, c) : 0.0f;
+  int share = FIN_LINES;  // lines to a row of the gate
+  while (share > 1 && share * a.groups > FIN_LINES) share >>= 1;
+  const int line = ty % share;
+  float dw = 0.0f, db = 0.0f, t1 = 0.0f, t0 = 0.0f;
+  for (int64_t g0 = 0; g0 < a.groups; g0 += FIN_LINES / share) {
+    const int64_t g = g0 + ty / share;
+    float s[4] = {};
+    if (g < a.groups) {
+      const float* slice = a.part + g * a.chunks * step + c;
+      for (int b = line; b < a.chunks; b += FIN_BATCH * share) {
+        float v[FIN_BATCH][NACC];
 #pragma unroll
-    for (int k = 0; k < 32; ++k) t += sums[k][tx];
-    return t;
-  };
-
-  if (a.dw_pre || a.db_pre) {
-    float t1 = 0.0f, t0 = 0.0f;
-    for (int64_t b = ty; in && b < blocks; b += 32) {
-      t1 += base[b * step + H];
-      if (layer) t0 += base[b * step + 3 * (int64_t)H];
-    }
-    t1 = column(t1);
-    t0 = column(t0);
-    if (in && ty == 0) {
-      if (a.dw_pre) a.dw_pre[col] = t1;
-      if (a.db_pre) a.db_pre[col] = t0;
-    }
-  }
-  if (!a.dw_post && !a.db_post && !a.dgate) return;
-  const float w = in && a.w_post ? load_param(a.w_post, a.p_bf16, col) : 1.0f;
-  const float b0 = in && a.b_post ? load_param(a.b_post, a.p_bf16, col) : 0.0f;
-  float dw = 0.0f, db = 0.0f;
-  if (a.groups >= 32) {
-    for (int64_t g = ty; in && g < a.groups; g += 32) {
-      float s1 = 0.0f, s0 = 0.0f;
-      for (int c = 0; c < a.chunks; ++c) {
-        s1 += base[(g * a.chunks + c) * step];
-        if (layer) s0 += base[(g * a.chunks + c) * step + 2 * (int64_t)H];
-      }
-      const float gate = a.gate ? load_param(a.gate, a.p_bf16, g * a.ld_gate + col) : 1.0f;
-      dw += gate * s1;
-      db += gate * s0;
-      if (a.dgate) a.dgate[g * H + col] = w * s1 + b0 * s0;
-    }
-  } else {
-    for (int64_t g = 0; g < a.groups; ++g) {
-      float s1 = 0.0f, s0 = 0.0f;
-      for (int c = ty; in && c < a.chunks; c += 32) {
-        s1 += base[(g * a.chunks + c) * step];
-        if (layer) s0 += base[(g * a.chunks + c) * step + 2 * (int64_t)H];
-      }
-      s1 = column(s1);
-      s0 = column(s0);
-      if (in && ty == 0) {
-        const float gate = a.gate ? load_param(a.gate, a.p_bf16, g * a.ld_gate + col) : 1.0f;
-        dw += gate * s1;
-        db += gate * s0;
-        if (a.dgate) a.dgate[g * H + col] = w * s1 + b0 * s0;
+        for (int k = 0; k < FIN_BATCH; ++k)
+#pragma unroll
+          for (int j = 0; j < NACC; ++j) v[k][j] = slice[min(b + k * share, a.chunks - 1) * step + (int64_t)j * H];
+#pragma unroll
+        for (int k = 0; k < FIN_BATCH; ++k)
+#pragma unroll
+          for (int j = 0; j < NACC; ++j) s[j] += b + k * share < a.chunks ? v[k][j] : 0.0f;
       }
     }
+    t1 += s[1];
+    t0 += s[3];
+    float s1 = s[0], s0 = s[2];
+    if (share > 1) {  // uniform; then there is one pass over the groups
+      sums[0][ty][tx] = s1;
+      sums[1][ty][tx] = s0;
+      __syncthreads();
+      s1 = s0 = 0.0f;
+      if (line == 0)
+        for (int k = 0; k < share; ++k) {
+          s1 += sums[0][ty + k][tx];
+          s0 += sums[1][ty + k][tx];
+        }
+      __syncthreads();
+    }
+    if (line == 0 && g < a.groups) {
+      const float gate = a.gate ? load_param(a.gate, a.p_bf16, g * a.ld_gate + c) : 1.0f;
+      dw = __builtin_fmaf(gate, s1, dw);
+      db = __builtin_fmaf(gate, s0, db);
+      if (a.dgate && in) a.dgate[g * H + col] = w * s1 + b0 * s0;
+    }
   }
-  dw = column(dw);
-  db = column(db);
-  if (in && ty == 0) {
-    if (a.dw_post) a.dw_post[col] = dw;
-    if (a.db_post) a.db_post[col] = db;
-  }
+  sums[0][ty][tx] = t1;
+  sums[1][ty][tx] = t0;
+  sums[2][ty][tx] = dw;
+  sums[3][ty][tx] = db;
+  __syncthreads();
+  if (ty >= 4 || !in) return;
+  float* out = ty == 0 ? a.dw_pre : ty == 1 ? a.db_pre : ty == 2 ? a.dw_post : a.db_post;
+  if (!out) return;
+  float t = 0.0f;
+#pragma unroll
+  for (int k = 0; k < FIN_LINES; ++k) t += sums[ty][k][tx];
+  out[col] = t;
 }
 
 }  // namespace
+
+EdgeShape edge_bwd_shape(int H, bool full) {
+  if (!full) return H <= 1024 ? EDGE_ANY_4x1 : H <= 4096 ? EDGE_ANY_8x2 : EDGE_ANY_16x8;
+  return H <= 512 ? EDGE_1x2 : H <= 1024 ? EDGE_4x1 : H <= 2048 ? EDGE_4x2 : H <= 4096 ? EDGE_8x2 : H <= 8192 ? EDGE_16x2
+       : H <= 16384 ? EDGE_16x4 : H <= 20480 ? EDGE_16x5 : EDGE_16x8;
+}
 
 EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer) {
   EdgeBwdPlan p{};
@@ -94,30 +96,34 @@ EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer) {
   if (M < 1) return p;
   gate_rows = std::min(gate_rows, M);
   p.groups = (M + gate_rows - 1) / gate_rows;
-  // Workgroups that fill the 256 CUs: a workgroup of four one-row waves or of four
-  // waves to a row leaves room for several on a CU, one of 1024 threads does not.
-  const int64_t target = H <= 4096 ? 1024 : H <= 8192 ? 512 : 256;
-  const int64_t least = H <= 1024 ? 4 : 1;  // rows that a workgroup holds at once
+  // As many workgroups as the 256 CUs hold at once (a workgroup walks several
+  // rows), so that all of them end together.
+  const int64_t target = H <= 2048 ? 1024 : H <= 4096 ? 512 : 256;
+  // Rows that a workgroup takes at least: those it holds at once, and up to four while
+  // there is a workgroup for every CU, which keeps the slices below the data.
+  const int64_t least = std::max<int64_t>(H <= 512 ? 4 : 1, std::min<int64_t>(4, M / 256));
   const int64_t chunks = std::max<int64_t>(1, std::min(target / p.groups, (gate_rows + least - 1) / least));
-  p.chunk_rows = ((gate_rows + chunks - 1) / chunks + least - 1) / least * least;
+  p.chunk_rows = (gate_rows + chunks - 1) / chunks;
   p.chunks = (int)((gate_rows + p.chunk_rows - 1) / p.chunk_rows);
   p.ws_bytes = size_t(p.groups) * p.chunks * p.n_acc * H * 4;
   return p;
 }
 
-hipError_t launch_edge_bwd_rms(const EdgeBwdArgs& a, int64_t blocks, int y_type, int r_type, hipStream_t s) {
-  return edge::launch_types<false>(a, blocks, y_type, r_type, s);
+hipError_t launch_edge_bwd_rms(const EdgeBwdArgs& a, int64_t blocks, int y_type, int r_type, bool full, hipStream_t s) {
+  return edge::launch_types<false>(a, blocks, y_type, r_type, full, s);
 }
 
-hipError_t launch_edge_bwd(const EdgeBwdArgs& a, const EdgeBwdPlan& p, int y_type, int r_type, hipStream_t s) {
+hipError_t launch_edge_bwd(const EdgeBwdArgs& a, const EdgeBwdPlan& p, int y_type, int r_type, bool full, hipStream_t s) {
   const int64_t blocks = p.groups * p.chunks;
   if (a.M < 1 || blocks < 1 || blocks > INT32_MAX || a.H < 4) return hipErrorInvalidValue;
-  return p.n_acc == EDGE_ACC_LAYER ? launch_edge_bwd_layer(a, blocks, y_type, r_type, s)
-                                   : launch_edge_bwd_rms(a, blocks, y_type, r_type, s);
+  return p.n_acc == EDGE_ACC_LAYER ? launch_edge_bwd_layer(a, blocks, y_type, r_type, full, s)
+                                   : launch_edge_bwd_rms(a, blocks, y_type, r_type, full, s);
 }
 
 hipError_t launch_edge_finish(const EdgeFinishArgs& a, hipStream_t s) {
-  return launch_kernel(edge_finish_kernel, dim3((unsigned)((a.H + 31) / 32)), dim3(1024), s, a);
+  const dim3 grid((unsigned)((a.H + FIN_COLS - 1) / FIN_COLS)), block(FIN_COLS * FIN_LINES);
+  return a.n_acc == EDGE_ACC_LAYER ? launch_kernel(edge_finish_kernel<EDGE_ACC_LAYER>, grid, block, s, a)
+                                   : launch_kernel(edge_finish_kernel<EDGE_ACC_RMS>, grid, block, s, a);
 }
 
 }  // namespace tpmlp
