@@ -40,14 +40,11 @@ __device__ __forceinline__ void put1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put1(uint16_t* p, float v) { *p = f32_to_bf16(v); }
 
 // Elements i .. i+3 of a row of n >= 4 elements, zeros past its end.  Every lane
-// reads four elements inside the row (the last four where i + 4 > n), so no lane
+// reads four elements inside the row (the last four, v, where i + 4 > n), so no lane
 // branches around the load; a lane on the ragged end shifts what it read.
-template <class T>
-__device__ __forceinline__ f32x4 load4(const typename T::elem* row, int i, int n) {
-  const int at = min(i, n - 4);
-  f32x4 v = widen(*reinterpret_cast<const typename T::vec*>(row + at));
-  if (i > at) {
-    const int s = i - at;
+__device__ __forceinline__ f32x4 from4(f32x4 v, int i, int n) {
+  if (i > n - 4) {
+    const int s = i - (n - 4);
     f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
     if (s == 1) o = f32x4{v[1], v[2], v[3], 0.0f};
     if (s == 2) o = f32x4{v[2], v[3], 0.0f, 0.0f};
@@ -55,6 +52,10 @@ __device__ __forceinline__ f32x4 load4(const typename T::elem* row, int i, int n
     v = o;
   }
   return v;
+}
+template <class T>
+__device__ __forceinline__ f32x4 load4(const typename T::elem* row, int i, int n) {
+  return from4(widen(*reinterpret_cast<const typename T::vec*>(row + min(i, n - 4))), i, n);
 }
 
 // Stores elements i .. i+3 of a row of n elements, those inside it.
@@ -84,8 +85,12 @@ struct Row<T, false> {
   int n;
   __device__ __forceinline__ Row(const void* base, int64_t at, int n_)
       : p(const_cast<elem*>(static_cast<const elem*>(base)) + at), n(n_) {}
-  __device__ __forceinline__ f32x4 load(int i) const { return load4<T>(p, i, n); }
+  __device__ __forceinline__ f32x4 load(int i) const { return widen_raw(load_raw(i), i, n); }
   __device__ __forceinline__ void store(int i, f32x4 v) const { store4<T>(p, i, n, v); }
+  // The load and the conversion apart, for a row that is fetched before it is used.
+  typedef typename T::vec raw;
+  __device__ __forceinline__ raw load_raw(int i) const { return *reinterpret_cast<const raw*>(p + min(i, n - 4)); }
+  static __device__ __forceinline__ f32x4 widen_raw(raw v, int i, int n) { return from4(widen(v), i, n); }
 };
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
@@ -99,15 +104,21 @@ struct Row<T, true> {
       : rs(__builtin_amdgcn_make_buffer_rsrc(
             const_cast<typename T::elem*>(static_cast<const typename T::elem*>(base)) + at, (short)0,
             (int)(n * sizeof(typename T::elem)), 0x00020000)) {}
-  __device__ __forceinline__ f32x4 load(int i) const {
-    if constexpr (sizeof(typename T::elem) == 4) {
-      return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, i * 4, 0, 0));
-    } else {
-      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, i * 2, 0, 0));
+  typedef uint32_t raw __attribute__((ext_vector_type(sizeof(typename T::elem))));  // four elements
+  __device__ __forceinline__ raw load_raw(int i) const {
+    if constexpr (sizeof(typename T::elem) == 4)
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b128(rs, i * 4, 0, 0));
+    else
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(rs, i * 2, 0, 0));
+  }
+  static __device__ __forceinline__ f32x4 widen_raw(raw v, int, int) {
+    if constexpr (sizeof(typename T::elem) == 4)
+      return __builtin_bit_cast(f32x4, v);
+    else
       return f32x4{__builtin_bit_cast(float, v[0] << 16), __builtin_bit_cast(float, v[0] & 0xFFFF0000u),
                    __builtin_bit_cast(float, v[1] << 16), __builtin_bit_cast(float, v[1] & 0xFFFF0000u)};
-    }
   }
+  __device__ __forceinline__ f32x4 load(int i) const { return widen_raw(load_raw(i), i, 0); }
   __device__ __forceinline__ void store(int i, f32x4 v) const {
     if constexpr (sizeof(typename T::elem) == 4) {
       __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, i * 4, 0, 0);
@@ -125,7 +136,37 @@ struct Row<T, true> : Row<T, false> {
 };
 #endif
 
-// Parameter vectors are float32 or bf16 by a flag uniform over the launch.
+// NV chunks of a parameter vector that is float32 or bf16 by a flag uniform over the
+// launch: loaded under the flag, converted later under the flag again, so that the
+// loads of several vectors are in flight together.
+template <int NV, bool FULL>
+struct Params {
+  typedef typename Row<F32, FULL>::raw raw32;
+  typedef typename Row<BF16, FULL>::raw raw16;
+  raw32 v[NV];  // bf16: the first half of each
+  template <class At>
+  __device__ __forceinline__ void fetch(const void* p, int bf16, int64_t at, At&& place, int n) {
+    if (bf16) {
+      const Row<BF16, FULL> m(p, at, n);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const raw16 t = m.load_raw(place(k));
+        __builtin_memcpy(&v[k], &t, sizeof t);
+      }
+    } else {
+      const Row<F32, FULL> m(p, at, n);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) v[k] = m.load_raw(place(k));
+    }
+  }
+  __device__ __forceinline__ f32x4 get(int k, int bf16, int i, int n) const {
+    raw16 t;
+    __builtin_memcpy(&t, &v[k], sizeof t);
+    return bf16 ? Row<BF16, FULL>::widen_raw(t, i, n) : Row<F32, FULL>::widen_raw(v[k], i, n);
+  }
+};
+
+// One chunk of such a vector.
 template <bool FULL>
 __device__ __forceinline__ f32x4 load_params(const void* p, int bf16, int64_t at, int i, int n) {
   return bf16 ? Row<BF16, FULL>(p, at, n).load(i) : Row<F32, FULL>(p, at, n).load(i);
@@ -134,11 +175,32 @@ __device__ __forceinline__ float load_param(const void* p, int bf16, int64_t i) 
   return bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+// Sum over the wave, on every lane, in the register file: within quads, the halves
+// of a 16-lane row and its two halves by DPP moves, between rows by the swaps of
+// gfx950.  No LDS access, whose latency six times over was most of a short row's time.
+#if defined(__HIP_DEVICE_COMPILE__)
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true);
+  return v + __builtin_bit_cast(float, o);
 }
+__device__ __forceinline__ float wave_sum(float v) {
+  v = add_dpp<0xB1>(v);   // quad_perm [1,0,3,2]
+  v = add_dpp<0x4E>(v);   // quad_perm [2,3,0,1]
+  v = add_dpp<0x141>(v);  // row_half_mirror: the other quad of eight lanes
+  v = add_dpp<0x140>(v);  // row_mirror: the other eight lanes of the row
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto rows = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t r0 = rows[0], r1 = rows[1];  // values: a bit cast of a vector's element would take its first
+  v = __builtin_bit_cast(float, r0) + __builtin_bit_cast(float, r1);
+  const uint32_t c = __builtin_bit_cast(uint32_t, v);
+  const auto halves = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+  const uint32_t h0 = halves[0], h1 = halves[1];
+  return __builtin_bit_cast(float, h0) + __builtin_bit_cast(float, h1);
+}
+#else
+__device__ inline float wave_sum(float v) { return v; }
+#endif
 
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll

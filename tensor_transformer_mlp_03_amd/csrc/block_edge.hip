@@ -55,34 +55,62 @@ __device__ __forceinline__ void row_stats(const f32x4 (&v)[NV], int kind, int la
   rstd = 1.0f / sqrtf(__builtin_fmaf(q[0], inv, eps));
 }
 
-template <class YT, class RT, bool HAS_Y, int W, int NV, bool FULL>
+// Rows up to four chunks a lane have their parameters loaded with the row, so that no
+// load waits behind a sum; wider ones would lose a resident workgroup to the registers.
+template <class YT, class RT, class PT, bool HAS_Y, int W, int NV, bool FULL>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, W == 16 && NV <= 5 ? 8 : 1) edge_fwd_kernel(EdgeFwdArgs a) {
+  constexpr bool EARLY = NV <= 4 && W < 16;
   __shared__ float slots[4 * W];
   const int lane = W == 1 ? threadIdx.x & 63 : threadIdx.x;  // of the row
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
   if (row >= a.M) return;  // W == 1 only, where no barrier follows
   const int H = a.H;
+  auto at = [&](int p) { return 4 * (p * 64 * W + lane); };
+  const bool post = HAS_Y && a.post != TPMLP_NORM_NONE, gated = HAS_Y && a.gate;
+  const Row<PT, FULL> w_post(a.w_post, 0, H), b_post(a.b_post, 0, H), w_pre(a.w_pre, 0, H), b_pre(a.b_pre, 0, H);
+  const Row<PT, FULL> gate(a.gate, gated ? (row / a.gate_rows) * a.ld_gate : 0, H);
+  typedef typename Row<PT, FULL>::raw praw;
+  auto value = [&](praw v, int p) { return Row<PT, FULL>::widen_raw(v, at(p), H); };
+
   f32x4 r[NV], y[NV];
+  praw wp[NV], g[NV], wn[NV];
   const Row<RT, FULL> rr(a.r, row * a.ld_r, H);
+  const Row<YT, FULL> yr(a.y, HAS_Y ? row * a.ld_y : 0, H);
+  typename Row<RT, FULL>::raw r0[NV];
+  typename Row<YT, FULL>::raw y0[NV];
+  if (HAS_Y)
 #pragma unroll
-  for (int p = 0; p < NV; ++p) r[p] = rr.load(4 * (p * 64 * W + lane));
+    for (int p = 0; p < NV; ++p) y0[p] = yr.load_raw(at(p));
+#pragma unroll
+  for (int p = 0; p < NV; ++p) r0[p] = rr.load_raw(at(p));
+  if (EARLY) {
+    if (post)
+#pragma unroll
+      for (int p = 0; p < NV; ++p) wp[p] = w_post.load_raw(at(p));
+    if (gated)
+#pragma unroll
+      for (int p = 0; p < NV; ++p) g[p] = gate.load_raw(at(p));
+    if (a.x)
+#pragma unroll
+      for (int p = 0; p < NV; ++p) wn[p] = w_pre.load_raw(at(p));
+  }
+#pragma unroll
+  for (int p = 0; p < NV; ++p) {
+    if (HAS_Y) y[p] = Row<YT, FULL>::widen_raw(y0[p], at(p), H);
+    r[p] = Row<RT, FULL>::widen_raw(r0[p], at(p), H);
+  }
   if (HAS_Y) {
-    const Row<YT, FULL> yr(a.y, row * a.ld_y, H);
-#pragma unroll
-    for (int p = 0; p < NV; ++p) y[p] = yr.load(4 * (p * 64 * W + lane));
     float mean = 0.0f, rstd = 1.0f;
-    if (a.post != TPMLP_NORM_NONE) row_stats<W, NV, FULL>(y, a.post, lane, H, a.eps, slots, wave, mean, rstd);
-    const int64_t g0 = a.gate ? (row / a.gate_rows) * a.ld_gate : 0;
+    if (post) row_stats<W, NV, FULL>(y, a.post, lane, H, a.eps, slots, wave, mean, rstd);
 #pragma unroll
     for (int p = 0; p < NV; ++p) {
-      const int i = 4 * (p * 64 * W + lane);
       f32x4 n = y[p];
-      if (a.post != TPMLP_NORM_NONE) {
-        n = (n - mean) * rstd * load_params<FULL>(a.w_post, a.p_bf16, 0, i, H);
-        if (a.b_post) n += load_params<FULL>(a.b_post, a.p_bf16, 0, i, H);
+      if (post) {
+        n = (n - mean) * rstd * (EARLY ? value(wp[p], p) : w_post.load(at(p)));
+        if (a.b_post) n += b_post.load(at(p));
       }
-      if (a.gate) n *= load_params<FULL>(a.gate, a.p_bf16, g0, i, H);
+      if (gated) n *= EARLY ? value(g[p], p) : gate.load(at(p));
       r[p] = r[p] * a.alpha + n;
     }
   } else {
@@ -92,40 +120,48 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, W == 16 && NV <= 5 ? 8 
   if (a.r_out) {
     const Row<RT, FULL> ro(a.r_out, row * a.ld_r_out, H);
 #pragma unroll
-    for (int p = 0; p < NV; ++p) ro.store(4 * (p * 64 * W + lane), r[p]);
+    for (int p = 0; p < NV; ++p) ro.store(at(p), r[p]);
   }
   if (a.x) {
+    praw bn[NV];
+    if (EARLY && a.b_pre)
+#pragma unroll
+      for (int p = 0; p < NV; ++p) bn[p] = b_pre.load_raw(at(p));
     float mean, rstd;
     row_stats<W, NV, FULL>(r, a.pre, lane, H, a.eps, slots + 2 * W, wave, mean, rstd);
     const Row<BF16, FULL> xr(a.x, row * a.ld_x, H);
 #pragma unroll
     for (int p = 0; p < NV; ++p) {
-      const int i = 4 * (p * 64 * W + lane);
-      f32x4 n = (r[p] - mean) * rstd * load_params<FULL>(a.w_pre, a.p_bf16, 0, i, H);
-      if (a.b_pre) n += load_params<FULL>(a.b_pre, a.p_bf16, 0, i, H);
-      xr.store(i, n);
+      f32x4 n = (r[p] - mean) * rstd * (EARLY ? value(wn[p], p) : w_pre.load(at(p)));
+      if (a.b_pre) n += EARLY ? value(bn[p], p) : b_pre.load(at(p));
+      xr.store(at(p), n);
     }
   }
 }
 
-template <class YT, class RT, bool HAS_Y>
-hipError_t launch_shape(const EdgeFwdArgs& a, bool full, hipStream_t s) {
+template <class YT, class RT, class PT, bool HAS_Y>
+hipError_t launch_form(const EdgeFwdArgs& a, bool full, hipStream_t s) {
   const dim3 rows((unsigned)a.M), rows4((unsigned)((a.M + 3) / 4));
   if (!full) {
-    if (a.H <= 1024) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 1, 4, false>, rows4, dim3(256), s, a);
-    if (a.H <= 4096) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 4, 4, false>, rows, dim3(256), s, a);
-    if (a.H <= TPMLP_EDGE_MAX_H) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 16, 8, false>, rows, dim3(1024), s, a);
+    if (a.H <= 1024) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 1, 4, false>, rows4, dim3(256), s, a);
+    if (a.H <= 4096) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 4, 4, false>, rows, dim3(256), s, a);
+    if (a.H <= TPMLP_EDGE_MAX_H) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 16, 8, false>, rows, dim3(1024), s, a);
     return hipErrorInvalidValue;
   }
-  if (a.H <= 512) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 1, 2, true>, rows4, dim3(256), s, a);
-  if (a.H <= 1024) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 1, 4, true>, rows4, dim3(256), s, a);
-  if (a.H <= 2048) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 4, 2, true>, rows, dim3(256), s, a);
-  if (a.H <= 4096) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 4, 4, true>, rows, dim3(256), s, a);
-  if (a.H <= 8192) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 8, 4, true>, rows, dim3(512), s, a);
-  if (a.H <= 12288) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 16, 3, true>, rows, dim3(1024), s, a);
-  if (a.H <= 20480) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 16, 5, true>, rows, dim3(1024), s, a);
-  if (a.H <= TPMLP_EDGE_MAX_H) return launch_kernel(edge_fwd_kernel<YT, RT, HAS_Y, 16, 8, true>, rows, dim3(1024), s, a);
+  if (a.H <= 512) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 1, 2, true>, rows4, dim3(256), s, a);
+  if (a.H <= 1024) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 1, 4, true>, rows4, dim3(256), s, a);
+  if (a.H <= 2048) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 4, 2, true>, rows, dim3(256), s, a);
+  if (a.H <= 4096) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 4, 4, true>, rows, dim3(256), s, a);
+  if (a.H <= 8192) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 8, 4, true>, rows, dim3(512), s, a);
+  if (a.H <= 12288) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 16, 3, true>, rows, dim3(1024), s, a);
+  if (a.H <= 20480) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 16, 5, true>, rows, dim3(1024), s, a);
+  if (a.H <= TPMLP_EDGE_MAX_H) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 16, 8, true>, rows, dim3(1024), s, a);
   return hipErrorInvalidValue;
+}
+
+template <class YT, class RT, bool HAS_Y>
+hipError_t launch_shape(const EdgeFwdArgs& a, bool full, hipStream_t s) {
+  return a.p_bf16 ? launch_form<YT, RT, BF16, HAS_Y>(a, full, s) : launch_form<YT, RT, F32, HAS_Y>(a, full, s);
 }
 
 }  // namespace

@@ -30,11 +30,13 @@ namespace edge {
 // Rows whose elements a workgroup holds W waves wide and NV chunks deep.  Up to two
 // chunks a lane, the two parameter products stay in registers over all rows; with
 // four or more (wider rows than 16 waves hold in two) they are read again for every
-// row, and T1, which one lane alone adds to, lives in LDS.
-template <class YT, class RT, bool HAS_Y, bool LAYER, int W, int NV, bool FULL>
+// row, and T1, which one lane alone adds to, lives in LDS.  Where the registers allow
+// it without losing a resident workgroup, a row's loads are issued before the row
+// before it is worked on, so that they are in flight during its sums and barriers.
+template <class YT, class RT, bool HAS_Y, bool LAYER, class DXT, int W, int NV, bool FULL>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) edge_bwd_kernel(EdgeBwdArgs a) {
   constexpr int NACC = LAYER ? EDGE_ACC_LAYER : EDGE_ACC_RMS;
-  constexpr bool KEEP = NV <= 2, T_LDS = W == 16 && NV >= 4;
+  constexpr bool KEEP = NV <= 2, AHEAD = NV == 1 || (NV == 2 && !LAYER), T_LDS = W == 16 && NV >= 4;
   constexpr int SLOT = 8 * W;  // floats of one row's sums; two sets, used in turn
   __shared__ float slots[2 * SLOT];
   __shared__ f32x4 t_lds[T_LDS ? NV * 64 * W : 1];
@@ -69,43 +71,87 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) edge_bwd_kernel(EdgeBwd
     if (T_LDS) t_lds[p * 64 * W + lane] = zero;
     else T1[p] = zero;
     if (LAYER) S0[p] = T0[p] = zero;
-    if (KEEP) {
-      wu[p] = has_dx ? pre_scale(p) : zero;
-      if (HAS_Y) wv[p] = post_scale(p);
+  }
+  if constexpr (KEEP) {
+    Params<NV, FULL> w1, w2, w3;
+    if (has_dx) w1.fetch(a.w_pre, a.p_bf16, 0, at, H);
+    if (post) w2.fetch(a.w_post, a.p_bf16, 0, at, H);
+    if (HAS_Y && a.gate) w3.fetch(a.gate, a.p_bf16, gate_at, at, H);
+#pragma unroll
+    for (int p = 0; p < NV; ++p) {
+      wu[p] = has_dx ? w1.get(p, a.p_bf16, at(p), H) : zero;
+      wv[p] = f32x4{1.0f, 1.0f, 1.0f, 1.0f};
+      if (post) wv[p] = w2.get(p, a.p_bf16, at(p), H);
+      if (HAS_Y && a.gate) wv[p] *= w3.get(p, a.p_bf16, at(p), H);
     }
   }
 
-  int turn = 0;
-  for (int64_t row = row0 + (W == 1 ? wave : 0); row < row1; row += W == 1 ? 4 : 1, turn ^= 1) {
-    float* slot = slots + turn * SLOT;
-    f32x4 d[NV], y[NV];
+  // What a row needs, as loaded.
+  typedef typename Row<RT, FULL>::raw rraw;
+  struct In {
+    rraw d[NV], r[NV];
+    typename Row<YT, FULL>::raw y[NV];
+    typename Row<DXT, FULL>::raw u[NV];
+  };
+  auto fetch = [&](int64_t row, In& in) {
     if (a.dr_out) {
       const Row<RT, FULL> m(a.dr_out, row * a.ld_dr_out, H);
 #pragma unroll
-      for (int p = 0; p < NV; ++p) d[p] = m.load(at(p));
-    } else {
+      for (int p = 0; p < NV; ++p) in.d[p] = m.load_raw(at(p));
+    }
+    if (has_dx) {
+      const Row<RT, FULL> m(a.r, row * a.ld_r, H);
 #pragma unroll
-      for (int p = 0; p < NV; ++p) d[p] = zero;
+      for (int p = 0; p < NV; ++p) in.r[p] = m.load_raw(at(p));
+      const Row<DXT, FULL> mu(a.dx, row * a.ld_dx, H);
+#pragma unroll
+      for (int p = 0; p < NV; ++p) in.u[p] = mu.load_raw(at(p));
     }
     if (HAS_Y) {
       const Row<YT, FULL> m(a.y, row * a.ld_y, H);
 #pragma unroll
-      for (int p = 0; p < NV; ++p) y[p] = m.load(at(p));
+      for (int p = 0; p < NV; ++p) in.y[p] = m.load_raw(at(p));
     }
-    if (has_dx) {
-      f32x4 r[NV], u[NV];
-      const Row<RT, FULL> m(a.r, row * a.ld_r, H);
+  };
+
+  constexpr int STEP = W == 1 ? 4 : 1;
+  In in;
+  int64_t row = row0 + (W == 1 ? wave : 0);
+  if (AHEAD && row < row1) fetch(row, in);
+  for (int turn = 0; row < row1; row += STEP, turn ^= 1) {
+    float* slot = slots + turn * SLOT;
+    f32x4 d[NV], y[NV], r[NV], u[NV];
+    auto load_y = [&] {
+      const Row<YT, FULL> m(a.y, row * a.ld_y, H);
 #pragma unroll
-      for (int p = 0; p < NV; ++p) r[p] = m.load(at(p));
-      if (a.dx_bf16) {
-        const Row<BF16, FULL> mu(a.dx, row * a.ld_dx, H);
+      for (int p = 0; p < NV; ++p) y[p] = m.load(at(p));
+    };
+    if (AHEAD) {
 #pragma unroll
-        for (int p = 0; p < NV; ++p) u[p] = mu.load(at(p));
-      } else {
-        const Row<F32, FULL> mu(a.dx, row * a.ld_dx, H);
+      for (int p = 0; p < NV; ++p) {
+        d[p] = a.dr_out ? Row<RT, FULL>::widen_raw(in.d[p], at(p), H) : zero;
+        if (HAS_Y) y[p] = Row<YT, FULL>::widen_raw(in.y[p], at(p), H);
+        if (has_dx) {
+          r[p] = Row<RT, FULL>::widen_raw(in.r[p], at(p), H);
+          u[p] = Row<DXT, FULL>::widen_raw(in.u[p], at(p), H);
+        }
+      }
+      if (row + STEP < row1) fetch(row + STEP, in);
+    } else {
+      if (has_dx) {
+        const Row<RT, FULL> m(a.r, row * a.ld_r, H);
+        const Row<DXT, FULL> mu(a.dx, row * a.ld_dx, H);
+#pragma unroll
+        for (int p = 0; p < NV; ++p) r[p] = m.load(at(p));
 #pragma unroll
         for (int p = 0; p < NV; ++p) u[p] = mu.load(at(p));
       }
+      const Row<RT, FULL> m(a.dr_out, row * a.ld_dr_out, H);
+#pragma unroll
+      for (int p = 0; p < NV; ++p) d[p] = a.dr_out ? m.load(at(p)) : zero;
+      if (HAS_Y && (KEEP || !has_dx)) load_y();
+    }
+    if (has_dx) {
       if (pre_layer) {
         float t[1] = {0.0f};
 #pragma unroll
@@ -130,6 +176,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) edge_bwd_kernel(EdgeBwd
           if (LAYER) q[LAYER ? 2 : 0] += t;
         }
       }
+      if (HAS_Y && !KEEP) load_y();  // no sooner: beside r' and dx there is no room for it
       row_sum<W>(q, slot + W, wave);
       const float rstd = 1.0f / sqrtf(__builtin_fmaf(q[0], inv, a.eps));
       const float dot = q[1] * rstd * inv, mu = pre_layer ? q[LAYER ? 2 : 0] * inv : 0.0f;
@@ -231,23 +278,29 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) edge_bwd_kernel(EdgeBwd
   }
 }
 
-template <class YT, class RT, bool HAS_Y, bool LAYER>
-hipError_t launch_shape(const EdgeBwdArgs& a, int64_t blocks, bool full, hipStream_t s) {
+template <class YT, class RT, bool HAS_Y, bool LAYER, class DXT>
+hipError_t launch_form(const EdgeBwdArgs& a, int64_t blocks, bool full, hipStream_t s) {
   const dim3 grid((unsigned)blocks);
   switch (edge_bwd_shape(a.H, full)) {
-    case EDGE_1x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 1, 2, true>, grid, dim3(256), s, a);
-    case EDGE_4x1: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 4, 1, true>, grid, dim3(256), s, a);
-    case EDGE_4x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 4, 2, true>, grid, dim3(256), s, a);
-    case EDGE_8x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 8, 2, true>, grid, dim3(512), s, a);
-    case EDGE_16x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 2, true>, grid, dim3(1024), s, a);
-    case EDGE_16x4: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 4, true>, grid, dim3(1024), s, a);
-    case EDGE_16x5: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 5, true>, grid, dim3(1024), s, a);
-    case EDGE_16x8: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 8, true>, grid, dim3(1024), s, a);
-    case EDGE_ANY_4x1: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 4, 1, false>, grid, dim3(256), s, a);
-    case EDGE_ANY_8x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 8, 2, false>, grid, dim3(512), s, a);
-    case EDGE_ANY_16x8: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, 16, 8, false>, grid, dim3(1024), s, a);
+    case EDGE_1x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 1, 2, true>, grid, dim3(256), s, a);
+    case EDGE_4x1: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 4, 1, true>, grid, dim3(256), s, a);
+    case EDGE_4x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 4, 2, true>, grid, dim3(256), s, a);
+    case EDGE_8x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 8, 2, true>, grid, dim3(512), s, a);
+    case EDGE_16x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 16, 2, true>, grid, dim3(1024), s, a);
+    case EDGE_16x4: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 16, 4, true>, grid, dim3(1024), s, a);
+    case EDGE_16x5: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 16, 5, true>, grid, dim3(1024), s, a);
+    case EDGE_16x8: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 16, 8, true>, grid, dim3(1024), s, a);
+    case EDGE_ANY_4x1: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 4, 1, false>, grid, dim3(256), s, a);
+    case EDGE_ANY_8x2: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 8, 2, false>, grid, dim3(512), s, a);
+    case EDGE_ANY_16x8: return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, 16, 8, false>, grid, dim3(1024), s, a);
   }
   return hipErrorInvalidValue;
+}
+
+template <class YT, class RT, bool HAS_Y, bool LAYER>
+hipError_t launch_shape(const EdgeBwdArgs& a, int64_t blocks, bool full, hipStream_t s) {
+  return a.dx_bf16 ? launch_form<YT, RT, HAS_Y, LAYER, BF16>(a, blocks, full, s)
+                   : launch_form<YT, RT, HAS_Y, LAYER, F32>(a, blocks, full, s);
 }
 
 template <bool LAYER>
