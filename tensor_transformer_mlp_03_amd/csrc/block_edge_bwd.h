@@ -46,9 +46,12 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) edge_bwd_kernel(EdgeBwd
   const float inv = 1.0f / (float)H;
   const int64_t group = blockIdx.x / a.chunks;
   const int chunk = (int)(blockIdx.x % a.chunks);
-  const int64_t g_end = min((group + 1) * a.gate_rows, a.M);
-  const int64_t row0 = min(group * a.gate_rows + chunk * a.chunk_rows, g_end);
-  const int64_t row1 = min(row0 + a.chunk_rows, g_end);
+  // The group's workgroups take its rows in turn, so that those at work at one time
+  // read neighbouring rows: with a run of rows each, their addresses are a multiple of
+  // the run apart and fall on few memory channels.
+  constexpr int LINES = W == 1 ? 4 : 1;  // rows at once
+  const int64_t row1 = min((group + 1) * a.gate_rows, a.M), STEP = (int64_t)a.chunks * LINES;
+  const int64_t row0 = group * a.gate_rows + (int64_t)chunk * LINES;
   const int64_t gate_at = group * a.ld_gate;
   const bool has_dx = a.dx != nullptr, post = HAS_Y && a.post != TPMLP_NORM_NONE;
   const bool pre_layer = LAYER && a.pre == TPMLP_NORM_LAYER, post_layer = LAYER && a.post == TPMLP_NORM_LAYER;
@@ -114,7 +117,6 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W) edge_bwd_kernel(EdgeBwd
     }
   };
 
-  constexpr int STEP = W == 1 ? 4 : 1;
   In in;
   int64_t row = row0 + (W == 1 ? wave : 0);
   if (AHEAD && row < row1) fetch(row, in);
