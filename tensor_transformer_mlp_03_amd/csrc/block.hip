@@ -135,6 +135,15 @@ bool all_quads(int64_t H, const Mat (&outs)[NO], const Mat (&ins)[NI]) {
   return H % 4 == 0 && std::all_of(outs, outs + NO, quads) && std::all_of(ins, ins + NI, quads);
 }
 
+// Whether a launch over these matrices moves more than the caches hold.
+template <size_t NO, size_t NI>
+bool past_caches(const Mat (&outs)[NO], const Mat (&ins)[NI]) {
+  int64_t bytes = 0;
+  for (const Mat& m : outs) bytes += empty(m) ? 0 : m.rows * m.cols * m.elem;
+  for (const Mat& m : ins) bytes += empty(m) ? 0 : m.rows * m.cols * m.elem;
+  return bytes > BLOCK_NT_BYTES;
+}
+
 // The edge's parameters as inputs of the overlap check.
 #define EDGE_PARAMS(e)                                                                                  \
   {(e).w_post, 1, (e).H, (e).H, size_of((e).param_type), "w_post"},                                     \
@@ -184,6 +193,7 @@ tpmlp_status edge_fwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
   a.p_bf16 = e->param_type == TPMLP_BF16;
   a.alpha = e->alpha;
   a.eps = e->eps;
+  a.nt = past_caches(outs, ins);
   return launched(launch_edge_fwd(a, y ? e->y_type : -1, e->r_type, all_quads(H, outs, ins), stream_of(stream)), "tpmlp_edge_fwd launch");
 }
 
@@ -271,6 +281,7 @@ tpmlp_status edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
     a.dx_bf16 = dx_type == TPMLP_BF16;
     a.alpha = e->alpha;
     a.eps = e->eps;
+    a.nt = past_caches(outs, ins);
     TRY(launched(launch_edge_bwd(a, plan, y ? e->y_type : -1, e->r_type, all_quads(H, outs, ins), s), "tpmlp_edge_bwd launch"));
   }
   if (!any) return TPMLP_OK;

@@ -74,45 +74,52 @@ __device__ __forceinline__ void store4(typename T::elem* row, int i, int n, f32x
 // of 4, every row at a multiple of four elements) go through a buffer descriptor
 // of the row's length: a chunk past the end reads zeros and writes nothing, without
 // a branch or an address select, and the address is one 32-bit offset a lane.  The
-// row's pointer has to be uniform over the wave.  Other rows take load4 and store4.
-template <class T, bool FULL>
+// row's pointer has to be uniform over the wave.  Other rows take from4 and store4.
+// A row of length 0 reads zeros and touches no memory.  NT marks FULL rows' accesses
+// as non-temporal, for launches that move more than the caches hold (BLOCK_NT_BYTES).
+template <class T, bool FULL, bool NT = false>
 struct Row;
 
-template <class T>
-struct Row<T, false> {
+template <class T, bool NT>
+struct Row<T, false, NT> {
   typedef typename T::elem elem;
+  typedef typename T::vec raw;  // four elements as loaded
   elem* p;
   int n;
   __device__ __forceinline__ Row(const void* base, int64_t at, int n_)
       : p(const_cast<elem*>(static_cast<const elem*>(base)) + at), n(n_) {}
+  __device__ __forceinline__ raw load_raw(int i) const {
+    if (n == 0) return raw{0, 0, 0, 0};  // uniform
+    return *reinterpret_cast<const raw*>(p + min(i, n - 4));
+  }
+  // The conversion apart from the load, for a row that is fetched before it is used.
+  static __device__ __forceinline__ f32x4 widen_raw(raw v, int i, int n) { return from4(widen(v), i, n); }
   __device__ __forceinline__ f32x4 load(int i) const { return widen_raw(load_raw(i), i, n); }
   __device__ __forceinline__ void store(int i, f32x4 v) const { store4<T>(p, i, n, v); }
-  // The load and the conversion apart, for a row that is fetched before it is used.
-  typedef typename T::vec raw;
-  __device__ __forceinline__ raw load_raw(int i) const { return *reinterpret_cast<const raw*>(p + min(i, n - 4)); }
-  static __device__ __forceinline__ f32x4 widen_raw(raw v, int i, int n) { return from4(widen(v), i, n); }
 };
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 #if defined(__HIP_DEVICE_COMPILE__)
-template <class T>
-struct Row<T, true> {
+template <class T, bool NT>
+struct Row<T, true, NT> {
+  static constexpr bool WIDE = sizeof(typename T::elem) == 4;
+  static constexpr int AUX = NT ? 2 : 0;
+  typedef uint32_t raw __attribute__((ext_vector_type(sizeof(typename T::elem))));
   __amdgpu_buffer_rsrc_t rs;
   __device__ __forceinline__ Row(const void* base, int64_t at, int n)
       : rs(__builtin_amdgcn_make_buffer_rsrc(
             const_cast<typename T::elem*>(static_cast<const typename T::elem*>(base)) + at, (short)0,
             (int)(n * sizeof(typename T::elem)), 0x00020000)) {}
-  typedef uint32_t raw __attribute__((ext_vector_type(sizeof(typename T::elem))));  // four elements
   __device__ __forceinline__ raw load_raw(int i) const {
-    if constexpr (sizeof(typename T::elem) == 4)
-      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b128(rs, i * 4, 0, 0));
+    if constexpr (WIDE)
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b128(rs, i * 4, 0, AUX));
     else
-      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(rs, i * 2, 0, 0));
+      return __builtin_bit_cast(raw, __builtin_amdgcn_raw_buffer_load_b64(rs, i * 2, 0, AUX));
   }
   static __device__ __forceinline__ f32x4 widen_raw(raw v, int, int) {
-    if constexpr (sizeof(typename T::elem) == 4)
+    if constexpr (WIDE)
       return __builtin_bit_cast(f32x4, v);
     else
       return f32x4{__builtin_bit_cast(float, v[0] << 16), __builtin_bit_cast(float, v[0] & 0xFFFF0000u),
@@ -120,19 +127,19 @@ struct Row<T, true> {
   }
   __device__ __forceinline__ f32x4 load(int i) const { return widen_raw(load_raw(i), i, 0); }
   __device__ __forceinline__ void store(int i, f32x4 v) const {
-    if constexpr (sizeof(typename T::elem) == 4) {
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, i * 4, 0, 0);
+    if constexpr (WIDE) {
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, i * 4, 0, AUX);
     } else {
       const u32x2 o = {(uint32_t)f32_to_bf16(v[0]) | (uint32_t)f32_to_bf16(v[1]) << 16,
                        (uint32_t)f32_to_bf16(v[2]) | (uint32_t)f32_to_bf16(v[3]) << 16};
-      __builtin_amdgcn_raw_buffer_store_b64(o, rs, i * 2, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b64(o, rs, i * 2, 0, AUX);
     }
   }
 };
 #else
-template <class T>
-struct Row<T, true> : Row<T, false> {
-  using Row<T, false>::Row;
+template <class T, bool NT>
+struct Row<T, true, NT> : Row<T, false, NT> {
+  using Row<T, false, NT>::Row;
 };
 #endif
 
@@ -208,25 +215,41 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
-// Sums N values over the W waves that share a row, each lane receiving all of
-// them, in an order that depends on W alone.  `slot`: N * W floats of LDS that no
-// other sum uses before every wave has passed one more barrier.
+// Sums N values over the W waves that share a row (W 1, 4, 8 or 16), every lane
+// receiving all of them, in an order that depends on W alone.  Each wave's lanes read
+// one of the N W wave sums each, add them within groups of W lanes and hand the sums
+// to scalar registers, where they take no room of the rows'.  `slot`: N * W floats of
+// LDS that no other sum uses before every wave has passed one more barrier.
 template <int W, int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], float* slot, int wave) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  auto scalar = [](float x, int lane) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+  };
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] = wave_sum(v[j]);
-  if (W == 1) return;
-  if ((threadIdx.x & 63) == 0)
+  if (W == 1) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = scalar(v[j], 0);
+    return;
+  }
+  const int lane = threadIdx.x & 63;
+  if (lane == 0)
 #pragma unroll
     for (int j = 0; j < N; ++j) slot[j * W + wave] = v[j];
   __syncthreads();
+  constexpr int PER = 64 / W;  // sums of one pass
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    float t = 0.0f;
+  for (int j0 = 0; j0 < N; j0 += PER) {
+    float x = slot[min(j0 * W + lane, N * W - 1)];
+    x = add_dpp<0xB1>(x);
+    x = add_dpp<0x4E>(x);
+    if (W >= 8) x = add_dpp<0x141>(x);
+    if (W >= 16) x = add_dpp<0x140>(x);
 #pragma unroll
-    for (int w = 0; w < W; ++w) t += slot[j * W + w];
-    v[j] = t;
+    for (int j = j0; j < N && j < j0 + PER; ++j) v[j] = scalar(x, (j - j0) * W);
   }
+#endif
 }
 
 }  // namespace tpmlp

@@ -57,7 +57,7 @@ __device__ __forceinline__ void row_stats(const f32x4 (&v)[NV], int kind, int la
 
 // Rows up to four chunks a lane have their parameters loaded with the row, so that no
 // load waits behind a sum; wider ones would lose a resident workgroup to the registers.
-template <class YT, class RT, class PT, bool HAS_Y, int W, int NV, bool FULL>
+template <class YT, class RT, class PT, bool HAS_Y, int W, int NV, bool FULL, bool NT>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, W == 16 && NV <= 5 ? 8 : 1) edge_fwd_kernel(EdgeFwdArgs a) {
   constexpr bool EARLY = NV <= 4 && W < 16;
   __shared__ float slots[4 * W];
@@ -75,10 +75,10 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, W == 16 && NV <= 5 ? 8 
 
   f32x4 r[NV], y[NV];
   praw wp[NV], g[NV], wn[NV];
-  const Row<RT, FULL> rr(a.r, row * a.ld_r, H);
-  const Row<YT, FULL> yr(a.y, HAS_Y ? row * a.ld_y : 0, H);
-  typename Row<RT, FULL>::raw r0[NV];
-  typename Row<YT, FULL>::raw y0[NV];
+  const Row<RT, FULL, NT> rr(a.r, row * a.ld_r, H);
+  const Row<YT, FULL, NT> yr(a.y, row * a.ld_y, H);
+  typename Row<RT, FULL, NT>::raw r0[NV];
+  typename Row<YT, FULL, NT>::raw y0[NV];
   if (HAS_Y)
 #pragma unroll
     for (int p = 0; p < NV; ++p) y0[p] = yr.load_raw(at(p));
@@ -97,8 +97,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, W == 16 && NV <= 5 ? 8 
   }
 #pragma unroll
   for (int p = 0; p < NV; ++p) {
-    if (HAS_Y) y[p] = Row<YT, FULL>::widen_raw(y0[p], at(p), H);
-    r[p] = Row<RT, FULL>::widen_raw(r0[p], at(p), H);
+    if (HAS_Y) y[p] = Row<YT, FULL, NT>::widen_raw(y0[p], at(p), H);
+    r[p] = Row<RT, FULL, NT>::widen_raw(r0[p], at(p), H);
   }
   if (HAS_Y) {
     float mean = 0.0f, rstd = 1.0f;
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, W == 16 && NV <= 5 ? 8 
     for (int p = 0; p < NV; ++p) r[p] *= a.alpha;
   }
   if (a.r_out) {
-    const Row<RT, FULL> ro(a.r_out, row * a.ld_r_out, H);
+    const Row<RT, FULL, NT> ro(a.r_out, row * a.ld_r_out, H);
 #pragma unroll
     for (int p = 0; p < NV; ++p) ro.store(at(p), r[p]);
   }
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, W == 16 && NV <= 5 ? 8 
       for (int p = 0; p < NV; ++p) bn[p] = b_pre.load_raw(at(p));
     float mean, rstd;
     row_stats<W, NV, FULL>(r, a.pre, lane, H, a.eps, slots + 2 * W, wave, mean, rstd);
-    const Row<BF16, FULL> xr(a.x, row * a.ld_x, H);
+    const Row<BF16, FULL, NT> xr(a.x, row * a.ld_x, H);
 #pragma unroll
     for (int p = 0; p < NV; ++p) {
       f32x4 n = (r[p] - mean) * rstd * (EARLY ? value(wn[p], p) : w_pre.load(at(p)));
@@ -139,29 +139,33 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, W == 16 && NV <= 5 ? 8 
   }
 }
 
-template <class YT, class RT, class PT, bool HAS_Y>
+template <class YT, class RT, class PT, bool HAS_Y, bool NT>
 hipError_t launch_form(const EdgeFwdArgs& a, bool full, hipStream_t s) {
   const dim3 rows((unsigned)a.M), rows4((unsigned)((a.M + 3) / 4));
+#define EDGE_FORM(W, NV, FULL, NT_) \
+  return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, W, NV, FULL, NT_>, W == 1 ? rows4 : rows, dim3(W == 1 ? 256 : 64 * W), s, a)
+  if (a.H > TPMLP_EDGE_MAX_H) return hipErrorInvalidValue;
   if (!full) {
-    if (a.H <= 1024) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 1, 4, false>, rows4, dim3(256), s, a);
-    if (a.H <= 4096) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 4, 4, false>, rows, dim3(256), s, a);
-    if (a.H <= TPMLP_EDGE_MAX_H) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 16, 8, false>, rows, dim3(1024), s, a);
-    return hipErrorInvalidValue;
+    if (a.H <= 1024) EDGE_FORM(1, 4, false, false);
+    if (a.H <= 4096) EDGE_FORM(4, 4, false, false);
+    EDGE_FORM(16, 8, false, false);
   }
-  if (a.H <= 512) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 1, 2, true>, rows4, dim3(256), s, a);
-  if (a.H <= 1024) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 1, 4, true>, rows4, dim3(256), s, a);
-  if (a.H <= 2048) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 4, 2, true>, rows, dim3(256), s, a);
-  if (a.H <= 4096) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 4, 4, true>, rows, dim3(256), s, a);
-  if (a.H <= 8192) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 8, 4, true>, rows, dim3(512), s, a);
-  if (a.H <= 12288) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 16, 3, true>, rows, dim3(1024), s, a);
-  if (a.H <= 20480) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 16, 5, true>, rows, dim3(1024), s, a);
-  if (a.H <= TPMLP_EDGE_MAX_H) return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, 16, 8, true>, rows, dim3(1024), s, a);
-  return hipErrorInvalidValue;
+  if (a.H <= 512) EDGE_FORM(1, 2, true, NT);
+  if (a.H <= 1024) EDGE_FORM(1, 4, true, NT);
+  if (a.H <= 2048) EDGE_FORM(4, 2, true, NT);
+  if (a.H <= 4096) EDGE_FORM(4, 4, true, NT);
+  if (a.H <= 8192) EDGE_FORM(8, 4, true, NT);
+  if (a.H <= 12288) EDGE_FORM(16, 3, true, NT);
+  if (a.H <= 20480) EDGE_FORM(16, 5, true, NT);
+  EDGE_FORM(16, 8, true, NT);
+#undef EDGE_FORM
 }
 
 template <class YT, class RT, bool HAS_Y>
 hipError_t launch_shape(const EdgeFwdArgs& a, bool full, hipStream_t s) {
-  return a.p_bf16 ? launch_form<YT, RT, BF16, HAS_Y>(a, full, s) : launch_form<YT, RT, F32, HAS_Y>(a, full, s);
+  if (a.p_bf16)
+    return a.nt ? launch_form<YT, RT, BF16, HAS_Y, true>(a, full, s) : launch_form<YT, RT, BF16, HAS_Y, false>(a, full, s);
+  return a.nt ? launch_form<YT, RT, F32, HAS_Y, true>(a, full, s) : launch_form<YT, RT, F32, HAS_Y, false>(a, full, s);
 }
 
 }  // namespace
