@@ -384,9 +384,9 @@ typedef struct {
 tpmlp_status tpmlp_edge_fwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r, int64_t ld_r,
                             void* r_out, int64_t ld_r_out, tpmlp_bf16* x, int64_t ld_x, void* stream);
 
-/* Workspace bytes of tpmlp_edge_bwd (the workgroups' float32 column sums): a
- * function of M, H, gate_rows (if there is a gate) and whether a norm is a
- * LayerNorm.  0 if the description is invalid or M is 0. */
+/* Workspace bytes of tpmlp_edge_bwd (the workgroups' float32 column sums and, for
+ * H above 4096, eight floats a row): a function of M, H, gate_rows (if there is a
+ * gate) and whether a norm is a LayerNorm.  0 if the description is invalid or M is 0. */
 size_t tpmlp_edge_bwd_workspace_bytes(const tpmlp_edge* e);
 
 /* Backward.  r_out is the stream that the forward wrote (the norms' statistics are
@@ -397,7 +397,7 @@ size_t tpmlp_edge_bwd_workspace_bytes(const tpmlp_edge* e);
  * be dr_out itself), dy[M,H] in bf16 (the dZ of the MLP's backward; NULL without
  * y), and the float32 gradients dw_post, db_post, dw_pre, db_pre [H] and dgate
  * [ceil(M / gate_rows)][H], each nullable and only where its parameter exists.
- * ws is required if any of these five is. */
+ * ws is required if any of these five is, or H is above 4096. */
 tpmlp_status tpmlp_edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r_out, int64_t ld_r_out,
                             const void* dr_out, int64_t ld_dr_out, const void* dx, int dx_type, int64_t ld_dx,
                             void* dr, int64_t ld_dr, tpmlp_bf16* dy, int64_t ld_dy, float* dw_post, float* db_post,

@@ -37,11 +37,11 @@ struct EdgeBwdArgs {
   void* dr;
   uint16_t* dy;
   const void *w_post, *gate, *w_pre;
-  float* part;  // [groups * chunks][acc][H] column sums of each workgroup's rows
+  float* part;   // [groups * chunks][acc][H] column sums of each workgroup's rows, or null
+  float* terms;  // [M][8] what the second sweep of a wide row needs, or null
   int64_t ld_y, ld_r, ld_dr_out, ld_dx, ld_dr, ld_dy, ld_gate;
   int64_t M, gate_rows;
-  int64_t chunk_rows;  // rows of one workgroup, all in one gate group
-  int chunks;          // workgroups per gate group
+  int chunks;  // workgroups per gate group
   int H, post, pre, p_bf16, dx_bf16, nt;
   float alpha, eps;
 };
@@ -58,18 +58,21 @@ struct EdgeFinishArgs {
 //   S1 = sum d yh, T1 = sum dx xh; with a LayerNorm also S0 = sum d, T0 = sum dx.
 constexpr int EDGE_ACC_RMS = 2, EDGE_ACC_LAYER = 4;
 
-// The backward's row forms, waves x chunks a lane; ANY: rows that are not FULL.
+// The backward's row forms, waves x chunks a lane (WIDE: two kernels); ANY: rows that
+// are not FULL.
 enum EdgeShape : int {
-  EDGE_1x2, EDGE_4x1, EDGE_4x2, EDGE_8x2, EDGE_16x2, EDGE_16x4, EDGE_16x5, EDGE_16x8, EDGE_ANY_4x1, EDGE_ANY_8x2, EDGE_ANY_16x8
+  EDGE_1x2, EDGE_4x1, EDGE_4x2, EDGE_8x2, EDGE_16x2, EDGE_WIDE, EDGE_ANY_4x1, EDGE_ANY_8x2, EDGE_ANY_WIDE
 };
 EdgeShape edge_bwd_shape(int H, bool full);
+// Whether rows of H elements may take the WIDE form, which needs workspace.
+inline bool edge_bwd_wide(int H) { return H > 4096; }
 
 // How the backward's rows are cut: a function of the sizes alone, so the
 // workspace query and the launch agree.
 struct EdgeBwdPlan {
   int64_t groups, chunk_rows;
   int chunks, n_acc;
-  size_t ws_bytes;
+  size_t part_bytes, ws_bytes;  // the column sums; with them a wide row's terms
 };
 EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer);
 

@@ -239,12 +239,13 @@ tpmlp_status edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
     any |= m.p != nullptr;
   }
   const EdgeBwdPlan plan = plan_edge_bwd(M, (int)H, gate_rows_of(*e), has_layer(*e));
-  if (any && plan.ws_bytes) {
+  const bool use_ws = (any || edge_bwd_wide((int)H)) && plan.ws_bytes;
+  if (use_ws) {
     if (!ws) return fail(TPMLP_ERR_NULL, "ws is NULL");
     if (reinterpret_cast<uintptr_t>(ws) & 15) return fail(TPMLP_ERR_ALIGN, "ws is not 16-byte aligned");
     if (ws_bytes < plan.ws_bytes) return fail(TPMLP_ERR_WORKSPACE, "ws_bytes below tpmlp_edge_bwd_workspace_bytes");
   }
-  const int64_t ws_n = any ? (int64_t)(plan.ws_bytes / 4) : 0;
+  const int64_t ws_n = use_ws ? (int64_t)(plan.ws_bytes / 4) : 0;
   const Mat outs[] = {mdr, mdy, g[0], g[1], g[2], g[3], g[4], {ws, 1, ws_n, ws_n, 4, "ws"}};
   const Mat ins[] = {mdo, my, mr, mdx, EDGE_PARAMS(*e)};
   TRY(check_overlaps(outs, ins, 0, 0));
@@ -263,6 +264,7 @@ tpmlp_status edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
     a.gate = e->gate;
     a.w_pre = e->w_pre;
     a.part = any ? static_cast<float*>(ws) : nullptr;
+    a.terms = edge_bwd_wide((int)H) ? reinterpret_cast<float*>(static_cast<char*>(ws) + plan.part_bytes) : nullptr;
     a.ld_y = my.ld;
     a.ld_r = mr.ld;
     a.ld_dr_out = mdo.ld;
@@ -272,7 +274,6 @@ tpmlp_status edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
     a.ld_gate = ld_or(e->ld_gate, H);
     a.M = M;
     a.gate_rows = gate_rows_of(*e);
-    a.chunk_rows = plan.chunk_rows;
     a.chunks = plan.chunks;
     a.H = (int)H;
     a.post = e->post;

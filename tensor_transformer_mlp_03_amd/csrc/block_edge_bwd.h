@@ -27,6 +27,74 @@
 namespace tpmlp {
 namespace edge {
 
+// The sums of a row: c^2, t c, b^2, dr' v b, t v b, c v b, and with a LayerNorm t, v b,
+// dr' v, t v, c v, v (c, b, t and v as below).
+constexpr int SUMS_RMS = 6, SUMS_LAYER = 12;
+
+template <bool HAS_Y, bool LAYER, int N>
+__device__ __forceinline__ void add_sums(float (&q)[N], float r, float u, float d, float y, float w, float v, float mean_r,
+                                         float mean_y, bool in) {
+  const float c = LAYER ? (in ? r - mean_r : 0.0f) : r, t = u * w;
+  q[0] = __builtin_fmaf(c, c, q[0]);
+  q[1] = __builtin_fmaf(t, c, q[1]);
+  if constexpr (LAYER) q[6] += t;
+  if constexpr (HAS_Y) {
+    const float b = LAYER ? (in ? y - mean_y : 0.0f) : y, vb = v * b;
+    q[2] = __builtin_fmaf(b, b, q[2]);
+    q[3] = __builtin_fmaf(d, vb, q[3]);
+    q[4] = __builtin_fmaf(t, vb, q[4]);
+    q[5] = __builtin_fmaf(c, vb, q[5]);
+    if constexpr (LAYER) {
+      q[7] += vb;
+      q[8] = __builtin_fmaf(d, v, q[8]);
+      q[9] = __builtin_fmaf(t, v, q[9]);
+      q[10] = __builtin_fmaf(c, v, q[10]);
+      q[11] += v;
+    }
+  }
+}
+
+// What the second sweep needs of them:
+//   d = dr' + s (t - m - c k) with k = s^2 mean(t c),   dy = sy (d v - my - b ky).
+struct RowTerms {
+  float s, k, m, sy, ky, my;
+};
+
+template <bool LAYER, int N>
+__device__ __forceinline__ RowTerms row_terms(const float (&q)[N], float inv, float eps, bool has_dx, bool post,
+                                              bool pre_layer, bool post_layer) {
+  RowTerms z{0.0f, 0.0f, 0.0f, 1.0f, 0.0f, 0.0f};
+  if (has_dx) {
+    z.s = 1.0f / sqrtf(__builtin_fmaf(q[0], inv, eps));
+    z.k = q[1] * inv * z.s * z.s;
+    if constexpr (LAYER) z.m = pre_layer ? q[6] * inv : 0.0f;
+  }
+  if (post) {
+    z.sy = 1.0f / sqrtf(__builtin_fmaf(q[2], inv, eps));
+    float dvb = q[4] - z.k * q[5];
+    if constexpr (LAYER) {
+      dvb -= z.m * q[7];
+      z.my = post_layer ? __builtin_fmaf(z.s, q[9] - z.k * q[10] - z.m * q[11], q[8]) * inv : 0.0f;
+    }
+    z.ky = __builtin_fmaf(z.s, dvb, q[3]) * inv * z.sy * z.sy;
+  }
+  return z;
+}
+
+// One element of the second sweep.
+struct Out {
+  float d, dy;
+};
+template <bool LAYER>
+__device__ __forceinline__ Out row_out(const RowTerms& z, float c, float u, float d, float b, float w, float v) {
+  float g = __builtin_fmaf(-c, z.k, u * w);
+  if (LAYER) g -= z.m;
+  d = __builtin_fmaf(g, z.s, d);
+  float h = __builtin_fmaf(-b, z.ky, d * v);
+  if (LAYER) h -= z.my;
+  return Out{d, h * z.sy};
+}
+
 // Rows whose elements a workgroup holds W waves wide and NV chunks deep.
 //
 // A row is worked on in two sweeps over the registers that its loads filled.  The
@@ -40,16 +108,14 @@ namespace edge {
 // consumed, so that a row's loads are in flight during the stores and sums before it
 // without registers of their own.
 //
-// The parameter products stay in registers over all rows for up to two chunks a lane
-// and in LDS for more (loads of them between the row's would wait for those).
+// The parameter products stay in registers over all rows.  Rows wider than 16 waves
+// hold so take the two kernels below.
 template <class YT, class RT, bool HAS_Y, bool LAYER, class DXT, int W, int NV, bool FULL, bool NT>
 __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, FULL && NV <= 2 ? 4 : 1) edge_bwd_kernel(EdgeBwdArgs a) {
   constexpr int NACC = LAYER ? EDGE_ACC_LAYER : EDGE_ACC_RMS;
-  constexpr bool KEEP = NV <= 2, W_LDS = !KEEP && NV <= 4;
-  constexpr int NSUM = LAYER ? 12 : 6;
+  constexpr int NSUM = LAYER ? SUMS_LAYER : SUMS_RMS;
   constexpr int SLOT = (NSUM + (LAYER ? 2 : 0)) * W;  // floats of one row's sums; two sets, used in turn
   __shared__ float slots[2 * SLOT];
-  __shared__ f32x4 v_lds[KEEP ? 1 : NV * 64 * W], w_lds[W_LDS ? NV * 64 * W : 1];
   const int lane = W == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int H = a.H;
@@ -100,36 +166,19 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, FULL && NV <= 2 ? 4 : 1
 
   // w_pre, and v = g w_post
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f}, one = {1.0f, 1.0f, 1.0f, 1.0f};
-  f32x4 wu[KEEP ? NV : 1], wv[KEEP ? NV : 1];
+  f32x4 wu[NV], wv[NV];
   {
-    constexpr int N = KEEP ? NV : 1;
+    Params<NV, FULL> w1, w2, w3;
+    if (has_dx) w1.fetch(a.w_pre, a.p_bf16, 0, at, H);
+    if (post) w2.fetch(a.w_post, a.p_bf16, 0, at, H);
+    if (HAS_Y && a.gate) w3.fetch(a.gate, a.p_bf16, group * a.ld_gate, at, H);
 #pragma unroll
-    for (int p0 = 0; p0 < NV; p0 += N) {
-      auto place = [&](int p) { return at(p0 + p); };
-      Params<N, FULL> w1, w2, w3;
-      if (has_dx) w1.fetch(a.w_pre, a.p_bf16, 0, place, H);
-      if (post) w2.fetch(a.w_post, a.p_bf16, 0, place, H);
-      if (HAS_Y && a.gate) w3.fetch(a.gate, a.p_bf16, group * a.ld_gate, place, H);
-#pragma unroll
-      for (int p = 0; p < N; ++p) {
-        const f32x4 w = has_dx ? w1.get(p, a.p_bf16, place(p), H) : zero;
-        f32x4 v = post ? w2.get(p, a.p_bf16, place(p), H) : one;
-        if (HAS_Y && a.gate) v *= w3.get(p, a.p_bf16, place(p), H);
-        if (KEEP) {
-          wu[p] = w;
-          wv[p] = v;
-        } else {
-          v_lds[(p0 + p) * 64 * W + lane] = v;
-          if (W_LDS) w_lds[(p0 + p) * 64 * W + lane] = w;
-        }
-      }
+    for (int p = 0; p < NV; ++p) {
+      wu[p] = has_dx ? w1.get(p, a.p_bf16, at(p), H) : zero;
+      wv[p] = post ? w2.get(p, a.p_bf16, at(p), H) : one;
+      if (HAS_Y && a.gate) wv[p] *= w3.get(p, a.p_bf16, at(p), H);
     }
   }
-  // (each lane reads back only what it wrote)
-  auto w_at = [&](int p) {
-    return KEEP ? wu[KEEP ? p : 0] : W_LDS ? w_lds[p * 64 * W + lane] : load_params<FULL>(a.w_pre, a.p_bf16, 0, at(p), H);
-  };
-  auto v_at = [&](int p) { return KEEP ? wv[KEEP ? p : 0] : v_lds[p * 64 * W + lane]; };
 
   f32x4 S1[NV], T1[NV], S0[LAYER ? NV : 1], T0[LAYER ? NV : 1];
 #pragma unroll
@@ -157,84 +206,38 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, FULL && NV <= 2 ? 4 : 1
       mean[0] = pre_layer ? mean[0] * inv : 0.0f;
       mean[1] = post_layer ? mean[1] * inv : 0.0f;
     }
-    // sums of c^2, t c, b^2, dr' v b, t v b, c v b; LayerNorm: t, v b, dr' v, t v, c v, v
     float q[NSUM] = {};
 #pragma unroll
     for (int p = 0; p < NV; ++p) {
-      const f32x4 r = r_at(p), u = u_at(p), d = d_at(p), y = y_at(p), w = w_at(p), v = v_at(p);
+      const f32x4 r = r_at(p), u = u_at(p), d = d_at(p), y = y_at(p), w = wu[p], v = wv[p];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool in = FULL ? at(p) < H : at(p) + e < H;
-        const float c = LAYER ? (in ? r[e] - mean[0] : 0.0f) : r[e], t = u[e] * w[e];
-        q[0] = __builtin_fmaf(c, c, q[0]);
-        q[1] = __builtin_fmaf(t, c, q[1]);
-        if (LAYER) q[LAYER ? 6 : 0] += t;
-        if (HAS_Y) {
-          const float b = LAYER ? (in ? y[e] - mean[1] : 0.0f) : y[e], vb = v[e] * b;
-          q[2] = __builtin_fmaf(b, b, q[2]);
-          q[3] = __builtin_fmaf(d[e], vb, q[3]);
-          q[4] = __builtin_fmaf(t, vb, q[4]);
-          q[5] = __builtin_fmaf(c, vb, q[5]);
-          if (LAYER) {
-            q[LAYER ? 7 : 0] += vb;
-            q[LAYER ? 8 : 0] = __builtin_fmaf(d[e], v[e], q[LAYER ? 8 : 0]);
-            q[LAYER ? 9 : 0] = __builtin_fmaf(t, v[e], q[LAYER ? 9 : 0]);
-            q[LAYER ? 10 : 0] = __builtin_fmaf(c, v[e], q[LAYER ? 10 : 0]);
-            q[LAYER ? 11 : 0] += v[e];
-          }
-        }
-      }
+      for (int e = 0; e < 4; ++e)
+        add_sums<HAS_Y, LAYER>(q, r[e], u[e], d[e], y[e], w[e], v[e], mean[0], mean[1], FULL ? at(p) < H : at(p) + e < H);
     }
     row_sum<W>(q, slot, wave);
-    // pre: d = dr' + s (t - m - c k) with k = s^2 mean(t c); post: dy = sy (d v - my - b ky)
-    float s = 0.0f, k = 0.0f, m = 0.0f, sy = 1.0f, ky = 0.0f, my = 0.0f;
-    if (has_dx) {
-      s = 1.0f / sqrtf(__builtin_fmaf(q[0], inv, a.eps));
-      k = q[1] * inv * s * s;
-      m = pre_layer ? q[LAYER ? 6 : 0] * inv : 0.0f;
-    }
-    if (post) {
-      sy = 1.0f / sqrtf(__builtin_fmaf(q[2], inv, a.eps));
-      float dvb = q[4] - k * q[5], dv = 0.0f;
-      if (LAYER) {
-        dvb -= m * q[LAYER ? 7 : 0];
-        dv = q[LAYER ? 9 : 0] - k * q[LAYER ? 10 : 0] - m * q[LAYER ? 11 : 0];
-        my = post_layer ? __builtin_fmaf(s, dv, q[LAYER ? 8 : 0]) * inv : 0.0f;
-      }
-      ky = __builtin_fmaf(s, dvb, q[3]) * inv * sy * sy;
-    }
+    const RowTerms z = row_terms<LAYER>(q, inv, a.eps, has_dx, post, pre_layer, post_layer);
 
     const RR dr(a.dr, row * a.ld_dr, H);
     const Row<BF16, FULL, NT> dyr(a.dy, HAS_Y ? row * a.ld_dy : 0, H);
     const In next = rows_at(row + STEP);
 #pragma unroll
     for (int p = 0; p < NV; ++p) {
-      f32x4 d = d_at(p);
-      if (has_dx) {
-        const f32x4 u = u_at(p), c = LAYER ? r_at(p) - mean[0] : r_at(p);
-        T1[p] += u * (c * s);
-        if (LAYER) T0[p] += u;
-        f32x4 g = u * w_at(p) - c * k;
-        if (LAYER) g -= m;
-        d += g * s;
-      }
-      const f32x4 y = y_at(p);
+      const f32x4 r = r_at(p), u = u_at(p), d0p = d_at(p), y = y_at(p);
       load_chunk(next, p);
-      dr.store(at(p), d * a.alpha);
-      if (HAS_Y) {
-        f32x4 g = d * v_at(p);
-        if (post) {
-          const f32x4 b = LAYER ? y - mean[1] : y;
-          S1[p] += d * (b * sy);
-          if (LAYER) S0[p] += d;
-          g -= b * ky;
-          if (LAYER) g -= my;
-          g *= sy;
-        } else {
-          S1[p] += d * y;
-        }
-        dyr.store(at(p), g);
+      f32x4 d = zero, g = zero;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float c = LAYER ? r[e] - mean[0] : r[e], b = LAYER ? y[e] - mean[1] : y[e];
+        const Out o = row_out<LAYER>(z, c, u[e], d0p[e], b, wu[p][e], wv[p][e]);
+        d[e] = o.d;
+        g[e] = o.dy;
+        T1[p][e] = __builtin_fmaf(u[e], c * z.s, T1[p][e]);
+        if (LAYER) T0[p][e] += u[e];
+        if (HAS_Y) S1[p][e] = __builtin_fmaf(o.d, b * z.sy, S1[p][e]);
+        if (HAS_Y && LAYER) S0[p][e] += o.d;
       }
+      dr.store(at(p), d * a.alpha);
+      if (HAS_Y) dyr.store(at(p), g);
     }
   }
 
@@ -271,6 +274,117 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, FULL && NV <= 2 ? 4 : 1
   }
 }
 
+// ---------------------------------------------------------------------------
+// Wide rows (H above 8192, or above 4096 where the rows are not FULL): too much for
+// the registers of one workgroup, so the two sweeps are two kernels.  The first
+// makes a row's sums and keeps the six or eight numbers that come of them; the
+// second, a thread to four columns, walks the rows of its chunk with them.  It reads
+// the inputs once more, but neither kernel waits for anything but memory.
+// ---------------------------------------------------------------------------
+constexpr int WIDE_THREADS = 1024, WIDE_COLS = 1024;  // columns of one workgroup of the second kernel
+
+template <class YT, class RT, bool HAS_Y, bool LAYER, class DXT, bool FULL>
+__global__ void __launch_bounds__(WIDE_THREADS) edge_wide_sums_kernel(EdgeBwdArgs a) {
+  constexpr int W = WIDE_THREADS / 64, NSUM = LAYER ? SUMS_LAYER : SUMS_RMS;
+  __shared__ float slots[(NSUM + 2) * W];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), H = a.H;
+  const float inv = 1.0f / (float)H;
+  const int64_t row = blockIdx.x;
+  const bool has_dx = a.dx != nullptr, has_dr = a.dr_out != nullptr, post = HAS_Y && a.post != TPMLP_NORM_NONE;
+  const bool pre_layer = LAYER && a.pre == TPMLP_NORM_LAYER, post_layer = LAYER && a.post == TPMLP_NORM_LAYER;
+  const Row<RT, FULL> r(a.r, row * a.ld_r, has_dx ? H : 0), d(a.dr_out, row * a.ld_dr_out, has_dr ? H : 0);
+  const Row<DXT, FULL> u(a.dx, row * a.ld_dx, has_dx ? H : 0);
+  const Row<YT, FULL> y(a.y, row * a.ld_y, HAS_Y ? H : 0);
+  const int64_t gate_at = a.gate ? row / a.gate_rows * a.ld_gate : 0;
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f}, one = {1.0f, 1.0f, 1.0f, 1.0f};
+  float mean[2] = {0.0f, 0.0f};
+  if (LAYER) {
+#pragma unroll 4
+    for (int i = 4 * (int)threadIdx.x; i < H; i += 4 * WIDE_THREADS) {
+      const f32x4 rv = r.load(i), yv = HAS_Y ? y.load(i) : zero;
+      mean[0] += (rv[0] + rv[1]) + (rv[2] + rv[3]);
+      mean[1] += (yv[0] + yv[1]) + (yv[2] + yv[3]);
+    }
+    row_sum<W>(mean, slots + NSUM * W, wave);
+    mean[0] = pre_layer ? mean[0] * inv : 0.0f;
+    mean[1] = post_layer ? mean[1] * inv : 0.0f;
+  }
+  float q[NSUM] = {};
+#pragma unroll 2
+  for (int i = 4 * (int)threadIdx.x; i < H; i += 4 * WIDE_THREADS) {
+    const f32x4 rv = r.load(i), uv = u.load(i), dv = d.load(i), yv = HAS_Y ? y.load(i) : zero;
+    const f32x4 w = has_dx ? load_params<FULL>(a.w_pre, a.p_bf16, 0, i, H) : zero;
+    f32x4 v = post ? load_params<FULL>(a.w_post, a.p_bf16, 0, i, H) : one;
+    if (HAS_Y && a.gate) v *= load_params<FULL>(a.gate, a.p_bf16, gate_at, i, H);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      add_sums<HAS_Y, LAYER>(q, rv[e], uv[e], dv[e], yv[e], w[e], v[e], mean[0], mean[1], FULL || i + e < H);
+  }
+  row_sum<W>(q, slots, wave);
+  if (threadIdx.x == 0) {
+    const RowTerms z = row_terms<LAYER>(q, inv, a.eps, has_dx, post, pre_layer, post_layer);
+    float* t = a.terms + 8 * row;
+    *reinterpret_cast<f32x4*>(t) = f32x4{z.s, z.k, z.m, z.sy};
+    *reinterpret_cast<f32x4*>(t + 4) = f32x4{z.ky, z.my, mean[0], mean[1]};
+  }
+}
+
+template <class YT, class RT, bool HAS_Y, bool LAYER, class DXT, bool FULL>
+__global__ void __launch_bounds__(WIDE_COLS / 4) edge_wide_kernel(EdgeBwdArgs a) {
+  constexpr int NACC = LAYER ? EDGE_ACC_LAYER : EDGE_ACC_RMS;
+  const int H = a.H, tiles = (H + WIDE_COLS - 1) / WIDE_COLS;
+  const int64_t slice = blockIdx.x / tiles, group = slice / a.chunks;
+  const int i = (int)(blockIdx.x % tiles) * WIDE_COLS + 4 * (int)threadIdx.x;
+  if (i >= H) return;
+  const int64_t row1 = min((group + 1) * a.gate_rows, a.M), row0 = group * a.gate_rows + slice % a.chunks;
+  const bool has_dx = a.dx != nullptr, has_dr = a.dr_out != nullptr, post = HAS_Y && a.post != TPMLP_NORM_NONE;
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f}, one = {1.0f, 1.0f, 1.0f, 1.0f};
+  const f32x4 w = has_dx ? load_params<FULL>(a.w_pre, a.p_bf16, 0, i, H) : zero;
+  f32x4 v = post ? load_params<FULL>(a.w_post, a.p_bf16, 0, i, H) : one;
+  if (HAS_Y && a.gate) v *= load_params<FULL>(a.gate, a.p_bf16, group * a.ld_gate, i, H);
+  f32x4 S1 = zero, T1 = zero, S0 = zero, T0 = zero;
+#pragma unroll 2
+  for (int64_t row = row0; row < row1; row += a.chunks) {
+    const float* t = a.terms + 8 * row;
+    const RowTerms z{t[0], t[1], t[2], t[3], t[4], t[5]};
+    const f32x4 r = Row<RT, FULL, true>(a.r, row * a.ld_r, has_dx ? H : 0).load(i);
+    const f32x4 u = Row<DXT, FULL, true>(a.dx, row * a.ld_dx, has_dx ? H : 0).load(i);
+    const f32x4 d0 = Row<RT, FULL, true>(a.dr_out, row * a.ld_dr_out, has_dr ? H : 0).load(i);
+    const f32x4 y = Row<YT, FULL, true>(a.y, row * a.ld_y, HAS_Y ? H : 0).load(i);
+    f32x4 d = zero, g = zero;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float c = LAYER ? r[e] - t[6] : r[e], b = LAYER ? y[e] - t[7] : y[e];
+      const Out o = row_out<LAYER>(z, c, u[e], d0[e], b, w[e], v[e]);
+      d[e] = o.d;
+      g[e] = o.dy;
+      T1[e] = __builtin_fmaf(u[e], c * z.s, T1[e]);
+      if (LAYER) T0[e] += u[e];
+      if (HAS_Y) S1[e] = __builtin_fmaf(o.d, b * z.sy, S1[e]);
+      if (HAS_Y && LAYER) S0[e] += o.d;
+    }
+    Row<RT, FULL, true>(a.dr, row * a.ld_dr, H).store(i, d * a.alpha);
+    if (HAS_Y) Row<BF16, FULL, true>(a.dy, row * a.ld_dy, H).store(i, g);
+  }
+  if (!a.part) return;
+  const int64_t part = slice * NACC * H;
+  Row<F32, FULL>(a.part, part, H).store(i, S1);
+  Row<F32, FULL>(a.part, part + H, H).store(i, T1);
+  if (LAYER) {
+    Row<F32, FULL>(a.part, part + 2 * (int64_t)H, H).store(i, S0);
+    Row<F32, FULL>(a.part, part + 3 * (int64_t)H, H).store(i, T0);
+  }
+}
+
+template <class YT, class RT, bool HAS_Y, bool LAYER, class DXT, bool FULL>
+hipError_t launch_wide(const EdgeBwdArgs& a, int64_t slices, hipStream_t s) {
+  const int64_t blocks = slices * ((a.H + WIDE_COLS - 1) / WIDE_COLS);
+  if (!a.terms || blocks > INT32_MAX) return hipErrorInvalidValue;
+  const hipError_t e = launch_kernel(edge_wide_sums_kernel<YT, RT, HAS_Y, LAYER, DXT, FULL>, dim3((unsigned)a.M), dim3(WIDE_THREADS), s, a);
+  if (e != hipSuccess) return e;
+  return launch_kernel(edge_wide_kernel<YT, RT, HAS_Y, LAYER, DXT, FULL>, dim3((unsigned)blocks), dim3(WIDE_COLS / 4), s, a);
+}
+
 template <class YT, class RT, bool HAS_Y, bool LAYER, class DXT, bool NT>
 hipError_t launch_form(const EdgeBwdArgs& a, int64_t blocks, bool full, hipStream_t s) {
   const dim3 grid((unsigned)blocks);
@@ -282,13 +396,10 @@ hipError_t launch_form(const EdgeBwdArgs& a, int64_t blocks, bool full, hipStrea
     case EDGE_4x2: EDGE_FORM(4, 2, true, NT);
     case EDGE_8x2: EDGE_FORM(8, 2, true, NT);
     case EDGE_16x2: EDGE_FORM(16, 2, true, NT);
-    // rows this wide are seldom few: one form each
-    case EDGE_16x4: EDGE_FORM(16, 4, true, true);
-    case EDGE_16x5: EDGE_FORM(16, 5, true, true);
-    case EDGE_16x8: EDGE_FORM(16, 8, true, true);
+    case EDGE_WIDE: return launch_wide<YT, RT, HAS_Y, LAYER, DXT, true>(a, blocks, s);
     case EDGE_ANY_4x1: EDGE_FORM(4, 1, false, false);
     case EDGE_ANY_8x2: EDGE_FORM(8, 2, false, false);
-    case EDGE_ANY_16x8: EDGE_FORM(16, 8, false, false);
+    case EDGE_ANY_WIDE: return launch_wide<YT, RT, HAS_Y, LAYER, DXT, false>(a, blocks, s);
   }
 #undef EDGE_FORM
   return hipErrorInvalidValue;

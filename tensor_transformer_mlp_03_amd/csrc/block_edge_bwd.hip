@@ -85,9 +85,9 @@ __global__ void __launch_bounds__(FIN_COLS * FIN_LINES) edge_finish_kernel(EdgeF
 }  // namespace
 
 EdgeShape edge_bwd_shape(int H, bool full) {
-  if (!full) return H <= 1024 ? EDGE_ANY_4x1 : H <= 4096 ? EDGE_ANY_8x2 : EDGE_ANY_16x8;
+  if (!full) return H <= 1024 ? EDGE_ANY_4x1 : H <= 4096 ? EDGE_ANY_8x2 : EDGE_ANY_WIDE;
   return H <= 512 ? EDGE_1x2 : H <= 1024 ? EDGE_4x1 : H <= 2048 ? EDGE_4x2 : H <= 4096 ? EDGE_8x2 : H <= 8192 ? EDGE_16x2
-       : H <= 16384 ? EDGE_16x4 : H <= 20480 ? EDGE_16x5 : EDGE_16x8;
+                                                                                                     : EDGE_WIDE;
 }
 
 EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer) {
@@ -97,7 +97,9 @@ EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer) {
   gate_rows = std::min(gate_rows, M);
   p.groups = (M + gate_rows - 1) / gate_rows;
   // As many workgroups as the 256 CUs hold at once (a workgroup walks several
-  // rows), so that all of them end together.
+  // rows), so that all of them end together.  A wide row's slice is that of several
+  // workgroups.  (The cut does not depend on whether the rows are FULL, so that the
+  // workspace does not.)
   const int64_t target = H <= 2048 ? 1024 : H <= 4096 ? 512 : 256;
   // Rows that a workgroup takes at least: those it holds at once, and up to four while
   // there is a workgroup for every CU, which keeps the slices below the data.
@@ -105,7 +107,9 @@ EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer) {
   const int64_t chunks = std::max<int64_t>(1, std::min(target / p.groups, (gate_rows + least - 1) / least));
   p.chunk_rows = (gate_rows + chunks - 1) / chunks;
   p.chunks = (int)((gate_rows + p.chunk_rows - 1) / p.chunk_rows);
-  p.ws_bytes = size_t(p.groups) * p.chunks * p.n_acc * H * 4;
+  p.part_bytes = size_t(p.groups) * p.chunks * p.n_acc * H * 4;
+  p.part_bytes = (p.part_bytes + 15) / 16 * 16;
+  p.ws_bytes = p.part_bytes + (edge_bwd_wide(H) ? size_t(M) * 8 * 4 : 0);  // with a wide row's terms
   return p;
 }
 
