@@ -135,18 +135,21 @@ hipError_t launch_route_combine_bwd(RouteCombineBwdArgs a, int dy_type, int z_ty
 // Gradient norm and clipping (block_clip.hip)
 // ---------------------------------------------------------------------------
 // Tensors of one launch: the table travels in the kernel's arguments, which
-// keeps a call free of host-to-device copies (and so capturable); 28 bytes a
+// keeps a call free of host-to-device copies (and so capturable); 29 bytes a
 // tensor stay below the 4 KiB that every launch path takes.
 constexpr int CLIP_TENSORS = 128;
 constexpr int64_t CLIP_CHUNK = 16384;  // elements of one unit of work
-constexpr int CLIP_BLOCKS = 2048;      // most workgroups (and partial sums) of one launch
+constexpr int CLIP_BLOCKS = 2048;        // most workgroups (and partial sums) of a summing launch
+constexpr int CLIP_SCALE_BLOCKS = 8192;  // and of a scaling one, which has no partials
+constexpr uint32_t CLIP_KEEP = 4096;     // last chunks that the first pass reads so as to stay in the cache
 
 struct ClipArgs {
   const void* in[CLIP_TENSORS];
   void* out[CLIP_TENSORS];
   int64_t size[CLIP_TENSORS];       // elements; bit 62 set: bf16
-  uint32_t first[CLIP_TENSORS + 1]; // first chunk of each tensor; [n] = all chunks
-  int n;
+  uint32_t first[CLIP_TENSORS];       // first chunk of each tensor; past the last one, `chunks`
+  uint32_t eighth[CLIP_TENSORS / 8];  // every eighth of these
+  uint32_t chunks;                    // of all tensors
   double* part;       // sumsq launches: one partial per workgroup; clip launches: n_part partials
   int n_part;
   float scale, max_norm;

@@ -453,10 +453,10 @@ tpmlp_status route_combine_bwd(const void* dY, int dy_type, int64_t ld_dy, const
 int64_t chunks_of(int64_t size) { return (size + CLIP_CHUNK - 1) / CLIP_CHUNK; }
 
 // Workgroups of the launch that covers tensors [t0, t1).
-int clip_blocks(const int64_t* sizes, int t0, int t1) {
+int clip_blocks(const int64_t* sizes, int t0, int t1, int most = CLIP_BLOCKS) {
   int64_t c = 0;
   for (int t = t0; t < t1; ++t) c += chunks_of(sizes[t]);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(c, CLIP_BLOCKS));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(c, most));
 }
 
 // Calls f(first tensor, end, workgroups) for each launch.
@@ -501,7 +501,6 @@ tpmlp_status check_grads(const void* const* grads, void* const* outs, const int6
 
 void fill_clip(ClipArgs& a, const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types, int t0,
                int t1) {
-  a.n = t1 - t0;
   uint32_t chunk = 0;
   for (int t = t0; t < t1; ++t) {
     const int i = t - t0;
@@ -511,7 +510,9 @@ void fill_clip(ClipArgs& a, const void* const* grads, void* const* outs, const i
     a.first[i] = chunk;
     chunk += (uint32_t)chunks_of(sizes[t]);
   }
-  a.first[a.n] = chunk;
+  a.chunks = chunk;
+  for (int i = t1 - t0; i < CLIP_TENSORS; ++i) a.first[i] = chunk;
+  for (int k = 0; k < CLIP_TENSORS / 8; ++k) a.eighth[k] = a.first[8 * k];
 }
 
 // The partial sums of all launches into ws; *count of them.
@@ -537,6 +538,7 @@ tpmlp_status enqueue_scale(const void* const* grads, void* const* outs, const in
     a.scale = scale;
     a.max_norm = max_norm;
     a.norm = t0 == 0 ? norm : nullptr;
+    blocks = clip_blocks(sizes, t0, t1, CLIP_SCALE_BLOCKS);
     return launched(launch_clip_scale(a, blocks, s), "gradient clipping launch");
   });
 }

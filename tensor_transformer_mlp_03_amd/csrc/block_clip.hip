@@ -26,45 +26,66 @@ __device__ __forceinline__ double block_sum(double v, double* slot) {
 }
 
 // Tensor of a chunk: the last one whose first chunk is at or before it (tensors
-// without elements have no chunk).
+// without elements have no chunk).  The table is in the kernel's arguments; two
+// looks at neighbouring entries cost two loads' latency where a binary search costs
+// seven.
 __device__ __forceinline__ int tensor_of(const ClipArgs& a, uint32_t chunk) {
-  int lo = 0, hi = a.n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.first[mid] <= chunk) lo = mid;
-    else hi = mid;
-  }
-  return lo;
+  int t = -1;
+#pragma unroll
+  for (int k = 0; k < CLIP_TENSORS / 8; ++k) t += a.eighth[k] <= chunk;
+  t *= 8;
+  int n = -1;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) n += a.first[t + k] <= chunk;
+  return t + n;
 }
 
-template <class T>
+// Batches of four vectors a thread are loaded before the first is used.
+template <class T, bool NT>
+__device__ __forceinline__ typename T::vec load_vec(const typename T::elem* p) {
+  const typename T::vec* v = reinterpret_cast<const typename T::vec*>(p);
+  return NT ? __builtin_nontemporal_load(v) : *v;
+}
+
+template <class T, bool NT>
 __device__ __forceinline__ double chunk_sumsq(const typename T::elem* g, int n) {
-  double s0 = 0.0, s1 = 0.0;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  auto add = [&](f32x4 v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = __builtin_fma((double)v[e], (double)v[e], s[e]);
+  };
   int i = 4 * (int)threadIdx.x;
-#pragma unroll 4
-  for (; i + 4 <= n; i += 1024) {
-    const f32x4 v = widen(*reinterpret_cast<const typename T::vec*>(g + i));
-    s0 = __builtin_fma((double)v[0], (double)v[0], s0);
-    s1 = __builtin_fma((double)v[1], (double)v[1], s1);
-    s0 = __builtin_fma((double)v[2], (double)v[2], s0);
-    s1 = __builtin_fma((double)v[3], (double)v[3], s1);
+  for (; i + 3 * 1024 + 4 <= n; i += 4 * 1024) {
+    typename T::vec v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = load_vec<T, NT>(g + i + k * 1024);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) add(widen(v[k]));
   }
+  for (; i + 4 <= n; i += 1024) add(widen(load_vec<T, false>(g + i)));
   for (; i < n && i >= (n & ~3); ++i) {
     const double v = widen(g[i]);
-    s0 = __builtin_fma(v, v, s0);
+    s[0] = __builtin_fma(v, v, s[0]);
   }
-  return s0 + s1;
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 __global__ void __launch_bounds__(256) clip_sumsq_kernel(ClipArgs a) {
   __shared__ double slot[4];
   double sum = 0.0;
-  for (uint32_t c = blockIdx.x; c < a.first[a.n]; c += gridDim.x) {
+  for (uint32_t c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     const int t = tensor_of(a, c);
     const int64_t at = (int64_t)(c - a.first[t]) * CLIP_CHUNK, size = a.size[t] & SIZE_MASK;
     const int n = (int)min(CLIP_CHUNK, size - at);
-    sum += (a.size[t] >> 62) ? chunk_sumsq<BF16>(static_cast<const uint16_t*>(a.in[t]) + at, n)
-                             : chunk_sumsq<F32>(static_cast<const float*>(a.in[t]) + at, n);
+    // What the second pass will still find in the Infinity Cache is read so as to stay there.
+    const bool keep = c + CLIP_KEEP >= a.chunks;
+    if (a.size[t] >> 62) {
+      const uint16_t* g = static_cast<const uint16_t*>(a.in[t]) + at;
+      sum += keep ? chunk_sumsq<BF16, false>(g, n) : chunk_sumsq<BF16, true>(g, n);
+    } else {
+      const float* g = static_cast<const float*>(a.in[t]) + at;
+      sum += keep ? chunk_sumsq<F32, false>(g, n) : chunk_sumsq<F32, true>(g, n);
+    }
   }
   sum = block_sum(sum, slot);
   if (threadIdx.x == 0) a.part[blockIdx.x] = sum;
@@ -91,8 +112,20 @@ __global__ void __launch_bounds__(256) clip_total_kernel(ClipTotalArgs a) {
 template <class T>
 __device__ __forceinline__ void chunk_scale(const typename T::elem* g, typename T::elem* o, int n, float m) {
   int i = 4 * (int)threadIdx.x;
-#pragma unroll 4
-  for (; i + 4 <= n; i += 1024) put(o + i, widen(*reinterpret_cast<const typename T::vec*>(g + i)) * m);
+  for (; i + 3 * 1024 + 4 <= n; i += 4 * 1024) {
+    typename T::vec v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = load_vec<T, true>(g + i + k * 1024);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const f32x4 x = widen(v[k]) * m;
+      typename T::vec t;
+      if constexpr (sizeof(typename T::elem) == 4) t = typename T::vec{x[0], x[1], x[2], x[3]};
+      else t = typename T::vec{f32_to_bf16(x[0]), f32_to_bf16(x[1]), f32_to_bf16(x[2]), f32_to_bf16(x[3])};
+      __builtin_nontemporal_store(t, reinterpret_cast<typename T::vec*>(o + i + k * 1024));
+    }
+  }
+  for (; i + 4 <= n; i += 1024) put(o + i, widen(load_vec<T, false>(g + i)) * m);
   for (; i < n && i >= (n & ~3); ++i) put1(o + i, widen(g[i]) * m);
 }
 
@@ -105,7 +138,9 @@ __global__ void __launch_bounds__(256) clip_scale_kernel(ClipArgs a) {
   const bool clip = norm > a.max_norm && norm <= 3.402823466e38f;
   const float m = clip ? (float)((double)a.scale * ((double)a.max_norm / (sqrt(total) * fabs((double)a.scale)))) : a.scale;
   if (blockIdx.x == 0 && threadIdx.x == 0 && a.norm) *a.norm = norm;
-  for (uint32_t c = blockIdx.x; c < a.first[a.n]; c += gridDim.x) {
+  const uint32_t all = a.chunks;
+  for (uint32_t k = blockIdx.x; k < all; k += gridDim.x) {
+    const uint32_t c = all - 1 - k;  // last chunks first: those are still in the Infinity Cache
     const int t = tensor_of(a, c);
     if (m == 1.0f && a.in[t] == a.out[t]) continue;  // in place and nothing to change
     const int64_t at = (int64_t)(c - a.first[t]) * CLIP_CHUNK, size = a.size[t] & SIZE_MASK;
