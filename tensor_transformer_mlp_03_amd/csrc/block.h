@@ -105,9 +105,11 @@ struct RouteDispatchArgs {
   const int32_t *row_of, *src_of;
   int64_t T, rows, ld_x, ld_xs;
   int K, H;
-  int token_blocks, segments;
+  int token_blocks, pad_rows;
 };
-hipError_t launch_route_dispatch(RouteDispatchArgs a, hipStream_t s);
+// full: H is a multiple of eight and every row starts at a multiple of eight elements
+// (dispatch), of four both (combine and its gradient); nt: non-temporal.
+hipError_t launch_route_dispatch(RouteDispatchArgs a, bool full, bool nt, hipStream_t s);
 
 struct RouteCombineArgs {
   const void* zs;
@@ -115,9 +117,9 @@ struct RouteCombineArgs {
   const float* w;  // nullable: 1
   const int32_t* row_of;
   int64_t T, rows, ld_zs, ld_y;
-  int K, H, segments;
+  int K, H;
 };
-hipError_t launch_route_combine(RouteCombineArgs a, int z_type, int y_type, hipStream_t s);
+hipError_t launch_route_combine(const RouteCombineArgs& a, int z_type, int y_type, bool full, bool nt, hipStream_t s);
 
 struct RouteCombineBwdArgs {
   const void *dy, *zs;  // zs nullable with dw
@@ -127,9 +129,9 @@ struct RouteCombineBwdArgs {
   const int32_t *row_of, *src_of;
   int64_t T, rows, ld_dy, ld_zs, ld_dzs;
   int K, H;
-  int token_blocks;
+  int token_blocks, pad_rows;
 };
-hipError_t launch_route_combine_bwd(RouteCombineBwdArgs a, int dy_type, int z_type, hipStream_t s);
+hipError_t launch_route_combine_bwd(RouteCombineBwdArgs a, int dy_type, int z_type, bool full, bool nt, hipStream_t s);
 
 // ---------------------------------------------------------------------------
 // Gradient norm and clipping (block_clip.hip)

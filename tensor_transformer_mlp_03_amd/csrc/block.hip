@@ -126,10 +126,11 @@ tpmlp_status check_edge(const tpmlp_edge* e, bool has_y) {
   return TPMLP_OK;
 }
 
-// Whether every row of the matrix starts at a multiple of four elements.
-bool quads(const Mat& m) {
-  return empty(m) || (reinterpret_cast<uintptr_t>(m.p) % (4 * m.elem) == 0 && (m.rows < 2 || m.ld % 4 == 0));
+// Whether every row of the matrix starts at a multiple of `n` elements.
+bool starts_at(const Mat& m, int n) {
+  return empty(m) || (reinterpret_cast<uintptr_t>(m.p) % (n * m.elem) == 0 && (m.rows < 2 || m.ld % n == 0));
 }
+bool quads(const Mat& m) { return starts_at(m, 4); }
 template <size_t NO, size_t NI>
 bool all_quads(int64_t H, const Mat (&outs)[NO], const Mat (&ins)[NI]) {
   return H % 4 == 0 && std::all_of(outs, outs + NO, quads) && std::all_of(ins, ins + NI, quads);
@@ -379,7 +380,8 @@ tpmlp_status route_dispatch(const tpmlp_bf16* X, int64_t ld_x, const int32_t* ro
   a.ld_xs = outs[0].ld;
   a.K = K;
   a.H = (int)H;
-  return launched(launch_route_dispatch(a, stream_of(stream)), "tpmlp_route_dispatch launch");
+  return launched(launch_route_dispatch(a, H % 8 == 0 && starts_at(outs[0], 8) && starts_at(ins[0], 8),
+                                        past_caches(outs, ins), stream_of(stream)), "tpmlp_route_dispatch launch");
 }
 
 tpmlp_status route_combine(const void* Zs, int z_type, int64_t ld_zs, const int32_t* row_of, const float* w, int64_t T,
@@ -406,7 +408,8 @@ tpmlp_status route_combine(const void* Zs, int z_type, int64_t ld_zs, const int3
   a.ld_y = outs[0].ld;
   a.K = K;
   a.H = (int)H;
-  return launched(launch_route_combine(a, z_type, y_type, stream_of(stream)), "tpmlp_route_combine launch");
+  return launched(launch_route_combine(a, z_type, y_type, H % 4 == 0 && quads(outs[0]) && quads(ins[0]),
+                                       past_caches(outs, ins), stream_of(stream)), "tpmlp_route_combine launch");
 }
 
 tpmlp_status route_combine_bwd(const void* dY, int dy_type, int64_t ld_dy, const void* Zs, int z_type, int64_t ld_zs,
@@ -444,7 +447,8 @@ tpmlp_status route_combine_bwd(const void* dY, int dy_type, int64_t ld_dy, const
   a.ld_dzs = outs[0].ld;
   a.K = K;
   a.H = (int)H;
-  return launched(launch_route_combine_bwd(a, dy_type, z_type, stream_of(stream)), "tpmlp_route_combine_bwd launch");
+  return launched(launch_route_combine_bwd(a, dy_type, z_type, H % 4 == 0 && quads(outs[0]) && quads(ins[0]) && quads(ins[1]),
+                                           past_caches(outs, ins), stream_of(stream)), "tpmlp_route_combine_bwd launch");
 }
 
 // ---------------------------------------------------------------------------

@@ -68,12 +68,13 @@ __device__ __forceinline__ uint64_t same_lanes(int v, int bits) {
 // lanes before it.  With one workgroup (ONE) there is no histogram to read.
 template <bool ONE>
 __global__ void __launch_bounds__(SORT_THREADS) route_place_kernel(RouteSortArgs a) {
-  __shared__ int lds[(SORT_WAVES + 2) * TPMLP_ROUTE_MAX_EXPERTS + 1 + SORT_WAVES];
+  __shared__ int lds[(SORT_WAVES + 4) * TPMLP_ROUTE_MAX_EXPERTS + 1 + SORT_WAVES];
   const int E = a.E, tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   int* next = lds;                        // [waves][E]
   int* start = next + SORT_WAVES * E;     // [E + 1] first row of each segment
   int* total = start + E + 1;             // [E] pairs of each expert
   int* scan = total + E;                  // [waves] sums of the scan over experts
+  int* sums = scan + SORT_WAVES;          // [2][E] pairs in all and in earlier workgroups
   for (int e = tid; e < SORT_WAVES * E; e += SORT_THREADS) next[e] = 0;
   __syncthreads();
   const int64_t p0 = (int64_t)blockIdx.x * a.per_block, p1 = min(p0 + a.per_block, a.pairs);
@@ -84,19 +85,35 @@ __global__ void __launch_bounds__(SORT_THREADS) route_place_kernel(RouteSortArgs
     if (e >= 0) atomicAdd(&next[wave * E + e], 1);
   }
   __syncthreads();
-  // Pairs of expert e in all workgroups and in those before this one.  E is at
-  // most the workgroup's size, so a thread has one expert.
-  const int e = tid;
-  int all = 0, before = 0, mine = 0;
-  if (e < E) {
-    if (ONE) {
-      for (int w = 0; w < SORT_WAVES; ++w) all += next[w * E + e];
-    } else {
-      for (int b = 0; b < a.blocks; ++b) {
-        const int n = a.hist[(int64_t)b * E + e];
+  // Pairs of each expert in all workgroups and in those before this one: the threads
+  // stand E wide on a row of the histogram and as many rows deep as they go.
+  if (!ONE) {
+    for (int i = tid; i < 2 * E; i += SORT_THREADS) sums[i] = 0;
+    __syncthreads();
+    const int lines = SORT_THREADS / E;  // E is at most half the workgroup's size
+    const int he = tid % E, line = tid / E;
+    if (line < lines) {
+      int all = 0, before = 0;
+#pragma unroll 8
+      for (int b = line; b < a.blocks; b += lines) {
+        const int n = a.hist[(int64_t)b * E + he];
         all += n;
         before += b < (int)blockIdx.x ? n : 0;
       }
+      atomicAdd(&sums[he], all);
+      atomicAdd(&sums[E + he], before);
+    }
+    __syncthreads();
+  }
+  const int e = tid;  // a thread has one expert at most
+  int before = 0, mine = 0;
+  if (e < E) {
+    int all = 0;
+    if (ONE) {
+      for (int w = 0; w < SORT_WAVES; ++w) all += next[w * E + e];
+    } else {
+      all = sums[e];
+      before = sums[E + e];
     }
     mine = a.capacity ? min(all, a.capacity) : all;
   }
@@ -165,134 +182,196 @@ __global__ void __launch_bounds__(SORT_THREADS) route_place_kernel(RouteSortArgs
 // ---------------------------------------------------------------------------
 // Dispatch, combine and their gradients
 // ---------------------------------------------------------------------------
+// The rows of up to 64 choices, one a lane: row_of of the token's choices k0 onward,
+// -1 where there is none, none inside the sorted buffer, or no such choice.
+__device__ __forceinline__ int choice_rows(const int32_t* row_of, int64_t t, int K, int k0, int64_t rows, int lane) {
+  const int k = k0 + lane;
+  const int r = k < K ? row_of[t * K + k] : -1;
+  return (uint32_t)r < (uint64_t)rows ? r : -1;
+}
+__device__ __forceinline__ int lane_value(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+
+// bf16 rows that are only moved, eight elements a lane; n a multiple of eight and rows
+// at multiples of eight elements (FULL), through a descriptor as Row has it; other
+// rows with n >= 8 read and write the row's last eight elements on the ragged end,
+// which overlap the neighbour's with equal values.
+typedef uint16_t u16x8 __attribute__((ext_vector_type(8)));
+
+template <bool FULL, bool NT>
+struct Row8;
+template <bool NT>
+struct Row8<false, NT> {
+  uint16_t* p;
+  int n;
+  __device__ __forceinline__ Row8(const uint16_t* base, int64_t at, int n_) : p(const_cast<uint16_t*>(base) + at), n(n_) {}
+  __device__ __forceinline__ u16x8 load(int i) const { return *reinterpret_cast<const u16x8_u*>(p + min(i, n - 8)); }
+  __device__ __forceinline__ void store(int i, u16x8 v) const {
+    if (i < n) *reinterpret_cast<u16x8_u*>(p + min(i, n - 8)) = v;
+  }
+};
+#if defined(__HIP_DEVICE_COMPILE__)
+template <bool NT>
+struct Row8<true, NT> {
+  __amdgpu_buffer_rsrc_t rs;
+  __device__ __forceinline__ Row8(const uint16_t* base, int64_t at, int n)
+      : rs(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base) + at, (short)0, n * 2, 0x00020000)) {}
+  __device__ __forceinline__ u16x8 load(int i) const {
+    return __builtin_bit_cast(u16x8, __builtin_amdgcn_raw_buffer_load_b128(rs, i * 2, 0, NT ? 2 : 0));
+  }
+  __device__ __forceinline__ void store(int i, u16x8 v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, i * 2, 0, NT ? 2 : 0);
+  }
+};
+#else
+template <bool NT>
+struct Row8<true, NT> : Row8<false, NT> {
+  using Row8<false, NT>::Row8;
+};
+#endif
+
 constexpr int DISPATCH_CHUNKS = 4;  // 512-element chunks of a row that a wave moves
 constexpr int DISPATCH_COLS = 512 * DISPATCH_CHUNKS;
 
-// Where the eight elements at i of a row of n >= 8 are read and written: a lane on
-// the ragged end takes the row's last eight, which overlap its neighbour's with
-// equal values.
-__device__ __forceinline__ int at8(int i, int n) { return min(i, n - 8); }
-
-// Zeros columns [c0, c1) of a row.
-__device__ __forceinline__ void zero_cols(uint16_t* row, int c0, int c1, int n, int lane) {
-  for (int i = c0 + 8 * lane; i < c1; i += 512) *reinterpret_cast<u16x8_u*>(row + at8(i, n)) = u16x8_u{0, 0, 0, 0, 0, 0, 0, 0};
+// Zeros columns [c0, c1) of the padding rows among pad_rows (at most 64) from r0 on.
+template <bool FULL, bool NT>
+__device__ __forceinline__ void zero_padding(uint16_t* out, int64_t ld, const int32_t* src_of, int64_t rows, int64_t r0,
+                                             int pad_rows, int c0, int c1, int n, int lane) {
+  uint64_t pad = __ballot(lane < pad_rows && r0 + lane < rows && src_of[min(r0 + lane, rows - 1)] < 0);
+  while (pad) {
+    const int b = __ffsll((unsigned long long)pad) - 1;
+    pad &= pad - 1;
+    const Row8<FULL, NT> o(out, (r0 + b) * ld, n);
+    for (int i = c0 + 8 * lane; i < c1; i += 512) o.store(i, u16x8{0, 0, 0, 0, 0, 0, 0, 0});
+  }
 }
 
+template <bool FULL, bool NT>
 __global__ void __launch_bounds__(256) route_dispatch_kernel(RouteDispatchArgs a) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int seg = (int)blockIdx.y, c0 = seg * DISPATCH_COLS, c1 = min(c0 + DISPATCH_COLS, a.H);
-  if ((int)blockIdx.x >= a.token_blocks) {  // padding: 64 rows a wave
-    const int64_t r0 = ((int64_t)((int)blockIdx.x - a.token_blocks) * 4 + wave) * 64;
-    if (r0 >= a.rows) return;
-    uint64_t pad = __ballot(r0 + lane < a.rows && a.src_of[r0 + lane] < 0);
-    while (pad) {
-      const int b = __ffsll((unsigned long long)pad) - 1;
-      pad &= pad - 1;
-      zero_cols(a.xs + (r0 + b) * a.ld_xs, c0, c1, a.H, lane);
-    }
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int c0 = (int)blockIdx.y * DISPATCH_COLS, c1 = min(c0 + DISPATCH_COLS, a.H);
+  if ((int)blockIdx.x >= a.token_blocks) {
+    const int64_t r0 = ((int64_t)((int)blockIdx.x - a.token_blocks) * 4 + wave) * a.pad_rows;
+    if (r0 < a.rows) zero_padding<FULL, NT>(a.xs, a.ld_xs, a.src_of, a.rows, r0, a.pad_rows, c0, c1, a.H, lane);
     return;
   }
   const int64_t t = (int64_t)blockIdx.x * 4 + wave;
   if (t >= a.T) return;
-  const uint16_t* x = a.x + t * a.ld_x;
-  u16x8_u v[DISPATCH_CHUNKS];
+  const int rows = choice_rows(a.row_of, t, a.K, 0, a.rows, lane);
+  const Row8<FULL, NT> x(a.x, t * a.ld_x, a.H);
+  u16x8 v[DISPATCH_CHUNKS];
 #pragma unroll
-  for (int c = 0; c < DISPATCH_CHUNKS; ++c) v[c] = *reinterpret_cast<const u16x8_u*>(x + at8(c0 + c * 512 + 8 * lane, a.H));
+  for (int c = 0; c < DISPATCH_CHUNKS; ++c) v[c] = x.load(c0 + c * 512 + 8 * lane);
   for (int k = 0; k < a.K; ++k) {
-    const int row = a.row_of[t * a.K + k];
-    if ((uint32_t)row >= (uint64_t)a.rows) continue;  // dropped
-    uint16_t* o = a.xs + row * a.ld_xs;
+    const int row = lane_value(rows, k);
+    if (row < 0) continue;  // dropped
+    const Row8<FULL, NT> o(a.xs, row * a.ld_xs, a.H);
 #pragma unroll
-    for (int c = 0; c < DISPATCH_CHUNKS; ++c) {
-      const int i = c0 + c * 512 + 8 * lane;
-      if (i < a.H) *reinterpret_cast<u16x8_u*>(o + at8(i, a.H)) = v[c];
-    }
+    for (int c = 0; c < DISPATCH_CHUNKS; ++c) o.store(c0 + c * 512 + 8 * lane, v[c]);
   }
 }
 
-constexpr int COMBINE_CHUNKS = 4;  // 256-element chunks of a row that a wave sums
-constexpr int COMBINE_COLS = 256 * COMBINE_CHUNKS;
+// A wave sums CHUNKS 256-element chunks of a token's rows, four choices' loads in
+// flight together.  A choice that takes no part is a row of length zero with weight
+// zero: it reads no memory and adds nothing.
+constexpr int COMBINE_CHOICES = 4;
 
-template <class ZT, class YT>
+template <class ZT, class YT, int CHUNKS, bool FULL, bool NT>
 __global__ void __launch_bounds__(256) route_combine_kernel(RouteCombineArgs a) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * 4 + wave;
   if (t >= a.T) return;
-  const int c0 = (int)blockIdx.y * COMBINE_COLS;
-  f32x4 sum[COMBINE_CHUNKS];
+  auto at = [&](int c) { return ((int)blockIdx.y * CHUNKS + c) * 256 + 4 * lane; };
+  const int rows = choice_rows(a.row_of, t, a.K, 0, a.rows, lane);
+  const float ws = rows >= 0 && a.w ? a.w[t * a.K + lane] : 1.0f;
+  f32x4 sum[CHUNKS];
 #pragma unroll
-  for (int c = 0; c < COMBINE_CHUNKS; ++c) sum[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for (int k = 0; k < a.K; ++k) {
-    const int row = a.row_of[t * a.K + k];
-    if ((uint32_t)row >= (uint64_t)a.rows) continue;
-    const float w = a.w ? a.w[t * a.K + k] : 1.0f;
-    const auto* z = static_cast<const typename ZT::elem*>(a.zs) + row * a.ld_zs;
+  for (int c = 0; c < CHUNKS; ++c) sum[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for (int k0 = 0; k0 < a.K; k0 += COMBINE_CHOICES) {
+    typedef Row<ZT, FULL, NT> RZ;
+    typename RZ::raw z[COMBINE_CHOICES][CHUNKS];
+    float w[COMBINE_CHOICES];
 #pragma unroll
-    for (int c = 0; c < COMBINE_CHUNKS; ++c) {
-      const f32x4 v = load4<ZT>(z, c0 + c * 256 + 4 * lane, a.H);
+    for (int j = 0; j < COMBINE_CHOICES; ++j) {
+      const int k = min(k0 + j, 63), row = k0 + j < a.K ? lane_value(rows, k) : -1;
+      w[j] = row >= 0 ? lane_value(ws, k) : 0.0f;
+      const RZ r(a.zs, row >= 0 ? row * a.ld_zs : 0, row >= 0 ? a.H : 0);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum[c][e] = __builtin_fmaf(v[e], w, sum[c][e]);
+      for (int c = 0; c < CHUNKS; ++c) z[j][c] = r.load_raw(at(c));
     }
-  }
-  auto* y = static_cast<typename YT::elem*>(a.y) + t * a.ld_y;
 #pragma unroll
-  for (int c = 0; c < COMBINE_CHUNKS; ++c) store4<YT>(y, c0 + c * 256 + 4 * lane, a.H, sum[c]);
+    for (int j = 0; j < COMBINE_CHOICES; ++j)
+#pragma unroll
+      for (int c = 0; c < CHUNKS; ++c) {
+        const f32x4 v = RZ::widen_raw(z[j][c], at(c), a.H);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[c][e] = __builtin_fmaf(v[e], w[j], sum[c][e]);
+      }
+  }
+  const Row<YT, FULL, NT> y(a.y, t * a.ld_y, a.H);
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) y.store(at(c), sum[c]);
 }
 
-constexpr int BWD_PAIRS = 8;  // choices of one token handled together
-
-template <class DT, class ZT>
+// One workgroup a token, NP choices together; a choice that takes no part is a row
+// of length zero.
+template <class DT, class ZT, int NP, bool FULL, bool NT>
 __global__ void __launch_bounds__(256) route_combine_bwd_kernel(RouteCombineBwdArgs a) {
-  __shared__ float dots[BWD_PAIRS][4];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  if ((int)blockIdx.x >= a.token_blocks) {  // padding rows of dZs: 64 a wave
-    const int64_t r0 = ((int64_t)((int)blockIdx.x - a.token_blocks) * 4 + wave) * 64;
-    if (r0 >= a.rows) return;
-    uint64_t pad = __ballot(r0 + lane < a.rows && a.src_of[r0 + lane] < 0);
-    while (pad) {
-      const int b = __ffsll((unsigned long long)pad) - 1;
-      pad &= pad - 1;
-      zero_cols(a.dzs + (r0 + b) * a.ld_dzs, 0, a.H, a.H, lane);
-    }
+  __shared__ float dots[NP][4];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if ((int)blockIdx.x >= a.token_blocks) {
+    const int64_t r0 = ((int64_t)((int)blockIdx.x - a.token_blocks) * 4 + wave) * a.pad_rows;
+    if (r0 < a.rows) zero_padding<false, NT>(a.dzs, a.ld_dzs, a.src_of, a.rows, r0, a.pad_rows, 0, a.H, a.H, lane);
     return;
   }
   const int64_t t = blockIdx.x;
-  const auto* dy = static_cast<const typename DT::elem*>(a.dy) + t * a.ld_dy;
-  for (int k0 = 0; k0 < a.K; k0 += BWD_PAIRS) {
-    const int n = min(BWD_PAIRS, a.K - k0);
-    int row[BWD_PAIRS];
-    float w[BWD_PAIRS], dot[BWD_PAIRS];
+  const int rows = choice_rows(a.row_of, t, a.K, 0, a.rows, lane);
+  const float ws = rows >= 0 && a.w ? a.w[t * a.K + lane] : 1.0f;
+  const Row<DT, FULL, NT> dy(a.dy, t * a.ld_dy, a.H);
+  for (int k0 = 0; k0 < a.K; k0 += NP) {
+    float w[NP], dot[NP];
+    int row[NP];
 #pragma unroll
-    for (int j = 0; j < BWD_PAIRS; ++j) {
-      const int r = j < n ? a.row_of[t * a.K + k0 + j] : -1;
-      row[j] = (uint32_t)r < (uint64_t)a.rows ? r : -1;
-      w[j] = j < n && a.w ? a.w[t * a.K + k0 + j] : 1.0f;
+    for (int j = 0; j < NP; ++j) {
+      const int k = min(k0 + j, 63);
+      row[j] = k0 + j < a.K ? lane_value(rows, k) : -1;
+      w[j] = lane_value(ws, k);
       dot[j] = 0.0f;
     }
     for (int i = 4 * (int)threadIdx.x; i < a.H; i += 1024) {
-      const f32x4 d = load4<DT>(dy, i, a.H);
+      typedef Row<ZT, FULL, NT> RZ;
+      typename RZ::raw z[NP];
+      const auto d0 = dy.load_raw(i);
+      if (a.dw)
 #pragma unroll
-      for (int j = 0; j < BWD_PAIRS; ++j) {
-        if (row[j] < 0) continue;  // uniform over the workgroup
-        if (a.dw) {
-          const f32x4 z = load4<ZT>(static_cast<const typename ZT::elem*>(a.zs) + row[j] * a.ld_zs, i, a.H);
+        for (int j = 0; j < NP; ++j) z[j] = RZ(a.zs, row[j] >= 0 ? row[j] * a.ld_zs : 0, row[j] >= 0 ? a.H : 0).load_raw(i);
+      const f32x4 d = Row<DT, FULL, NT>::widen_raw(d0, i, a.H);
+      if (a.dzs)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dot[j] = __builtin_fmaf(d[e], z[e], dot[j]);
+        for (int j = 0; j < NP; ++j)
+          if (row[j] >= 0) Row<BF16, FULL, NT>(a.dzs, row[j] * a.ld_dzs, a.H).store(i, d * w[j]);
+      if (a.dw)
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          const f32x4 v = RZ::widen_raw(z[j], i, a.H);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dot[j] = __builtin_fmaf(d[e], v[e], dot[j]);
         }
-        if (a.dzs) store4<BF16>(a.dzs + row[j] * a.ld_dzs, i, a.H, d * w[j]);
-      }
     }
     if (!a.dw) continue;
-    __syncthreads();  // the sums of the eight choices before are read
+    __syncthreads();  // the sums of the choices before are read
 #pragma unroll
-    for (int j = 0; j < BWD_PAIRS; ++j) {
+    for (int j = 0; j < NP; ++j) {
       const float s = wave_sum(dot[j]);
       if (lane == 0) dots[j][wave] = s;
     }
     __syncthreads();
-    if ((int)threadIdx.x < n) {
-      const float* s = dots[threadIdx.x];
-      a.dw[t * a.K + k0 + threadIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
+    const int j = (int)threadIdx.x;
+    if (j < NP && k0 + j < a.K) {
+      const float* s = dots[j];
+      a.dw[t * a.K + k0 + j] = (s[0] + s[1]) + (s[2] + s[3]);
     }
   }
 }
@@ -316,37 +395,74 @@ hipError_t launch_route_sort(const RouteSortArgs& a, hipStream_t s) {
   return launch_kernel(route_place_kernel<false>, dim3((unsigned)a.blocks), dim3(SORT_THREADS), s, a);
 }
 
-hipError_t launch_route_dispatch(RouteDispatchArgs a, hipStream_t s) {
-  if (a.H < 8) return hipErrorInvalidValue;
-  a.segments = blocks_of(a.H, DISPATCH_COLS);
+namespace {
+// Rows that one wave looks through for padding: few where there are few, so that the
+// zeroing of several rows is not one wave's work.
+int pad_rows_for(int64_t rows) { return rows <= 16384 ? 4 : 64; }
+}  // namespace
+
+hipError_t launch_route_dispatch(RouteDispatchArgs a, bool full, bool nt, hipStream_t s) {
+  if (a.H < 8 || a.K < 1 || a.K > 64) return hipErrorInvalidValue;
   a.token_blocks = blocks_of(a.T, 4);
-  const int64_t blocks = a.token_blocks + (a.rows + 255) / 256;
+  a.pad_rows = pad_rows_for(a.rows);
+  const int64_t blocks = a.token_blocks + blocks_of(a.rows, 4 * a.pad_rows);
   if (blocks < 1 || blocks > INT32_MAX) return blocks < 1 ? hipSuccess : hipErrorInvalidValue;
-  return launch_kernel(route_dispatch_kernel, dim3((unsigned)blocks, (unsigned)a.segments), dim3(256), s, a);
+  const dim3 grid((unsigned)blocks, (unsigned)blocks_of(a.H, DISPATCH_COLS)), block(256);
+  if (!full) return launch_kernel(route_dispatch_kernel<false, false>, grid, block, s, a);
+  return nt ? launch_kernel(route_dispatch_kernel<true, true>, grid, block, s, a)
+            : launch_kernel(route_dispatch_kernel<true, false>, grid, block, s, a);
 }
 
-hipError_t launch_route_combine(RouteCombineArgs a, int z_type, int y_type, hipStream_t s) {
-  if (a.H < 4 || a.T < 1) return hipErrorInvalidValue;
-  a.segments = blocks_of(a.H, COMBINE_COLS);
-  const dim3 grid((unsigned)blocks_of(a.T, 4), (unsigned)a.segments), block(256);
-  if (z_type == TPMLP_BF16)
-    return y_type == TPMLP_BF16 ? launch_kernel(route_combine_kernel<BF16, BF16>, grid, block, s, a)
-                                : launch_kernel(route_combine_kernel<BF16, F32>, grid, block, s, a);
-  return y_type == TPMLP_BF16 ? launch_kernel(route_combine_kernel<F32, BF16>, grid, block, s, a)
-                              : launch_kernel(route_combine_kernel<F32, F32>, grid, block, s, a);
+namespace {
+
+template <class ZT, class YT>
+hipError_t launch_combine(const RouteCombineArgs& a, bool full, bool nt, hipStream_t s) {
+  // Few tokens: a chunk to a wave, so that more waves share the latency.
+  const int chunks = a.T <= 2048 ? 1 : 2;
+  const dim3 grid((unsigned)blocks_of(a.T, 4), (unsigned)blocks_of(a.H, 256 * chunks)), block(256);
+  if (!full) return chunks == 1 ? launch_kernel(route_combine_kernel<ZT, YT, 1, false, false>, grid, block, s, a)
+                                : launch_kernel(route_combine_kernel<ZT, YT, 2, false, false>, grid, block, s, a);
+  if (chunks == 1) return launch_kernel(route_combine_kernel<ZT, YT, 1, true, false>, grid, block, s, a);
+  return nt ? launch_kernel(route_combine_kernel<ZT, YT, 2, true, true>, grid, block, s, a)
+            : launch_kernel(route_combine_kernel<ZT, YT, 2, true, false>, grid, block, s, a);
 }
 
-hipError_t launch_route_combine_bwd(RouteCombineBwdArgs a, int dy_type, int z_type, hipStream_t s) {
-  if (a.H < 8) return hipErrorInvalidValue;
-  a.token_blocks = (int)a.T;
-  const int64_t blocks = a.T + (a.dzs ? (a.rows + 255) / 256 : 0);
-  if (blocks < 1 || blocks > INT32_MAX) return blocks < 1 ? hipSuccess : hipErrorInvalidValue;
+template <class DT, class ZT>
+hipError_t launch_combine_bwd(const RouteCombineBwdArgs& a, int64_t blocks, bool full, bool nt, hipStream_t s) {
   const dim3 grid((unsigned)blocks), block(256);
+  if (a.K <= 2)
+    return !full ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 2, false, false>, grid, block, s, a)
+           : nt  ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 2, true, true>, grid, block, s, a)
+                 : launch_kernel(route_combine_bwd_kernel<DT, ZT, 2, true, false>, grid, block, s, a);
+  if (a.K <= 4)
+    return !full ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 4, false, false>, grid, block, s, a)
+           : nt  ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 4, true, true>, grid, block, s, a)
+                 : launch_kernel(route_combine_bwd_kernel<DT, ZT, 4, true, false>, grid, block, s, a);
+  return !full ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 8, false, false>, grid, block, s, a)
+         : nt  ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 8, true, true>, grid, block, s, a)
+               : launch_kernel(route_combine_bwd_kernel<DT, ZT, 8, true, false>, grid, block, s, a);
+}
+
+}  // namespace
+
+hipError_t launch_route_combine(const RouteCombineArgs& a, int z_type, int y_type, bool full, bool nt, hipStream_t s) {
+  if (a.H < 4 || a.T < 1 || a.K < 1 || a.K > 64) return hipErrorInvalidValue;
+  if (z_type == TPMLP_BF16)
+    return y_type == TPMLP_BF16 ? launch_combine<BF16, BF16>(a, full, nt, s) : launch_combine<BF16, F32>(a, full, nt, s);
+  return y_type == TPMLP_BF16 ? launch_combine<F32, BF16>(a, full, nt, s) : launch_combine<F32, F32>(a, full, nt, s);
+}
+
+hipError_t launch_route_combine_bwd(RouteCombineBwdArgs a, int dy_type, int z_type, bool full, bool nt, hipStream_t s) {
+  if (a.H < 8 || a.K < 1 || a.K > 64) return hipErrorInvalidValue;
+  a.token_blocks = (int)a.T;
+  a.pad_rows = pad_rows_for(a.rows);
+  const int64_t blocks = a.T + (a.dzs ? blocks_of(a.rows, 4 * a.pad_rows) : 0);
+  if (blocks < 1 || blocks > INT32_MAX) return blocks < 1 ? hipSuccess : hipErrorInvalidValue;
   if (dy_type == TPMLP_BF16)
-    return z_type == TPMLP_BF16 ? launch_kernel(route_combine_bwd_kernel<BF16, BF16>, grid, block, s, a)
-                                : launch_kernel(route_combine_bwd_kernel<BF16, F32>, grid, block, s, a);
-  return z_type == TPMLP_BF16 ? launch_kernel(route_combine_bwd_kernel<F32, BF16>, grid, block, s, a)
-                              : launch_kernel(route_combine_bwd_kernel<F32, F32>, grid, block, s, a);
+    return z_type == TPMLP_BF16 ? launch_combine_bwd<BF16, BF16>(a, blocks, full, nt, s)
+                                : launch_combine_bwd<BF16, F32>(a, blocks, full, nt, s);
+  return z_type == TPMLP_BF16 ? launch_combine_bwd<F32, BF16>(a, blocks, full, nt, s)
+                              : launch_combine_bwd<F32, F32>(a, blocks, full, nt, s);
 }
 
 }  // namespace tpmlp
