@@ -140,10 +140,23 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _current_stream() -> int:
+    """hipStream_t of torch's current stream.  torch.cuda.current_stream() builds a Stream
+    object for it, which takes longer than a small call's launch (2.8 us against 0.2)."""
+    global _current_stream
+    import torch
+    raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is not None and device is not None:
+        torch.cuda.init()
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _current_stream()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -467,14 +480,19 @@ EDGE_MAX_H = 32768                                     # TPMLP_EDGE_MAX_H
 ROUTE_MAX_EXPERTS, ROUTE_MAX_CHOICES = 512, 64         # TPMLP_ROUTE_MAX_*
 
 
+_KINDS = {}  # torch dtype -> tpmlp_dtype
+
+
 def _dtype(t, name) -> int:
     """tpmlp_dtype of a tensor (bf16 data may be uint16 or int16 bits)."""
-    import torch
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
-        return BF16
-    raise TypeError(f"{name} must be float32 or hold bf16 bits (bfloat16/uint16/int16), got {t.dtype}")
+    kind = _KINDS.get(t.dtype)
+    if kind is None:
+        import torch
+        _KINDS.update({torch.float32: F32, torch.bfloat16: BF16, torch.int16: BF16, torch.uint16: BF16})
+        kind = _KINDS.get(t.dtype)
+        if kind is None:
+            raise TypeError(f"{name} must be float32 or hold bf16 bits (bfloat16/uint16/int16), got {t.dtype}")
+    return kind
 
 
 def _rows(t, shape, name, kind=None):
@@ -482,12 +500,12 @@ def _rows(t, shape, name, kind=None):
     checking its shape and, if given, its tpmlp_dtype."""
     if t is None:
         return None, 0
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if kind is not None and _dtype(t, name) != kind:
         raise TypeError(f"{name} must be {'float32' if kind == F32 else 'bf16'}, got {t.dtype}")
     row, col = t.stride()
-    if shape[1] > 1 and col != 1:
+    if col != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous columns")
     return t.data_ptr(), (row if shape[0] > 1 else 0)
 
