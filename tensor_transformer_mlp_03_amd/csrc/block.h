@@ -105,7 +105,7 @@ struct RouteDispatchArgs {
   const int32_t *row_of, *src_of;
   int64_t T, rows, ld_x, ld_xs;
   int K, H;
-  int token_blocks, pad_rows;
+  int segments, pad_blocks, pad_rows;
 };
 // full: H is a multiple of eight and every row starts at a multiple of eight elements
 // (dispatch), of four both (combine and its gradient); nt: non-temporal.
@@ -129,7 +129,7 @@ struct RouteCombineBwdArgs {
   const int32_t *row_of, *src_of;
   int64_t T, rows, ld_dy, ld_zs, ld_dzs;
   int K, H;
-  int token_blocks, pad_rows;
+  int pad_blocks, pad_rows;
 };
 hipError_t launch_route_combine_bwd(RouteCombineBwdArgs a, int dy_type, int z_type, bool full, bool nt, hipStream_t s);
 

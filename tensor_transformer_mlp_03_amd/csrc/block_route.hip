@@ -251,13 +251,16 @@ __device__ __forceinline__ void zero_padding(uint16_t* out, int64_t ld, const in
 template <bool FULL, bool NT>
 __global__ void __launch_bounds__(256) route_dispatch_kernel(RouteDispatchArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int c0 = (int)blockIdx.y * DISPATCH_COLS, c1 = min(c0 + DISPATCH_COLS, a.H);
-  if ((int)blockIdx.x >= a.token_blocks) {
-    const int64_t r0 = ((int64_t)((int)blockIdx.x - a.token_blocks) * 4 + wave) * a.pad_rows;
-    if (r0 < a.rows) zero_padding<FULL, NT>(a.xs, a.ld_xs, a.src_of, a.rows, r0, a.pad_rows, c0, c1, a.H, lane);
+  // A row's segments are neighbouring workgroups, so that whole rows are written at
+  // about one time; the padding comes first, where it runs beside the tokens.
+  const int block = (int)(blockIdx.x / a.segments), c0 = (int)(blockIdx.x % a.segments) * DISPATCH_COLS;
+  if (block < a.pad_blocks) {
+    const int64_t r0 = ((int64_t)block * 4 + wave) * a.pad_rows;
+    if (r0 < a.rows)
+      zero_padding<FULL, NT>(a.xs, a.ld_xs, a.src_of, a.rows, r0, a.pad_rows, c0, min(c0 + DISPATCH_COLS, a.H), a.H, lane);
     return;
   }
-  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  const int64_t t = (int64_t)(block - a.pad_blocks) * 4 + wave;
   if (t >= a.T) return;
   const int rows = choice_rows(a.row_of, t, a.K, 0, a.rows, lane);
   const Row8<FULL, NT> x(a.x, t * a.ld_x, a.H);
@@ -321,12 +324,12 @@ template <class DT, class ZT, int NP, bool FULL, bool NT>
 __global__ void __launch_bounds__(256) route_combine_bwd_kernel(RouteCombineBwdArgs a) {
   __shared__ float dots[NP][4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if ((int)blockIdx.x >= a.token_blocks) {
-    const int64_t r0 = ((int64_t)((int)blockIdx.x - a.token_blocks) * 4 + wave) * a.pad_rows;
+  if ((int)blockIdx.x < a.pad_blocks) {  // first, where it runs beside the tokens
+    const int64_t r0 = ((int64_t)blockIdx.x * 4 + wave) * a.pad_rows;
     if (r0 < a.rows) zero_padding<false, NT>(a.dzs, a.ld_dzs, a.src_of, a.rows, r0, a.pad_rows, 0, a.H, a.H, lane);
     return;
   }
-  const int64_t t = blockIdx.x;
+  const int64_t t = (int)blockIdx.x - a.pad_blocks;
   const int rows = choice_rows(a.row_of, t, a.K, 0, a.rows, lane);
   const float ws = rows >= 0 && a.w ? a.w[t * a.K + lane] : 1.0f;
   const Row<DT, FULL, NT> dy(a.dy, t * a.ld_dy, a.H);
@@ -403,11 +406,12 @@ int pad_rows_for(int64_t rows) { return rows <= 16384 ? 4 : 64; }
 
 hipError_t launch_route_dispatch(RouteDispatchArgs a, bool full, bool nt, hipStream_t s) {
   if (a.H < 8 || a.K < 1 || a.K > 64) return hipErrorInvalidValue;
-  a.token_blocks = blocks_of(a.T, 4);
+  a.segments = blocks_of(a.H, DISPATCH_COLS);
   a.pad_rows = pad_rows_for(a.rows);
-  const int64_t blocks = a.token_blocks + blocks_of(a.rows, 4 * a.pad_rows);
+  a.pad_blocks = blocks_of(a.rows, 4 * a.pad_rows);
+  const int64_t blocks = ((int64_t)a.pad_blocks + blocks_of(a.T, 4)) * a.segments;
   if (blocks < 1 || blocks > INT32_MAX) return blocks < 1 ? hipSuccess : hipErrorInvalidValue;
-  const dim3 grid((unsigned)blocks, (unsigned)blocks_of(a.H, DISPATCH_COLS)), block(256);
+  const dim3 grid((unsigned)blocks), block(256);
   if (!full) return launch_kernel(route_dispatch_kernel<false, false>, grid, block, s, a);
   return nt ? launch_kernel(route_dispatch_kernel<true, true>, grid, block, s, a)
             : launch_kernel(route_dispatch_kernel<true, false>, grid, block, s, a);
@@ -454,9 +458,9 @@ hipError_t launch_route_combine(const RouteCombineArgs& a, int z_type, int y_typ
 
 hipError_t launch_route_combine_bwd(RouteCombineBwdArgs a, int dy_type, int z_type, bool full, bool nt, hipStream_t s) {
   if (a.H < 8 || a.K < 1 || a.K > 64) return hipErrorInvalidValue;
-  a.token_blocks = (int)a.T;
   a.pad_rows = pad_rows_for(a.rows);
-  const int64_t blocks = a.T + (a.dzs ? blocks_of(a.rows, 4 * a.pad_rows) : 0);
+  a.pad_blocks = a.dzs ? blocks_of(a.rows, 4 * a.pad_rows) : 0;
+  const int64_t blocks = a.T + a.pad_blocks;
   if (blocks < 1 || blocks > INT32_MAX) return blocks < 1 ? hipSuccess : hipErrorInvalidValue;
   if (dy_type == TPMLP_BF16)
     return z_type == TPMLP_BF16 ? launch_combine_bwd<BF16, BF16>(a, blocks, full, nt, s)
