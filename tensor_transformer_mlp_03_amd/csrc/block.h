@@ -61,7 +61,8 @@ constexpr int EDGE_ACC_RMS = 2, EDGE_ACC_LAYER = 4;
 // The backward's row forms, waves x chunks a lane (WIDE: two kernels); ANY: rows that
 // are not FULL.
 enum EdgeShape : int {
-  EDGE_1x2, EDGE_4x1, EDGE_4x2, EDGE_8x2, EDGE_16x2, EDGE_WIDE, EDGE_ANY_4x1, EDGE_ANY_8x2, EDGE_ANY_WIDE
+  EDGE_1x1, EDGE_1x2, EDGE_4x1, EDGE_4x2, EDGE_8x2, EDGE_16x2, EDGE_WIDE,
+  EDGE_ANY_1x1, EDGE_ANY_1x2, EDGE_ANY_4x1, EDGE_ANY_8x2, EDGE_ANY_WIDE
 };
 EdgeShape edge_bwd_shape(int H, bool full);
 // Whether rows of H elements may take the WIDE form, which needs workspace.
@@ -105,7 +106,7 @@ struct RouteDispatchArgs {
   const int32_t *row_of, *src_of;
   int64_t T, rows, ld_x, ld_xs;
   int K, H;
-  int segments, pad_blocks, pad_rows;
+  int segments, pad_blocks, pad_rows, lanes;
 };
 // full: H is a multiple of eight and every row starts at a multiple of eight elements
 // (dispatch), of four both (combine and its gradient); nt: non-temporal.
@@ -131,7 +132,7 @@ struct RouteCombineBwdArgs {
   int K, H;
   int pad_blocks, pad_rows;
 };
-hipError_t launch_route_combine_bwd(RouteCombineBwdArgs a, int dy_type, int z_type, bool full, bool nt, hipStream_t s);
+hipError_t launch_route_combine_bwd(const RouteCombineBwdArgs& a, int dy_type, int z_type, bool full, bool nt, hipStream_t s);
 
 // ---------------------------------------------------------------------------
 // Gradient norm and clipping (block_clip.hip)

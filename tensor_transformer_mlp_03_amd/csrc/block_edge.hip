@@ -146,10 +146,12 @@ hipError_t launch_form(const EdgeFwdArgs& a, bool full, hipStream_t s) {
   return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, W, NV, FULL, NT_>, W == 1 ? rows4 : rows, dim3(W == 1 ? 256 : 64 * W), s, a)
   if (a.H > TPMLP_EDGE_MAX_H) return hipErrorInvalidValue;
   if (!full) {
+    if (a.H <= 256) EDGE_FORM(1, 1, false, false);
     if (a.H <= 1024) EDGE_FORM(1, 4, false, false);
     if (a.H <= 4096) EDGE_FORM(4, 4, false, false);
     EDGE_FORM(16, 8, false, false);
   }
+  if (a.H <= 256) EDGE_FORM(1, 1, true, NT);
   if (a.H <= 512) EDGE_FORM(1, 2, true, NT);
   if (a.H <= 1024) EDGE_FORM(1, 4, true, NT);
   if (a.H <= 2048) EDGE_FORM(4, 2, true, NT);

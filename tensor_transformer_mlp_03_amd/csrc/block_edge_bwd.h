@@ -391,12 +391,15 @@ hipError_t launch_form(const EdgeBwdArgs& a, int64_t blocks, bool full, hipStrea
 #define EDGE_FORM(W, NV, FULL, NT_) \
   return launch_kernel(edge_bwd_kernel<YT, RT, HAS_Y, LAYER, DXT, W, NV, FULL, NT_>, grid, dim3(W == 1 ? 256 : 64 * W), s, a)
   switch (edge_bwd_shape(a.H, full)) {
+    case EDGE_1x1: EDGE_FORM(1, 1, true, NT);
     case EDGE_1x2: EDGE_FORM(1, 2, true, NT);
     case EDGE_4x1: EDGE_FORM(4, 1, true, NT);
     case EDGE_4x2: EDGE_FORM(4, 2, true, NT);
     case EDGE_8x2: EDGE_FORM(8, 2, true, NT);
     case EDGE_16x2: EDGE_FORM(16, 2, true, NT);
     case EDGE_WIDE: return launch_wide<YT, RT, HAS_Y, LAYER, DXT, true>(a, blocks, s);
+    case EDGE_ANY_1x1: EDGE_FORM(1, 1, false, false);
+    case EDGE_ANY_1x2: EDGE_FORM(1, 2, false, false);
     case EDGE_ANY_4x1: EDGE_FORM(4, 1, false, false);
     case EDGE_ANY_8x2: EDGE_FORM(8, 2, false, false);
     case EDGE_ANY_WIDE: return launch_wide<YT, RT, HAS_Y, LAYER, DXT, false>(a, blocks, s);

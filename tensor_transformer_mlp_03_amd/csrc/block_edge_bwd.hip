@@ -85,9 +85,11 @@ __global__ void __launch_bounds__(FIN_COLS * FIN_LINES) edge_finish_kernel(EdgeF
 }  // namespace
 
 EdgeShape edge_bwd_shape(int H, bool full) {
-  if (!full) return H <= 1024 ? EDGE_ANY_4x1 : H <= 4096 ? EDGE_ANY_8x2 : EDGE_ANY_WIDE;
-  return H <= 512 ? EDGE_1x2 : H <= 1024 ? EDGE_4x1 : H <= 2048 ? EDGE_4x2 : H <= 4096 ? EDGE_8x2 : H <= 8192 ? EDGE_16x2
-                                                                                                     : EDGE_WIDE;
+  if (H <= 256) return full ? EDGE_1x1 : EDGE_ANY_1x1;
+  if (H <= 512) return full ? EDGE_1x2 : EDGE_ANY_1x2;
+  if (H <= 1024) return full ? EDGE_4x1 : EDGE_ANY_4x1;
+  if (H <= 4096) return !full ? EDGE_ANY_8x2 : H <= 2048 ? EDGE_4x2 : EDGE_8x2;
+  return !full ? EDGE_ANY_WIDE : H <= 8192 ? EDGE_16x2 : EDGE_WIDE;
 }
 
 EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer) {

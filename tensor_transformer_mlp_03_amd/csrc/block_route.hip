@@ -276,6 +276,26 @@ __global__ void __launch_bounds__(256) route_dispatch_kernel(RouteDispatchArgs a
   }
 }
 
+// Short rows (at most 256 elements): a row is `lanes` lanes of eight elements (a power
+// of two), and the wave writes 64 / lanes of the token's rows at once.
+__global__ void __launch_bounds__(256) route_dispatch_short_kernel(RouteDispatchArgs a) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if ((int)blockIdx.x < a.pad_blocks) {
+    const int64_t r0 = ((int64_t)blockIdx.x * 4 + wave) * a.pad_rows;
+    if (r0 < a.rows) zero_padding<false, false>(a.xs, a.ld_xs, a.src_of, a.rows, r0, a.pad_rows, 0, a.H, a.H, lane);
+    return;
+  }
+  const int64_t t = (int64_t)((int)blockIdx.x - a.pad_blocks) * 4 + wave;
+  if (t >= a.T) return;
+  const int rows = choice_rows(a.row_of, t, a.K, 0, a.rows, lane);
+  const int i = 8 * (lane & (a.lanes - 1)), group = lane / a.lanes, groups = 64 / a.lanes, at = min(i, a.H - 8);
+  const u16x8_u v = *reinterpret_cast<const u16x8_u*>(a.x + t * a.ld_x + at);
+  for (int k0 = 0; k0 < a.K; k0 += groups) {
+    const int row = __shfl(rows, min(k0 + group, 63), 64);
+    if (k0 + group < a.K && row >= 0 && i < a.H) *reinterpret_cast<u16x8_u*>(a.xs + row * a.ld_xs + at) = v;
+  }
+}
+
 // A wave sums CHUNKS 256-element chunks of a token's rows, four choices' loads in
 // flight together.  A choice that takes no part is a row of length zero with weight
 // zero: it reads no memory and adds nothing.
@@ -318,9 +338,9 @@ __global__ void __launch_bounds__(256) route_combine_kernel(RouteCombineArgs a) 
   for (int c = 0; c < CHUNKS; ++c) y.store(at(c), sum[c]);
 }
 
-// One workgroup a token, NP choices together; a choice that takes no part is a row
-// of length zero.
-template <class DT, class ZT, int NP, bool FULL, bool NT>
+// W waves a token (one where a row is no longer than a wave's four passes), NP choices
+// together; a choice that takes no part is a row of length zero.
+template <class DT, class ZT, int W, int NP, bool FULL, bool NT>
 __global__ void __launch_bounds__(256) route_combine_bwd_kernel(RouteCombineBwdArgs a) {
   __shared__ float dots[NP][4];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -329,7 +349,8 @@ __global__ void __launch_bounds__(256) route_combine_bwd_kernel(RouteCombineBwdA
     if (r0 < a.rows) zero_padding<false, NT>(a.dzs, a.ld_dzs, a.src_of, a.rows, r0, a.pad_rows, 0, a.H, a.H, lane);
     return;
   }
-  const int64_t t = (int)blockIdx.x - a.pad_blocks;
+  const int64_t t = W == 1 ? (int64_t)((int)blockIdx.x - a.pad_blocks) * 4 + wave : (int64_t)((int)blockIdx.x - a.pad_blocks);
+  if (t >= a.T) return;  // W == 1 only, where no barrier follows
   const int rows = choice_rows(a.row_of, t, a.K, 0, a.rows, lane);
   const float ws = rows >= 0 && a.w ? a.w[t * a.K + lane] : 1.0f;
   const Row<DT, FULL, NT> dy(a.dy, t * a.ld_dy, a.H);
@@ -343,7 +364,7 @@ __global__ void __launch_bounds__(256) route_combine_bwd_kernel(RouteCombineBwdA
       w[j] = lane_value(ws, k);
       dot[j] = 0.0f;
     }
-    for (int i = 4 * (int)threadIdx.x; i < a.H; i += 1024) {
+    for (int i = 4 * (W == 1 ? lane : (int)threadIdx.x); i < a.H; i += 256 * W) {
       typedef Row<ZT, FULL, NT> RZ;
       typename RZ::raw z[NP];
       const auto d0 = dy.load_raw(i);
@@ -364,6 +385,14 @@ __global__ void __launch_bounds__(256) route_combine_bwd_kernel(RouteCombineBwdA
         }
     }
     if (!a.dw) continue;
+    if (W == 1) {
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const float s = wave_sum(dot[j]);
+        if (lane == j && k0 + j < a.K) a.dw[t * a.K + k0 + j] = s;
+      }
+      continue;
+    }
     __syncthreads();  // the sums of the choices before are read
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
@@ -412,6 +441,10 @@ hipError_t launch_route_dispatch(RouteDispatchArgs a, bool full, bool nt, hipStr
   const int64_t blocks = ((int64_t)a.pad_blocks + blocks_of(a.T, 4)) * a.segments;
   if (blocks < 1 || blocks > INT32_MAX) return blocks < 1 ? hipSuccess : hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(256);
+  if (a.H <= 256) {  // 32768 tokens of 64 with 8 choices: 37 us by whole waves
+    for (a.lanes = 1; 8 * a.lanes < a.H;) a.lanes *= 2;
+    return launch_kernel(route_dispatch_short_kernel, grid, block, s, a);
+  }
   if (!full) return launch_kernel(route_dispatch_kernel<false, false>, grid, block, s, a);
   return nt ? launch_kernel(route_dispatch_kernel<true, true>, grid, block, s, a)
             : launch_kernel(route_dispatch_kernel<true, false>, grid, block, s, a);
@@ -431,20 +464,26 @@ hipError_t launch_combine(const RouteCombineArgs& a, bool full, bool nt, hipStre
             : launch_kernel(route_combine_kernel<ZT, YT, 2, true, false>, grid, block, s, a);
 }
 
-template <class DT, class ZT>
-hipError_t launch_combine_bwd(const RouteCombineBwdArgs& a, int64_t blocks, bool full, bool nt, hipStream_t s) {
+template <class DT, class ZT, int W>
+hipError_t launch_combine_bwd(RouteCombineBwdArgs a, bool full, bool nt, hipStream_t s) {
+  a.pad_rows = pad_rows_for(a.rows);
+  a.pad_blocks = a.dzs ? blocks_of(a.rows, 4 * a.pad_rows) : 0;
+  const int64_t blocks = a.pad_blocks + (W == 1 ? blocks_of(a.T, 4) : a.T);
+  if (blocks < 1 || blocks > INT32_MAX) return blocks < 1 ? hipSuccess : hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(256);
-  if (a.K <= 2)
-    return !full ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 2, false, false>, grid, block, s, a)
-           : nt  ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 2, true, true>, grid, block, s, a)
-                 : launch_kernel(route_combine_bwd_kernel<DT, ZT, 2, true, false>, grid, block, s, a);
-  if (a.K <= 4)
-    return !full ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 4, false, false>, grid, block, s, a)
-           : nt  ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 4, true, true>, grid, block, s, a)
-                 : launch_kernel(route_combine_bwd_kernel<DT, ZT, 4, true, false>, grid, block, s, a);
-  return !full ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 8, false, false>, grid, block, s, a)
-         : nt  ? launch_kernel(route_combine_bwd_kernel<DT, ZT, 8, true, true>, grid, block, s, a)
-               : launch_kernel(route_combine_bwd_kernel<DT, ZT, 8, true, false>, grid, block, s, a);
+#define BWD_FORM(NP)                                                                                            \
+  return !full ? launch_kernel(route_combine_bwd_kernel<DT, ZT, W, NP, false, false>, grid, block, s, a)        \
+         : nt  ? launch_kernel(route_combine_bwd_kernel<DT, ZT, W, NP, true, true>, grid, block, s, a)          \
+               : launch_kernel(route_combine_bwd_kernel<DT, ZT, W, NP, true, false>, grid, block, s, a)
+  if (a.K <= 2) BWD_FORM(2);
+  if (a.K <= 4) BWD_FORM(4);
+  BWD_FORM(8);
+#undef BWD_FORM
+}
+
+template <class DT, class ZT>
+hipError_t launch_combine_bwd(const RouteCombineBwdArgs& a, bool full, bool nt, hipStream_t s) {
+  return a.H <= 1024 ? launch_combine_bwd<DT, ZT, 1>(a, full, nt, s) : launch_combine_bwd<DT, ZT, 4>(a, full, nt, s);
 }
 
 }  // namespace
@@ -456,17 +495,11 @@ hipError_t launch_route_combine(const RouteCombineArgs& a, int z_type, int y_typ
   return y_type == TPMLP_BF16 ? launch_combine<F32, BF16>(a, full, nt, s) : launch_combine<F32, F32>(a, full, nt, s);
 }
 
-hipError_t launch_route_combine_bwd(RouteCombineBwdArgs a, int dy_type, int z_type, bool full, bool nt, hipStream_t s) {
+hipError_t launch_route_combine_bwd(const RouteCombineBwdArgs& a, int dy_type, int z_type, bool full, bool nt, hipStream_t s) {
   if (a.H < 8 || a.K < 1 || a.K > 64) return hipErrorInvalidValue;
-  a.pad_rows = pad_rows_for(a.rows);
-  a.pad_blocks = a.dzs ? blocks_of(a.rows, 4 * a.pad_rows) : 0;
-  const int64_t blocks = a.T + a.pad_blocks;
-  if (blocks < 1 || blocks > INT32_MAX) return blocks < 1 ? hipSuccess : hipErrorInvalidValue;
   if (dy_type == TPMLP_BF16)
-    return z_type == TPMLP_BF16 ? launch_combine_bwd<BF16, BF16>(a, blocks, full, nt, s)
-                                : launch_combine_bwd<BF16, F32>(a, blocks, full, nt, s);
-  return z_type == TPMLP_BF16 ? launch_combine_bwd<F32, BF16>(a, blocks, full, nt, s)
-                              : launch_combine_bwd<F32, F32>(a, blocks, full, nt, s);
+    return z_type == TPMLP_BF16 ? launch_combine_bwd<BF16, BF16>(a, full, nt, s) : launch_combine_bwd<BF16, F32>(a, full, nt, s);
+  return z_type == TPMLP_BF16 ? launch_combine_bwd<F32, BF16>(a, full, nt, s) : launch_combine_bwd<F32, F32>(a, full, nt, s);
 }
 
 }  // namespace tpmlp
