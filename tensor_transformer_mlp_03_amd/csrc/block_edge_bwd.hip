@@ -102,7 +102,7 @@ EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer) {
   // rows), so that all of them end together.  A wide row's slice is that of several
   // workgroups.  (The cut does not depend on whether the rows are FULL, so that the
   // workspace does not.)
-  const int64_t target = H <= 2048 ? 1024 : H <= 4096 ? 512 : 256;
+  const int64_t target = H <= 2048 ? 768 : H <= 4096 ? 512 : 256;
   // Rows that a workgroup takes at least: those it holds at once, and up to four while
   // there is a workgroup for every CU, which keeps the slices below the data.
   const int64_t least = std::max<int64_t>(H <= 512 ? 4 : 1, std::min<int64_t>(4, M / 256));

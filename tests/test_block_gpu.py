@@ -138,8 +138,8 @@ def run_edge(seed, M, H, post, pre, y, r, p, rows, pad=0, offset=0, **over):
         close("d" + k, g[k], back[k], back[k + "_mag"], 450 + M)
 
 
-SIZES = [(1, 8), (3, 9), (5, 13), (4, 64), (7, 257), (33, 511), (2, 512), (6, 513), (130, 1000), (9, 1024), (5, 1025),
-         (3, 2048), (4, 2050), (21, 3584), (3, 4096), (3, 4100), (2, 8192), (3, 8200), (2, 16384), (2, 16392), (3, 20480),
+SIZES = [(1, 8), (3, 9), (5, 13), (4, 64), (9, 255), (6, 256), (7, 257), (5, 260), (33, 511), (2, 512), (6, 513), (130, 1000), (9, 1024), (5, 1025),
+         (3, 2048), (4, 2050), (21, 3584), (3, 4096), (3, 4100), (2, 8192), (3, 8200), (3, 8196), (2, 8195), (2, 16384), (2, 16392), (3, 20480),
          (2, 20483), (2, 32768)]
 
 
@@ -350,7 +350,9 @@ def put(v, pad=0, offset=0):
 
 @pytest.mark.parametrize("T,K,E,H,capacity", [(1, 1, 4, 8, 0), (5, 2, 8, 9, 0), (33, 3, 7, 331, 0), (8, 2, 8, 4096, 0),
                                               (200, 8, 16, 512, 64), (77, 9, 60, 2049, 0), (300, 1, 1, 1032, 0),
-                                              (50, 20, 64, 136, 8), (10, 4, 512, 5000, 0)])
+                                              (50, 20, 64, 136, 8), (10, 4, 512, 5000, 0),
+                                              (40, 5, 8, 72, 0), (40, 12, 8, 255, 0), (33, 2, 4, 256, 16),
+                                              (90, 3, 4, 8, 0), (2100, 2, 4, 264, 0), (60, 64, 32, 16, 0)])
 @pytest.mark.parametrize("pad,offset", [(0, 0), (3, 1)])
 def test_route_moves(T, K, E, H, capacity, pad, offset):
     """There and back, both gradients; dropped pairs and padding rows hold NaN where they are read."""
