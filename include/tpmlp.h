@@ -366,7 +366,7 @@ typedef enum {
  * one sequence: a gate per sequence; 1: a gate per token).  Without a block before
  * it (y NULL: no norm after it, no gate) the edge is x = N_pre(alpha r). */
 typedef struct {
-  int64_t M, H;            /* tokens (0 .. 2^31 - 1), hidden size (8 .. TPMLP_EDGE_MAX_H) */
+  int64_t M, H;            /* tokens (0 .. 2^23), hidden size (8 .. TPMLP_EDGE_MAX_H) */
   int32_t post, pre;       /* tpmlp_norm of y and of r' */
   int32_t y_type;          /* tpmlp_dtype of y */
   int32_t r_type;          /* tpmlp_dtype of r, r', and their gradients */
@@ -375,7 +375,7 @@ typedef struct {
   const void *w_post, *b_post; /* [H]; w with a norm, b (nullable) with a LayerNorm */
   const void *w_pre, *b_pre;   /* [H], likewise */
   const void* gate;        /* [ceil(M / gate_rows)][H] or NULL (1) */
-  int64_t gate_rows, ld_gate;
+  int64_t gate_rows, ld_gate; /* gate_rows positive, at most 2^21 rows of the gate */
 } tpmlp_edge;
 
 /* Forward.  x (bf16) is required with a norm before the next block and NULL
@@ -416,8 +416,8 @@ tpmlp_status tpmlp_edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, co
 
 /* Rows of the sorted buffers: E * capacity, or, with capacity 0, enough for any
  * choice, T K + min(E, T K) (align - 1) rounded down to a multiple of align.  -1 if
- * an argument is invalid (T >= 0, 1 <= K <= TPMLP_ROUTE_MAX_CHOICES, 1 <= E <=
- * TPMLP_ROUTE_MAX_EXPERTS, align >= 1, T K and the rows at most 2^31 - 1). */
+ * an argument is invalid (0 <= T <= 2^23, 1 <= K <= TPMLP_ROUTE_MAX_CHOICES, 1 <= E
+ * <= TPMLP_ROUTE_MAX_EXPERTS, align >= 1, at most 2^31 - 1 rows). */
 int64_t tpmlp_route_rows(int64_t T, int K, int E, int align, int capacity);
 
 /* Workspace bytes of tpmlp_route_sort; 0 if none is needed or T K is invalid. */
@@ -461,7 +461,8 @@ tpmlp_status tpmlp_route_combine_bwd(const void* dY, int dy_type, int64_t ld_dy,
  * finite is reported and clips nothing, so the caller can skip the step.  grads,
  * outs, sizes and types (tpmlp_dtype) are host arrays of n entries; outs NULL (or an
  * entry equal to its gradient) scales in place, and a gradient in place that needs
- * no change is not written.  Squares are summed in float64. */
+ * no change is not written.  What is written must be disjoint from everything else
+ * (TPMLP_ERR_ALIAS).  Squares are summed in float64. */
 
 /* Workspace bytes of tpmlp_grad_sumsq and tpmlp_clip_grad_norm; 0 if invalid. */
 size_t tpmlp_grad_workspace_bytes(const int64_t* sizes, int n);

@@ -18,6 +18,11 @@ namespace tpmlp {
 // 3584 backward (2.6 GB) 488 -> 467 us; but 4096 x 1024 forward (59 MB) 10.2 -> 11.1 us.
 constexpr int64_t BLOCK_NT_BYTES = int64_t(256) << 20;
 
+// A launch holds fewer than 2^32 threads along a dimension: rows of one launch of up
+// to 1024 threads a row, and whether a grid stays below.
+constexpr int64_t BLOCK_LAUNCH_ROWS = int64_t(1) << 21;
+inline bool block_grid_ok(int64_t blocks, int64_t threads) { return blocks > 0 && blocks <= (int64_t(1) << 32) / threads - 1; }
+
 // ---------------------------------------------------------------------------
 // The edge between two blocks (block_edge.hip, block_edge_bwd.hip)
 // ---------------------------------------------------------------------------
@@ -27,7 +32,7 @@ struct EdgeFwdArgs {
   uint16_t* x;   // nullable
   const void *w_post, *b_post, *gate, *w_pre, *b_pre;  // nullable
   int64_t ld_y, ld_r, ld_r_out, ld_x, ld_gate;
-  int64_t M, gate_rows;
+  int64_t M, gate_rows, first_row;  // rows first_row .. M - 1, up to a launch's
   int H, post, pre, p_bf16, nt;
   float alpha, eps;
 };
@@ -40,7 +45,7 @@ struct EdgeBwdArgs {
   float* part;   // [groups * chunks][acc][H] column sums of each workgroup's rows, or null
   float* terms;  // [M][8] what the second sweep of a wide row needs, or null
   int64_t ld_y, ld_r, ld_dr_out, ld_dx, ld_dr, ld_dy, ld_gate;
-  int64_t M, gate_rows;
+  int64_t M, gate_rows, first_row;  // first_row: of the wide form's first kernel
   int chunks;  // workgroups per gate group
   int H, post, pre, p_bf16, dx_bf16, nt;
   float alpha, eps;
@@ -79,7 +84,7 @@ EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer);
 
 // y_type -1: no y.  full: H is a multiple of 4 and every row of every matrix and
 // vector starts at a multiple of four elements.
-hipError_t launch_edge_fwd(const EdgeFwdArgs& a, int y_type, int r_type, bool full, hipStream_t s);
+hipError_t launch_edge_fwd(EdgeFwdArgs a, int y_type, int r_type, bool full, hipStream_t s);
 hipError_t launch_edge_bwd(const EdgeBwdArgs& a, const EdgeBwdPlan& p, int y_type, int r_type, bool full, hipStream_t s);
 hipError_t launch_edge_finish(const EdgeFinishArgs& a, hipStream_t s);
 

@@ -9,12 +9,15 @@
 #include <new>
 #include <string>
 #include <utility>
+#include <vector>
 
 namespace tpmlp {
 namespace {
 
-constexpr int64_t MAX_ROWS = INT32_MAX;
+constexpr int64_t MAX_TOKENS = int64_t(1) << 23;  // as the MLP's M
+constexpr int64_t MAX_ROWS = INT32_MAX;           // of a sorted buffer
 constexpr int64_t MAX_H = int64_t(1) << 23;
+constexpr int64_t MAX_GATES = int64_t(1) << 21;   // rows of the gate: a workgroup of the backward each
 constexpr int64_t MAX_LD = int64_t(1) << 31;
 
 // Runs an entry point's body; an exception (the host is out of memory while it
@@ -98,7 +101,7 @@ int64_t ld_or(int64_t ld, int64_t cols) { return ld ? ld : cols; }
 
 tpmlp_status check_edge(const tpmlp_edge* e, bool has_y) {
   if (!e) return fail(TPMLP_ERR_NULL, "the edge is NULL");
-  if (e->M < 0 || e->M > MAX_ROWS) return fail(TPMLP_ERR_SHAPE, "M outside 0 .. 2^31 - 1");
+  if (e->M < 0 || e->M > MAX_TOKENS) return fail(TPMLP_ERR_SHAPE, "M outside 0 .. 2^23");
   if (e->H < 8 || e->H > TPMLP_EDGE_MAX_H) return fail(TPMLP_ERR_SHAPE, "H outside 8 .. TPMLP_EDGE_MAX_H");
   for (int n : {e->post, e->pre})
     if (n < TPMLP_NORM_NONE || n > TPMLP_NORM_LAYER) return fail(TPMLP_ERR_SHAPE, "post and pre must be a tpmlp_norm");
@@ -121,6 +124,7 @@ tpmlp_status check_edge(const tpmlp_edge* e, bool has_y) {
   }
   if (e->gate) {
     if (e->gate_rows < 1) return fail(TPMLP_ERR_SHAPE, "gate_rows must be positive");
+    if (gate_groups(*e) > MAX_GATES) return fail(TPMLP_ERR_SHAPE, "gate_rows gives a gate of more than 2^21 rows");
     TRY(check_mat({e->gate, gate_groups(*e), e->H, ld_or(e->ld_gate, e->H), ps, "gate"}));
   }
   return TPMLP_OK;
@@ -310,11 +314,11 @@ tpmlp_status edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
 // Route
 // ---------------------------------------------------------------------------
 bool pairs_ok(int64_t T, int K) {
-  return T >= 0 && K >= 1 && K <= TPMLP_ROUTE_MAX_CHOICES && T <= MAX_ROWS / K;
+  return T >= 0 && T <= MAX_TOKENS && K >= 1 && K <= TPMLP_ROUTE_MAX_CHOICES;
 }
 
 tpmlp_status check_route(int64_t T, int K, int64_t H, int64_t rows) {
-  if (!pairs_ok(T, K)) return fail(TPMLP_ERR_SHAPE, "T and K: T >= 0, 1 <= K <= TPMLP_ROUTE_MAX_CHOICES, T K below 2^31");
+  if (!pairs_ok(T, K)) return fail(TPMLP_ERR_SHAPE, "T outside 0 .. 2^23 or K outside 1 .. TPMLP_ROUTE_MAX_CHOICES");
   if (H < 8 || H > MAX_H) return fail(TPMLP_ERR_SHAPE, "H outside 8 .. 2^23");
   if (rows < 0 || rows > MAX_ROWS) return fail(TPMLP_ERR_SHAPE, "rows outside 0 .. 2^31 - 1");
   return TPMLP_OK;
@@ -495,11 +499,43 @@ tpmlp_status check_grads(const void* const* grads, void* const* outs, const int6
     const uintptr_t mask = size_of(types[t]) - 1, g = reinterpret_cast<uintptr_t>(grads[t]), u = reinterpret_cast<uintptr_t>(o);
     if ((g & mask) || (u & mask))
       return fail(TPMLP_ERR_ALIGN, ((g & mask) ? "grads[" : "outs[") + std::to_string(t) + "] is not aligned to its elements");
-    // An output over a part of its own gradient would be read after it is written.
-    const uint64_t bytes = uint64_t(sizes[t]) * size_of(types[t]);
-    if (g != u && g < u + bytes && u < g + bytes)
-      return fail(TPMLP_ERR_ALIAS, "outs[" + std::to_string(t) + "] overlaps its gradient and is not the same");
   }
+  return TPMLP_OK;
+}
+
+// What is written must be disjoint from everything else, a tensor scaled in place from
+// all but itself.  Written and read stretches in the order of their addresses: merged,
+// none may begin before an earlier one ends if one of the two is written.  Tensors
+// that were allocated one after another are in order already.
+tpmlp_status check_grad_overlaps(const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types, int n) {
+  struct Stretch {
+    uintptr_t from, to;
+    bool operator<(const Stretch& o) const { return from < o.from; }
+  };
+  std::vector<Stretch> written, read;
+  written.reserve(n);
+  if (outs) read.reserve(n);
+  for (int t = 0; t < n; ++t) {
+    if (!sizes[t]) continue;
+    const uintptr_t bytes = uintptr_t(sizes[t]) * size_of(types[t]), g = reinterpret_cast<uintptr_t>(grads[t]);
+    const uintptr_t o = outs ? reinterpret_cast<uintptr_t>(outs[t]) : g;
+    written.push_back({o, o + bytes});
+    if (o != g) read.push_back({g, g + bytes});
+  }
+  for (auto* v : {&written, &read})
+    if (!std::is_sorted(v->begin(), v->end())) std::sort(v->begin(), v->end());
+  uintptr_t written_to = 0, read_to = 0;
+  size_t r = 0;
+  for (const Stretch& w : written) {
+    for (; r < read.size() && read[r].from <= w.from; ++r) {
+      if (read[r].from < written_to) return fail(TPMLP_ERR_ALIAS, "an output overlaps another gradient");
+      read_to = std::max(read_to, read[r].to);
+    }
+    if (w.from < read_to) return fail(TPMLP_ERR_ALIAS, "an output overlaps another gradient");
+    if (w.from < written_to) return fail(TPMLP_ERR_ALIAS, "two outputs overlap");
+    written_to = w.to;
+  }
+  if (r < read.size() && read[r].from < written_to) return fail(TPMLP_ERR_ALIAS, "an output overlaps another gradient");
   return TPMLP_OK;
 }
 
@@ -574,7 +610,8 @@ tpmlp_status tpmlp_edge_fwd(const tpmlp_edge* e, const void* y, int64_t ld_y, co
 }
 
 size_t tpmlp_edge_bwd_workspace_bytes(const tpmlp_edge* e) {
-  if (!e || e->M < 1 || e->M > MAX_ROWS || e->H < 8 || e->H > TPMLP_EDGE_MAX_H || (e->gate && e->gate_rows < 1)) return 0;
+  if (!e || e->M < 1 || e->M > MAX_TOKENS || e->H < 8 || e->H > TPMLP_EDGE_MAX_H) return 0;
+  if (e->gate && (e->gate_rows < 1 || gate_groups(*e) > MAX_GATES)) return 0;
   return plan_edge_bwd(e->M, (int)e->H, gate_rows_of(*e), has_layer(*e)).ws_bytes;
 }
 
@@ -654,6 +691,7 @@ tpmlp_status tpmlp_grad_clip(const void* const* grads, void* const* outs, const 
                              const double* sumsq, float scale, float max_norm, float* norm, void* stream) {
   return guarded([&]() -> tpmlp_status {
     TRY(check_grads(grads, outs, sizes, types, n));
+    TRY(check_grad_overlaps(grads, outs, sizes, types, n));
     if (!sumsq) return fail(TPMLP_ERR_NULL, "sumsq is NULL");
     if (reinterpret_cast<uintptr_t>(sumsq) & 7) return fail(TPMLP_ERR_ALIGN, "sumsq is not aligned to its elements");
     TRY(check_factors(scale, max_norm, norm));
@@ -666,6 +704,7 @@ tpmlp_status tpmlp_clip_grad_norm(const void* const* grads, void* const* outs, c
                                   int n, float scale, float max_norm, float* norm, void* ws, size_t ws_bytes, void* stream) {
   return guarded([&]() -> tpmlp_status {
     TRY(check_grads(grads, outs, sizes, types, n));
+    TRY(check_grad_overlaps(grads, outs, sizes, types, n));
     TRY(check_factors(scale, max_norm, norm));
     TRY(check_ws(sizes, n, ws, ws_bytes));
     TRY(check_device());

@@ -19,6 +19,8 @@
 
 #include "block_dev.h"
 
+#include <algorithm>
+
 namespace tpmlp {
 namespace {
 
@@ -63,7 +65,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, W == 16 && NV <= 5 ? 8 
   __shared__ float slots[4 * W];
   const int lane = W == 1 ? threadIdx.x & 63 : threadIdx.x;  // of the row
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t row = W == 1 ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x;
+  const int64_t row = a.first_row + (W == 1 ? (int64_t)blockIdx.x * 4 + wave : (int64_t)blockIdx.x);
   if (row >= a.M) return;  // W == 1 only, where no barrier follows
   const int H = a.H;
   auto at = [&](int p) { return 4 * (p * 64 * W + lane); };
@@ -141,7 +143,8 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, W == 16 && NV <= 5 ? 8 
 
 template <class YT, class RT, class PT, bool HAS_Y, bool NT>
 hipError_t launch_form(const EdgeFwdArgs& a, bool full, hipStream_t s) {
-  const dim3 rows((unsigned)a.M), rows4((unsigned)((a.M + 3) / 4));
+  const int64_t n = std::min(BLOCK_LAUNCH_ROWS, a.M - a.first_row);
+  const dim3 rows((unsigned)n), rows4((unsigned)((n + 3) / 4));
 #define EDGE_FORM(W, NV, FULL, NT_) \
   return launch_kernel(edge_fwd_kernel<YT, RT, PT, HAS_Y, W, NV, FULL, NT_>, W == 1 ? rows4 : rows, dim3(W == 1 ? 256 : 64 * W), s, a)
   if (a.H > TPMLP_EDGE_MAX_H) return hipErrorInvalidValue;
@@ -172,12 +175,22 @@ hipError_t launch_shape(const EdgeFwdArgs& a, bool full, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_edge_fwd(const EdgeFwdArgs& a, int y_type, int r_type, bool full, hipStream_t s) {
-  if (a.M < 1 || a.M > INT32_MAX || a.H < 4 || (a.gate && a.gate_rows < 1)) return hipErrorInvalidValue;
+namespace {
+hipError_t launch_rows(const EdgeFwdArgs& a, int y_type, int r_type, bool full, hipStream_t s) {
   const bool rb = r_type == TPMLP_BF16;
   if (y_type < 0) return rb ? launch_shape<F32, BF16, false>(a, full, s) : launch_shape<F32, F32, false>(a, full, s);
   if (y_type == TPMLP_BF16) return rb ? launch_shape<BF16, BF16, true>(a, full, s) : launch_shape<BF16, F32, true>(a, full, s);
   return rb ? launch_shape<F32, BF16, true>(a, full, s) : launch_shape<F32, F32, true>(a, full, s);
+}
+}  // namespace
+
+hipError_t launch_edge_fwd(EdgeFwdArgs a, int y_type, int r_type, bool full, hipStream_t s) {
+  if (a.M < 1 || a.H < 8 || (a.gate && a.gate_rows < 1)) return hipErrorInvalidValue;
+  for (a.first_row = 0; a.first_row < a.M; a.first_row += BLOCK_LAUNCH_ROWS) {
+    const hipError_t e = launch_rows(a, y_type, r_type, full, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace tpmlp

@@ -24,6 +24,8 @@
 
 #include "block_dev.h"
 
+#include <algorithm>
+
 namespace tpmlp {
 namespace edge {
 
@@ -86,13 +88,17 @@ struct Out {
   float d, dy;
 };
 template <bool LAYER>
-__device__ __forceinline__ Out row_out(const RowTerms& z, float c, float u, float d, float b, float w, float v) {
+__device__ __forceinline__ Out row_out(const RowTerms& z, float c, float u, float d, float b, float w, float v, bool post) {
   float g = __builtin_fmaf(-c, z.k, u * w);
   if (LAYER) g -= z.m;
   d = __builtin_fmaf(g, z.s, d);
-  float h = __builtin_fmaf(-b, z.ky, d * v);
-  if (LAYER) h -= z.my;
-  return Out{d, h * z.sy};
+  float h = d * v;
+  if (post) {  // uniform; without a norm y has no part in dy, not even an infinite one
+    h = __builtin_fmaf(-b, z.ky, h);
+    if (LAYER) h -= z.my;
+    h *= z.sy;
+  }
+  return Out{d, h};
 }
 
 // Rows whose elements a workgroup holds W waves wide and NV chunks deep.
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, FULL && NV <= 2 ? 4 : 1
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float c = LAYER ? r[e] - mean[0] : r[e], b = LAYER ? y[e] - mean[1] : y[e];
-        const Out o = row_out<LAYER>(z, c, u[e], d0p[e], b, wu[p][e], wv[p][e]);
+        const Out o = row_out<LAYER>(z, c, u[e], d0p[e], b, wu[p][e], wv[p][e], post);
         d[e] = o.d;
         g[e] = o.dy;
         T1[p][e] = __builtin_fmaf(u[e], c * z.s, T1[p][e]);
@@ -289,7 +295,7 @@ __global__ void __launch_bounds__(WIDE_THREADS) edge_wide_sums_kernel(EdgeBwdArg
   __shared__ float slots[(NSUM + 2) * W];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), H = a.H;
   const float inv = 1.0f / (float)H;
-  const int64_t row = blockIdx.x;
+  const int64_t row = a.first_row + blockIdx.x;
   const bool has_dx = a.dx != nullptr, has_dr = a.dr_out != nullptr, post = HAS_Y && a.post != TPMLP_NORM_NONE;
   const bool pre_layer = LAYER && a.pre == TPMLP_NORM_LAYER, post_layer = LAYER && a.post == TPMLP_NORM_LAYER;
   const Row<RT, FULL> r(a.r, row * a.ld_r, has_dx ? H : 0), d(a.dr_out, row * a.ld_dr_out, has_dr ? H : 0);
@@ -355,7 +361,7 @@ __global__ void __launch_bounds__(WIDE_COLS / 4) edge_wide_kernel(EdgeBwdArgs a)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float c = LAYER ? r[e] - t[6] : r[e], b = LAYER ? y[e] - t[7] : y[e];
-      const Out o = row_out<LAYER>(z, c, u[e], d0[e], b, w[e], v[e]);
+      const Out o = row_out<LAYER>(z, c, u[e], d0[e], b, w[e], v[e], post);
       d[e] = o.d;
       g[e] = o.dy;
       T1[e] = __builtin_fmaf(u[e], c * z.s, T1[e]);
@@ -379,9 +385,14 @@ __global__ void __launch_bounds__(WIDE_COLS / 4) edge_wide_kernel(EdgeBwdArgs a)
 template <class YT, class RT, bool HAS_Y, bool LAYER, class DXT, bool FULL>
 hipError_t launch_wide(const EdgeBwdArgs& a, int64_t slices, hipStream_t s) {
   const int64_t blocks = slices * ((a.H + WIDE_COLS - 1) / WIDE_COLS);
-  if (!a.terms || blocks > INT32_MAX) return hipErrorInvalidValue;
-  const hipError_t e = launch_kernel(edge_wide_sums_kernel<YT, RT, HAS_Y, LAYER, DXT, FULL>, dim3((unsigned)a.M), dim3(WIDE_THREADS), s, a);
-  if (e != hipSuccess) return e;
+  if (!a.terms || !block_grid_ok(blocks, WIDE_COLS / 4)) return hipErrorInvalidConfiguration;
+  EdgeBwdArgs b = a;
+  for (b.first_row = 0; b.first_row < a.M; b.first_row += BLOCK_LAUNCH_ROWS) {
+    const int64_t rows = std::min(BLOCK_LAUNCH_ROWS, a.M - b.first_row);
+    const hipError_t e = launch_kernel(edge_wide_sums_kernel<YT, RT, HAS_Y, LAYER, DXT, FULL>, dim3((unsigned)rows),
+                                       dim3(WIDE_THREADS), s, b);
+    if (e != hipSuccess) return e;
+  }
   return launch_kernel(edge_wide_kernel<YT, RT, HAS_Y, LAYER, DXT, FULL>, dim3((unsigned)blocks), dim3(WIDE_COLS / 4), s, a);
 }
 

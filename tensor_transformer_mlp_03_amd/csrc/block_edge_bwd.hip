@@ -3,8 +3,6 @@
 
 #include "block_edge_bwd.h"
 
-#include <algorithm>
-
 namespace tpmlp {
 namespace {
 
@@ -121,7 +119,8 @@ hipError_t launch_edge_bwd_rms(const EdgeBwdArgs& a, int64_t blocks, int y_type,
 
 hipError_t launch_edge_bwd(const EdgeBwdArgs& a, const EdgeBwdPlan& p, int y_type, int r_type, bool full, hipStream_t s) {
   const int64_t blocks = p.groups * p.chunks;
-  if (a.M < 1 || blocks < 1 || blocks > INT32_MAX || a.H < 4) return hipErrorInvalidValue;
+  if (a.M < 1 || a.H < 8) return hipErrorInvalidValue;
+  if (!block_grid_ok(blocks, 1024)) return hipErrorInvalidConfiguration;
   return p.n_acc == EDGE_ACC_LAYER ? launch_edge_bwd_layer(a, blocks, y_type, r_type, full, s)
                                    : launch_edge_bwd_rms(a, blocks, y_type, r_type, full, s);
 }

@@ -413,8 +413,9 @@ int blocks_of(int64_t n, int64_t per) { return (int)((n + per - 1) / per); }
 }  // namespace
 
 int64_t route_sort_blocks(int64_t pairs, int64_t* per_block) {
-  // One workgroup sorts up to 4096 pairs by itself; larger sorts give each 2048.
-  const int64_t per = pairs <= 4096 ? 4096 : 2048;
+  // One workgroup sorts up to 4096 pairs by itself; larger sorts give each 2048, and
+  // more where that would be over 256 of them: each reads all the others' histograms.
+  const int64_t per = pairs <= 4096 ? 4096 : pairs <= 256 * 2048 ? 2048 : (pairs + 255) / 256;
   *per_block = per;
   return pairs <= per ? 1 : (pairs + per - 1) / per;
 }
@@ -439,7 +440,8 @@ hipError_t launch_route_dispatch(RouteDispatchArgs a, bool full, bool nt, hipStr
   a.pad_rows = pad_rows_for(a.rows);
   a.pad_blocks = blocks_of(a.rows, 4 * a.pad_rows);
   const int64_t blocks = ((int64_t)a.pad_blocks + blocks_of(a.T, 4)) * a.segments;
-  if (blocks < 1 || blocks > INT32_MAX) return blocks < 1 ? hipSuccess : hipErrorInvalidValue;
+  if (blocks < 1) return hipSuccess;
+  if (!block_grid_ok(blocks, 256)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks), block(256);
   if (a.H <= 256) {  // 32768 tokens of 64 with 8 choices: 37 us by whole waves
     for (a.lanes = 1; 8 * a.lanes < a.H;) a.lanes *= 2;
@@ -469,7 +471,8 @@ hipError_t launch_combine_bwd(RouteCombineBwdArgs a, bool full, bool nt, hipStre
   a.pad_rows = pad_rows_for(a.rows);
   a.pad_blocks = a.dzs ? blocks_of(a.rows, 4 * a.pad_rows) : 0;
   const int64_t blocks = a.pad_blocks + (W == 1 ? blocks_of(a.T, 4) : a.T);
-  if (blocks < 1 || blocks > INT32_MAX) return blocks < 1 ? hipSuccess : hipErrorInvalidValue;
+  if (blocks < 1) return hipSuccess;
+  if (!block_grid_ok(blocks, 256)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks), block(256);
 #define BWD_FORM(NP)                                                                                            \
   return !full ? launch_kernel(route_combine_bwd_kernel<DT, ZT, W, NP, false, false>, grid, block, s, a)        \

@@ -76,7 +76,8 @@ def test_edge_accepts():
 
 def test_edge_refuses():
     assert L.lib().tpmlp_edge_fwd(None, *[None, 0] * 4, None) == NULL
-    for kw, text in ((dict(M=-1), "M outside"), (dict(H=7), "H outside"), (dict(H=32769), "H outside"),
+    for kw, text in ((dict(M=-1), "M outside"), (dict(M=(1 << 23) + 1), "M outside"),
+                     (dict(M=1 << 23, gate=_p(13), gate_rows=3), "2^21 rows"), (dict(H=7), "H outside"), (dict(H=32769), "H outside"),
                      (dict(post=3), "tpmlp_norm"), (dict(r_type=2), "tpmlp_dtype"), (dict(param_type=-1), "tpmlp_dtype"),
                      (dict(alpha=float("nan")), "alpha"), (dict(eps=-1.0), "eps"), (dict(eps=float("inf")), "eps"),
                      (dict(post=0), "w_post"), (dict(b_post=_p(12)), "b_post"), (dict(b_pre=_p(12)), "b_pre"),
@@ -138,7 +139,7 @@ def test_route_rows():
     assert rows(16, 2, 8, 8, 0) == 32 + 8 * 7
     assert rows(1, 1, 8, 8, 0) == 8 and rows(0, 1, 8, 8, 0) == 0
     assert rows(5, 3, 4, 1, 0) == 15 and rows(5, 3, 4, 8, 24) == 96
-    for bad in ((-1, 1, 8, 8, 0), (4, 0, 8, 8, 0), (4, 65, 8, 8, 0), (4, 1, 0, 8, 0), (4, 1, 513, 8, 0), (4, 1, 8, 0, 0),
+    for bad in (((1 << 23) + 1, 1, 8, 8, 0), (-1, 1, 8, 8, 0), (4, 0, 8, 8, 0), (4, 65, 8, 8, 0), (4, 1, 0, 8, 0), (4, 1, 513, 8, 0), (4, 1, 8, 0, 0),
                 (4, 1, 8, 8, 12), (4, 1, 8, 8, -8), (1 << 31, 1, 8, 8, 0), (1 << 30, 2, 8, 8, 0),
                 (4, 1, 512, 8, 1 << 23)):
         assert rows(*bad) == -1, bad
@@ -228,7 +229,12 @@ def test_clip_arguments():
         assert _clip(**kw)[0] == SHAPE, kw
     assert _clip(ptrs=(None, _p(1)))[0] == NULL and _clip(outs=(None, _p(1)))[0] == NULL and _clip(ws=None)[0] == NULL
     assert _clip(ptrs=(_p(0, 2), _p(1)))[0] == ALIGN and _clip(norm=_p(2, 1))[0] == ALIGN and _clip(ws=_p(3, 8))[0] == ALIGN
-    assert _clip(outs=(_p(0, 4), _p(5)))[0] == ALIAS
+    for kw in (dict(outs=(_p(0, 4), _p(5))), dict(outs=(_p(1), _p(5))), dict(outs=(_p(5), _p(5, 64))),
+               dict(outs=(_p(1, 4), _p(0))), dict(outs=(_p(5), _p(0, 398))), dict(ptrs=(_p(0), _p(0))), dict(ptrs=(_p(0), _p(0, 396))),
+               dict(ptrs=(_p(0, 4), _p(0)))):
+        assert _clip(**kw)[0] == ALIAS, kw
+    assert _clip(ptrs=(_p(0), _p(0)), outs=(_p(4), _p(5)))[0] in PASSED    # read twice, written apart
+    assert _clip(ptrs=(_p(0), _p(0, 400)))[0] in PASSED                    # slices of one buffer
     g, _, s, t, n = _arrays((_p(0), _p(1)), None, (100, 7), (0, 1))
     need = L.lib().tpmlp_grad_workspace_bytes(s, n)
     assert _clip(n_ws=need)[0] in PASSED and _clip(n_ws=need - 1)[0] == WS
@@ -239,6 +245,26 @@ def test_clip_arguments():
     assert lib.tpmlp_grad_clip(g, None, s, t, -1, _p(4), 1.0, 1.0, None, None) == SHAPE
     assert lib.tpmlp_grad_clip(None, None, s, t, n, _p(4), 1.0, 1.0, None, None) == NULL
     assert lib.tpmlp_clip_grad_norm(None, None, None, None, 0, 1.0, 1.0, _p(2), _p(3), 1 << 20, None) in PASSED
+
+
+def test_clip_overlaps_against_every_pair():
+    """The merged walk over the addresses refuses exactly what comparing every pair refuses."""
+    import random
+    rng = random.Random(0)
+    for _ in range(4000):
+        n = rng.randint(1, 4)
+        sizes = [rng.randint(0, 5) for _ in range(n)]
+        at = lambda: _p(0, 4 * rng.randint(0, 24))  # noqa: E731
+        grads = [at() for _ in range(n)]
+        outs = [g if rng.random() < 0.4 else at() for g in grads]
+
+        def meet(a, i, b, j):
+            return sizes[i] and sizes[j] and a[i] < b[j] + 4 * sizes[j] and b[j] < a[i] + 4 * sizes[i]
+
+        want = any(meet(outs, i, outs, j) for i in range(n) for j in range(i)) or \
+            any(meet(outs, i, grads, j) and not (i == j and outs[i] == grads[i]) for i in range(n) for j in range(n))
+        st = _clip(ptrs=grads, outs=outs, sizes=sizes, types=[0] * n)[0]
+        assert (st == ALIAS) == bool(want), (grads, outs, sizes, st)
 
 
 def test_python_checks():

@@ -241,6 +241,40 @@ def test_edge_bad_rows_stay_alone():
         assert bool(torch.isfinite(x2[5]).all()) and bool(torch.isnan(x2[1]).all())
 
 
+def test_edge_infinite_y_without_a_norm():
+    """dy = gate * d has no part of y where no norm follows the block."""
+    for H in (64, 1000, 20480, 20001):
+        c, params, t = edge_case(5, 3, H, "none", "rms", F32, F32, F32, 3)
+        e = make_edge(c, params, H, 3)
+        y = t["y"].cuda()
+        ro, x = torch.empty(3, H, device="cuda"), torch.empty(3, H, dtype=BF16, device="cuda")
+        e.forward(y, t["r"].cuda(), ro, x)
+        outs = []
+        for bad in (False, True):
+            if bad:
+                y[1, 5], y[2, 6] = float("inf"), float("nan")
+            dr, dy = torch.empty_like(ro), torch.empty_like(x)
+            e.backward(y, ro, t["dr"].cuda(), t["dx"].cuda(), dr, dy)
+            outs.append((dr, dy))
+        assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1]), H
+
+
+def test_edge_more_rows_than_one_launch():
+    """2^21 rows go into one launch."""
+    M, H = (1 << 21) + 3, 8
+    c, params, _ = edge_case(5, 1, H, "rms", "rms", BF16, BF16, F32, 0)
+    e = make_edge(c, params, H, 0)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    y, r = (torch.randn(M, H, generator=gen, device="cuda").to(BF16) for _ in range(2))
+    ro, x = torch.empty_like(r), torch.empty_like(r)
+    e.forward(y, r, ro, x)
+    part_r, part_x = torch.empty(5, H, dtype=BF16, device="cuda"), torch.empty(5, H, dtype=BF16, device="cuda")
+    for at in (0, (1 << 21) - 2):
+        e.forward(y[at:at + 5], r[at:at + 5], part_r, part_x)
+        assert torch.equal(ro[at:at + 5], part_r) and torch.equal(x[at:at + 5], part_x)
+    assert bool(torch.isfinite(x).all())
+
+
 def test_edge_large_values():
     """A LayerNorm of values far from zero keeps its variance."""
     H = 1000
@@ -334,6 +368,25 @@ def test_route_sort(T, K, E):
     check_sort(route_ids(T + E, T, K, E), E, 1, 0, torch.int64)
     cap = -(-T * K // (2 * E)) // 8 * 8 + 8
     check_sort(route_ids(T + E, T, K, E, 0.1), E, 8, cap, torch.int64)
+
+
+def test_route_sort_many_pairs():
+    """More pairs than 256 workgroups of 2048: every expert's rows hold its pairs, in their order."""
+    from tensor_transformer_mlp_03_amd.block import Route
+    T, K, E = 300007, 2, 60
+    ids = route_ids(4, T, K, E, 0.1).cuda()
+    h = Route(T, K, E)
+    h.sort(ids)
+    flat = ids.reshape(-1)
+    on = flat >= 0
+    assert torch.equal(h.counts.long(), torch.bincount(flat[on], minlength=E))
+    rows = h.row_of.reshape(-1).long()
+    assert bool(((rows >= 0) == on).all())
+    pairs = torch.arange(T * K, device="cuda")
+    assert torch.equal(h.src_of.long()[rows[on]], pairs[on])
+    assert int((h.src_of >= 0).sum()) == int(on.sum())
+    order = torch.sort(torch.where(on, flat, E), stable=True).indices[:int(on.sum())]
+    assert torch.equal(h.src_of[h.src_of >= 0].long(), order)
 
 
 def test_route_sort_one_sided():
