@@ -10,6 +10,12 @@
 // Every workgroup writes its own partial sum and the partials are added in their
 // order, so the norm does not depend on timing.  A norm that is not finite leaves
 // the gradients as they are (times scale): the caller sees it and skips the step.
+//
+// Bound by bandwidth: 420M float32 summed in 250 us (6.7 TB/s) and scaled into other
+// buffers in 565 us (5.9 TB/s).  The summing pass marks its loads as non-temporal except
+// for the last 256 MB, which the scaling pass begins with (857 us without the first,
+// 861 without the second, 823 with both); 4096 to 16384 scaling workgroups are alike,
+// 2048 are 2% slower.  60 small tensors: 4.1 + 4.6 us, latency.
 
 #include "block_dev.h"
 

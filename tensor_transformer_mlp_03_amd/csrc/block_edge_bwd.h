@@ -18,6 +18,11 @@
 // finishing kernel adds the slices in their order.  No atomics: the results do
 // not depend on timing.
 //
+// Bound by bandwidth where there are many rows: 32768 x 3584 in float32 478 us with the
+// finish, 5.4 TB/s (a plain kernel of four reads and two writes reaches 5.25); 8192 x
+// 4096 with LayerNorms 145 us, 5.1 TB/s.  With few rows by latency: 1001 x 1000 with 13
+// gate rows 11 + 6 us for 20 MB.
+//
 // Instantiated by the two .hip files that include this (RMSNorm only, and with a
 // LayerNorm on either side, which needs twice the column sums).
 #pragma once
@@ -285,7 +290,9 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, FULL && NV <= 2 ? 4 : 1
 // the registers of one workgroup, so the two sweeps are two kernels.  The first
 // makes a row's sums and keeps the six or eight numbers that come of them; the
 // second, a thread to four columns, walks the rows of its chunk with them.  It reads
-// the inputs once more, but neither kernel waits for anything but memory.
+// the inputs once more, but neither kernel waits for anything but memory.  2048 x 20480:
+// 277 us; the one-kernel form took 338 with its spills, 410 with the next row in flight
+// and more of them, and 1060 us for 2048 x 20001.
 // ---------------------------------------------------------------------------
 constexpr int WIDE_THREADS = 1024, WIDE_COLS = 1024;  // columns of one workgroup of the second kernel
 
