@@ -12,11 +12,14 @@
 
 namespace tpmlp {
 
-// Launches that read and write more than this (the Infinity Cache's 256 MB) mark
-// their rows' accesses as non-temporal: nothing of them would be found in a cache
-// again.  Measured on the edge: 2048 x 20480 forward (420 MB) 94 -> 76 us, 32768 x
-// 3584 backward (2.6 GB) 488 -> 467 us; but 4096 x 1024 forward (59 MB) 10.2 -> 11.1 us.
-constexpr int64_t BLOCK_NT_BYTES = int64_t(256) << 20;
+// Launches that read and write more than this mark their rows' accesses as
+// non-temporal: half of the Infinity Cache's 256 MB, since what stands before and after
+// a call wants room there too.  Above it nothing is lost: 2048 x 20480 edge forward
+// (420 MB) 94 -> 76 us, 32768 x 3584 backward (2.6 GB) 488 -> 467, 2048 x 4096 backward
+// of float32 (160 MB) 48.8 -> 42.9, and 32768 x 512 forward (235 MB) between a kernel that
+// writes y and one that reads x 70.4 -> 67.8 for the three.  Below it those lose: 8192 x
+// 1024 forward (117 MB) 35.4 -> 37.7 for the three, 4096 x 1024 (59 MB) 10.3 -> 11.3.
+constexpr int64_t BLOCK_NT_BYTES = int64_t(128) << 20;
 
 // A launch holds fewer than 2^32 threads along a dimension: rows of one launch of up
 // to 1024 threads a row, and whether a grid stays below.

@@ -140,7 +140,7 @@ bool all_quads(int64_t H, const Mat (&outs)[NO], const Mat (&ins)[NI]) {
   return H % 4 == 0 && std::all_of(outs, outs + NO, quads) && std::all_of(ins, ins + NI, quads);
 }
 
-// Whether a launch over these matrices moves more than the caches hold.
+// Whether a launch over these matrices moves more than BLOCK_NT_BYTES.
 template <size_t NO, size_t NI>
 bool past_caches(const Mat (&outs)[NO], const Mat (&ins)[NI]) {
   int64_t bytes = 0;

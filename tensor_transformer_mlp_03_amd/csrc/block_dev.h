@@ -53,10 +53,6 @@ __device__ __forceinline__ f32x4 from4(f32x4 v, int i, int n) {
   }
   return v;
 }
-template <class T>
-__device__ __forceinline__ f32x4 load4(const typename T::elem* row, int i, int n) {
-  return from4(widen(*reinterpret_cast<const typename T::vec*>(row + min(i, n - 4))), i, n);
-}
 
 // Stores elements i .. i+3 of a row of n elements, those inside it.
 template <class T>
@@ -76,7 +72,7 @@ __device__ __forceinline__ void store4(typename T::elem* row, int i, int n, f32x
 // a branch or an address select, and the address is one 32-bit offset a lane.  The
 // row's pointer has to be uniform over the wave.  Other rows take from4 and store4.
 // A row of length 0 reads zeros and touches no memory.  NT marks FULL rows' accesses
-// as non-temporal, for launches that move more than the caches hold (BLOCK_NT_BYTES).
+// as non-temporal, for launches that move more than BLOCK_NT_BYTES.
 template <class T, bool FULL, bool NT = false>
 struct Row;
 
