@@ -507,7 +507,11 @@ def _rows(t, shape, name, kind=None):
     row, col = t.stride()
     if col != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous columns")
-    return t.data_ptr(), (row if shape[0] > 1 else 0)
+    if shape[0] < 2:
+        return t.data_ptr(), 0
+    if row < shape[1]:  # 0 too, a broadcast: the library takes it as dense rows
+        raise ValueError(f"the rows of {name} overlap (stride {row})")
+    return t.data_ptr(), row
 
 
 def _flat(t, n, dtype, name):

@@ -299,3 +299,29 @@ def test_python_checks():
         L.GradTable([torch.zeros(4, 4).t()])
     with pytest.raises(TypeError, match="float32 or hold"):
         L.GradTable([torch.zeros(4, dtype=torch.float64)])
+
+
+def test_rows_that_share_memory():
+    """A broadcast tensor's rows lie on one another: its stride of 0 is not the 0 that stands for dense rows."""
+    torch = pytest.importorskip("torch")
+    bf = torch.bfloat16
+    d = L.edge_desc(16, pre="rms", w_pre=torch.ones(16))
+    r, x = torch.zeros(4, 16), torch.zeros(4, 16, dtype=bf)
+    wide, none = torch.zeros(1, 16).expand(4, 16), torch.zeros(0, 16)
+    with pytest.raises(ValueError, match="rows of r .*stride"):
+        L.tpmlp_edge_fwd(d, None, wide, None, x, stream=0)
+    with pytest.raises(ValueError, match="rows of dr_out .*stride"):
+        L.tpmlp_edge_bwd(d, None, r, wide, x, r.clone(), None, stream=0)
+    with pytest.raises(ValueError, match="rows of dx .*stride"):
+        L.tpmlp_edge_bwd(d, None, r, None, wide, r.clone(), None, stream=0)
+    with pytest.raises(ValueError, match="rows of gate .*stride"):
+        L.edge_desc(16, gate=wide, gate_rows=2)
+    with pytest.raises(ValueError, match="rows of y .*stride"):
+        L.tpmlp_edge_fwd(d, torch.zeros(40).as_strided((4, 16), (8, 1)), r, None, x, stream=0)
+    idx = torch.zeros(4, 2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="rows of X .*stride"):
+        L.tpmlp_route_dispatch(wide.to(bf)[:1].expand(4, 16), idx, torch.zeros(8, dtype=torch.int32), torch.zeros(8, 16, dtype=bf),
+                               stream=0)
+    with pytest.raises(ValueError, match="rows of dY .*stride"):
+        L.tpmlp_route_combine_bwd(wide, torch.zeros(8, 16), idx, None, None, None, torch.zeros(4, 2), stream=0)
+    assert L._rows(none, (0, 16), "r")[1] == 0 and L._rows(wide[:1], (1, 16), "r")[1] == 0  # no second row: any stride
