@@ -48,6 +48,7 @@ class EdgeDesc(ctypes.Structure):
                 ("y_type", ctypes.c_int32), ("r_type", ctypes.c_int32), ("param_type", ctypes.c_int32),
                 ("alpha", ctypes.c_float), ("eps", ctypes.c_float), ("w_post", _vp), ("b_post", _vp),
                 ("w_pre", _vp), ("b_pre", _vp), ("gate", _vp), ("gate_rows", _i64), ("ld_gate", _i64)]
+    gate_tokens = None  # how many tokens the gate's rows are enough for, where it is known
 
 
 _EP = ctypes.POINTER(EdgeDesc)
@@ -532,7 +533,8 @@ def _ws(ws):
 def edge_desc(H: int, post="none", pre="none", w_post=None, b_post=None, w_pre=None, b_pre=None, gate=None,
               gate_rows: int = 0, alpha: float = 1.0, eps: float = 1e-5) -> EdgeDesc:
     """A tpmlp_edge with its parameters (all float32 or all bf16; the gate [G, H], or [H] for
-    one row); M, y_type and r_type are set by each call.  gate_rows 0: one row for all tokens."""
+    one row); M, y_type and r_type are set by each call.  gate_rows 0: one row for all tokens.
+    Holds the parameters' addresses: they have to stay alive and where they are."""
     params = [(n, t) for n, t in (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre),
                                   ("gate", gate)) if t is not None]
     kinds = {_dtype(t, n) for n, t in params}
@@ -543,13 +545,21 @@ def edge_desc(H: int, post="none", pre="none", w_post=None, b_post=None, w_pre=N
             _flat(t, H, t.dtype, n)
     d = EdgeDesc(M=0, H=H, post=NORMS[post], pre=NORMS[pre], param_type=kinds.pop() if kinds else F32, alpha=alpha,
                  eps=eps, w_post=_ptr(w_post), b_post=_ptr(b_post), w_pre=_ptr(w_pre), b_pre=_ptr(b_pre))
+    if gate_rows < 0:
+        raise ValueError("gate_rows must not be negative")
     if gate is not None:
         g = gate if gate.dim() == 2 else gate.unsqueeze(0)
         d.gate, d.ld_gate = _rows(g, (g.shape[0], H), "gate")
-        d.gate_rows = gate_rows if gate_rows > 0 else (1 << 31) - 1
-    elif gate_rows < 0:
-        raise ValueError("gate_rows must not be negative")
+        if gate_rows == 0 and g.shape[0] != 1:
+            raise ValueError(f"a gate of {g.shape[0]} rows needs gate_rows")
+        d.gate_rows = gate_rows or (1 << 31) - 1
+        d.gate_tokens = g.shape[0] * d.gate_rows
     return d
+
+
+def _check_gate(d: EdgeDesc, M: int) -> None:
+    if d.gate_tokens is not None and M > d.gate_tokens:
+        raise ValueError(f"gate has {d.gate_tokens // d.gate_rows} rows for {d.gate_rows} tokens each, the call has {M} tokens")
 
 
 def _gate_groups(d: EdgeDesc, M: int) -> int:
@@ -560,6 +570,7 @@ def tpmlp_edge_fwd(d: EdgeDesc, y, r, r_out, x, stream=None):
     """r_out = alpha r + gate * N_post(y), x = N_pre(r_out); y None: no block before the edge."""
     M, H = r.shape[0], d.H
     d.M, d.r_type = M, _dtype(r, "r")
+    _check_gate(d, M)
     pr, lr = _rows(r, (M, H), "r")
     py = ly = None
     if y is not None:
@@ -583,6 +594,7 @@ def tpmlp_edge_bwd(d: EdgeDesc, y, r_out, dr_out, dx, dr, dy, dw_post=None, db_p
     import torch
     M, H = dr.shape[0], d.H
     d.M, d.r_type = M, _dtype(dr, "dr")
+    _check_gate(d, M)
     pr, lr = _rows(r_out, (M, H), "r_out", d.r_type)
     po, lo = _rows(dr_out, (M, H), "dr_out", d.r_type)
     px, lx = _rows(dx, (M, H), "dx")

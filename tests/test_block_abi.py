@@ -325,3 +325,31 @@ def test_rows_that_share_memory():
     with pytest.raises(ValueError, match="rows of dY .*stride"):
         L.tpmlp_route_combine_bwd(wide, torch.zeros(8, 16), idx, None, None, None, torch.zeros(4, 2), stream=0)
     assert L._rows(none, (0, 16), "r")[1] == 0 and L._rows(wide[:1], (1, 16), "r")[1] == 0  # no second row: any stride
+
+
+def test_gate_rows_for_every_token():
+    """A gate's rows times gate_rows cover the call's tokens, in both directions; and rows beyond the
+    one that stands for all tokens need a gate_rows."""
+    torch = pytest.importorskip("torch")
+    bf = torch.bfloat16
+    gate = torch.ones(3, 16)
+    for M, rows in ((13, 4), (4, 1), (7, 2)):
+        d = L.edge_desc(16, gate=gate, gate_rows=rows)
+        y, r = torch.zeros(M, 16), torch.zeros(M, 16)
+        with pytest.raises(ValueError, match="gate has 3 rows"):
+            L.tpmlp_edge_fwd(d, y, r, r, None, stream=0)
+        with pytest.raises(ValueError, match="gate has 3 rows"):
+            L.tpmlp_edge_bwd(d, y, None, r, None, r, torch.zeros(M, 16, dtype=bf), stream=0)
+        y, r = y[:3 * rows], r[:3 * rows]  # as many as it covers
+        with pytest.raises(L.TpmlpError, match="HIP|UNSUPPORTED"):  # every check passed
+            L.tpmlp_edge_fwd(d, y, r, r, None, stream=0)
+    d = L.edge_desc(16, gate=gate[0], gate_rows=2)
+    with pytest.raises(ValueError, match="gate has 1 rows"):
+        L.tpmlp_edge_fwd(d, torch.zeros(3, 16), torch.zeros(3, 16), torch.zeros(3, 16), None, stream=0)
+    d = L.edge_desc(16, gate=gate[0])  # one row for all
+    with pytest.raises(L.TpmlpError, match="HIP|UNSUPPORTED"):
+        L.tpmlp_edge_fwd(d, torch.zeros(30, 16), torch.zeros(30, 16), torch.zeros(30, 16), None, stream=0)
+    with pytest.raises(ValueError, match="gate_rows"):
+        L.edge_desc(16, gate=gate)
+    with pytest.raises(ValueError, match="gate_rows"):
+        L.edge_desc(16, gate=gate, gate_rows=-1)
