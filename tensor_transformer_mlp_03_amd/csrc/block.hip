@@ -539,6 +539,35 @@ tpmlp_status check_grad_overlaps(const void* const* grads, void* const* outs, co
   return TPMLP_OK;
 }
 
+// A buffer of the call beside the tensors (p NULL: absent).
+struct Own {
+  const void* p;
+  size_t bytes;
+  bool written;
+  const char* name;
+};
+
+bool meet(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
+// The two are disjoint from each other if one is written, each from the outputs of a call
+// that scales, and from the gradients if it is written.
+tpmlp_status check_own(const void* const* grads, void* const* outs, bool scales, const int64_t* sizes, const int32_t* types,
+                       int n, const Own (&own)[2]) {
+  if ((own[0].written || own[1].written) && meet(own[0].p, own[0].bytes, own[1].p, own[1].bytes))
+    return fail(TPMLP_ERR_ALIAS, std::string(own[0].name) + " overlaps " + own[1].name);
+  for (int t = 0; t < n; ++t) {
+    const size_t bytes = size_t(sizes[t]) * size_of(types[t]);
+    const void* o = outs ? outs[t] : grads[t];
+    for (const Own& b : own)
+      if (bytes && ((b.written && meet(b.p, b.bytes, grads[t], bytes)) || (scales && meet(b.p, b.bytes, o, bytes))))
+        return fail(TPMLP_ERR_ALIAS, std::string(b.name) + " overlaps gradient " + std::to_string(t) + " or its output");
+  }
+  return TPMLP_OK;
+}
+
 void fill_clip(ClipArgs& a, const void* const* grads, void* const* outs, const int64_t* sizes, const int32_t* types, int t0,
                int t1) {
   uint32_t chunk = 0;
@@ -679,6 +708,8 @@ tpmlp_status tpmlp_grad_sumsq(const void* const* grads, const int64_t* sizes, co
     if (!sumsq) return fail(TPMLP_ERR_NULL, "sumsq is NULL");
     if (reinterpret_cast<uintptr_t>(sumsq) & 7) return fail(TPMLP_ERR_ALIGN, "sumsq is not aligned to its elements");
     TRY(check_ws(sizes, n, ws, ws_bytes));
+    TRY(check_own(grads, nullptr, false, sizes, types, n,
+                  {{sumsq, sizeof(double), true, "sumsq"}, {ws, tpmlp_grad_workspace_bytes(sizes, n), true, "ws"}}));
     TRY(check_device());
     hipStream_t s = stream_of(stream);
     int count = 0;
@@ -695,6 +726,8 @@ tpmlp_status tpmlp_grad_clip(const void* const* grads, void* const* outs, const 
     if (!sumsq) return fail(TPMLP_ERR_NULL, "sumsq is NULL");
     if (reinterpret_cast<uintptr_t>(sumsq) & 7) return fail(TPMLP_ERR_ALIGN, "sumsq is not aligned to its elements");
     TRY(check_factors(scale, max_norm, norm));
+    TRY(check_own(grads, outs, true, sizes, types, n,
+                  {{norm, sizeof(float), true, "norm"}, {sumsq, sizeof(double), false, "sumsq"}}));
     TRY(check_device());
     return enqueue_scale(grads, outs, sizes, types, n, sumsq, 1, scale, max_norm, norm, stream_of(stream));
   });
@@ -707,6 +740,8 @@ tpmlp_status tpmlp_clip_grad_norm(const void* const* grads, void* const* outs, c
     TRY(check_grad_overlaps(grads, outs, sizes, types, n));
     TRY(check_factors(scale, max_norm, norm));
     TRY(check_ws(sizes, n, ws, ws_bytes));
+    TRY(check_own(grads, outs, true, sizes, types, n,
+                  {{norm, sizeof(float), true, "norm"}, {ws, tpmlp_grad_workspace_bytes(sizes, n), true, "ws"}}));
     TRY(check_device());
     hipStream_t s = stream_of(stream);
     double* part = static_cast<double*>(ws);

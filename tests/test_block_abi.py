@@ -353,3 +353,28 @@ def test_gate_rows_for_every_token():
         L.edge_desc(16, gate=gate)
     with pytest.raises(ValueError, match="gate_rows"):
         L.edge_desc(16, gate=gate, gate_rows=-1)
+
+
+def test_clip_own_buffers_apart():
+    """norm, sumsq and the workspace are disjoint from the gradients, the outputs and one another."""
+    lib = L.lib()
+    norm, ws = _p(2), _p(3)
+    need = lib.tpmlp_grad_workspace_bytes(_arrays((0, 0), None, (100, 7), (0, 1))[2], 2)
+    apart = dict(outs=(_p(4), _p(5)), norm=norm, ws=ws, n_ws=need)
+    assert _clip(**apart)[0] in PASSED
+    for kw in (dict(norm=_p(0, 396)), dict(norm=_p(1)), dict(norm=_p(4)), dict(norm=_p(5, 12)), dict(norm=ws), dict(norm=_p(3, need - 4)),
+               dict(ws=_p(0, 384)), dict(ws=_p(1)), dict(ws=_p(4, 16)), dict(ws=_p(5)), dict(ws=norm)):
+        st, text = _clip(**{**apart, **kw})
+        assert st == ALIAS and "overlaps" in text, (kw, st, text)
+    for kw in (dict(norm=_p(0, 400)), dict(norm=_p(4, -4)), dict(norm=_p(3, need)), dict(ws=_p(0, 400)), dict(n_ws=1 << 40),
+               dict(norm=None)):
+        assert _clip(**{**apart, **kw})[0] in PASSED, kw
+    g, o, s, t, n = _arrays((_p(0), _p(1)), (_p(4), _p(5)), (100, 7), (0, 1))
+    for sumsq, w in ((_p(0, 392), ws), (_p(1, 8), ws), (_p(3, 0), ws), (_p(6), _p(0)), (_p(3, need - 8), ws)):
+        assert lib.tpmlp_grad_sumsq(g, s, t, n, sumsq, w, need, None) == ALIAS, (hex(sumsq), hex(w))
+    assert lib.tpmlp_grad_sumsq(g, s, t, n, _p(3, need), ws, need, None) in PASSED
+    for sumsq, nm in ((_p(6), _p(6)), (_p(6), _p(6, 4)), (_p(4, 8), norm), (_p(5, 8), None), (_p(6), _p(0)), (_p(6), _p(5))):
+        assert lib.tpmlp_grad_clip(g, o, s, t, n, sumsq, 1.0, 1.0, nm, None) == ALIAS, (hex(sumsq), nm)
+    assert lib.tpmlp_grad_clip(g, o, s, t, n, _p(6), 1.0, 1.0, _p(6, 8), None) in PASSED
+    assert lib.tpmlp_grad_clip(g, o, s, t, n, _p(0), 1.0, 1.0, norm, None) in PASSED  # only read, as the gradient is
+    assert lib.tpmlp_grad_clip(g, None, s, t, n, _p(0), 1.0, 1.0, norm, None) == ALIAS
