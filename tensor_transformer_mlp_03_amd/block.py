@@ -12,6 +12,11 @@ from __future__ import annotations
 from . import _lib as L
 
 
+def _capturing():
+    import torch
+    return torch.cuda.is_current_stream_capturing()
+
+
 class Edge:
     """The edge between two blocks:  r' = alpha r + gate * N_post(y),  x = N_pre(r').
 
@@ -27,6 +32,7 @@ class Edge:
                                          ("gate", gate)) if t is not None}
         self.desc = L.edge_desc(H, post, pre, w_post, b_post, w_pre, b_pre, gate, gate_rows, alpha, eps)
         self.grads, self._grad_args, self._ws, self._M = {}, {}, None, -1
+        self._captured = []  # buffers that graphs write to, which another M replaces
 
     def forward(self, y, r, r_out, x, stream=None):
         """y [M,H] float32 or bf16 (None: no block before); r, r_out [M,H] (r_out may be r);
@@ -36,10 +42,13 @@ class Edge:
     def backward(self, y, r_out, dr_out, dx, dr, dy, stream=None):
         """Gradients from r_out as the forward wrote it, dr_out (None: zeros) and dx [M,H]
         float32 or bf16.  Writes dr (may be dr_out) and dy (bf16) and returns the parameters'
-        float32 gradients by name, which the next backward overwrites."""
+        float32 gradients by name, which the next backward overwrites.  What a backward that
+        is captured into a graph writes to stays allocated as long as this object does."""
         M = dr.shape[0]
         if M != self._M:
             self._place(M, dr.device)
+        if _capturing():
+            self._captured.append((self._ws, *self.grads.values()))
         L.tpmlp_edge_bwd(self.desc, y, r_out, dr_out, dx, dr, dy, ws=self._ws, stream=stream, **self._grad_args)
         return self.grads
 
@@ -47,6 +56,7 @@ class Edge:
         import torch
         d = self.desc
         f32 = dict(dtype=torch.float32, device=device)
+        self.grads = dict(self.grads)  # the last one's holder keeps its tensors
         for k in self.params:
             shape = (-(-M // d.gate_rows), d.H) if k == "gate" else (d.H,)
             if k not in self.grads or self.grads[k].shape != shape:

@@ -378,3 +378,26 @@ def test_clip_own_buffers_apart():
     assert lib.tpmlp_grad_clip(g, o, s, t, n, _p(6), 1.0, 1.0, _p(6, 8), None) in PASSED
     assert lib.tpmlp_grad_clip(g, o, s, t, n, _p(0), 1.0, 1.0, norm, None) in PASSED  # only read, as the gradient is
     assert lib.tpmlp_grad_clip(g, None, s, t, n, _p(0), 1.0, 1.0, norm, None) == ALIAS
+
+
+def test_edge_keeps_what_a_graph_writes_to(monkeypatch):
+    """Another M replaces the gate's gradient and the workspace; those that a captured backward
+    writes to stay allocated, others do not."""
+    torch = pytest.importorskip("torch")
+    import weakref
+    from tensor_transformer_mlp_03_amd import block
+    bf, used = torch.bfloat16, []
+    monkeypatch.setattr(L, "tpmlp_edge_bwd", lambda d, *a, **k: used.append([weakref.ref(t) for t in (k["ws"], k["dgate"])]))
+    for capturing in (False, True):
+        monkeypatch.setattr(block, "_capturing", lambda: capturing, raising=False)
+        edge = block.Edge(16, post="rms", w_post=torch.ones(16), gate=torch.ones(500, 16), gate_rows=2)
+        for M in (8, 1000, 6):
+            r = torch.zeros(M, 16)
+            g = edge.backward(r, None, r, None, r, torch.zeros(M, 16, dtype=bf))
+            first = g if M == 8 else first
+        assert first["gate"].shape == (4, 16) and g["gate"].shape == (3, 16)  # a caller's dict stays that call's
+        del first, g
+        alive = [[t() is not None for t in refs] for refs in used]
+        used.clear()
+        # The largest workspace and the last gradient are the object's own.
+        assert alive == ([[True, True]] * 3 if capturing else [[False, False], [True, False], [True, True]]), (capturing, alive)

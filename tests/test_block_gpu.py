@@ -681,3 +681,32 @@ def test_the_same_bits_twice():
         norm = GradClip([v.clone() for v in g.values()]).clip(1e-3)
         runs.append([dr, dy, norm.clone(), *(v.clone() for v in g.values())])
     assert all(torch.equal(a, b) for other in runs[1:] for a, b in zip(runs[0], other))
+
+
+def test_graph_of_a_backward_outlives_other_sizes():
+    """A captured backward's gradients and workspace stay its own while the object runs other sizes."""
+    H, rows = 512, 4
+    c, params, t = edge_case(6, 2000, H, "rms", "layer", F32, F32, BF16, rows)
+    e = make_edge(c, params, H, rows)
+    y, r, d, dx = (t[k].cuda() for k in ("y", "r", "dr", "dx"))
+
+    def backward(M):
+        dr, dy = torch.empty(M, H, device="cuda"), torch.empty(M, H, device="cuda", dtype=BF16)
+        return e.backward(y[:M], r[:M], d[:M], dx[:M], dr, dy), dr, dy
+
+    want = {k: v.clone() for k, v in backward(40)[0].items()}
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got, dr, dy = backward(40)
+    torch.cuda.current_stream().wait_stream(side)
+    for M in (2000, 3, 801):
+        other = {k: v.clone() for k, v in backward(M)[0].items()}
+        junk = [torch.full((n,), 7.0, device="cuda") for n in (10 * H, 500 * H, 1 << 22)]  # takes what was freed
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(got[k], want[k]) for k in want), M
+        assert all(bool((j == 7.0).all()) for j in junk), M
+        assert all(torch.equal(v, other[k]) for k, v in backward(M)[0].items()), M
