@@ -18,9 +18,11 @@
 // The moves are bound by bandwidth: 32768 x 3584 to four experts each 234 us, 5.05 TB/s,
 // four fifths of it scattered row writes; the gradient of 2048 x 4096 to eight each
 // 90 us for 436 MB, and its way back (combine without weights) 55 us, 5.5 TB/s.  The sort
-// is bound by latency: 16 pairs 3.7 us, 131072 pairs 5.0 + 8.5 us.
+// is bound by latency: 16 pairs 3.7 us, 131072 pairs 5.0 + 7.6 us.
 
 #include "block_dev.h"
+
+#include <algorithm>
 
 namespace tpmlp {
 namespace {
@@ -28,7 +30,7 @@ namespace {
 // ---------------------------------------------------------------------------
 // Sort
 // ---------------------------------------------------------------------------
-constexpr int SORT_THREADS = 1024, SORT_WAVES = SORT_THREADS / 64;
+constexpr int SORT_THREADS = 1024, SORT_WAVES = SORT_THREADS / 64, SORT_MOST_BLOCKS = 256;
 
 // The pair's expert, or -1 where its id names none.
 __device__ __forceinline__ int expert_of(const RouteSortArgs& a, int64_t p) {
@@ -71,6 +73,9 @@ __device__ __forceinline__ uint64_t same_lanes(int v, int bits) {
 // earlier workgroups, plus those of earlier waves), and the waves walk their runs
 // 64 pairs at a time, a pair's place among equal experts of the 64 given by the
 // lanes before it.  With one workgroup (ONE) there is no histogram to read.
+// Workgroups past a.blocks place nothing: they share the marking of padding rows, of
+// which a capacity can give many times the pairs, and so make the segments themselves,
+// with ONE from a count of all pairs.
 template <bool ONE>
 __global__ void __launch_bounds__(SORT_THREADS) route_place_kernel(RouteSortArgs a) {
   __shared__ int lds[(SORT_WAVES + 4) * TPMLP_ROUTE_MAX_EXPERTS + 1 + SORT_WAVES];
@@ -82,7 +87,7 @@ __global__ void __launch_bounds__(SORT_THREADS) route_place_kernel(RouteSortArgs
   int* sums = scan + SORT_WAVES;          // [2][E] pairs in all and in earlier workgroups
   for (int e = tid; e < SORT_WAVES * E; e += SORT_THREADS) next[e] = 0;
   __syncthreads();
-  const int64_t p0 = (int64_t)blockIdx.x * a.per_block, p1 = min(p0 + a.per_block, a.pairs);
+  const int64_t p0 = ONE ? 0 : min((int64_t)blockIdx.x * a.per_block, a.pairs), p1 = min(p0 + a.per_block, a.pairs);
   const int64_t run = ((p1 - p0 + SORT_WAVES - 1) / SORT_WAVES + 63) / 64 * 64;
   const int64_t w0 = min(p0 + wave * run, p1), w1 = min(w0 + run, p1);
   for (int64_t p = w0 + lane; p < w1; p += 64) {
@@ -123,7 +128,7 @@ __global__ void __launch_bounds__(SORT_THREADS) route_place_kernel(RouteSortArgs
     mine = a.capacity ? min(all, a.capacity) : all;
   }
   // Exclusive scan of the segment lengths over the experts.
-  const int len = e < E ? (a.capacity ? a.capacity : (mine + a.align - 1) / a.align * a.align) : 0;
+  const int len = e < E ? (a.capacity ? a.capacity : (int)(((uint32_t)mine + a.align - 1) / a.align * a.align)) : 0;
   int inc = len;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -152,7 +157,8 @@ __global__ void __launch_bounds__(SORT_THREADS) route_place_kernel(RouteSortArgs
   }
   __syncthreads();
   const int bits = 32 - __clz(E);  // of 0 .. E, E standing for a dropped pair
-  for (int64_t p = w0 + lane; p - lane < w1; p += 64) {  // all lanes stay for the ballots
+  const int64_t place_to = (int)blockIdx.x < a.blocks ? w1 : w0;
+  for (int64_t p = w0 + lane; p - lane < place_to; p += 64) {  // all lanes stay for the ballots
     const bool in = p < w1;
     const int id = in ? expert_of(a, p) : -1;
     const int key = id < 0 ? E : id;
@@ -175,7 +181,8 @@ __global__ void __launch_bounds__(SORT_THREADS) route_place_kernel(RouteSortArgs
   const int64_t stride = (int64_t)gridDim.x * SORT_THREADS;
   for (int64_t r = (int64_t)blockIdx.x * SORT_THREADS + tid; r < a.rows; r += stride) {
     int lo = 0, hi = E;  // the last segment that starts at or before r (start[0] = 0)
-    while (hi - lo > 1) {
+    if (a.capacity) lo = (int)((uint32_t)r / (uint32_t)a.capacity);  // rows are E * capacity
+    else while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (start[mid] <= r) lo = mid;
       else hi = mid;
@@ -420,17 +427,21 @@ int blocks_of(int64_t n, int64_t per) { return (int)((n + per - 1) / per); }
 int64_t route_sort_blocks(int64_t pairs, int64_t* per_block) {
   // One workgroup sorts up to 4096 pairs by itself; larger sorts give each 2048, and
   // more where that would be over 256 of them: each reads all the others' histograms.
-  const int64_t per = pairs <= 4096 ? 4096 : pairs <= 256 * 2048 ? 2048 : (pairs + 255) / 256;
+  const int64_t per = pairs <= 4096 ? 4096 : pairs <= SORT_MOST_BLOCKS * 2048 ? 2048 : (pairs + SORT_MOST_BLOCKS - 1) / SORT_MOST_BLOCKS;
   *per_block = per;
   return pairs <= per ? 1 : (pairs + per - 1) / per;
 }
 
 hipError_t launch_route_sort(const RouteSortArgs& a, hipStream_t s) {
   if (a.E < 1 || a.E > TPMLP_ROUTE_MAX_EXPERTS || a.blocks < 1) return hipErrorInvalidValue;
-  if (a.blocks == 1) return launch_kernel(route_place_kernel<true>, dim3(1), dim3(SORT_THREADS), s, a);
+  // A workgroup for each 1024 rows.  With as many as place pairs (one up to 4096 pairs) 4096
+  // pairs to 256 experts took 104 us for 131072 rows and 12.4 for 5888, now 8.9 and 9.3.
+  const int64_t pad = std::min<int64_t>((a.rows + SORT_THREADS - 1) / SORT_THREADS, SORT_MOST_BLOCKS);
+  const dim3 place((unsigned)std::max<int64_t>(a.blocks, pad));
+  if (a.blocks == 1) return launch_kernel(route_place_kernel<true>, place, dim3(SORT_THREADS), s, a);
   hipError_t e = launch_kernel(route_hist_kernel, dim3((unsigned)a.blocks), dim3(SORT_THREADS), s, a);
   if (e != hipSuccess) return e;
-  return launch_kernel(route_place_kernel<false>, dim3((unsigned)a.blocks), dim3(SORT_THREADS), s, a);
+  return launch_kernel(route_place_kernel<false>, place, dim3(SORT_THREADS), s, a);
 }
 
 namespace {

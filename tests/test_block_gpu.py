@@ -710,3 +710,11 @@ def test_graph_of_a_backward_outlives_other_sizes():
         assert all(torch.equal(got[k], want[k]) for k in want), M
         assert all(bool((j == 7.0).all()) for j in junk), M
         assert all(torch.equal(v, other[k]) for k, v in backward(M)[0].items()), M
+
+
+@pytest.mark.parametrize("T,K,E,cap", [(0, 2, 5, 1000), (1, 1, 512, 40), (8, 2, 8, 3000), (512, 8, 256, 512), (700, 6, 3, 4104),
+                                       (1100, 8, 512, 64), (70000, 2, 64, 9000)])
+def test_route_sort_mostly_padding(T, K, E, cap):
+    """A capacity far above what the pairs fill: workgroups that place nothing mark the padding."""
+    check_sort(route_ids(T + E, T, K, E, 0.2, bad=T > 4), E, 8, cap, torch.int32)
+    check_sort(torch.full((T, K), E - 1), E, 8, cap, torch.int64)
