@@ -17,7 +17,7 @@
 //
 // The moves are bound by bandwidth: 32768 x 3584 to four experts each 234 us, 5.05 TB/s,
 // four fifths of it scattered row writes; the gradient of 2048 x 4096 to eight each
-// 90 us for 436 MB, and its way back (combine without weights) 55 us, 5.5 TB/s.  The sort
+// 88 us for 436 MB, and its way back (combine without weights) 43.5 us for 302 MB.  The sort
 // is bound by latency: 16 pairs 3.7 us, 131072 pairs 5.0 + 7.6 us.
 
 #include "block_dev.h"
@@ -472,14 +472,16 @@ namespace {
 
 template <class ZT, class YT>
 hipError_t launch_combine(const RouteCombineArgs& a, bool full, bool nt, hipStream_t s) {
-  // Few tokens: a chunk to a wave, so that more waves share the latency.
-  const int chunks = a.T <= 2048 ? 1 : 2;
+  // Few tokens: a chunk to a wave, so that more waves share the latency.  Launches bound by
+  // memory: four, 2048 x 4096 of eight choices 52 us (56.9 with two, 59.2 with one); smaller
+  // ones are better with two (16384 x 200 11.8 against 12.8 us).
+  const int chunks = full && nt ? 4 : a.T <= 2048 ? 1 : 2;
   const dim3 grid((unsigned)blocks_of(a.T, 4), (unsigned)blocks_of(a.H, 256 * chunks)), block(256);
   if (!full) return chunks == 1 ? launch_kernel(route_combine_kernel<ZT, YT, 1, false, false>, grid, block, s, a)
                                 : launch_kernel(route_combine_kernel<ZT, YT, 2, false, false>, grid, block, s, a);
-  if (chunks == 1) return launch_kernel(route_combine_kernel<ZT, YT, 1, true, false>, grid, block, s, a);
-  return nt ? launch_kernel(route_combine_kernel<ZT, YT, 2, true, true>, grid, block, s, a)
-            : launch_kernel(route_combine_kernel<ZT, YT, 2, true, false>, grid, block, s, a);
+  if (chunks == 4) return launch_kernel(route_combine_kernel<ZT, YT, 4, true, true>, grid, block, s, a);
+  return chunks == 1 ? launch_kernel(route_combine_kernel<ZT, YT, 1, true, false>, grid, block, s, a)
+                     : launch_kernel(route_combine_kernel<ZT, YT, 2, true, false>, grid, block, s, a);
 }
 
 template <class DT, class ZT, int W>

@@ -718,3 +718,29 @@ def test_route_sort_mostly_padding(T, K, E, cap):
     """A capacity far above what the pairs fill: workgroups that place nothing mark the padding."""
     check_sort(route_ids(T + E, T, K, E, 0.2, bad=T > 4), E, 8, cap, torch.int32)
     check_sort(torch.full((T, K), E - 1), E, 8, cap, torch.int64)
+
+
+@pytest.mark.parametrize("T,H,K,z,y", [(2048, 4096, 8, F32, F32), (9001, 1032, 6, F32, BF16), (601, 20480, 8, BF16, F32)])
+def test_route_large_moves_equal_their_parts(T, H, K, z, y):
+    """Launches past the size from which accesses are non-temporal give the bits of small ones."""
+    from tensor_transformer_mlp_03_amd import _lib as L
+    h = check_sort(route_ids(T, T, K, 24, 0.1), 24, 8, 0, torch.int32)
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    rnd = lambda *s, dtype: torch.randn(*s, generator=gen, device="cuda").to(dtype)  # noqa: E731
+    Zs, w, dY = rnd(h.rows, H, dtype=z), rnd(T, K, dtype=F32), rnd(T, H, dtype=y)
+    assert Zs.numel() * Zs.element_size() + dY.numel() * dY.element_size() > 1 << 27
+    Y, dZs, dw = torch.empty_like(dY), torch.empty(h.rows, H, dtype=BF16, device="cuda"), torch.empty_like(w)
+    h.combine(Zs, w, Y)
+    h.combine_backward(dY, Zs, w, dZs, dw)
+    for t0 in range(0, T, 300):
+        t = slice(t0, min(t0 + 300, T))
+        keep, rows = torch.unique(h.row_of[t][h.row_of[t] >= 0].long(), return_inverse=True)
+        sub = torch.full_like(h.row_of[t], -1)
+        sub[h.row_of[t] >= 0] = rows.int()
+        Zp, Yp, dwp = Zs[keep].contiguous(), torch.empty_like(Y[t]), torch.empty_like(dw[t])
+        L.tpmlp_route_combine(Zp, sub, w[t], Yp)
+        L.tpmlp_route_combine_bwd(dY[t], Zp, sub, None, w[t], None, dwp)
+        assert torch.equal(Yp, Y[t]) and torch.equal(dwp, dw[t]), t0
+        pair = h.src_of[keep].long()
+        assert torch.equal(dZs[keep], (dY.float()[pair // K] * w.view(-1)[pair, None]).to(BF16)), t0
+    assert not bool(dZs[h.src_of < 0].any())
