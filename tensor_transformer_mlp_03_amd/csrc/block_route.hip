@@ -400,7 +400,8 @@ __global__ void __launch_bounds__(256) route_combine_bwd_kernel(RouteCombineBwdA
     if (W == 1) {
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
-        const float s = wave_sum(dot[j]);
+        // A dropped pair's dot is with zeros, and an infinity of dY times them is no 0.
+        const float s = row[j] >= 0 ? wave_sum(dot[j]) : 0.0f;
         if (lane == j && k0 + j < a.K) a.dw[t * a.K + k0 + j] = s;
       }
       continue;
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(256) route_combine_bwd_kernel(RouteCombineBwdA
     __syncthreads();  // the sums of the choices before are read
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
-      const float s = wave_sum(dot[j]);
+      const float s = row[j] >= 0 ? wave_sum(dot[j]) : 0.0f;
       if (lane == 0) dots[j][wave] = s;
     }
     __syncthreads();

@@ -744,3 +744,20 @@ def test_route_large_moves_equal_their_parts(T, H, K, z, y):
         pair = h.src_of[keep].long()
         assert torch.equal(dZs[keep], (dY.float()[pair // K] * w.view(-1)[pair, None]).to(BF16)), t0
     assert not bool(dZs[h.src_of < 0].any())
+
+
+@pytest.mark.parametrize("T,K,H,pad", [(5, 2, 64, 0), (9, 5, 331, 3), (6, 9, 1024, 0), (5, 3, 1032, 0), (7, 12, 2050, 1)])
+def test_route_dropped_pair_of_a_bad_row(T, K, H, pad):
+    """A dropped pair's dw is 0 whatever its token's dY holds; the token's other pairs see it."""
+    h = check_sort(route_ids(T, T, K, 4, 0.4), 4, 8, 0, torch.int32)
+    gen = torch.Generator().manual_seed(H)
+    dY, Z, w = normal(gen, T, H), normal(gen, h.rows, H), torch.rand(T, K, generator=gen)
+    dY[0, 3], dY[2, H - 1], dY[4] = float("inf"), float("nan"), float("-inf")
+    kept, bad = h.row_of.cpu() >= 0, ~torch.isfinite(dY).all(1)
+    assert bool((~kept[bad]).any()) and bool(kept[bad].any())
+    dZs, dw = torch.empty(h.rows, H, dtype=BF16, device="cuda"), torch.full((T, K), 5.0, device="cuda")
+    h.combine_backward(put(dY, pad), put(Z, pad), w.cuda(), dZs, dw)
+    dw = dw.cpu()
+    assert bool((dw[~kept] == 0.0).all()) and not bool(torch.isfinite(dw[kept & bad[:, None]]).any())
+    want, mag = OB.route_combine_backward(f64(dY[~bad]), f64(Z), h.row_of.cpu().numpy()[~bad.numpy()], f64(w[~bad]), h.rows)[1:]
+    close("dw", dw[~bad], want, mag, H / 256 + 16)
