@@ -533,7 +533,7 @@ def _ws(ws):
 def edge_desc(H: int, post="none", pre="none", w_post=None, b_post=None, w_pre=None, b_pre=None, gate=None,
               gate_rows: int = 0, alpha: float = 1.0, eps: float = 1e-5) -> EdgeDesc:
     """A tpmlp_edge with its parameters (all float32 or all bf16; the gate [G, H], or [H] for
-    one row); M, y_type and r_type are set by each call.  gate_rows 0: one row for all tokens.
+    one row); M, y_type and r_type are each call's own, which leaves this one as it is.  gate_rows 0: one row for all tokens.
     Holds the parameters' addresses: they have to stay alive and where they are."""
     params = [(n, t) for n, t in (("w_post", w_post), ("b_post", b_post), ("w_pre", w_pre), ("b_pre", b_pre),
                                   ("gate", gate)) if t is not None]
@@ -557,6 +557,14 @@ def edge_desc(H: int, post="none", pre="none", w_post=None, b_post=None, w_pre=N
     return d
 
 
+def _of_call(d: EdgeDesc, M: int) -> EdgeDesc:
+    """The description with one call's M, for the call's types to be added.  A copy: the library reads it without
+    the interpreter's lock, while another thread may call through the same description."""
+    c = EdgeDesc.from_buffer_copy(d)
+    c.M = M
+    return c
+
+
 def _check_gate(d: EdgeDesc, M: int) -> None:
     if d.gate_tokens is not None and M > d.gate_tokens:
         raise ValueError(f"gate has {d.gate_tokens // d.gate_rows} rows for {d.gate_rows} tokens each, the call has {M} tokens")
@@ -569,23 +577,23 @@ def _gate_groups(d: EdgeDesc, M: int) -> int:
 def tpmlp_edge_fwd(d: EdgeDesc, y, r, r_out, x, stream=None):
     """r_out = alpha r + gate * N_post(y), x = N_pre(r_out); y None: no block before the edge."""
     M, H = r.shape[0], d.H
-    d.M, d.r_type = M, _dtype(r, "r")
     _check_gate(d, M)
+    c = _of_call(d, M)
+    c.r_type = _dtype(r, "r")
     pr, lr = _rows(r, (M, H), "r")
     py = ly = None
     if y is not None:
-        d.y_type = _dtype(y, "y")
+        c.y_type = _dtype(y, "y")
         py, ly = _rows(y, (M, H), "y")
-    po, lo = _rows(r_out, (M, H), "r_out", d.r_type)
+    po, lo = _rows(r_out, (M, H), "r_out", c.r_type)
     px, lx = _rows(x, (M, H), "x", BF16)
-    st = lib().tpmlp_edge_fwd(ctypes.byref(d), py, ly or 0, pr, lr, po, lo, px, lx, _stream(stream))
+    st = lib().tpmlp_edge_fwd(ctypes.byref(c), py, ly or 0, pr, lr, po, lo, px, lx, _stream(stream))
     if st:
         _check(st, "tpmlp_edge_fwd")
 
 
 def tpmlp_edge_bwd_workspace_bytes(d: EdgeDesc, M: int) -> int:
-    d.M = M
-    return lib().tpmlp_edge_bwd_workspace_bytes(ctypes.byref(d))
+    return lib().tpmlp_edge_bwd_workspace_bytes(ctypes.byref(_of_call(d, M)))
 
 
 def tpmlp_edge_bwd(d: EdgeDesc, y, r_out, dr_out, dx, dr, dy, dw_post=None, db_post=None, dw_pre=None, db_pre=None,
@@ -593,22 +601,23 @@ def tpmlp_edge_bwd(d: EdgeDesc, y, r_out, dr_out, dx, dr, dy, dw_post=None, db_p
     """Backward of the edge; r_out is the stream the forward wrote, dr and dy are written."""
     import torch
     M, H = dr.shape[0], d.H
-    d.M, d.r_type = M, _dtype(dr, "dr")
     _check_gate(d, M)
-    pr, lr = _rows(r_out, (M, H), "r_out", d.r_type)
-    po, lo = _rows(dr_out, (M, H), "dr_out", d.r_type)
+    c = _of_call(d, M)
+    c.r_type = _dtype(dr, "dr")
+    pr, lr = _rows(r_out, (M, H), "r_out", c.r_type)
+    po, lo = _rows(dr_out, (M, H), "dr_out", c.r_type)
     px, lx = _rows(dx, (M, H), "dx")
     pd, ld = _rows(dr, (M, H), "dr")
     py, ly = _rows(y, (M, H), "y")
     if y is not None:
-        d.y_type = _dtype(y, "y")
+        c.y_type = _dtype(y, "y")
     pg, lg = _rows(dy, (M, H), "dy", BF16)
     f32 = torch.float32
     grads = [_flat(dw_post, H, f32, "dw_post"), _flat(db_post, H, f32, "db_post"), _flat(dw_pre, H, f32, "dw_pre"),
              _flat(db_pre, H, f32, "db_pre"),
              _flat(dgate, _gate_groups(d, M) * H, f32, "dgate") if dgate is not None else None]
     pw, nw = _ws(ws)
-    st = lib().tpmlp_edge_bwd(ctypes.byref(d), py, ly, pr, lr, po, lo, px, _dtype(dx, "dx") if dx is not None else F32,
+    st = lib().tpmlp_edge_bwd(ctypes.byref(c), py, ly, pr, lr, po, lo, px, _dtype(dx, "dx") if dx is not None else F32,
                               lx, pd, ld, pg, lg, *grads, pw, nw, _stream(stream))
     if st:
         _check(st, "tpmlp_edge_bwd")

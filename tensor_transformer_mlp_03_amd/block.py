@@ -5,7 +5,8 @@ tokens to experts and back, and the global gradient norm with clipping.
 Each holds its parameters, index buffers and workspace; every call takes the caller's inputs
 and outputs, enqueues kernels on a stream (the current one by default) and returns.  No
 arithmetic happens here.  Buffers and workspaces belong to one stream at a time: a program
-that uses an object on two streams orders them itself.
+that uses an object on two streams orders them itself, and two threads do not call one
+object at once, but for Edge.forward, which holds no buffer.
 """
 from __future__ import annotations
 

@@ -401,3 +401,45 @@ def test_edge_keeps_what_a_graph_writes_to(monkeypatch):
         used.clear()
         # The largest workspace and the last gradient are the object's own.
         assert alive == ([[True, True]] * 3 if capturing else [[False, False], [True, False], [True, True]]), (capturing, alive)
+
+
+def test_edge_call_keeps_its_own_sizes(monkeypatch):
+    """The library is entered without the interpreter's lock: another thread's call through the same description,
+    at any point of this one, changes neither its M nor its types."""
+    torch = pytest.importorskip("torch")
+    bf, seen, d = torch.bfloat16, [], L.edge_desc(16, pre="rms", w_pre=torch.ones(16), gate=torch.ones(16))
+
+    def fwd(M, dtype):
+        r = torch.zeros(M, 16, dtype=dtype)
+        L.tpmlp_edge_fwd(d, r.clone(), r, r.clone(), torch.zeros(M, 16, dtype=bf), stream=0)
+
+    def bwd(M, dtype):
+        r = torch.zeros(M, 16, dtype=dtype)
+        L.tpmlp_edge_bwd(d, r.clone(), r, r, r, r.clone(), torch.zeros(M, 16, dtype=bf), stream=0)
+
+    def query(M, dtype):
+        assert L.tpmlp_edge_bwd_workspace_bytes(d, M) == 0
+
+    class Library:
+        other, depth = None, 0
+
+        def enter(self, ref, *_):
+            Library.depth += 1
+            if Library.depth == 1:  # the other thread's turn
+                Library.other(4096, bf)
+            e = ref._obj
+            seen.append((e.M, e.r_type, e.y_type, e.H, e.gate))
+            Library.depth -= 1
+            return 0
+
+        tpmlp_edge_fwd = tpmlp_edge_bwd = tpmlp_edge_bwd_workspace_bytes = enter
+
+    monkeypatch.setattr(L, "lib", lambda: Library())
+    for call in (fwd, bwd, query):
+        for Library.other in (fwd, bwd, query):
+            seen.clear()
+            call(8, torch.float32)
+            (M, r, y, H, gate), outer = seen
+            assert M == 4096 and outer[0] == 8 and outer[3:] == (H, gate) == (16, d.gate), (seen, call)
+            if call is not query:
+                assert outer[1:3] == (L.F32, L.F32), (seen, call)
