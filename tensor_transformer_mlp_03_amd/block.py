@@ -6,7 +6,10 @@ Each holds its parameters, index buffers and workspace; every call takes the cal
 and outputs, enqueues kernels on a stream (the current one by default) and returns.  No
 arithmetic happens here.  Buffers and workspaces belong to one stream at a time: a program
 that uses an object on two streams orders them itself, and two threads do not call one
-object at once, but for Edge.forward, which holds no buffer.
+object at once, but for Edge.forward, which holds no buffer.  Route and GradClip make theirs
+when they are made, on the current stream, as torch does any tensor's: a program that uses
+them on another one makes them under it, or orders the two.  Edge makes its backward's with
+the first call of a size, on the stream of that call.
 """
 from __future__ import annotations
 
@@ -16,6 +19,15 @@ from . import _lib as L
 def _capturing():
     import torch
     return torch.cuda.is_current_stream_capturing()
+
+
+def _on(stream, device):
+    """Makes the stream that a call is given the current one: what is allocated then is that stream's."""
+    import torch
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = L._stream(stream)
+        stream = torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 class Edge:
@@ -34,6 +46,7 @@ class Edge:
         self.desc = L.edge_desc(H, post, pre, w_post, b_post, w_pre, b_pre, gate, gate_rows, alpha, eps)
         self.grads, self._grad_args, self._ws, self._M = {}, {}, None, -1
         self._captured = []  # buffers that graphs write to, which another M replaces
+        self._streams = set()  # that the buffers were used on
 
     def forward(self, y, r, r_out, x, stream=None):
         """y [M,H] float32 or bf16 (None: no block before); r, r_out [M,H] (r_out may be r);
@@ -45,13 +58,29 @@ class Edge:
         float32 or bf16.  Writes dr (may be dr_out) and dy (bf16) and returns the parameters'
         float32 gradients by name, which the next backward overwrites.  What a backward that
         is captured into a graph writes to stays allocated as long as this object does."""
+        if stream is None:
+            self._ready(dr)
+        else:
+            with _on(stream, dr.device):
+                self._ready(dr)
+        L.tpmlp_edge_bwd(self.desc, y, r_out, dr_out, dx, dr, dy, ws=self._ws, stream=stream, **self._grad_args)
+        return self.grads
+
+    def _ready(self, dr):
+        """Buffers for dr's rows.  The current stream is the call's: another M's buffers go back to the stream that
+        they were made on, where they are free once what ran before is done, and are marked as used on others."""
         M = dr.shape[0]
         if M != self._M:
             self._place(M, dr.device)
+        if dr.is_cuda:
+            self._streams.add(L._current_stream())
+            if len(self._streams) > 1:
+                import torch
+                stream = torch.cuda.current_stream()
+                for t in (self._ws, *self.grads.values()):
+                    t.record_stream(stream)
         if _capturing():
             self._captured.append((self._ws, *self.grads.values()))
-        L.tpmlp_edge_bwd(self.desc, y, r_out, dr_out, dx, dr, dy, ws=self._ws, stream=stream, **self._grad_args)
-        return self.grads
 
     def _place(self, M, device):
         import torch

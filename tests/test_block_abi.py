@@ -443,3 +443,41 @@ def test_edge_call_keeps_its_own_sizes(monkeypatch):
             assert M == 4096 and outer[0] == 8 and outer[3:] == (H, gate) == (16, d.gate), (seen, call)
             if call is not query:
                 assert outer[1:3] == (L.F32, L.F32), (seen, call)
+
+
+def test_edge_places_buffers_on_the_stream_of_the_call(monkeypatch):
+    """What a backward allocates and lets go belongs to the stream that its kernels run on, and that stream is the
+    one asked whether it is being captured."""
+    torch = pytest.importorskip("torch")
+    from tensor_transformer_mlp_03_amd import block
+    current, asked, made = ["current"], [], []
+
+    class On:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            current.append(self.stream)
+
+        def __exit__(self, *_):
+            current.pop()
+
+    def capturing():
+        asked.append(current[-1])
+        return current[-1] == 77
+
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(current[-1]) or empty(*a, **k))
+    monkeypatch.setattr(torch.cuda, "stream", On)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: handle)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: "default")
+    monkeypatch.setattr(block, "_capturing", capturing)
+    monkeypatch.setattr(L, "tpmlp_edge_bwd", lambda *a, **k: None)
+    for stream, name in ((77, 77), (0, "default"), (None, "current")):
+        edge = block.Edge(16, post="rms", w_post=torch.ones(16), gate=torch.ones(500, 16), gate_rows=2)
+        for M in (8, 1000):
+            r = torch.zeros(M, 16)
+            made.clear(), asked.clear()
+            edge.backward(r, None, r, None, r, torch.zeros(M, 16, dtype=torch.bfloat16), stream=stream)
+            assert set(made) == {name} and asked == [name], (stream, made, asked)
+        assert bool(edge._captured) == (stream == 77)

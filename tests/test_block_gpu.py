@@ -761,3 +761,51 @@ def test_route_dropped_pair_of_a_bad_row(T, K, H, pad):
     assert bool((dw[~kept] == 0.0).all()) and not bool(torch.isfinite(dw[kept & bad[:, None]]).any())
     want, mag = OB.route_combine_backward(f64(dY[~bad]), f64(Z), h.row_of.cpu().numpy()[~bad.numpy()], f64(w[~bad]), h.rows)[1:]
     close("dw", dw[~bad], want, mag, H / 256 + 16)
+
+
+def test_edge_backward_on_given_streams():
+    """While a backward runs on the stream that it was given, what another size has replaced is not handed out to
+    other streams, neither if the object keeps to one stream nor if it goes from one to another."""
+    H, rows = 512, 4
+    c, params, t = edge_case(6, 2000, H, "rms", "layer", F32, F32, BF16, rows)
+    y, r, d, dx = (t[k].cuda() for k in ("y", "r", "dr", "dx"))
+
+    def backward(e, M, stream):
+        dr, dy = torch.empty(M, H, device="cuda"), torch.empty(M, H, device="cuda", dtype=BF16)
+        torch.cuda.current_stream().synchronize()
+        return [dr, dy, *e.backward(y[:M], r[:M], d[:M], dx[:M], dr, dy, stream=stream).values()]
+
+    want = {}
+    for M in (40, 2000):
+        want[M] = [v.clone() for v in backward(make_edge(c, params, H, rows), M, None)]
+    torch.cuda.synchronize()
+    for streams in ([1, 1], [1, 2], [None, 1]):
+        s = {1: torch.cuda.Stream(), 2: torch.cuda.Stream(), None: torch.cuda.current_stream()}
+        e = make_edge(c, params, H, rows)
+        backward(e, 40, s[1] if streams[0] else None)
+        torch.cuda.synchronize()
+        last = s[streams[1]]
+        with torch.cuda.stream(last):
+            torch.cuda._sleep(100_000_000)
+        small = backward(e, 40, last)
+        old = [(v.data_ptr(), v.numel(), v.dtype) for v in (e._ws, e.grads["gate"])]
+        large = backward(e, 2000, last)
+        assert e._ws.data_ptr() != old[0][0] and e.grads["gate"].data_ptr() != old[1][0]
+        del small[2:]  # the gate's gradient, which nothing holds now, and those that the second call overwrote
+        junk = []
+        for own in (torch.cuda.current_stream(), s[streams[0]]):
+            if own != last:
+                with torch.cuda.stream(own):
+                    junk += [torch.full((n,), 7, dtype=k, device="cuda") for _, n, k in old for _ in range(3)]
+        if not last.query():  # still at work
+            assert not {j.data_ptr() for j in junk} & {a for a, _, _ in old}, streams
+        torch.cuda.synchronize()
+        assert all(bool((j == 7).all()) for j in junk)
+        assert all(torch.equal(a, b) for a, b in zip(want[40], small)), streams
+        assert all(torch.equal(a, b) for a, b in zip(want[2000], large)), streams
+        handle = backward(make_edge(c, params, H, rows), 40, s[1].cuda_stream)
+        s[1].synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[40], handle))
+        zero = backward(make_edge(c, params, H, rows), 40, 0)  # the default stream's handle
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want[40], zero))
