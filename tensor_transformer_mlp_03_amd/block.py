@@ -45,7 +45,7 @@ class Edge:
                                          ("gate", gate)) if t is not None}
         self.desc = L.edge_desc(H, post, pre, w_post, b_post, w_pre, b_pre, gate, gate_rows, alpha, eps)
         self.grads, self._grad_args, self._ws, self._M = {}, {}, None, -1
-        self._captured = []  # buffers that graphs write to, which another M replaces
+        self._captured = {}  # buffers that graphs write to, which another M replaces, each once, by identity
         self._streams = set()  # that the buffers were used on
 
     def forward(self, y, r, r_out, x, stream=None):
@@ -80,7 +80,7 @@ class Edge:
                 for t in (self._ws, *self.grads.values()):
                     t.record_stream(stream)
         if _capturing():
-            self._captured.append((self._ws, *self.grads.values()))
+            self._captured.update((id(t), t) for t in (self._ws, *self.grads.values()))
 
     def _place(self, M, device):
         import torch

@@ -481,3 +481,16 @@ def test_edge_places_buffers_on_the_stream_of_the_call(monkeypatch):
             edge.backward(r, None, r, None, r, torch.zeros(M, 16, dtype=torch.bfloat16), stream=stream)
             assert set(made) == {name} and asked == [name], (stream, made, asked)
         assert bool(edge._captured) == (stream == 77)
+
+
+def test_edge_keeps_captured_buffers_once(monkeypatch):
+    """Captures over the same buffers hold them, not a note of each capture."""
+    torch = pytest.importorskip("torch")
+    from tensor_transformer_mlp_03_amd import block
+    monkeypatch.setattr(block, "_capturing", lambda: True)
+    monkeypatch.setattr(L, "tpmlp_edge_bwd", lambda *a, **k: None)
+    edge = block.Edge(16, post="rms", w_post=torch.ones(16))
+    for M in (1000, 8, 1000, 8, 8):
+        r = torch.zeros(M, 16)
+        edge.backward(r, None, r, None, r, torch.zeros(M, 16, dtype=torch.bfloat16))
+    assert len(edge._captured) == 2  # w_post's gradient and the larger workspace
