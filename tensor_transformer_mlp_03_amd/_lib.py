@@ -496,11 +496,25 @@ def _dtype(t, name) -> int:
     return kind
 
 
+def _gpu_here() -> bool:
+    import torch
+    return torch.cuda.device_count() > 0
+
+
+def _host(t, name) -> None:
+    """Refuses a tensor in host memory that kernels cannot reach (pinned memory they can).  Where there is no GPU the
+    library refuses the call itself."""
+    if t.numel() and _gpu_here() and not t.is_pinned():
+        raise ValueError(f"{name} is not on the GPU")
+
+
 def _rows(t, shape, name, kind=None):
     """(pointer, row stride) of a [rows, columns] tensor with contiguous columns, after
     checking its shape and, if given, its tpmlp_dtype."""
     if t is None:
         return None, 0
+    if not t.is_cuda:
+        _host(t, name)
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if kind is not None and _dtype(t, name) != kind:
@@ -519,6 +533,8 @@ def _flat(t, n, dtype, name):
     """Pointer of a contiguous tensor of n elements."""
     if t is None:
         return None
+    if not t.is_cuda:
+        _host(t, name)
     if t.dtype != dtype or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous {dtype} tensor")
     if t.numel() != n:
@@ -527,7 +543,11 @@ def _flat(t, n, dtype, name):
 
 
 def _ws(ws):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda:
+        _host(ws, "ws")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def edge_desc(H: int, post="none", pre="none", w_post=None, b_post=None, w_pre=None, b_pre=None, gate=None,
@@ -637,6 +657,8 @@ def tpmlp_route_sort(ids, E: int, align: int, capacity: int, counts, offsets, ro
     T, K = ids.shape
     if ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
         raise TypeError("ids must be a contiguous int32 or int64 tensor")
+    if not ids.is_cuda:
+        _host(ids, "ids")
     i32, rows = torch.int32, max(0, tpmlp_route_rows(T, K, E, align, capacity))
     pw, nw = _ws(ws)
     st = lib().tpmlp_route_sort(ids.data_ptr(), 32 if ids.dtype == i32 else 64, T, K, E, align, capacity,
@@ -706,6 +728,8 @@ class GradTable:
             o = g if self.outs is None else self.outs[i]
             if not g.is_contiguous() or not o.is_contiguous():
                 raise ValueError(f"gradient {i} and its output must be contiguous")
+            if not g.is_cuda or not o.is_cuda:
+                _host(g if not g.is_cuda else o, f"gradient {i} or its output")
             if o.dtype != g.dtype or o.numel() != g.numel():
                 raise ValueError(f"outs[{i}] differs from its gradient in type or size")
             self.ptrs[i], self.out_ptrs[i] = g.data_ptr(), o.data_ptr()
@@ -719,6 +743,8 @@ def tpmlp_grad_workspace_bytes(table: GradTable) -> int:
 def _one(t, dtype, name):
     if t.dtype != dtype or t.numel() != 1:
         raise TypeError(f"{name} must be one {dtype}")
+    if not t.is_cuda:
+        _host(t, name)
     return t.data_ptr()
 
 

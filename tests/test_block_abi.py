@@ -494,3 +494,52 @@ def test_edge_keeps_captured_buffers_once(monkeypatch):
         r = torch.zeros(M, 16)
         edge.backward(r, None, r, None, r, torch.zeros(M, 16, dtype=torch.bfloat16))
     assert len(edge._captured) == 2  # w_post's gradient and the larger workspace
+
+
+def test_host_tensors_are_refused(monkeypatch):
+    """Where there is a GPU, a tensor in host memory is refused by name: its address would fault in a kernel."""
+    torch = pytest.importorskip("torch")
+    i32, bf, called = torch.int32, torch.bfloat16, []
+
+    class Library:
+        def __getattr__(self, name):
+            if name == "tpmlp_route_rows":
+                return lambda *a: 8
+            return lambda *a: called.append(name) or 0
+
+    class OnGpu(torch.Tensor):  # a host tensor that says it is not
+        is_cuda = True
+
+    def gpu(*shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype).as_subclass(OnGpu)
+
+    monkeypatch.setattr(L, "lib", lambda: Library())
+    monkeypatch.setattr(L, "_gpu_here", lambda: True, raising=False)
+    d = L.edge_desc(16, post="rms", pre="rms", w_post=gpu(16), w_pre=gpu(16), gate=gpu(1, 16))
+
+    def each(call, **tensors):
+        call(**tensors)
+        assert called.pop() and not called
+        for name, t in tensors.items():
+            host = [t[0].as_subclass(torch.Tensor)] if isinstance(t, list) else t.as_subclass(torch.Tensor)
+            with pytest.raises(ValueError, match="not on the GPU"):
+                call(**{**tensors, name: host})
+            assert not called, (call, name)
+
+    s = dict(stream=0)
+    each(lambda **k: L.edge_desc(16, post="layer", **k) and called.append(1), w_post=gpu(16), b_post=gpu(16), gate=gpu(1, 16))
+    each(lambda **k: L.tpmlp_edge_fwd(d, **k, **s), y=gpu(4, 16), r=gpu(4, 16), r_out=gpu(4, 16), x=gpu(4, 16, dtype=bf))
+    each(lambda **k: L.tpmlp_edge_bwd(d, **k, **s), y=gpu(4, 16), r_out=gpu(4, 16), dr_out=gpu(4, 16), dx=gpu(4, 16), dr=gpu(4, 16),
+         dy=gpu(4, 16, dtype=bf), dw_post=gpu(16), dw_pre=gpu(16), dgate=gpu(1, 16), ws=gpu(64))
+    ids, rows = gpu(4, 2, dtype=i32), gpu(8, dtype=i32)
+    each(lambda **k: L.tpmlp_route_sort(E=4, align=1, capacity=0, **k, **s), ids=ids, counts=gpu(4, dtype=i32),
+         offsets=gpu(5, dtype=i32), row_of=ids, src_of=rows, ws=gpu(64))
+    each(lambda **k: L.tpmlp_route_dispatch(**k, **s), X=gpu(4, 16, dtype=bf), row_of=ids, src_of=rows, Xs=gpu(8, 16, dtype=bf))
+    each(lambda **k: L.tpmlp_route_combine(**k, **s), Zs=gpu(8, 16), row_of=ids, w=gpu(4, 2), Y=gpu(4, 16))
+    each(lambda **k: L.tpmlp_route_combine_bwd(**k, **s), dY=gpu(4, 16), Zs=gpu(8, 16), row_of=ids, src_of=rows, w=gpu(4, 2),
+         dZs=gpu(8, 16, dtype=bf), dw=gpu(4, 2))
+    each(lambda **k: L.GradTable(**k) and called.append(1), grads=[gpu(5)], outs=[gpu(5)])
+    table, one = L.GradTable([gpu(5)]), gpu(1, dtype=torch.float64)
+    each(lambda **k: L.tpmlp_grad_sumsq(table, **k, **s), sumsq=one, ws=gpu(64))
+    each(lambda **k: L.tpmlp_grad_clip(table, max_norm=1.0, **k, **s), sumsq=one, norm=gpu(1))
+    each(lambda **k: L.tpmlp_clip_grad_norm(table, 1.0, **k, **s), norm=gpu(1), ws=gpu(64))
