@@ -828,3 +828,78 @@ def test_pinned_host_memory():
         h.sort(ids)
     with pytest.raises(ValueError, match="not on the GPU"):
         L.GradTable([torch.ones(3)])
+
+
+# Each row form of the backward with three to nine rows a workgroup (a wave, up to 512 elements); the whole ones past
+# 128 MB, from where their accesses are non-temporal.
+LOOPS = [(24003, 256), (12003, 512), (6203, 1000), (3003, 2048), (2050, 3000), (1030, 6000), (1030, 8200),
+         (12003, 255), (9301, 511), (2500, 1001), (2050, 2050), (1030, 4101)]
+
+
+@pytest.mark.parametrize("M,H", LOOPS)
+@pytest.mark.parametrize("kind,groups", [("rms", 1), ("layer", 3)])
+def test_edge_backward_of_several_rows(M, H, kind, groups):
+    from tensor_transformer_mlp_03_amd import _lib as L
+    rows = -(-M // groups)
+    c, params, _ = edge_case(1, 1, H, kind, kind, F32, F32, BF16, 1)
+    e = make_edge(c, {**params, "gate": torch.ones(groups, H, dtype=BF16)}, H, rows)
+    n = L.tpmlp_edge_bwd_workspace_bytes(e.desc, M) - (32 * M if H > 4096 else 0)
+    at_once = n // (H * (8 if kind == "rms" else 16)) * (4 if H <= 512 else 1)
+    assert 3 <= M / at_once <= 9
+    assert H % 4 or 22 * M * H > 1 << 27
+    run_edge(2 * H + 1, M, H, kind, kind, F32, F32, BF16, rows)
+
+
+@pytest.mark.parametrize("H", [256, 512, 1000, 2048, 3000, 6000, 12000, 20000, 32768])
+@pytest.mark.parametrize("kind,p", [("rms", F32), ("layer", BF16)])
+def test_edge_forward_past_the_caches_equals_its_parts(H, kind, p):
+    """Launches past 128 MB, in each row form, give the bits of small ones."""
+    M = (1 << 27) // (14 * H) + 300
+    c, params, _ = edge_case(3, 1, H, kind, kind, F32, F32, p, 0)
+    params["gate"] = normal(torch.Generator().manual_seed(H), 1, H, dtype=p)
+    e = make_edge(c, params, H, 0)
+    gen = torch.Generator(device="cuda").manual_seed(H)
+    y, r = (torch.randn(M, H, generator=gen, device="cuda") for _ in range(2))
+    ro, x = torch.empty_like(r), torch.empty(M, H, dtype=BF16, device="cuda")
+    e.forward(y, r, ro, x)
+    step = (1 << 25) // (14 * H)
+    assert step < M and bool(torch.isfinite(x).all())
+    part_r, part_x = torch.empty(step, H, device="cuda"), torch.empty(step, H, dtype=BF16, device="cuda")
+    for at in range(0, M, step):
+        n = min(step, M - at)
+        e.forward(y[at:at + n], r[at:at + n], part_r[:n], part_x[:n])
+        assert torch.equal(ro[at:at + n], part_r[:n]) and torch.equal(x[at:at + n], part_x[:n]), at
+
+
+@pytest.mark.parametrize("T,H,K,E,capacity", [(5003, 2048, 7, 24, 0), (5003, 2056, 7, 24, 1600), (160, 33000, 20, 8, 0)])
+def test_route_dispatch_past_the_caches(T, H, K, E, capacity):
+    """A dispatch past 128 MB: every row is its token's, padding rows are zeros."""
+    h = check_sort(route_ids(T, T, K, E, 0.1), E, 8, capacity, torch.int32)
+    assert 2 * H * (T + h.rows) > 1 << 27
+    X = torch.randn(T, H, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda").to(BF16)
+    Xs = torch.full((h.rows, H), float("nan"), dtype=BF16, device="cuda")
+    h.dispatch(X, Xs)
+    on = h.src_of >= 0
+    assert torch.equal(Xs[on], X[h.src_of[on].long() // K]) and not bool(Xs[~on].any())
+
+
+def test_clip_many_tables():
+    """More than one launch's 128 tensors and more than 2048 partial sums, which are then added up beforehand."""
+    from tensor_transformer_mlp_03_amd.block import GradClip
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    g = [(torch.randn(163840 - 3 * i, generator=gen, device="cuda") * 0.1).to(BF16 if i % 3 == 1 else F32) for i in range(260)]
+    total = sum(float(t.double().square().sum()) for t in g)
+    norm = np.sqrt(total)
+    for scale in (1.0, -0.5):
+        max_norm = float(np.float32(0.3 * norm))
+        outs = [torch.full_like(t, 9.0) for t in g]
+        close("norm", GradClip(g, outs).clip(max_norm, scale), np.float64(norm * abs(scale)), norm * abs(scale), 2)
+        factor = scale * min(1.0, max_norm / (norm * abs(scale)))
+        for o, t in zip(outs, g):
+            want = t.double() * factor
+            half = torch.finfo(o.dtype).eps / 2
+            assert bool(((o.double() - want).abs() <= (half + 4 * (1 + half) * U) * want.abs() + 1e-37).all())
+    h = GradClip(g)
+    assert abs(float(h.sumsq()) - total) <= 1e-12 * total
+    h.scale(max_norm, scale)
+    assert all(torch.equal(a, b) for a, b in zip(g, outs))
