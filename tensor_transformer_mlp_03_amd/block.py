@@ -46,7 +46,7 @@ class Edge:
         self.desc = L.edge_desc(H, post, pre, w_post, b_post, w_pre, b_pre, gate, gate_rows, alpha, eps)
         self.grads, self._grad_args, self._ws, self._M = {}, {}, None, -1
         self._captured = {}  # buffers that graphs write to, which another M replaces, each once, by identity
-        self._streams = set()  # that the buffers were used on
+        self._stream, self._several = None, False  # of the last backward; whether there were several
 
     def forward(self, y, r, r_out, x, stream=None):
         """y [M,H] float32 or bf16 (None: no block before); r, r_out [M,H] (r_out may be r);
@@ -72,13 +72,13 @@ class Edge:
         M = dr.shape[0]
         if M != self._M:
             self._place(M, dr.device)
-        if dr.is_cuda:
-            self._streams.add(L._current_stream())
-            if len(self._streams) > 1:
-                import torch
-                stream = torch.cuda.current_stream()
-                for t in (self._ws, *self.grads.values()):
-                    t.record_stream(stream)
+        if dr.is_cuda and L._current_stream() != self._stream:
+            self._several, self._stream = self._stream is not None, L._current_stream()
+        if self._several:
+            import torch
+            stream = torch.cuda.current_stream()
+            for t in (self._ws, *self.grads.values()):
+                t.record_stream(stream)
         if _capturing():
             self._captured.update((id(t), t) for t in (self._ws, *self.grads.values()))
 
