@@ -152,7 +152,7 @@ constexpr int CLIP_TENSORS = 128;
 constexpr int64_t CLIP_CHUNK = 16384;  // elements of one unit of work
 constexpr int CLIP_BLOCKS = 2048;        // most workgroups (and partial sums) of a summing launch
 constexpr int CLIP_SCALE_BLOCKS = 8192;  // and of a scaling one, which has no partials
-constexpr uint32_t CLIP_KEEP = 4096;     // last chunks that the first pass reads so as to stay in the cache
+constexpr uint32_t CLIP_KEEP = 4096;     // last chunks of a launch that the first pass reads so as to stay in the cache
 
 struct ClipArgs {
   const void* in[CLIP_TENSORS];

@@ -291,8 +291,10 @@ __global__ void __launch_bounds__(W == 1 ? 256 : 64 * W, FULL && NV <= 2 ? 4 : 1
 // makes a row's sums and keeps the six or eight numbers that come of them; the
 // second, a thread to four columns, walks the rows of its chunk with them.  It reads
 // the inputs once more, but neither kernel waits for anything but memory.  2048 x 20480:
-// 277 us; the one-kernel form took 338 with its spills, 410 with the next row in flight
-// and more of them, and 1060 us for 2048 x 20001.
+// 277 us (176 at the rate of one reading); the one-kernel form took 338 with its spills, 410
+// with the next row in flight and more of them, and 1060 us for 2048 x 20001, which takes
+// 333.  The second kernel takes the rows in the first's order, which evicts what the cache
+// still holds before it is reached; bands of rows or the reverse order were not tried.
 // ---------------------------------------------------------------------------
 constexpr int WIDE_THREADS = 1024, WIDE_COLS = 1024;  // columns of one workgroup of the second kernel
 

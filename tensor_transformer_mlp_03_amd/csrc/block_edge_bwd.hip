@@ -11,7 +11,10 @@ namespace {
 // lets the 64 work on different rows of the gate shares one row's slices.  A line
 // adds all four sums of its slices in one walk, eight slices' loads issued before
 // the first is added: the slices come from other XCDs' writes, through memory, and
-// the kernel is bound by the latency of these loads.
+// the kernel is bound by the latency of these loads.  With a gate row for every few
+// tokens a group is one slice, which the eight loads of a batch share, and the sums are as
+// many as the data: 8192 x 4096 in float32 takes 134 us with one gate row, 155 with one for
+// 16 tokens and 445 with one for each (268 MB of sums).
 constexpr int FIN_COLS = 16, FIN_LINES = 64, FIN_BATCH = 8;
 
 template <int NACC>

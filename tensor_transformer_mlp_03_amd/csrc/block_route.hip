@@ -16,9 +16,10 @@
 // the expert's product) reaches no output.
 //
 // The moves are bound by bandwidth: 32768 x 3584 to four experts each 234 us, 5.05 TB/s,
-// four fifths of it scattered row writes; the gradient of 2048 x 4096 to eight each
-// 88 us for 436 MB, and its way back (combine without weights) 43.5 us for 302 MB.  The sort
-// is bound by latency: 16 pairs 3.7 us, 131072 pairs 5.0 + 7.6 us.
+// four fifths of it scattered row writes; the gradient of 2048 x 4096 to eight each, of which
+// a capacity keeps 12160 of 16384 pairs, 88 us for 401 MB (4.6 TB/s), and its way back
+// (combine without weights) 43.5 us for 233 MB (5.4 TB/s).  The sort is bound by latency: 16
+// pairs 3.7 us, 131072 pairs 5.0 + 7.6 us.
 
 #include "block_dev.h"
 
