@@ -41,7 +41,6 @@ _vp, _sz, _i64, _int = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int64, ctypes.
 _PP = ctypes.POINTER(ctypes.c_void_p)
 
 
-
 class EdgeDesc(ctypes.Structure):
     """tpmlp_edge: the description of the edge between two blocks."""
     _fields_ = [("M", _i64), ("H", _i64), ("post", ctypes.c_int32), ("pre", ctypes.c_int32),
@@ -480,9 +479,6 @@ def tpmlp_fp8_quantize(T, fmt: int, transpose: bool, codes, amax, stream=None):
 # --- block operators ----------------------------------------------------------------
 F32, BF16 = 0, 1                                       # tpmlp_dtype
 NORMS = {"none": 0, "rms": 1, "layer": 2}              # tpmlp_norm
-EDGE_MAX_H = 32768                                     # TPMLP_EDGE_MAX_H
-ROUTE_MAX_EXPERTS, ROUTE_MAX_CHOICES = 512, 64         # TPMLP_ROUTE_MAX_*
-
 
 _KINDS = {}  # torch dtype -> tpmlp_dtype
 
