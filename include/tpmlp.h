@@ -46,6 +46,15 @@ extern "C" {
 
 typedef uint16_t tpmlp_bf16; /* raw bf16 bits */
 
+/* Activations of the gated MLP and of the 4-bit products. */
+typedef enum {
+  TPMLP_ACT_NONE = 0,
+  TPMLP_ACT_SILU = 1,    /* x / (1 + exp(-x)) */
+  TPMLP_ACT_GELU = 2,    /* x Phi(x) */
+  TPMLP_ACT_RELU = 3,    /* max(x, 0) */
+  TPMLP_ACT_SIGMOID = 4  /* 1 / (1 + exp(-x)) */
+} tpmlp_act;
+
 typedef enum {
   TPMLP_OK = 0,
   TPMLP_ERR_NULL = 1,        /* a required pointer is NULL */
@@ -481,6 +490,103 @@ tpmlp_status tpmlp_grad_clip(const void* const* grads, void* const* outs, const 
 tpmlp_status tpmlp_clip_grad_norm(const void* const* grads, void* const* outs, const int64_t* sizes,
                                   const int32_t* types, int n, float scale, float max_norm, float* norm, void* ws,
                                   size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* The gated block: a gated MLP, dropout, 8-bit inputs and 4-bit weights     */
+/* ------------------------------------------------------------------------ */
+/* None of these calls is among the kernel kinds that timing records. */
+
+/* The gated MLP, one rank's share:
+ *   [P_g | P_u] = X A,   h = act(P_g) (.) P_u,   Z = h B
+ * with A[H, 2 F] = [A_g | A_u] (a rank's column blocks of the gate and the up weight side by
+ * side) and B[F, H].  The conventions at the top hold (contiguous, 16-byte aligned), but M
+ * is any number from 0 to 2^23; H and F are positive multiples of 8 up to 2^23 and 2^22;
+ * act is a tpmlp_act other than TPMLP_ACT_NONE.  h, the kept P and the gradients of P pass
+ * through bf16 between the products, sums are float32. */
+size_t tpmlp_glu_fwd_workspace_bytes(int64_t M, int64_t H, int64_t F);
+
+/* Z[M,H] in z_type (tpmlp_dtype).  P_save (nullable) receives P[M, 2 F] in bf16 for a
+ * backward that keeps it. */
+tpmlp_status tpmlp_glu_fwd(const tpmlp_bf16* X, const tpmlp_bf16* A, const tpmlp_bf16* B, void* Z, int z_type,
+                           tpmlp_bf16* P_save, int act, int64_t M, int64_t H, int64_t F, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* `recompute` is 1 when P_saved will be NULL. */
+size_t tpmlp_glu_bwd_workspace_bytes(int64_t M, int64_t H, int64_t F, int recompute);
+
+/* From dZ[M,H] (bf16), with g = P_g, u = P_u and dh = dZ B^T:
+ *   dP = [dh u act'(g) | dh act(g)],  dB = h^T dZ,  dA = X^T dP,  dX = dP A^T
+ * dX[M,H] in dx_type, dA[H, 2 F] and dB[F, H] in dw_type.  P_saved NULL recomputes P.
+ * With M = 0, dA and dB are zero. */
+tpmlp_status tpmlp_glu_bwd(const tpmlp_bf16* dZ, const tpmlp_bf16* X, const tpmlp_bf16* A, const tpmlp_bf16* B,
+                           const tpmlp_bf16* P_saved, void* dX, int dx_type, void* dA, void* dB, int dw_type, int act,
+                           int64_t M, int64_t H, int64_t F, void* ws, size_t ws_bytes, void* stream);
+
+/* Dropout of a block's output with its bias, added to the residual stream (the conventions
+ * of the block operators hold from here on):
+ *   out = r + m (.) (y + bias) s
+ * m[i,j] is 1 where the element's 16-bit random number is at least d = round(65536 p), s =
+ * 65536 / (65536 - d) (0 for d = 65536).  The numbers are those of Philox 4x32 with ten
+ * rounds, key (seed low, seed high), counter (j / 8, first_row + i, site, step low): its
+ * words hold the numbers of eight columns, low half first.  state: device {seed, step}, read
+ * when the kernel runs, so that a captured graph can advance it.  A rank that holds rows
+ * first_row onward of a tensor drops the same elements as one that holds it all.  A
+ * dropped element's value (NaN too) reaches no output.  M from 0 to 2^23, H from 1 to 2^23,
+ * p from 0 to 1, first_row + M at most 2^32.  bias[H] (bias_type) and r (out_type) are
+ * nullable; out may be r, or y of one type with it (same address and stride). */
+tpmlp_status tpmlp_dropout_fwd(const void* y, int y_type, int64_t ld_y, const void* bias, int bias_type, const void* r,
+                               int64_t ld_r, void* out, int out_type, int64_t ld_out, int64_t M, int64_t H, float p,
+                               const uint64_t* state, uint32_t site, int64_t first_row, void* stream);
+
+/* Workspace bytes of tpmlp_dropout_bwd with db; 0 if the sizes are invalid. */
+size_t tpmlp_dropout_bwd_workspace_bytes(int64_t M, int64_t H);
+
+/* dy = m (.) dout s (may be dout itself if the types are one) and db[H] = the sum of dy's
+ * unrounded rows (float32; nullable, ws is unused then).  dout is r's gradient too. */
+tpmlp_status tpmlp_dropout_bwd(const void* dout, int out_type, int64_t ld_dout, void* dy, int y_type, int64_t ld_dy,
+                               float* db, int64_t M, int64_t H, float p, const uint64_t* state, uint32_t site,
+                               int64_t first_row, void* ws, size_t ws_bytes, void* stream);
+
+/* Scales of E4M3 codes. */
+typedef enum {
+  TPMLP_SCALE_ROW = 0, /* a float32 for each row */
+  TPMLP_SCALE_MX = 1   /* a byte e for every 32 values of a row, 2^(e - 127); 255 is not a number */
+} tpmlp_scale;
+
+/* tpmlp_edge_fwd with x as E4M3 codes[M,H] and scales, x = code * scale: [M] float32 (a
+ * row's largest magnitude / 448; 1 for a row of zeros, at least 2^-126), or [M, H / 32] bytes
+ * (the smallest power of two with a block's largest magnitude at most 448 times it; 1 for
+ * zeros; H a multiple of 32).  The codes are x / scale rounded to nearest even, from float32.
+ * NaN is NaN's code and counts for no scale. */
+tpmlp_status tpmlp_edge_fwd_fp8(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r, int64_t ld_r,
+                                void* r_out, int64_t ld_r_out, uint8_t* codes, int64_t ld_codes, void* scales,
+                                int64_t ld_scales, int scale_kind, void* stream);
+
+/* 4-bit weights W[N,K]: codes[N, K / 2], an E2M1 value (0, .5, 1, 1.5, 2, 3, 4, 6, and 8
+ * added to the code for the negatives) a half byte, the lower k in the low half; scales[N, K /
+ * 32], as TPMLP_SCALE_MX.  K is a multiple of 32 from 32 to 2^23, N from 1 to 2^23, codes
+ * 16-byte aligned.
+ *
+ * From bf16 weights W^T[K,N] (N contiguous, as the MLP's A_i[H,F_i] and B_i[F_i,H] lie): each
+ * block's scale is the smallest power of two with its largest magnitude at most 6 times it
+ * (1 for zeros; 255 if a value is not finite), codes are rounded to nearest even. */
+tpmlp_status tpmlp_fp4_quantize(const tpmlp_bf16* W, int64_t ld_w, int64_t K, int64_t N, uint8_t* codes,
+                                uint8_t* scales, void* stream);
+
+/* How X[M,K] of a 4-bit product is given. */
+typedef enum {
+  TPMLP_X_BF16 = 0,
+  TPMLP_X_E4M3_ROW = 1, /* codes with x_scales as TPMLP_SCALE_ROW */
+  TPMLP_X_E4M3_MX = 2   /* codes with x_scales[M, K / 32] as TPMLP_SCALE_MX */
+} tpmlp_x;
+
+/* Y[M,N] = act(X W^T), or with `gated` act(X W_g^T) (.) (X W_u^T) for W[2 N, K] = [W_g; W_u].
+ * For few tokens, whose time is the reading of W; any M from 0 to 2^23 is taken.  The products
+ * are exact, sums float32, Y (y_type) rounded once.  Rows of X start at multiples of 16 bytes
+ * (TPMLP_ERR_ALIGN) at most 2^23 elements apart.  No workspace. */
+tpmlp_status tpmlp_fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scales, const uint8_t* codes,
+                           const uint8_t* scales, void* Y, int y_type, int64_t ld_y, int act, int gated, int64_t M,
+                           int64_t N, int64_t K, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Kernel timing (measurement aid; not needed to compute anything)           */

@@ -3,7 +3,8 @@
 The compute path is the HIP library ``libtpmlp.so`` (C ABI in ``include/tpmlp.h``);
 ``_lib`` binds it with ctypes.  Importing the package does not load the library;
 the first call does, and fails loudly if it has not been built.  ``block`` holds the
-operators that stand around the MLP as objects (edge, expert route, gradient clipping).
+operators that stand around the MLP as objects (edge, expert route, gradient clipping), ``gated``
+the gated MLP, dropout and products with 4-bit weights.
 """
 from ._lib import (  # noqa: F401
     TpmlpError,
@@ -12,11 +13,21 @@ from ._lib import (  # noqa: F401
     tpmlp_bwd,
     tpmlp_bwd_workspace_bytes,
     tpmlp_clip_grad_norm,
+    tpmlp_dropout_bwd,
+    tpmlp_dropout_bwd_workspace_bytes,
+    tpmlp_dropout_fwd,
     tpmlp_edge_bwd,
     tpmlp_edge_bwd_workspace_bytes,
     tpmlp_edge_fwd,
+    tpmlp_edge_fwd_fp8,
+    tpmlp_fp4_fwd,
+    tpmlp_fp4_quantize,
     tpmlp_fwd,
     tpmlp_fwd_workspace_bytes,
+    tpmlp_glu_bwd,
+    tpmlp_glu_bwd_workspace_bytes,
+    tpmlp_glu_fwd,
+    tpmlp_glu_fwd_workspace_bytes,
     tpmlp_grad_clip,
     tpmlp_grad_sumsq,
     tpmlp_grad_workspace_bytes,
@@ -37,3 +48,4 @@ from ._lib import (  # noqa: F401
     tpmlp_tp_workspace_bytes,
 )
 from .block import Edge, GradClip, Route  # noqa: F401
+from .gated import Dropout, Fp4Linear, GatedMLP  # noqa: F401

@@ -91,6 +91,18 @@ _SIGS = {
     "tpmlp_grad_sumsq": ([_vp, _vp, _vp, _int, _vp, _vp, _sz, _vp], _int),
     "tpmlp_grad_clip": ([_vp, _vp, _vp, _vp, _int, _vp, ctypes.c_float, ctypes.c_float, _vp, _vp], _int),
     "tpmlp_clip_grad_norm": ([_vp, _vp, _vp, _vp, _int, ctypes.c_float, ctypes.c_float, _vp, _vp, _sz, _vp], _int),
+    "tpmlp_glu_fwd_workspace_bytes": ([_i64, _i64, _i64], _sz),
+    "tpmlp_glu_fwd": ([_vp, _vp, _vp, _vp, _int, _vp, _int, _i64, _i64, _i64, _vp, _sz, _vp], _int),
+    "tpmlp_glu_bwd_workspace_bytes": ([_i64, _i64, _i64, _int], _sz),
+    "tpmlp_glu_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _int, _int, _i64, _i64, _i64, _vp, _sz, _vp], _int),
+    "tpmlp_dropout_fwd": ([_vp, _int, _i64, _vp, _int, _vp, _i64, _vp, _int, _i64, _i64, _i64, ctypes.c_float, _vp,
+                           ctypes.c_uint32, _i64, _vp], _int),
+    "tpmlp_dropout_bwd_workspace_bytes": ([_i64, _i64], _sz),
+    "tpmlp_dropout_bwd": ([_vp, _int, _i64, _vp, _int, _i64, _vp, _i64, _i64, ctypes.c_float, _vp, ctypes.c_uint32, _i64,
+                           _vp, _sz, _vp], _int),
+    "tpmlp_edge_fwd_fp8": ([_EP, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp], _int),
+    "tpmlp_fp4_quantize": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp], _int),
+    "tpmlp_fp4_fwd": ([_vp, _int, _i64, _vp, _vp, _vp, _vp, _int, _i64, _int, _int, _i64, _i64, _i64, _vp], _int),
     "tpmlp_timing_begin": ([_int], _int),
     "tpmlp_timing_begin_kinds": ([_int, ctypes.c_uint], _int),
     "tpmlp_timing_end": ([ctypes.POINTER(_int), ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_int)], _int),
@@ -780,6 +792,194 @@ def tpmlp_clip_grad_norm(table: GradTable, max_norm: float, norm, ws, scale: flo
                                     _stream(stream))
     if st:
         _check(st, "tpmlp_clip_grad_norm")
+
+
+# --- the gated block ------------------------------------------------------------------
+ACTS = {"none": 0, "silu": 1, "gelu": 2, "relu": 3, "sigmoid": 4}  # tpmlp_act
+SCALE_ROW, SCALE_MX = 0, 1                                         # tpmlp_scale
+X_BF16, X_E4M3_ROW, X_E4M3_MX = 0, 1, 2                            # tpmlp_x
+
+
+def _on_gpu(t, name):
+    if t is not None and not t.is_cuda:
+        _host(t, name)
+    return t
+
+
+def _dense(t, shape, name, kind=None):
+    """Pointer of a contiguous tensor of this shape and, if given, tpmlp_dtype."""
+    if t is None:
+        return None
+    _on_gpu(t, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if kind is not None and _dtype(t, name) != kind:
+        raise TypeError(f"{name} must be {'float32' if kind == F32 else 'bf16'}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _glu_sizes(A, B):
+    (F, H), (h, f2) = B.shape, A.shape
+    if h != H or f2 != 2 * F:
+        raise ValueError(f"A has shape {tuple(A.shape)}, expected {(H, 2 * F)} for B {tuple(B.shape)}")
+    return H, F
+
+
+def tpmlp_glu_fwd_workspace_bytes(M: int, H: int, F: int) -> int:
+    return lib().tpmlp_glu_fwd_workspace_bytes(M, H, F)
+
+
+def tpmlp_glu_bwd_workspace_bytes(M: int, H: int, F: int, recompute: bool) -> int:
+    return lib().tpmlp_glu_bwd_workspace_bytes(M, H, F, int(bool(recompute)))
+
+
+def tpmlp_glu_fwd(X, A, B, Z, P_save, act: str, ws, stream=None):
+    """Z[M,H] = (act(P_g) * P_u) B with P = X A; A[H, 2F], B[F,H], X bf16; Z float32 or bf16."""
+    H, F = _glu_sizes(A, B)
+    M = X.shape[0]
+    pw, nw = _ws(ws)
+    st = lib().tpmlp_glu_fwd(_dense(X, (M, H), "X", BF16), _dense(A, (H, 2 * F), "A", BF16), _dense(B, (F, H), "B", BF16),
+                             _dense(Z, (M, H), "Z"), _dtype(Z, "Z"), _dense(P_save, (M, 2 * F), "P_save", BF16), ACTS[act], M,
+                             H, F, pw, nw, _stream(stream))
+    if st:
+        _check(st, "tpmlp_glu_fwd")
+
+
+def tpmlp_glu_bwd(dZ, X, A, B, P_saved, dX, dA, dB, act: str, ws, stream=None):
+    """The gated MLP's gradients; dX, and dA with dB, float32 or bf16; P_saved None recomputes P."""
+    H, F = _glu_sizes(A, B)
+    M = X.shape[0]
+    kind = _dtype(dA, "dA")
+    pw, nw = _ws(ws)
+    st = lib().tpmlp_glu_bwd(_dense(dZ, (M, H), "dZ", BF16), _dense(X, (M, H), "X", BF16), _dense(A, (H, 2 * F), "A", BF16),
+                             _dense(B, (F, H), "B", BF16), _dense(P_saved, (M, 2 * F), "P_saved", BF16),
+                             _dense(dX, (M, H), "dX"), _dtype(dX, "dX"), _dense(dA, (H, 2 * F), "dA"),
+                             _dense(dB, (F, H), "dB", kind), kind, ACTS[act], M, H, F, pw, nw, _stream(stream))
+    if st:
+        _check(st, "tpmlp_glu_bwd")
+
+
+def _state(state):
+    import torch
+    if state.dtype not in (torch.int64, torch.uint64) or state.numel() != 2 or not state.is_contiguous():
+        raise TypeError("state must be two contiguous int64 values, the seed and the step")
+    return _on_gpu(state, "state").data_ptr()
+
+
+def tpmlp_dropout_fwd(y, bias, r, out, p: float, state, site: int = 0, first_row: int = 0, stream=None):
+    """out = r + mask * (y + bias) / (1 - p); y float32 or bf16, out and r of one type, bias and r nullable."""
+    M, H = y.shape
+    kind = _dtype(out, "out")
+    py, ly = _rows(y, (M, H), "y")
+    po, lo = _rows(out, (M, H), "out")
+    pr, lr = _rows(r, (M, H), "r", kind)
+    st = lib().tpmlp_dropout_fwd(py, _dtype(y, "y"), ly, _flat(bias, H, bias.dtype, "bias") if bias is not None else None,
+                                 _dtype(bias, "bias") if bias is not None else F32, pr, lr, po, kind, lo, M, H, p,
+                                 _state(state), _u32(site, "site"), first_row, _stream(stream))
+    if st:
+        _check(st, "tpmlp_dropout_fwd")
+
+
+def _u32(v: int, name: str) -> int:
+    if not 0 <= v < 1 << 32:  # ctypes would take its low bits
+        raise ValueError(f"{name} must be from 0 to 2^32 - 1")
+    return v
+
+
+def tpmlp_dropout_bwd_workspace_bytes(M: int, H: int) -> int:
+    return lib().tpmlp_dropout_bwd_workspace_bytes(M, H)
+
+
+def tpmlp_dropout_bwd(dout, dy, db, p: float, state, site: int = 0, first_row: int = 0, ws=None, stream=None):
+    """dy = mask * dout / (1 - p); db[H] (float32, nullable) = the sum of its rows."""
+    import torch
+    M, H = dout.shape
+    pg, lg = _rows(dout, (M, H), "dout")
+    py, ly = _rows(dy, (M, H), "dy")
+    pw, nw = _ws(ws)
+    st = lib().tpmlp_dropout_bwd(pg, _dtype(dout, "dout"), lg, py, _dtype(dy, "dy"), ly, _flat(db, H, torch.float32, "db"), M, H,
+                                 p, _state(state), _u32(site, "site"), first_row, pw, nw, _stream(stream))
+    if st:
+        _check(st, "tpmlp_dropout_bwd")
+
+
+def _bytes(t, shape, name):
+    """(pointer, row stride) of a [rows, columns] tensor of one-byte values with contiguous columns."""
+    if t.element_size() != 1:
+        raise TypeError(f"{name} must hold one-byte values, got {t.dtype}")
+    return _rows(t, shape, name)
+
+
+def _scales(t, M, blocks, name):
+    """(pointer, row stride, tpmlp_scale) of the scales of [M, 32 blocks] codes."""
+    import torch
+    if t.dtype == torch.float32:
+        return _flat(t, M, torch.float32, name), 0, SCALE_ROW
+    p, ld = _bytes(t, (M, blocks), name)
+    return p, ld, SCALE_MX
+
+
+def tpmlp_edge_fwd_fp8(d: EdgeDesc, y, r, r_out, codes, scales, stream=None):
+    """tpmlp_edge_fwd with x as E4M3 codes [M,H] (one-byte values) and scales: float32 [M], or a byte
+    for every 32 values, [M, H / 32]."""
+    M, H = r.shape[0], d.H
+    if d.gate_tokens is not None:
+        _check_gate(d, M)
+    c = _of_call(d, M)
+    c.r_type = _dtype(r, "r")
+    pr, lr = _rows(r, (M, H), "r")
+    py = ly = None
+    if y is not None:
+        c.y_type = _dtype(y, "y")
+        py, ly = _rows(y, (M, H), "y")
+    po, lo = _rows(r_out, (M, H), "r_out", c.r_type)
+    pc, lc = _bytes(codes, (M, H), "codes")
+    ps, ls, kind = _scales(scales, M, H // 32, "scales")
+    st = lib().tpmlp_edge_fwd_fp8(ctypes.byref(c), py, ly or 0, pr, lr, po, lo, pc, lc, ps, ls, kind, _stream(stream))
+    if st:
+        _check(st, "tpmlp_edge_fwd_fp8")
+
+
+def tpmlp_fp4_quantize(W, codes, scales, stream=None):
+    """E2M1 codes [N, K/2] and scales [N, K/32] (one-byte values) of bf16 weights W[K,N]."""
+    K, N = W.shape
+    pw, lw = _rows(W, (K, N), "W", BF16)
+    pc, lc = _bytes(codes, (N, K // 2), "codes")
+    ps, ls = _bytes(scales, (N, K // 32), "scales")
+    if lc or ls:
+        raise ValueError("codes and scales must be contiguous")
+    _check(lib().tpmlp_fp4_quantize(pw, lw, K, N, pc, ps, _stream(stream)), "tpmlp_fp4_quantize")
+
+
+def tpmlp_fp4_fwd(X, x_scales, codes, scales, Y, act: str = "none", gated: bool = False, stream=None):
+    """Y[M,N] = act(X W^T), or act(X W_g^T) * (X W_u^T) with W = [W_g; W_u]; X[M,K] bf16, or E4M3 codes
+    (one-byte values) with x_scales as tpmlp_edge_fwd_fp8 writes them; Y float32 or bf16."""
+    (M, K), N = X.shape, Y.shape[1]
+    rows = 2 * N if gated else N
+    ps, kind = None, X_BF16
+    if X.element_size() == 1:
+        if x_scales is None:
+            raise ValueError("X in E4M3 needs x_scales")
+        px, lx = _rows(X, (M, K), "X")
+        ps, ls, scale = _scales(x_scales, M, K // 32, "x_scales")
+        if ls:
+            raise ValueError("x_scales must be contiguous")
+        kind = X_E4M3_MX if scale == SCALE_MX else X_E4M3_ROW
+    else:
+        px, lx = _rows(X, (M, K), "X", BF16)
+        if x_scales is not None:
+            raise ValueError("x_scales is given with a bf16 X")
+    pc, lc = _bytes(codes, (rows, K // 2), "codes")
+    pk, lk = _bytes(scales, (rows, K // 32), "scales")
+    if lc or lk:
+        raise ValueError("codes and scales must be contiguous")
+    py, ly = _rows(Y, (M, N), "Y")
+    st = lib().tpmlp_fp4_fwd(px, kind, lx, ps, pc, pk, py, _dtype(Y, "Y"), ly, ACTS[act], int(bool(gated)), M, N, K,
+                             _stream(stream))
+    if st:
+        _check(st, "tpmlp_fp4_fwd")
 
 
 def tpmlp_timing_begin(capacity: int):

@@ -6,7 +6,7 @@ Each holds its parameters, index buffers and workspace; every call takes the cal
 and outputs, enqueues kernels on a stream (the current one by default) and returns.  No
 arithmetic happens here.  Buffers and workspaces belong to one stream at a time: a program
 that uses an object on two streams orders them itself, and two threads do not call one
-object at once, but for Edge.forward, which holds no buffer.  Route and GradClip make theirs
+object at once, but for Edge.forward and forward_fp8, which hold no buffer.  Route and GradClip make theirs
 when they are made, on the current stream, as torch does any tensor's: a program that uses
 them on another one makes them under it, or orders the two.  Edge makes its backward's with
 the first call of a size, on the stream of that call.
@@ -52,6 +52,12 @@ class Edge:
         """y [M,H] float32 or bf16 (None: no block before); r, r_out [M,H] (r_out may be r);
         x [M,H] bf16 (None without a norm before the next block)."""
         L.tpmlp_edge_fwd(self.desc, y, r, r_out, x, stream)
+
+    def forward_fp8(self, y, r, r_out, codes, scales, stream=None):
+        """forward with x in 8 bits: E4M3 codes [M,H] (float8_e4m3fn or uint8) and scales, x = code *
+        scale: float32 [M], one a row, or [M, H / 32] bytes (uint8 or float8_e8m0fnu), a power of two
+        for every 32 values.  Either feeds Fp4Linear."""
+        L.tpmlp_edge_fwd_fp8(self.desc, y, r, r_out, codes, scales, stream)
 
     def backward(self, y, r_out, dr_out, dx, dr, dy, stream=None):
         """Gradients from r_out as the forward wrote it, dr_out (None: zeros) and dx [M,H]

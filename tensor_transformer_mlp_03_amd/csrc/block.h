@@ -38,6 +38,11 @@ struct EdgeFwdArgs {
   int64_t M, gate_rows, first_row;  // rows first_row .. M - 1, up to a launch's
   int H, post, pre, p_bf16, nt;
   float alpha, eps;
+  // Output in 8 bits: x holds codes (rows of ld_x bytes), scales a float32 a row, or,
+  // with scale_mx, H / 32 powers of two a row (rows of ld_scales).
+  void* scales;
+  int64_t ld_scales;
+  int scale_mx;
 };
 
 struct EdgeBwdArgs {
@@ -88,6 +93,7 @@ EdgeBwdPlan plan_edge_bwd(int64_t M, int H, int64_t gate_rows, bool layer);
 // y_type -1: no y.  full: H is a multiple of 4 and every row of every matrix and
 // vector starts at a multiple of four elements.
 hipError_t launch_edge_fwd(EdgeFwdArgs a, int y_type, int r_type, bool full, hipStream_t s);
+hipError_t launch_edge_fwd_fp8(EdgeFwdArgs a, int y_type, int r_type, bool full, hipStream_t s);
 hipError_t launch_edge_bwd(const EdgeBwdArgs& a, const EdgeBwdPlan& p, int y_type, int r_type, bool full, hipStream_t s);
 hipError_t launch_edge_finish(const EdgeFinishArgs& a, hipStream_t s);
 

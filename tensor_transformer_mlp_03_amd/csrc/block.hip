@@ -2,7 +2,7 @@
 // before any HIP call, and launches.  Nothing thrown crosses the boundary.
 
 #include "block.h"
-#include "host.h"
+#include "checks.h"
 
 #include <algorithm>
 #include <cmath>
@@ -14,80 +14,9 @@
 namespace tpmlp {
 namespace {
 
-constexpr int64_t MAX_TOKENS = int64_t(1) << 23;  // as the MLP's M
 constexpr int64_t MAX_ROWS = INT32_MAX;           // of a sorted buffer
 constexpr int64_t MAX_H = int64_t(1) << 23;
 constexpr int64_t MAX_GATES = int64_t(1) << 21;   // rows of the gate: a workgroup of the backward each
-constexpr int64_t MAX_LD = int64_t(1) << 31;
-
-// Runs an entry point's body; an exception (the host is out of memory while it
-// writes an error's text) becomes a status.
-template <class F>
-tpmlp_status guarded(F&& body) {
-  try {
-    g_last_error.clear();
-    return body();
-  } catch (...) {
-    return TPMLP_ERR_HIP;
-  }
-}
-
-#define TRY(x)                          \
-  do {                                  \
-    if (tpmlp_status st_ = (x)) return st_; \
-  } while (0)
-
-// A strided matrix that a call reads or writes (p NULL: absent).
-struct Mat {
-  const void* p;
-  int64_t rows, cols, ld;
-  int elem;  // bytes
-  const char* name;
-};
-
-int size_of(int type) { return type == TPMLP_BF16 ? 2 : 4; }
-bool type_ok(int t) { return t == TPMLP_F32 || t == TPMLP_BF16; }
-
-bool empty(const Mat& m) { return !m.p || m.rows < 1 || m.cols < 1; }
-
-bool overlap(const Mat& a, const Mat& b) {
-  if (empty(a) || empty(b)) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  const uint64_t pa = uint64_t(a.ld) * a.elem, pb = uint64_t(b.ld) * b.elem;
-  const uint64_t wa = uint64_t(a.cols) * a.elem, wb = uint64_t(b.cols) * b.elem;
-  if (a0 >= b0 + (b.rows - 1) * pb + wb || b0 >= a0 + (a.rows - 1) * pa + wa) return false;
-  if (pa != pb) return true;
-  // Equal pitches: column blocks of one buffer are disjoint if their columns are.
-  const uint64_t off = b0 >= a0 ? (b0 - a0) % pa : (pa - (a0 - b0) % pa) % pa;
-  return off < wa || off + wb > pa;
-}
-
-// Pointer and stride of a matrix that has to be there unless it has no elements.
-tpmlp_status check_mat(const Mat& m) {
-  if (m.ld < m.cols || m.ld > MAX_LD) return fail(TPMLP_ERR_SHAPE, std::string("ld of ") + m.name + " is below its row length or above 2^31");
-  if (m.rows > 0 && m.cols > 0 && !m.p) return fail(TPMLP_ERR_NULL, std::string(m.name) + " is NULL");
-  if (reinterpret_cast<uintptr_t>(m.p) % m.elem) return fail(TPMLP_ERR_ALIGN, std::string(m.name) + " is not aligned to its elements");
-  return TPMLP_OK;
-}
-
-// Each output must be disjoint from every other matrix.  `same`: (output, input)
-// indices that may also be one matrix.
-template <size_t NO, size_t NI>
-tpmlp_status check_overlaps(const Mat (&outs)[NO], const Mat (&ins)[NI], int same_out = -1, int same_in = -1) {
-  for (size_t i = 0; i < NO; ++i) {
-    for (size_t j = i + 1; j < NO; ++j)
-      if (overlap(outs[i], outs[j])) return fail(TPMLP_ERR_ALIAS, std::string(outs[i].name) + " overlaps " + outs[j].name);
-    for (size_t j = 0; j < NI; ++j) {
-      if ((int)i == same_out && (int)j == same_in && outs[i].p == ins[j].p && outs[i].ld == ins[j].ld) continue;
-      if (overlap(outs[i], ins[j])) return fail(TPMLP_ERR_ALIAS, std::string(outs[i].name) + " overlaps " + ins[j].name);
-    }
-  }
-  return TPMLP_OK;
-}
-
-hipStream_t stream_of(void* s) { return static_cast<hipStream_t>(s); }
-
-tpmlp_status launched(hipError_t e, const char* what) { return e == hipSuccess ? TPMLP_OK : hip_fail(e, what); }
 
 // ---------------------------------------------------------------------------
 // Edge
@@ -97,7 +26,6 @@ int64_t gate_rows_of(const tpmlp_edge& e) {
 }
 int64_t gate_groups(const tpmlp_edge& e) { return e.gate ? (e.M + gate_rows_of(e) - 1) / gate_rows_of(e) : 0; }
 bool has_layer(const tpmlp_edge& e) { return e.post == TPMLP_NORM_LAYER || e.pre == TPMLP_NORM_LAYER; }
-int64_t ld_or(int64_t ld, int64_t cols) { return ld ? ld : cols; }
 
 tpmlp_status check_edge(const tpmlp_edge* e, bool has_y) {
   if (!e) return fail(TPMLP_ERR_NULL, "the edge is NULL");
@@ -130,25 +58,6 @@ tpmlp_status check_edge(const tpmlp_edge* e, bool has_y) {
   return TPMLP_OK;
 }
 
-// Whether every row of the matrix starts at a multiple of `n` elements.
-bool starts_at(const Mat& m, int n) {
-  return empty(m) || (reinterpret_cast<uintptr_t>(m.p) % (n * m.elem) == 0 && (m.rows < 2 || m.ld % n == 0));
-}
-bool quads(const Mat& m) { return starts_at(m, 4); }
-template <size_t NO, size_t NI>
-bool all_quads(int64_t H, const Mat (&outs)[NO], const Mat (&ins)[NI]) {
-  return H % 4 == 0 && std::all_of(outs, outs + NO, quads) && std::all_of(ins, ins + NI, quads);
-}
-
-// Whether a launch over these matrices moves more than BLOCK_NT_BYTES.
-template <size_t NO, size_t NI>
-bool past_caches(const Mat (&outs)[NO], const Mat (&ins)[NI]) {
-  int64_t bytes = 0;
-  for (const Mat& m : outs) bytes += empty(m) ? 0 : m.rows * m.cols * m.elem;
-  for (const Mat& m : ins) bytes += empty(m) ? 0 : m.rows * m.cols * m.elem;
-  return bytes > BLOCK_NT_BYTES;
-}
-
 // The edge's parameters as inputs of the overlap check.
 #define EDGE_PARAMS(e)                                                                                  \
   {(e).w_post, 1, (e).H, (e).H, size_of((e).param_type), "w_post"},                                     \
@@ -158,20 +67,40 @@ bool past_caches(const Mat (&outs)[NO], const Mat (&ins)[NI]) {
     (e).gate, gate_groups(e), (e).H, ld_or((e).ld_gate, (e).H), size_of((e).param_type), "gate"         \
   }
 
+// The forward's output in 8 bits: codes in place of x, with scales.
+struct EdgeCodes {
+  uint8_t* codes;
+  int64_t ld;
+  void* scales;
+  int64_t ld_scales;
+  int kind;
+};
+
 tpmlp_status edge_fwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r, int64_t ld_r, void* r_out,
-                      int64_t ld_r_out, tpmlp_bf16* x, int64_t ld_x, void* stream) {
+                      int64_t ld_r_out, tpmlp_bf16* x, int64_t ld_x, const EdgeCodes* c, void* stream) {
   const bool has_y = y != nullptr || (e && e->M == 0);
   TRY(check_edge(e, has_y));
   const int64_t M = e->M, H = e->H;
   const int ys = size_of(e->y_type), rs = size_of(e->r_type);
   if (e->pre == TPMLP_NORM_NONE && x) return fail(TPMLP_ERR_SHAPE, "x is given without a norm before the next block");
+  Mat mx{x, M, H, ld_or(ld_x, H), 2, "x"}, ms{nullptr, 0, 1, 1, 1, "scales"};
+  if (c) {
+    if (e->pre == TPMLP_NORM_NONE) return fail(TPMLP_ERR_SHAPE, "codes need a norm before the next block");
+    if (c->kind != TPMLP_SCALE_ROW && c->kind != TPMLP_SCALE_MX) return fail(TPMLP_ERR_SHAPE, "scale_kind must be a tpmlp_scale");
+    if (c->kind == TPMLP_SCALE_MX && H % 32) return fail(TPMLP_ERR_SHAPE, "H must be a multiple of 32 with TPMLP_SCALE_MX");
+    if (c->kind == TPMLP_SCALE_ROW && c->ld_scales) return fail(TPMLP_ERR_SHAPE, "ld_scales must be 0 with TPMLP_SCALE_ROW");
+    mx = Mat{c->codes, M, H, ld_or(c->ld, H), 1, "codes"};
+    if (c->kind == TPMLP_SCALE_MX) ms = Mat{c->scales, M, H / 32, ld_or(c->ld_scales, H / 32), 1, "scales"};
+    else ms = Mat{c->scales, M > 0 ? 1 : 0, M, M, 4, "scales"};
+    TRY(check_mat(ms));
+  }
   const Mat my{y, M, H, ld_or(ld_y, H), ys, "y"}, mr{r, M, H, ld_or(ld_r, H), rs, "r"};
-  const Mat mo{r_out, M, H, ld_or(ld_r_out, H), rs, "r_out"}, mx{x, M, H, ld_or(ld_x, H), 2, "x"};
+  const Mat mo{r_out, M, H, ld_or(ld_r_out, H), rs, "r_out"};
   TRY(check_mat(mr));
   if (y) TRY(check_mat(my));
   if (r_out || e->pre == TPMLP_NORM_NONE) TRY(check_mat(mo));
   if (e->pre != TPMLP_NORM_NONE) TRY(check_mat(mx));
-  const Mat outs[] = {mo, mx}, ins[] = {mr, my, EDGE_PARAMS(*e)};
+  const Mat outs[] = {mo, mx, ms}, ins[] = {mr, my, EDGE_PARAMS(*e)};
   TRY(check_overlaps(outs, ins, 0, 0));
   if (M == 0) return TPMLP_OK;
   TRY(check_device());
@@ -179,7 +108,7 @@ tpmlp_status edge_fwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
   a.y = y;
   a.r = r;
   a.r_out = r_out;
-  a.x = x;
+  a.x = c ? reinterpret_cast<uint16_t*>(c->codes) : x;
   a.w_post = e->w_post;
   a.b_post = e->b_post;
   a.gate = e->gate;
@@ -198,8 +127,18 @@ tpmlp_status edge_fwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const vo
   a.p_bf16 = e->param_type == TPMLP_BF16;
   a.alpha = e->alpha;
   a.eps = e->eps;
-  a.nt = past_caches(outs, ins);
-  return launched(launch_edge_fwd(a, y ? e->y_type : -1, e->r_type, all_quads(H, outs, ins), stream_of(stream)), "tpmlp_edge_fwd launch");
+  const int y_type = y ? e->y_type : -1;
+  if (c) {
+    a.scales = c->scales;
+    a.ld_scales = ms.ld;
+    a.scale_mx = c->kind == TPMLP_SCALE_MX;
+    a.nt = past_caches(outs, ins);
+    const Mat rows[] = {mo, mx};
+    return launched(launch_edge_fwd_fp8(a, y_type, e->r_type, all_quads(H, rows, ins), stream_of(stream)), "tpmlp_edge_fwd_fp8 launch");
+  }
+  const Mat rows[] = {mo, mx};
+  a.nt = past_caches(rows, ins);
+  return launched(launch_edge_fwd(a, y_type, e->r_type, all_quads(H, rows, ins), stream_of(stream)), "tpmlp_edge_fwd launch");
 }
 
 tpmlp_status edge_bwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r_out, int64_t ld_r_out,
@@ -635,7 +574,16 @@ extern "C" {
 
 tpmlp_status tpmlp_edge_fwd(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r, int64_t ld_r, void* r_out,
                             int64_t ld_r_out, tpmlp_bf16* x, int64_t ld_x, void* stream) {
-  return guarded([&] { return edge_fwd(e, y, ld_y, r, ld_r, r_out, ld_r_out, x, ld_x, stream); });
+  return guarded([&] { return edge_fwd(e, y, ld_y, r, ld_r, r_out, ld_r_out, x, ld_x, nullptr, stream); });
+}
+
+tpmlp_status tpmlp_edge_fwd_fp8(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r, int64_t ld_r, void* r_out,
+                                int64_t ld_r_out, uint8_t* codes, int64_t ld_codes, void* scales, int64_t ld_scales,
+                                int scale_kind, void* stream) {
+  return guarded([&] {
+    const EdgeCodes c{codes, ld_codes, scales, ld_scales, scale_kind};
+    return edge_fwd(e, y, ld_y, r, ld_r, r_out, ld_r_out, nullptr, 0, &c, stream);
+  });
 }
 
 size_t tpmlp_edge_bwd_workspace_bytes(const tpmlp_edge* e) {

@@ -201,8 +201,28 @@ __device__ __forceinline__ float wave_sum(float v) {
   const uint32_t h0 = halves[0], h1 = halves[1];
   return __builtin_bit_cast(float, h0) + __builtin_bit_cast(float, h1);
 }
+// The largest of eight neighbouring lanes' values, and of the wave's, by the same moves.
+template <int CTRL>
+__device__ __forceinline__ float max_dpp(float v) {
+  const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true);
+  return fmaxf(v, __builtin_bit_cast(float, o));
+}
+__device__ __forceinline__ float max8(float v) { return max_dpp<0x141>(max_dpp<0x4E>(max_dpp<0xB1>(v))); }
+__device__ __forceinline__ float wave_max_dpp(float v) {
+  v = max_dpp<0x140>(max8(v));
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  const auto rows = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t r0 = rows[0], r1 = rows[1];
+  v = fmaxf(__builtin_bit_cast(float, r0), __builtin_bit_cast(float, r1));
+  const uint32_t c = __builtin_bit_cast(uint32_t, v);
+  const auto halves = __builtin_amdgcn_permlane32_swap(c, c, false, false);
+  const uint32_t h0 = halves[0], h1 = halves[1];
+  return fmaxf(__builtin_bit_cast(float, h0), __builtin_bit_cast(float, h1));
+}
 #else
 __device__ inline float wave_sum(float v) { return v; }
+__device__ inline float max8(float v) { return v; }
+__device__ inline float wave_max_dpp(float v) { return v; }
 #endif
 
 __device__ __forceinline__ double wave_sum(double v) {
@@ -246,6 +266,19 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float* slot, int wave) {
     for (int j = j0; j < N && j < j0 + PER; ++j) v[j] = scalar(x, (j - j0) * W);
   }
 #endif
+}
+
+// The largest of a value over the W waves that share a row, on every lane; `slot` as above,
+// W floats.
+template <int W>
+__device__ __forceinline__ float row_max(float v, float* slot, int wave) {
+  v = wave_max_dpp(v);
+  if (W == 1) return v;
+  if ((threadIdx.x & 63) == 0) slot[wave] = v;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < W; ++k) v = fmaxf(v, slot[k]);
+  return v;
 }
 
 }  // namespace tpmlp

@@ -55,7 +55,18 @@ enum Epi : int {
   // them in order, as two launches of EPI_F32 / EPI_F32_ACC would:
   EPI_F32_PAIR = 5,      // out_f32[m,n] = acc0 + acc1
   EPI_F32_ACC_PAIR = 6,  // out_f32[m,n] = (out_f32[m,n] + acc0) + acc1
+  // The gated MLP (unsplit; gemm_glu.hip), plus a tpmlp_act.  EPI_GLU: B has 2 N
+  // columns, N gate columns and then N up columns; a tile of BN columns takes BN / 2 of
+  // each, in blocks of 32, so that a lane of the epilogue holds both of a pair:
+  //   out_bf16[m,n] = act(acc[m,n]) acc[m,N+n]; if out2: out2_bf16[m, n and N+n] = acc (rows of ldt)
+  EPI_GLU = 16,
+  // EPI_DGLU: with g = aux_bf16[m,n], u = aux_bf16[m,N+n], acc the gradient of act(g) u:
+  //   out_bf16[m,n] = acc u act'(g), out_bf16[m,N+n] = acc act(g); transposed:
+  //   out2_bf16[n,m] = act(g) u, zeros for the rows m that pad M to a multiple of 8
+  EPI_DGLU = 32,
 };
+constexpr bool is_glu(int epi) { return epi >= EPI_GLU && epi < EPI_DGLU; }
+constexpr bool is_dglu(int epi) { return epi >= EPI_DGLU; }
 
 // Largest output row stride of an EPI_F32_ACC product (its loads of the running
 // sum take 32-bit byte offsets within a 64-row band).
@@ -110,6 +121,10 @@ enum TileCfg : int {
 hipError_t launch_gemm(TileCfg tile, Layout la, Layout lb, Epi epi, const GemmArgs& args,
                        int splits, hipStream_t stream);
 
+// The gated MLP's products (EPI_GLU or EPI_DGLU without the activation; dglu takes B
+// K-contiguous), unsplit.  act: a tpmlp_act other than TPMLP_ACT_NONE.
+hipError_t launch_gemm_glu(TileCfg tile, Layout lb, bool dglu, int act, const GemmArgs& args, hipStream_t stream);
+
 // out[j] = sum over i < n_parts of parts[i][j], left to right, j < n (n % 4 == 0).
 hipError_t launch_sum(const float* const* parts, int n_parts, float* out, int64_t n,
                       hipStream_t stream);
@@ -127,8 +142,8 @@ hipError_t launch_splitk_epilogue(Epi epi, const float* part, int splits, int64_
 
 // out[c][r] = in[r][c] for a bf16 matrix in[R][C] with rows of ld_in >= C
 // elements, into out with rows of ld_out >= R elements (0: R), so that the
-// transpose can be a column block of a wider matrix (R, C, ld_in, ld_out
-// multiples of 8).
+// transpose can be a column block of a wider matrix (C, ld_in, ld_out multiples of
+// 8; for an R that is none, ld_out >= R rounded up, and out is zero up to there).
 hipError_t launch_transpose(const uint16_t* in, int64_t R, int64_t C, int64_t ld_in, uint16_t* out,
                             hipStream_t stream, int64_t ld_out = 0);
 // Two matrices of the same shape and strides in one launch (in1 null: one).

@@ -112,6 +112,46 @@ __device__ __forceinline__ float dgelu_f32(float dg, uint16_t p_bits) {
   return dg * __builtin_fmaf(p, n.f, cdf);
 }
 
+// The activations of the gated MLP and of the 4-bit products (tpmlp_act).  The sigmoid is
+// 1 / (1 + exp(-x)) on the hardware's exp2 and reciprocal (an ulp each): exp(-x) may
+// overflow to infinity, whose reciprocal is the 0 that it stands for.
+__device__ __forceinline__ float sigmoid_f32(float x) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -1.4426950408889634f));
+}
+
+template <int ACT>
+__device__ __forceinline__ float act_f32(float x) {
+  if constexpr (ACT == 1) return x * sigmoid_f32(x);
+  else if constexpr (ACT == 2) return gelu_f32(x);
+  else if constexpr (ACT == 3) return x > 0.0f ? x : x * 0.0f;  // NaN stays NaN
+  else if constexpr (ACT == 4) return sigmoid_f32(x);
+  else return x;
+}
+
+// act(x) and its derivative.
+template <int ACT>
+__device__ __forceinline__ void act_grad_f32(float x, float& a, float& da) {
+  if constexpr (ACT == 1) {
+    const float s = sigmoid_f32(x);
+    a = x * s;
+    da = s * __builtin_fmaf(x, 1.0f - s, 1.0f);
+  } else if constexpr (ACT == 2) {
+    const NormalTailDensity n = normal_tail_density(x);
+    const float cdf = x >= 0.0f ? 1.0f - n.he : n.he;
+    a = x * cdf;
+    da = __builtin_fmaf(x, n.f, cdf);
+  } else if constexpr (ACT == 3) {
+    a = x > 0.0f ? x : x * 0.0f;
+    da = x > 0.0f ? 1.0f : 0.0f;
+  } else if constexpr (ACT == 4) {
+    a = sigmoid_f32(x);
+    da = a * (1.0f - a);
+  } else {
+    a = x;
+    da = 1.0f;
+  }
+}
+
 // ---------------------------------------------------------------------------
 // FP8 operands ("大模型训练" notes §6.1: E4M3, 4 exponent and 3 mantissa bits,
 // range +-448; E5M2, 5 and 2 bits, range +-57344) under per-tensor scaling: a

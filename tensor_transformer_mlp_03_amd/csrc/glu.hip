@@ -1,0 +1,357 @@
+// The gated MLP, Z = h B with h = act(P_g) * P_u and [P_g | P_u] = X [A_g | A_u], and its
+// gradients, on the MLP's GEMM kernel (gemm_kernel.h, gemm_glu.hip):
+//
+//   forward   h, P = X A       gated product      6 M H F flops in all
+//             Z = h B
+//   backward  P = X A          where it was not kept
+//             dh = dZ B^T      with dP_g = dh u act'(g), dP_u = dh act(g), h^T
+//             dB = h^T dZ,  dA = X^T dP,  dX = dP A^T          12 M H F
+//
+// with g = P_g, u = P_u.  h, P and dP are bf16 between the products, as the plain MLP's G
+// and dP are; every sum is float32.  Tokens need not be a multiple of 8: X^T and h^T, whose
+// rows are the tokens, are padded with zeros, and rows past the last token are masked in
+// the loads of the other operands.
+
+#include "checks.h"
+#include "epilogue.h"
+#include "gated.h"
+#include "product.h"
+
+namespace tpmlp {
+namespace {
+
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x4_t __attribute__((ext_vector_type(4)));
+typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
+
+int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+
+// ---------------------------------------------------------------------------
+// The gated product split along K: the slices' sum with the epilogue of EPI_GLU
+// ---------------------------------------------------------------------------
+template <int ACT>
+__global__ void __launch_bounds__(256) glu_split_kernel(GluSplitArgs a) {
+  const int64_t n4 = a.M * a.F / 4, plane = 2 * a.M * a.F, stride = (int64_t)gridDim.x * blockDim.x;
+  const uint32_t f4 = (uint32_t)(a.F / 4);
+  for (int64_t j = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; j < n4; j += stride) {
+    const int64_t row = (uint64_t)j / f4, col = 4 * ((uint64_t)j % f4);
+    const float* pg = a.part + row * 2 * a.F + col;
+    f32x4_t g = *reinterpret_cast<const f32x4_t*>(pg), u = *reinterpret_cast<const f32x4_t*>(pg + a.F);
+    for (int i = 1; i < a.splits; ++i) {
+      g += *reinterpret_cast<const f32x4_t*>(pg + i * plane);
+      u += *reinterpret_cast<const f32x4_t*>(pg + i * plane + a.F);
+    }
+    u16x4_t h, bg, bu;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      h[e] = f32_to_bf16(act_f32<ACT>(g[e]) * u[e]);
+      bg[e] = f32_to_bf16(g[e]);
+      bu[e] = f32_to_bf16(u[e]);
+    }
+    *reinterpret_cast<u16x4_t*>(a.h + row * a.F + col) = h;
+    if (a.p) {
+      *reinterpret_cast<u16x4_t*>(a.p + row * 2 * a.F + col) = bg;
+      *reinterpret_cast<u16x4_t*>(a.p + row * 2 * a.F + a.F + col) = bu;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dh split along K: the slices' sum with the epilogue of EPI_DGLU.  One 64 x 64 tile a
+// workgroup: a thread finishes eight columns of two rows, then, through LDS, 16 rows of
+// one column of h^T.
+// ---------------------------------------------------------------------------
+template <int ACT>
+__global__ void __launch_bounds__(256) dglu_split_kernel(DGluSplitArgs a) {
+  __shared__ uint16_t s_h[64][72];  // 8 elements of padding a row
+  const int64_t tiles_n = (a.F + 63) / 64;
+  const int64_t m0 = (blockIdx.x / tiles_n) * 64, n0 = (blockIdx.x % tiles_n) * 64;
+  const int t = threadIdx.x;
+  const int64_t plane = a.M * a.F;
+  const int rq = t >> 3, c = 8 * (t & 7);
+  const int64_t col = n0 + c;
+#pragma unroll
+  for (int v = 0; v < 2; ++v) {
+    const int r = rq + 32 * v;
+    const int64_t row = m0 + r;
+    u16x8_t h = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (row < a.M && col < a.F) {  // F % 8 == 0: eight columns in or out together
+      const float* x = a.part + row * a.F + col;
+      f32x4_t s0 = *reinterpret_cast<const f32x4_t*>(x), s1 = *reinterpret_cast<const f32x4_t*>(x + 4);
+      for (int i = 1; i < a.splits; ++i) {
+        s0 += *reinterpret_cast<const f32x4_t*>(x + i * plane);
+        s1 += *reinterpret_cast<const f32x4_t*>(x + i * plane + 4);
+      }
+      const int64_t o = row * 2 * a.F + col;
+      const u16x8_t gb = *reinterpret_cast<const u16x8_t*>(a.p + o), ub = *reinterpret_cast<const u16x8_t*>(a.p + o + a.F);
+      u16x8_t dg, du;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float dh = e < 4 ? s0[e & 3] : s1[e & 3], u = bf16_to_f32(ub[e]);
+        float f, df;
+        act_grad_f32<ACT>(bf16_to_f32(gb[e]), f, df);
+        dg[e] = f32_to_bf16(dh * u * df);
+        du[e] = f32_to_bf16(dh * f);
+        h[e] = f32_to_bf16(f * u);
+      }
+      *reinterpret_cast<u16x8_t*>(a.dp + o) = dg;
+      *reinterpret_cast<u16x8_t*>(a.dp + o + a.F) = du;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s_h[r][c + e] = h[e];
+  }
+  __syncthreads();
+  const int ct = t >> 2, r0 = 16 * (t & 3);
+  if (n0 + ct < a.F)
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      const int64_t row = m0 + r0 + 8 * v;
+      if (row >= a.M) continue;
+      u16x8_t hv;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) hv[e] = s_h[r0 + 8 * v + e][ct];
+      *reinterpret_cast<u16x8_t*>(a.ht + (n0 + ct) * a.ldt + row) = hv;
+    }
+}
+
+struct ZeroArgs {
+  void* p;
+  int64_t n;  // bytes, a multiple of 16
+};
+__global__ void __launch_bounds__(256) glu_zero_kernel(ZeroArgs a) {
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 16; i < a.n; i += (int64_t)gridDim.x * 4096) *reinterpret_cast<f32x4_t*>(static_cast<char*>(a.p) + i) = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+}
+hipError_t zero(void* p, int64_t bytes, hipStream_t s) {
+  return launch_kernel(glu_zero_kernel, dim3((unsigned)std::min<int64_t>(2048, (bytes + 4095) / 4096)), dim3(256), s, ZeroArgs{p, bytes});
+}
+
+template <class A, class K1, class K2, class K3, class K4>
+hipError_t launch_act(int act, int64_t blocks, const A& a, hipStream_t s, K1 silu, K2 gelu, K3 relu, K4 sigmoid) {
+  void (*k)(A) = act == TPMLP_ACT_SILU ? silu : act == TPMLP_ACT_GELU ? gelu : act == TPMLP_ACT_RELU ? relu : sigmoid;
+  return launch_kernel(k, dim3((unsigned)blocks), dim3(256), s, a);
+}
+#define BY_ACT(kernel) kernel<TPMLP_ACT_SILU>, kernel<TPMLP_ACT_GELU>, kernel<TPMLP_ACT_RELU>, kernel<TPMLP_ACT_SIGMOID>
+
+// ---------------------------------------------------------------------------
+// Plans: functions of the sizes alone
+// ---------------------------------------------------------------------------
+struct GluFwdPlan {
+  GemmPlan g1, g2;
+  bool wt;  // the products read A^T and B^T from the workspace
+  size_t off_h, off_At, off_Bt, off_part, total;
+};
+
+GluFwdPlan plan_glu_fwd(int64_t M, int64_t H, int64_t F) {
+  GluFwdPlan p;
+  p.g1 = plan_gemm(M, 2 * F, H, false);
+  p.g2 = plan_gemm(M, H, F);
+  p.wt = transpose_weights(M, H, F);
+  p.off_h = 0;
+  p.off_At = align_up(size_t(M) * F * 2);
+  p.off_Bt = p.off_At + (p.wt ? align_up(size_t(H) * F * 4) : 0);
+  p.off_part = p.off_Bt + (p.wt ? align_up(size_t(H) * F * 2) : 0);
+  p.total = p.off_part + align_up(std::max(part_bytes(p.g1, M, 2 * F), part_bytes(p.g2, M, H)));
+  return p;
+}
+
+struct GluBwdPlan {
+  GemmPlan g0, g1, gdb, gda, gdx;
+  bool wt, tdp;  // the recomputed product reads A^T; dA reads dP^T
+  size_t off_Xt, off_dZt, off_At, off_P, off_ht, off_dP, off_dPt, off_part, total;
+};
+
+GluBwdPlan plan_glu_bwd(int64_t M, int64_t H, int64_t F, bool recompute) {
+  GluBwdPlan p;
+  const int64_t M8 = up8(M);
+  p.g0 = plan_gemm(M, 2 * F, H);
+  p.g1 = plan_gemm(M, F, H, false);
+  p.gdb = plan_gemm(F, H, M8);
+  p.gda = plan_gemm(H, 2 * F, M8);
+  p.gdx = plan_gemm(M, H, 2 * F);
+  p.wt = recompute && transpose_weights(M, H, F);
+  p.tdp = transpose_dp(M, H, F);
+  const size_t mh = align_up(size_t(M8) * H * 2), mf = align_up(size_t(M8) * F * 2), m2f = align_up(size_t(M8) * F * 4);
+  p.off_Xt = 0;
+  p.off_dZt = mh;
+  p.off_At = 2 * mh;
+  p.off_P = p.off_At + (p.wt ? align_up(size_t(H) * F * 4) : 0);
+  p.off_ht = p.off_P + (recompute ? m2f : 0);
+  p.off_dP = p.off_ht + mf;
+  p.off_dPt = p.off_dP + m2f;
+  p.off_part = p.off_dPt + (p.tdp ? m2f : 0);
+  size_t part = recompute ? part_bytes(p.g0, M, 2 * F) : 0;
+  part = std::max({part, part_bytes(p.g1, M, F), part_bytes(p.gdb, F, H), part_bytes(p.gda, H, 2 * F),
+                   part_bytes(p.gdx, M, H)});
+  p.total = p.off_part + align_up(part);
+  return p;
+}
+
+bool glu_sizes_ok(int64_t M, int64_t H, int64_t F) {
+  return M >= 0 && M <= MAX_DIM && H > 0 && H <= MAX_DIM && H % 8 == 0 && F > 0 && F <= MAX_DIM / 2 && F % 8 == 0;
+}
+
+template <class T>
+T* at(void* ws, size_t off) {
+  return reinterpret_cast<T*>(static_cast<char*>(ws) + off);
+}
+
+// ---------------------------------------------------------------------------
+// The launches
+// ---------------------------------------------------------------------------
+hipError_t enqueue_glu_fwd(const uint16_t* X, const uint16_t* A, const uint16_t* B, void* Z, Epi z_epi, uint16_t* P, int act,
+                           int64_t M, int64_t H, int64_t F, void* ws, hipStream_t s) {
+  const GluFwdPlan p = plan_glu_fwd(M, H, F);
+  uint16_t *h = at<uint16_t>(ws, p.off_h), *At = at<uint16_t>(ws, p.off_At), *Bt = at<uint16_t>(ws, p.off_Bt);
+  float* part = at<float>(ws, p.off_part);
+  hipError_t e;
+  if (p.wt) {
+    if ((e = launch_transpose(A, H, 2 * F, 2 * F, At, s)) != hipSuccess) return e;
+    if ((e = launch_transpose(B, F, H, H, Bt, s)) != hipSuccess) return e;
+  }
+  // h = act(P_g) P_u        X: [M][H], A: [H][2 F] or A^T [2 F][H]
+  if (p.g1.splits == 1) {
+    GemmArgs g = gemm_args(X, H, p.wt ? At : A, p.wt ? H : 2 * F, M, F, H, p.g1, h, F);
+    g.tiles_n = ceil_div(F, tile_bn(p.g1.tile) / 2);
+    g.out2 = P;
+    g.ldt = 2 * F;
+    e = launch_gemm_glu(p.g1.tile, p.wt ? KC : MC, false, act, g, s);
+  } else {
+    GemmArgs g = gemm_args(X, H, p.wt ? At : A, p.wt ? H : 2 * F, M, 2 * F, H, p.g1, part, 2 * F);
+    e = launch_gemm(p.g1.tile, KC, p.wt ? KC : MC, EPI_F32, g, p.g1.splits, s);
+    if (e != hipSuccess) return e;
+    const GluSplitArgs a{part, p.g1.splits, act, M, F, h, P};
+    e = launch_act(act, std::min<int64_t>(2048, (M * F / 4 + 255) / 256), a, s, BY_ACT(glu_split_kernel));
+  }
+  if (e != hipSuccess) return e;
+  // Z = h B                 h: [M][F], B: [F][H] or B^T [H][F]
+  return run_gemm(-1, KC, p.wt ? KC : MC, z_epi, h, F, p.wt ? Bt : B, p.wt ? F : H, M, H, F, p.g2, Z, nullptr, nullptr, part, s);
+}
+
+hipError_t enqueue_glu_bwd(const uint16_t* dZ, const uint16_t* X, const uint16_t* A, const uint16_t* B, const uint16_t* P, void* dX,
+                           Epi x_epi, void* dA, void* dB, Epi w_epi, int act, int64_t M, int64_t H, int64_t F, void* ws,
+                           hipStream_t s) {
+  const GluBwdPlan p = plan_glu_bwd(M, H, F, P == nullptr);
+  const int64_t M8 = up8(M);
+  uint16_t *Xt = at<uint16_t>(ws, p.off_Xt), *dZt = at<uint16_t>(ws, p.off_dZt), *ht = at<uint16_t>(ws, p.off_ht);
+  uint16_t* dP = at<uint16_t>(ws, p.off_dP);
+  float* part = at<float>(ws, p.off_part);
+  hipError_t e = launch_transpose2(X, Xt, dZ, dZt, M, H, H, s, M8);
+  if (e != hipSuccess) return e;
+  if (!P) {
+    uint16_t *Pw = at<uint16_t>(ws, p.off_P), *At = at<uint16_t>(ws, p.off_At);
+    if (p.wt && (e = launch_transpose(A, H, 2 * F, 2 * F, At, s)) != hipSuccess) return e;
+    e = run_gemm(-1, KC, p.wt ? KC : MC, EPI_BF16, X, H, p.wt ? At : A, p.wt ? H : 2 * F, M, 2 * F, H, p.g0, Pw, nullptr, nullptr,
+                 part, s);
+    if (e != hipSuccess) return e;
+    P = Pw;
+  }
+  // dh = dZ B^T -> dP [M][2 F], h^T [F][M8]       dZ: [M][H], B: [F][H] = [N][K]
+  if (p.g1.splits == 1) {
+    GemmArgs g = gemm_args(dZ, H, B, H, M, F, H, p.g1, dP, 2 * F);
+    g.out2 = ht;
+    g.aux = P;
+    g.ldt = M8;
+    e = launch_gemm_glu(p.g1.tile, KC, true, act, g, s);
+  } else {
+    GemmArgs g = gemm_args(dZ, H, B, H, M, F, H, p.g1, part, F);
+    e = launch_gemm(p.g1.tile, KC, KC, EPI_F32, g, p.g1.splits, s);
+    if (e != hipSuccess) return e;
+    const DGluSplitArgs a{part, p.g1.splits, act, M, F, M8, P, dP, ht};
+    e = launch_act(act, ((M + 63) / 64) * ((F + 63) / 64), a, s, BY_ACT(dglu_split_kernel));
+  }
+  if (e != hipSuccess) return e;
+  // dB = h^T dZ             h^T: [F][M8], dZ^T: [H][M8]
+  e = run_gemm(-1, KC, KC, w_epi, ht, M8, dZt, M8, F, H, M8, p.gdb, dB, nullptr, nullptr, part, s);
+  if (e != hipSuccess) return e;
+  // dA = X^T dP             X^T: [H][M8], dP: [M][2 F] (rows past M masked) or dP^T [2 F][M8]
+  if (p.tdp) {
+    uint16_t* dPt = at<uint16_t>(ws, p.off_dPt);
+    if ((e = launch_transpose(dP, M, 2 * F, 2 * F, dPt, s, M8)) != hipSuccess) return e;
+    e = run_gemm(-1, KC, KC, w_epi, Xt, M8, dPt, M8, H, 2 * F, M8, p.gda, dA, nullptr, nullptr, part, s);
+  } else {
+    e = run_gemm(-1, KC, MC, w_epi, Xt, M8, dP, 2 * F, H, 2 * F, M, p.gda, dA, nullptr, nullptr, part, s);
+  }
+  if (e != hipSuccess) return e;
+  // dX = dP A^T             dP: [M][2 F], A: [H][2 F] = [N][K]
+  return run_gemm(-1, KC, KC, x_epi, dP, 2 * F, A, 2 * F, M, H, 2 * F, p.gdx, dX, nullptr, nullptr, part, s);
+}
+
+tpmlp_status check_glu(int act, int64_t M, int64_t H, int64_t F) {
+  if (!glu_sizes_ok(M, H, F))
+    return fail(TPMLP_ERR_SHAPE, "M outside 0 .. 2^23, or H or F not a positive multiple of 8 up to 2^23 (F: 2^22)");
+  if (act < TPMLP_ACT_SILU || act > TPMLP_ACT_SIGMOID) return fail(TPMLP_ERR_SHAPE, "act must be a tpmlp_act other than TPMLP_ACT_NONE");
+  return TPMLP_OK;
+}
+
+tpmlp_status check_ws(const void* ws, size_t ws_bytes, size_t need, const char* query) {
+  if (!ws) return fail(TPMLP_ERR_NULL, "ws is NULL");
+  if (!aligned16(ws)) return fail(TPMLP_ERR_ALIGN, "ws is not 16-byte aligned");
+  if (ws_bytes < need) return fail(TPMLP_ERR_WORKSPACE, std::string("ws_bytes below ") + query);
+  return TPMLP_OK;
+}
+
+}  // namespace
+}  // namespace tpmlp
+
+using namespace tpmlp;
+
+extern "C" {
+
+size_t tpmlp_glu_fwd_workspace_bytes(int64_t M, int64_t H, int64_t F) {
+  return glu_sizes_ok(M, H, F) && M > 0 ? plan_glu_fwd(M, H, F).total : 0;
+}
+
+size_t tpmlp_glu_bwd_workspace_bytes(int64_t M, int64_t H, int64_t F, int recompute) {
+  return glu_sizes_ok(M, H, F) && M > 0 ? plan_glu_bwd(M, H, F, recompute != 0).total : 0;
+}
+
+tpmlp_status tpmlp_glu_fwd(const tpmlp_bf16* X, const tpmlp_bf16* A, const tpmlp_bf16* B, void* Z, int z_type, tpmlp_bf16* P_save,
+                           int act, int64_t M, int64_t H, int64_t F, void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> tpmlp_status {
+    TRY(check_glu(act, M, H, F));
+    if (!type_ok(z_type)) return fail(TPMLP_ERR_SHAPE, "z_type must be a tpmlp_dtype");
+    if (M == 0) return TPMLP_OK;
+    TRY(check_ptrs({{X, "X"}, {A, "A"}, {B, "B"}, {Z, "Z"}}));
+    if (P_save && !aligned16(P_save)) return fail(TPMLP_ERR_ALIGN, "P_save is not 16-byte aligned");
+    const size_t need = plan_glu_fwd(M, H, F).total, mh = size_t(M) * H, mf = size_t(M) * F, hf = size_t(H) * F;
+    TRY(check_ws(ws, ws_bytes, need, "tpmlp_glu_fwd_workspace_bytes"));
+    TRY(check_alias({{Z, mh * size_of(z_type), "Z"}, {P_save, mf * 4, "P_save"}, {ws, need, "ws"}},
+                    {{X, mh * 2, "X"}, {A, hf * 4, "A"}, {B, hf * 2, "B"}}));
+    TRY(check_device());
+    return launched(enqueue_glu_fwd(X, A, B, Z, z_type == TPMLP_BF16 ? EPI_BF16 : EPI_F32, P_save, act, M, H, F, ws,
+                                    stream_of(stream)),
+                    "tpmlp_glu_fwd launch");
+  });
+}
+
+tpmlp_status tpmlp_glu_bwd(const tpmlp_bf16* dZ, const tpmlp_bf16* X, const tpmlp_bf16* A, const tpmlp_bf16* B,
+                           const tpmlp_bf16* P_saved, void* dX, int dx_type, void* dA, void* dB, int dw_type, int act, int64_t M,
+                           int64_t H, int64_t F, void* ws, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> tpmlp_status {
+    TRY(check_glu(act, M, H, F));
+    if (!type_ok(dx_type) || !type_ok(dw_type)) return fail(TPMLP_ERR_SHAPE, "dx_type and dw_type must be a tpmlp_dtype");
+    const size_t mh = size_t(M) * H, mf = size_t(M) * F, hf = size_t(H) * F;
+    const size_t xs = size_of(dx_type), wsz = size_of(dw_type);
+    TRY(check_ptrs({{dA, "dA"}, {dB, "dB"}}));
+    size_t need = 0;
+    if (M > 0) {
+      TRY(check_ptrs({{dZ, "dZ"}, {X, "X"}, {A, "A"}, {B, "B"}, {dX, "dX"}}));
+      if (P_saved && !aligned16(P_saved)) return fail(TPMLP_ERR_ALIGN, "P_saved is not 16-byte aligned");
+      need = plan_glu_bwd(M, H, F, P_saved == nullptr).total;
+      TRY(check_ws(ws, ws_bytes, need, "tpmlp_glu_bwd_workspace_bytes"));
+    }
+    TRY(check_alias({{dX, mh * xs, "dX"}, {dA, hf * 2 * wsz, "dA"}, {dB, hf * wsz, "dB"}, {ws, need, "ws"}},
+                    {{dZ, mh * 2, "dZ"}, {X, mh * 2, "X"}, {A, hf * 4, "A"}, {B, hf * 2, "B"}, {P_saved, mf * 4, "P_saved"}}));
+    TRY(check_device());
+    hipStream_t s = stream_of(stream);
+    if (M == 0) {  // sums over no tokens
+      TRY(launched(zero(dA, (int64_t)(hf * 2 * wsz), s), "tpmlp_glu_bwd launch"));
+      return launched(zero(dB, (int64_t)(hf * wsz), s), "tpmlp_glu_bwd launch");
+    }
+    return launched(enqueue_glu_bwd(dZ, X, A, B, P_saved, dX, dx_type == TPMLP_BF16 ? EPI_BF16 : EPI_F32, dA, dB,
+                                    dw_type == TPMLP_BF16 ? EPI_BF16 : EPI_F32, act, M, H, F, ws, s),
+                    "tpmlp_glu_bwd launch");
+  });
+}
+
+}  // extern "C"

@@ -1,0 +1,47 @@
+// How the MLP's products are planned and launched (tpmlp.hip), for the calls that are
+// made of such products.
+#pragma once
+
+#include "common.h"
+
+namespace tpmlp {
+
+constexpr int64_t MAX_DIM = int64_t(1) << 23;  // largest size of a product's matrices
+constexpr int NUM_CU = 256;  // MI355X compute units, used to size split-K
+constexpr size_t WS_ALIGN = 256;
+inline size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
+inline int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+struct GemmPlan {
+  TileCfg tile;
+  int splits;
+  int k_split;
+  // Hybrid plan (n_full > 0): output columns [0, n_full) are whole waves of
+  // unsplit 256 x 256 tiles with the product's own epilogue; only the tail
+  // columns [n_full, N) are split along K (splits, k_split) and reduced.
+  int n_full = 0;
+};
+
+// The plan of C[M,N] over K; hybrid: its columns may be cut as above.
+GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool hybrid = true);
+
+// Bytes of a plan's float32 split-K slices.
+inline size_t part_bytes(const GemmPlan& p, int64_t M, int64_t N) {
+  return p.splits > 1 ? size_t(p.splits) * M * (N - p.n_full) * 4 : 0;
+}
+
+// Whether the forward's weights, and dP for dA, are transposed first.
+bool transpose_weights(int64_t M, int64_t H, int64_t F);
+bool transpose_dp(int64_t M, int64_t H, int64_t F);
+
+GemmArgs gemm_args(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N, int64_t K,
+                   const GemmPlan& p, void* out, int64_t ldo);
+
+// One product with its epilogue, recorded under timing kind `kind` (negative: not
+// recorded).  Split along K, the slices go to `part` as float32 and the reduction
+// applies the epilogue.
+hipError_t run_gemm(int kind, Layout la, Layout lb, Epi epi, const void* a, int64_t lda, const void* b, int64_t ldb,
+                    int64_t M, int64_t N, int64_t K, const GemmPlan& p, void* out, uint16_t* out2, const uint16_t* aux,
+                    float* part, hipStream_t s, int64_t ldo = 0, int64_t ldt = 0);
+
+}  // namespace tpmlp

@@ -209,7 +209,9 @@ struct TransposeArgs {
   int blocks;      // workgroups per matrix
 };
 
-__global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs a) {
+// PAD: R need not be a multiple of 8; the output's rows are filled up to one with zeros.
+template <bool PAD>
+__device__ __forceinline__ void transpose_tile(const TransposeArgs& a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   const int lane = threadIdx.x & 63;
   const int job = (int)blockIdx.x >= a.blocks ? 1 : 0;  // uniform over the workgroup
@@ -230,9 +232,11 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs a) {
       __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(in + tr * a.ld_in + tc), (short)0, 0x7FFFFFF0, 0x00020000);
   u32x4_t v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    v[i] = __builtin_bit_cast(u32x4_t,
-                              __builtin_amdgcn_raw_buffer_load_b128(rs, (uint32_t)(((lr + i) * a.ld_in + lc) * 2), 0, 0));
+  for (int i = 0; i < 8; ++i) {
+    uint32_t off = (uint32_t)(((lr + i) * a.ld_in + lc) * 2);
+    if (PAD && r0 + i >= a.R) off = 0x7FFFFFF0u;  // past the descriptor: zeros
+    v[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+  }
   // Output row c0 + j takes element j of each of the 8 input rows: dword e
   // packs input rows 2e and 2e+1, i.e. the halves of v[2e] and v[2e+1] that
   // hold column j (low halves for even j, high halves for odd j).
@@ -248,6 +252,9 @@ __global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs a) {
   (void)a;
 #endif
 }
+
+__global__ void __launch_bounds__(256) transpose_kernel(TransposeArgs a) { transpose_tile<false>(a); }
+__global__ void __launch_bounds__(256) transpose_pad_kernel(TransposeArgs a) { transpose_tile<true>(a); }
 
 }  // namespace
 
@@ -285,7 +292,7 @@ hipError_t launch_splitk_epilogue(Epi epi, const float* part, int splits, int64_
 hipError_t launch_transpose2(const uint16_t* in0, uint16_t* out0, const uint16_t* in1, uint16_t* out1, int64_t R,
                              int64_t C, int64_t ld_in, hipStream_t stream, int64_t ld_out) {
   if (ld_out == 0) ld_out = R;
-  if (ld_in < C || (ld_in & 7) || ld_out < R || (ld_out & 7)) return hipErrorInvalidValue;
+  if (ld_in < C || (ld_in & 7) || (C & 7) || ld_out < R || (ld_out & 7)) return hipErrorInvalidValue;
   if (!in0 || !out0 || (in1 && !out1)) return hipErrorInvalidValue;
   TransposeArgs a;
   a.in[0] = in0;
@@ -301,7 +308,7 @@ hipError_t launch_transpose2(const uint16_t* in0, uint16_t* out0, const uint16_t
   const int jobs = in1 ? 2 : 1;
   if (blocks * jobs > INT32_MAX) return hipErrorInvalidValue;
   a.blocks = (int)blocks;
-  return launch_kernel(transpose_kernel, dim3((unsigned)(blocks * jobs)), dim3(256), stream, a);
+  return launch_kernel((R & 7) ? transpose_pad_kernel : transpose_kernel, dim3((unsigned)(blocks * jobs)), dim3(256), stream, a);
 }
 
 hipError_t launch_transpose(const uint16_t* in, int64_t R, int64_t C, int64_t ld_in, uint16_t* out,

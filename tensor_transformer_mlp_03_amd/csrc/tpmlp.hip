@@ -21,8 +21,10 @@
 // products that make the partials.
 
 #include "../../include/tpmlp.h"
+#include "checks.h"
 #include "common.h"
 #include "host.h"
+#include "product.h"
 
 #include <algorithm>
 #include <mutex>
@@ -50,11 +52,8 @@ __device__ __align__(256) unsigned char scratch[TPMLP_NOALLOC_SCRATCH_BYTES];
 // address operands through buffer descriptors with 32-bit byte offsets from a
 // wave-uniform base, spanning at most 128 rows of a row-major operand:
 // 127 * 2^23 * 2 bytes stays below the descriptors' 2^31-byte range.
-constexpr int64_t MAX_DIM = int64_t(1) << 23;
-constexpr int NUM_CU = 256;  // MI355X compute units, used to size split-K
-constexpr size_t WS_ALIGN = 256;
+static_assert(MAX_DIM == int64_t(1) << 23, "the descriptors' range");
 
-size_t align_up(size_t x) { return (x + WS_ALIGN - 1) / WS_ALIGN * WS_ALIGN; }
 
 bool shape_ok(int64_t v) { return v > 0 && v <= MAX_DIM && (v % 8) == 0; }
 
@@ -62,17 +61,6 @@ bool shape_ok(int64_t v) { return v > 0 && v <= MAX_DIM && (v % 8) == 0; }
 // Launch plan: tile shape and split-K count of each GEMM, workspace layout.
 // Depends on shapes only, so workspace queries need no device.
 // ---------------------------------------------------------------------------
-struct GemmPlan {
-  TileCfg tile;
-  int splits;
-  int k_split;
-  // Hybrid plan (n_full > 0): output columns [0, n_full) are whole waves of
-  // unsplit 256 x 256 tiles with the product's own epilogue; only the tail
-  // columns [n_full, N) are split along K (splits, k_split) and reduced.
-  int n_full = 0;
-};
-
-int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 // Time model used to pick a tile and a split-K count: workgroups run in waves
 // over the chip's CUs (one block per CU: every tile takes the whole LDS); a
@@ -85,7 +73,9 @@ constexpr double CU_RATE_128 = 3.3e12;      // flop/s per CU, 128x128 tile (a qu
 constexpr double SPLIT_BW = 4.0e12;         // bytes/s for the slices' write and re-read
 constexpr double LAUNCH_S = 5e-6;
 
-GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K) {
+}  // namespace
+
+GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool hybrid) {
   GemmPlan best{TILE_256x256, 1, (int)((K + TILE_BK - 1) / TILE_BK * TILE_BK)};
   double best_t = 1e30;
   for (TileCfg tile : {TILE_256x256, TILE_256x128, TILE_128x128}) {
@@ -110,7 +100,7 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K) {
   // Hybrid: when the 256 x 256 tiles are not a whole number of waves, run the
   // largest block of columns that is as whole waves unsplit, and split only the
   // tail.  The split-K round trip then covers the tail alone.
-  {
+  if (hybrid) {
     const int64_t tm = ceil_div(M, 256), tn = ceil_div(N, 256);
     int64_t c = tn - 1;
     while (c > 0 && (tm * c) % NUM_CU != 0) --c;
@@ -134,9 +124,7 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K) {
   return best;
 }
 
-size_t part_bytes(const GemmPlan& p, int64_t M, int64_t N) {
-  return p.splits > 1 ? size_t(p.splits) * M * (N - p.n_full) * 4 : 0;
-}
+namespace {
 
 // Batches of the t-shard drivers' first products.  F1, the recompute and dGeLU
 // of different shards share their A operand (X or dZ) and differ only in the
@@ -186,11 +174,15 @@ BatchPlan plan_batch(int64_t M, int64_t N, int64_t K, int t) {
 // M = 32768, qualifies; M = 2048 and 4096 do not).
 constexpr double RATE_KC = 1.2e15, RATE_MC = 1.14e15, TRANSPOSE_BW = 5.5e12, TRANSPOSE_MARGIN = 1.5;
 
+}  // namespace
+
 bool transpose_weights(int64_t M, int64_t H, int64_t F) {
   const double saved = 2.0 * 2.0 * double(M) * H * F * (1.0 / RATE_MC - 1.0 / RATE_KC);
   const double cost = 4.0 * double(H) * F / TRANSPOSE_BW;
   return saved > TRANSPOSE_MARGIN * cost;
 }
+
+namespace {
 
 // The fused forward (both products and GeLU in one launch, G kept in LDS) is
 // taken for hidden sizes it holds (H a multiple of 64, at most 256) when its
@@ -235,11 +227,15 @@ FwdPlan plan_fwd(int64_t M, int64_t H, int64_t F) {
 // dA_i = X^T dP_i reads dP_i N-contiguous unless dP_i is transposed first; the
 // transpose (4 M F bytes) pays when the one product's saving, at the rates above,
 // is 1.5 times its cost, i.e. for H above about 12400 (the 530B-class shard).
+}  // namespace
+
 bool transpose_dp(int64_t M, int64_t H, int64_t F) {
   const double saved = 2.0 * double(M) * H * F * (1.0 / RATE_MC - 1.0 / RATE_KC);
   const double cost = 4.0 * double(M) * F / TRANSPOSE_BW;
   return saved > TRANSPOSE_MARGIN * cost;
 }
+
+namespace {
 
 struct BwdPlan {
   GemmPlan g0, g1, gdb, gda, gdx;
@@ -346,12 +342,12 @@ struct Timing {
 };
 thread_local Timing g_timing;
 
-// One timing record of kind `kind` around `launch`, which enqueues `dispatches`
-// kernels (a hybrid split product is two).
+// One timing record of kind `kind` (negative: none) around `launch`, which enqueues
+// `dispatches` kernels (a hybrid split product is two).
 template <class F>
 hipError_t timed(int kind, hipStream_t s, F&& launch, int dispatches = 1) {
   Timing& t = g_timing;
-  if (!t.on || !((t.kinds >> kind) & 1u)) return launch();
+  if (!t.on || kind < 0 || !((t.kinds >> kind) & 1u)) return launch();
   if (t.n >= t.cap) {
     ++t.dropped;
     return launch();
@@ -375,43 +371,9 @@ hipError_t timed(int kind, hipStream_t s, F&& launch, int dispatches = 1) {
 // ---------------------------------------------------------------------------
 // Argument checks
 // ---------------------------------------------------------------------------
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-struct Range {
-  const void* p;
-  size_t bytes;
-  const char* name;
-};
-
-bool overlap(const Range& a, const Range& b) {
-  if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-// Each output must be disjoint from every other range.
-tpmlp_status check_alias(const std::vector<Range>& outs, const std::vector<Range>& ins) {
-  for (size_t i = 0; i < outs.size(); ++i) {
-    for (size_t j = i + 1; j < outs.size(); ++j)
-      if (overlap(outs[i], outs[j]))
-        return fail(TPMLP_ERR_ALIAS, std::string(outs[i].name) + " overlaps " + outs[j].name);
-    for (const Range& r : ins)
-      if (overlap(outs[i], r)) return fail(TPMLP_ERR_ALIAS, std::string(outs[i].name) + " overlaps " + r.name);
-  }
-  return TPMLP_OK;
-}
-
 tpmlp_status check_shape(int64_t M, int64_t H, int64_t F) {
   if (!shape_ok(M) || !shape_ok(H) || !shape_ok(F))
     return fail(TPMLP_ERR_SHAPE, "M, H and F_i must be positive multiples of 8, at most 2^23");
-  return TPMLP_OK;
-}
-
-tpmlp_status check_ptrs(std::initializer_list<std::pair<const void*, const char*>> ptrs) {
-  for (auto& p : ptrs)
-    if (!p.first) return fail(TPMLP_ERR_NULL, std::string(p.second) + " is NULL");
-  for (auto& p : ptrs)
-    if (!aligned16(p.first)) return fail(TPMLP_ERR_ALIGN, std::string(p.second) + " is not 16-byte aligned");
   return TPMLP_OK;
 }
 
@@ -426,6 +388,8 @@ namespace {
 // ---------------------------------------------------------------------------
 // GEMM launch helpers
 // ---------------------------------------------------------------------------
+}  // namespace
+
 GemmArgs gemm_args(const void* a, int64_t lda, const void* b, int64_t ldb, int64_t M, int64_t N,
                    int64_t K, const GemmPlan& p, void* out, int64_t ldo) {
   GemmArgs g{};
@@ -449,7 +413,7 @@ GemmArgs gemm_args(const void* a, int64_t lda, const void* b, int64_t ldb, int64
 // float32 and the reduction applies the epilogue.
 hipError_t run_gemm(int kind, Layout la, Layout lb, Epi epi, const void* a, int64_t lda, const void* b,
                     int64_t ldb, int64_t M, int64_t N, int64_t K, const GemmPlan& p, void* out, uint16_t* out2,
-                    const uint16_t* aux, float* part, hipStream_t s, int64_t ldo = 0, int64_t ldt = 0) {
+                    const uint16_t* aux, float* part, hipStream_t s, int64_t ldo, int64_t ldt) {
   // ldo: row stride of out (and of out2 and aux for the GeLU and dGeLU
   // epilogues); 0 means N.  ldt: row stride of the dGeLU epilogue's transposed
   // out2; 0 means M (the product's rows can be a row block of a taller one).
@@ -495,6 +459,8 @@ hipError_t run_gemm(int kind, Layout la, Layout lb, Epi epi, const void* a, int6
   return timed(TPMLP_K_SPLITK_REDUCE, s,
                [&] { return launch_splitk_epilogue(epi, part, p.splits, M, N, out, out2, aux, ldo, ldt, s); });
 }
+
+namespace {
 
 // g products of one plan (unsplit) in one launch: product j's A operand a[j],
 // B operand b[j] and outputs out[j], out2[j] (nullable array), aux[j]
