@@ -21,7 +21,10 @@ from ._lib import (  # noqa: F401
     tpmlp_edge_fwd,
     tpmlp_edge_fwd_fp8,
     tpmlp_fp4_fwd,
+    tpmlp_fp4_pack,
+    tpmlp_fp4_packed_bytes,
     tpmlp_fp4_quantize,
+    tpmlp_fp4_workspace_bytes,
     tpmlp_fwd,
     tpmlp_fwd_workspace_bytes,
     tpmlp_glu_bwd,

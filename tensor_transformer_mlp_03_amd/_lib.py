@@ -102,7 +102,10 @@ _SIGS = {
                            _vp, _sz, _vp], _int),
     "tpmlp_edge_fwd_fp8": ([_EP, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _int, _vp], _int),
     "tpmlp_fp4_quantize": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp], _int),
-    "tpmlp_fp4_fwd": ([_vp, _int, _i64, _vp, _vp, _vp, _vp, _int, _i64, _int, _int, _i64, _i64, _i64, _vp], _int),
+    "tpmlp_fp4_packed_bytes": ([_i64, _i64, _int], _sz),
+    "tpmlp_fp4_pack": ([_vp, _vp, _vp, _int, _i64, _i64, _vp], _int),
+    "tpmlp_fp4_workspace_bytes": ([_i64, _i64, _i64, _int], _sz),
+    "tpmlp_fp4_fwd": ([_vp, _int, _i64, _vp, _vp, _vp, _int, _i64, _int, _int, _i64, _i64, _i64, _vp, _sz, _vp], _int),
     "tpmlp_timing_begin": ([_int], _int),
     "tpmlp_timing_begin_kinds": ([_int, ctypes.c_uint], _int),
     "tpmlp_timing_end": ([ctypes.POINTER(_int), ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_int)], _int),
@@ -953,11 +956,35 @@ def tpmlp_fp4_quantize(W, codes, scales, stream=None):
     _check(lib().tpmlp_fp4_quantize(pw, lw, K, N, pc, ps, _stream(stream)), "tpmlp_fp4_quantize")
 
 
-def tpmlp_fp4_fwd(X, x_scales, codes, scales, Y, act: str = "none", gated: bool = False, stream=None):
-    """Y[M,N] = act(X W^T), or act(X W_g^T) * (X W_u^T) with W = [W_g; W_u]; X[M,K] bf16, or E4M3 codes
-    (one-byte values) with x_scales as tpmlp_edge_fwd_fp8 writes them; Y float32 or bf16."""
+def tpmlp_fp4_packed_bytes(N: int, K: int, gated: bool = False) -> int:
+    return lib().tpmlp_fp4_packed_bytes(N, K, int(bool(gated)))
+
+
+def tpmlp_fp4_pack(codes, scales, packed, gated: bool = False, stream=None):
+    """Codes [N, K/2] and scales [N, K/32] (gated: 2N rows) in the order that tpmlp_fp4_fwd reads;
+    packed: tpmlp_fp4_packed_bytes one-byte values."""
+    import torch
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    if gated and rows % 2:
+        raise ValueError(f"a gated weight has an even number of rows, not {rows}")
+    N = rows // 2 if gated else rows
+    pc, lc = _bytes(codes, (rows, K // 2), "codes")
+    ps, ls = _bytes(scales, (rows, K // 32), "scales")
+    if lc or ls:
+        raise ValueError("codes and scales must be contiguous")
+    pp = _flat(packed, tpmlp_fp4_packed_bytes(N, K, gated), torch.uint8, "packed")
+    _check(lib().tpmlp_fp4_pack(pc, ps, pp, int(bool(gated)), N, K, _stream(stream)), "tpmlp_fp4_pack")
+
+
+def tpmlp_fp4_workspace_bytes(M: int, N: int, K: int, gated: bool = False) -> int:
+    return lib().tpmlp_fp4_workspace_bytes(M, N, K, int(bool(gated)))
+
+
+def tpmlp_fp4_fwd(X, x_scales, packed, Y, act: str = "none", gated: bool = False, ws=None, stream=None):
+    """Y[M,N] = act(X W^T), or act(X W_g^T) * (X W_u^T) with W = [W_g; W_u], from a packed weight; X[M,K]
+    bf16, or E4M3 codes (one-byte values) with x_scales as tpmlp_edge_fwd_fp8 writes them; Y float32 or bf16."""
+    import torch
     (M, K), N = X.shape, Y.shape[1]
-    rows = 2 * N if gated else N
     ps, kind = None, X_BF16
     if X.element_size() == 1:
         if x_scales is None:
@@ -971,12 +998,10 @@ def tpmlp_fp4_fwd(X, x_scales, codes, scales, Y, act: str = "none", gated: bool 
         px, lx = _rows(X, (M, K), "X", BF16)
         if x_scales is not None:
             raise ValueError("x_scales is given with a bf16 X")
-    pc, lc = _bytes(codes, (rows, K // 2), "codes")
-    pk, lk = _bytes(scales, (rows, K // 32), "scales")
-    if lc or lk:
-        raise ValueError("codes and scales must be contiguous")
+    pp = _flat(packed, tpmlp_fp4_packed_bytes(N, K, gated), torch.uint8, "packed")
     py, ly = _rows(Y, (M, N), "Y")
-    st = lib().tpmlp_fp4_fwd(px, kind, lx, ps, pc, pk, py, _dtype(Y, "Y"), ly, ACTS[act], int(bool(gated)), M, N, K,
+    pw, nw = _ws(ws)
+    st = lib().tpmlp_fp4_fwd(px, kind, lx, ps, pp, py, _dtype(Y, "Y"), ly, ACTS[act], int(bool(gated)), M, N, K, pw, nw,
                              _stream(stream))
     if st:
         _check(st, "tpmlp_fp4_fwd")

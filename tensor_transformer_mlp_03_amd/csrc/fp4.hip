@@ -2,21 +2,26 @@
 //
 //   Y = act(X W^T), or, gated, Y = act(X W_g^T) * (X W_u^T) with W = [W_g; W_u]
 //
-// W[n, k] is an E2M1 code (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives; two a byte, the
-// lower k in the low half) times a power of two for every 32 values along K (a byte e: 2^(e
-// - 127)).  X is bf16, or E4M3 with a float32 scale a token or such a power of two for
-// every 32 values.
+// W[n, k] is an E2M1 code (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives) times a power of
+// two for every 32 values along K (a byte e: 2^(e - 127)).  X is bf16, or E4M3 with a
+// float32 scale a token or such a power of two for every 32 values.
 //
-// A wave multiplies 16 rows of W (several such tiles) with 16 tokens (several tiles too),
-// 128 k at a time: lane l reads 16 bytes, 32 weights, of row l % 16 at 32 (l / 16), 1 KiB an
-// instruction, with no repacking of W.  They become bf16, exactly, by
-// v_cvt_scalef32_pk_bf16_fp4 with the block's scale (one instruction for two weights), as
-// E4M3 values of X do by v_cvt_scalef32_pk_bf16_fp8, and four v_mfma_f32_16x16x32_bf16
-// follow.  (v_mfma_scale_f32_16x16x128_f8f6f4 takes the codes and scales as they are, but
-// aligns its products to the largest with too few bits for a float32 sum: on codes of
-// the whole E4M3 range it was off by 2^-15 of the magnitude.)
-// The waves of a workgroup share its rows and split K; their float32 sums meet in LDS, in
-// the order of K, where the activation follows.
+// Layout.  A wave multiplies 16 rows of W (several such tiles) with 16 tokens (several
+// tiles too), 128 k at a time: lane l holds 32 weights of row l % 16 from 32 (l / 16) on, 16
+// bytes.  In a row-major W the 64 lanes of such a load lie in 16 rows, 64 accesses where
+// 1 KiB of neighbours takes 16: 20480 x 20480 weights by one token took 64 us, whatever
+// the tiles, the prefetch or the order of K.  So W is packed once into these blocks of 1
+// KiB, padded with zeros, and its scales into a word a lane for every four blocks; X, which
+// every wave reads whole, is packed by a small kernel before the product (unless fp4_direct
+// says that this costs more than it gives), in bf16 whatever it was: E4M3 values times a power
+// of two are exact in it.
+//
+// The weights become bf16, exactly, by v_cvt_scalef32_pk_bf16_fp4 with the block's scale (one
+// instruction for two weights); four v_mfma_f32_16x16x32_bf16 follow.
+// (v_mfma_scale_f32_16x16x128_f8f6f4 takes the codes and scales as they are, but aligns its
+// products to the largest with too few bits for a float32 sum: on codes of the whole E4M3
+// range it was off by 2^-15 of the magnitude.)  The waves of a workgroup share its rows and
+// split K; their float32 sums meet in LDS, where the activation follows.
 
 #include "block_dev.h"
 #include "gated.h"
@@ -28,7 +33,8 @@ namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-[[maybe_unused]] constexpr uint32_t OOB = 0x7FFFFFF0u;  // an offset past the descriptor: the load returns 0
+
+constexpr int X_PACKED = 3;  // beside the tpmlp_x
 
 // 2^(e - 127) as a float: 2^-127 is subnormal, and 255 (not a number) is infinity here,
 // which the conversions turn into NaN.
@@ -48,50 +54,86 @@ __device__ __forceinline__ float act_of(float x, int act) {
   }
 }
 
+#if defined(__HIP_DEVICE_COMPILE__)
+// Eight E4M3 values times a scale, in bf16.
+__device__ __forceinline__ bf16x8_t from_e4m3(uint32_t lo, uint32_t hi, float scale) {
+  return join(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, scale, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, scale, true),
+              __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, scale, false), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, scale, true));
+}
+#endif
+
+// X[m, 8 k8 .. 8 k8 + 7] as it lies, and its scale; m and k8 inside X.
+template <int KIND>
+__device__ __forceinline__ u32x4 x_raw(const Fp4Args& a, int64_t m, int k8, uint32_t& scale) {
+  if constexpr (KIND == TPMLP_X_BF16) return *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) + m * a.ld_x + 8 * k8);
+  const u32x2 c = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.x) + m * a.ld_x + 8 * k8);
+  scale = KIND == TPMLP_X_E4M3_MX ? static_cast<const uint8_t*>(a.x_scale)[m * (a.K / 32) + k8 / 4] : 127u;
+  return u32x4{c[0], c[1], 0, 0};
+}
+// The eight values in bf16, as the matrix instructions take them; zeros where it is not `in`.
+template <int KIND>
+__device__ __forceinline__ u32x4 x_values(u32x4 v, uint32_t scale, bool in) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  if constexpr (KIND != TPMLP_X_BF16) v = __builtin_bit_cast(u32x4, from_e4m3(v[0], v[1], power(scale)));
+#endif
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = in ? v[e] : 0;
+  return v;
+}
+
+// X into the order in which lanes take it: [token tile][block of 128 k][j][lane] 16 bytes, lane l the
+// eight values of token l % 16 at 32 (l / 16) + 8 j.
+template <int KIND>
+__global__ void __launch_bounds__(256) fp4_pack_x_kernel(Fp4Args a) {
+  const int64_t block = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // [token tile][block of 128 k]
+  const int blocks = (a.K + 127) / 128;
+  const int64_t tile = block / blocks;
+  if (tile * 16 >= a.M) return;
+  const int kb = (int)(block - tile * blocks), lane = threadIdx.x & 63;
+  const int64_t m = tile * 16 + (lane & 15);
+  u32x4* out = static_cast<u32x4*>(a.packed_x) + block * 256 + lane;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int k8 = 16 * kb + 4 * (lane >> 4) + j;
+    const bool in = m < a.M && 8 * k8 < a.K;  // K is a multiple of 8
+    uint32_t scale = 127;
+    const u32x4 v = x_raw<KIND>(a, in ? m : 0, in ? k8 : 0, scale);
+    out[64 * j] = x_values<KIND>(v, scale, in);
+  }
+}
+
 }  // namespace
 
 namespace kern {
 
 // NT tiles of 16 rows of W (gated: NT / 2 of gate rows, then the same pairs' up rows) by MT
-// tiles of 16 tokens a wave; WK waves split K.
-template <bool X8, int NT, int MT, int WK, bool GATED>
+// tiles of 16 tokens a wave; the WK waves take the blocks of 128 k in turn.  D blocks'
+// loads are in flight at a time.  KIND: a tpmlp_x, read where it lies, or X_PACKED.
+template <int KIND, int NT, int MT, int WK, int D, bool GATED>
 __global__ void __launch_bounds__(64 * WK) fp4_kernel(Fp4Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NO = GATED ? NT / 2 : NT;  // tiles of outputs
   __shared__ f32x4 sums[WK][NT][64];
-  const int lane = threadIdx.x & 63, i = lane & 15, q = lane >> 4;
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * (16 * NO);
-  const int64_t m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int K = a.K, K2 = K / 2, KS = K / 32;
+  const int tiles = (a.N + 15) / 16, t0 = blockIdx.x * NO;  // tiles of outputs: of all, first of the workgroup's
+  const int64_t mt0 = (int64_t)blockIdx.y * MT;
+  const int blocks = (a.K + 127) / 128;
 
-  auto rsrc = [](const void* p) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)OOB, 0x00020000);
-  };
-  // Descriptors at the workgroup's first row of each half of W, so that offsets stay in 31 bits.
-  __amdgpu_buffer_rsrc_t rw[GATED ? 2 : 1], rs[GATED ? 2 : 1];
-#pragma unroll
-  for (int h = 0; h < (GATED ? 2 : 1); ++h) {
-    const int64_t row = n0 + (h ? (int64_t)a.N : 0);
-    rw[h] = rsrc(a.w + row * K2);
-    rs[h] = rsrc(a.w_scale + row * KS);
-  }
-  uint32_t w_off[NT], s_off[NT];
+  // A tile past the last one is read as the last one and not stored.
+  const u32x4* w[NT];
+  const uint8_t* ws[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int r = 16 * (t % NO) + i;
-    w_off[t] = n0 + r < a.N ? (uint32_t)(r * K2 + 16 * q) : OOB;
-    s_off[t] = n0 + r < a.N ? (uint32_t)(r * KS + q) : OOB;
+    const int64_t tile = min(t0 + t % NO, tiles - 1) + (t >= NO ? (int64_t)tiles : 0);
+    w[t] = static_cast<const u32x4*>(a.w) + tile * blocks * 64 + lane;
+    ws[t] = reinterpret_cast<const uint8_t*>(static_cast<const u32x4*>(a.w) + (GATED ? 2 : 1) * (int64_t)tiles * blocks * 64) +
+            tile * blocks * 64 + lane;
   }
-  const __amdgpu_buffer_rsrc_t rx = rsrc(static_cast<const char*>(a.x) + m0 * a.ld_x * (X8 ? 1 : 2));
-  const __amdgpu_buffer_rsrc_t rxs = rsrc(static_cast<const uint8_t*>(a.x_scale) + (X8 && a.x_mx ? m0 * KS : 0));
-  uint32_t x_off[MT], xs_off[MT];
+  const u32x4* x[MT];
+  if (KIND == X_PACKED)
 #pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int r = 16 * t + i;
-    x_off[t] = m0 + r < a.M ? (uint32_t)((r * a.ld_x + 32 * q) * (X8 ? 1 : 2)) : OOB;
-    xs_off[t] = m0 + r < a.M ? (uint32_t)(r * KS + q) : OOB;
-  }
+    for (int m = 0; m < MT; ++m) x[m] = static_cast<const u32x4*>(a.packed_x) + min(mt0 + m, (a.M + 15) / 16 - 1) * blocks * 256 + lane;
 
   f32x4 acc[MT][NT];
 #pragma unroll
@@ -99,55 +141,67 @@ __global__ void __launch_bounds__(64 * WK) fp4_kernel(Fp4Args a) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  const int blocks = (K + 127) / 128, per = (blocks + WK - 1) / WK;
-  const int last = min(blocks, (wave + 1) * per);
-  for (int kb = wave * per; kb < last; ++kb) {
-    const bool in = 128 * kb + 32 * q < K;  // K is a multiple of 32: a lane's weights are in or out together
-    u32x4 w[NT];
-    uint32_t s[NT];
+  u32x4 wv[D][NT], xv[D][MT][4];
+  uint32_t sv[D][NT], xs[D][MT][4];
+  constexpr bool PACKED = KIND == X_PACKED;
+  // Past the last block its data are read again, so that no load stands behind a branch and the
+  // compiler knows which are in flight.
+  auto load = [&](int d, int kb) {
+    kb = min(kb, blocks - 1);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int h = GATED && t >= NO ? 1 : 0;
-      w[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw[h], in ? w_off[t] + 64 * kb : OOB, 0, 0));
-      s[t] = __builtin_amdgcn_raw_buffer_load_b8(rs[h], in ? s_off[t] + 4 * kb : OOB, 0, 0);
-    }
-    bf16x8_t x[MT][4];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const bool ok = in && x_off[m] != OOB;
-      if constexpr (X8) {
-        const uint32_t o = x_off[m] + 128 * kb;
-        const u32x4 lo = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? o : OOB, 0, 0));
-        const u32x4 hi = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? o + 16 : OOB, 0, 0));
-        const float scale = a.x_mx ? power(__builtin_amdgcn_raw_buffer_load_b8(rxs, ok ? xs_off[m] + 4 * kb : OOB, 0, 0)) : 1.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x4& v = j < 2 ? lo : hi;
-          x[m][j] = join(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v[2 * (j & 1)], scale, false),
-                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v[2 * (j & 1)], scale, true),
-                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v[2 * (j & 1) + 1], scale, false),
-                         __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)v[2 * (j & 1) + 1], scale, true));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          x[m][j] = __builtin_bit_cast(bf16x8_t, __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? x_off[m] + 256 * kb + 16 * j : OOB, 0, 0));
-      }
+      wv[d][t] = __builtin_nontemporal_load(w[t] + (int64_t)kb * 64);
+      sv[d][t] = ws[t][(int64_t)kb * 64];
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float scale = power(s[t]);
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bf16x8_t wt = join(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[t][j], scale, 0),
-                                 __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[t][j], scale, 1),
-                                 __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[t][j], scale, 2),
-                                 __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[t][j], scale, 3));
+        if constexpr (PACKED) {
+          xv[d][m][j] = x[m][(int64_t)kb * 256 + 64 * j];
+        } else {  // a token or k outside X is read as the last one's
+          const int k8 = 16 * kb + 4 * (lane >> 4) + j;
+          xv[d][m][j] = x_raw<KIND>(a, min((mt0 + m) * 16 + (lane & 15), a.M - 1), min(k8, a.K / 8 - 1), xs[d][m][j]);
+        }
+      }
+  };
+  auto multiply = [&](int d, int kb) {
+    if constexpr (!PACKED) {
 #pragma unroll
-        for (int m = 0; m < MT; ++m) acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wt, x[m][j], acc[m][t], 0, 0, 0);
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k8 = 16 * kb + 4 * (lane >> 4) + j;
+          xv[d][m][j] = x_values<KIND>(xv[d][m][j], xs[d][m][j], (mt0 + m) * 16 + (lane & 15) < a.M && 8 * k8 < a.K);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float scale = power(sv[d][t]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8_t b = join(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wv[d][t][j], scale, 0), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wv[d][t][j], scale, 1),
+                                __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wv[d][t][j], scale, 2), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wv[d][t][j], scale, 3));
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, __builtin_bit_cast(bf16x8_t, xv[d][m][j]), acc[m][t], 0, 0, 0);
       }
     }
+  };
+#pragma unroll
+  for (int d = 0; d < D; ++d) load(d, wave + d * WK);
+  int kb = wave;
+  for (; kb + (D - 1) * WK < blocks; kb += D * WK) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      multiply(d, kb + d * WK);
+      load(d, kb + (d + D) * WK);
+      __builtin_amdgcn_sched_barrier(0);  // the loads stay where they are issued
+    }
   }
+#pragma unroll
+  for (int d = 0; d < D - 1; ++d)
+    if (kb + d * WK < blocks) multiply(d, kb + d * WK);
 
   // Register e of a tile holds W row 4 (l / 16) + e by token l % 16.
 #pragma unroll
@@ -165,10 +219,10 @@ __global__ void __launch_bounds__(64 * WK) fp4_kernel(Fp4Args a) {
 #pragma unroll
         for (int k = 1; k < WK; ++k) u += sums[k][NO + t][l];
       }
-      const int64_t token = m0 + 16 * m + (l & 15);
-      const int n = n0 + 16 * t + 4 * (l >> 4);
+      const int64_t token = (mt0 + m) * 16 + (l & 15);
+      const int n = 16 * (t0 + t) + 4 * (l >> 4);
       if (token >= a.M || n >= a.N) continue;
-      if (X8 && !a.x_mx) {
+      if (a.x_kind == TPMLP_X_E4M3_ROW) {
         const float xs = static_cast<const float*>(a.x_scale)[token];
         v *= xs;
         u *= xs;
@@ -201,29 +255,94 @@ __global__ void __launch_bounds__(64 * WK) fp4_kernel(Fp4Args a) {
 
 namespace {
 
-template <bool X8, int NT, int MT, int WK>
-hipError_t launch_form(Fp4Args a, hipStream_t s) {
-  const int per = 16 * (a.gated ? NT / 2 : NT);
-  const int64_t M = a.M, most = int64_t(32768) * 16 * MT;  // tokens of one launch
-  for (int64_t m = 0; m < M; m += most) {
-    Fp4Args b = a;
-    b.M = std::min(most, M - m);
-    b.x = static_cast<const char*>(a.x) + m * a.ld_x * (X8 ? 1 : 2);
-    if (X8) b.x_scale = static_cast<const char*>(a.x_scale) + m * (a.x_mx ? a.K / 32 : 4);
-    b.y = static_cast<char*>(a.y) + m * a.ld_y * (a.y_bf16 ? 2 : 4);
-    const dim3 grid((unsigned)((b.N + per - 1) / per), (unsigned)((b.M + 16 * MT - 1) / (16 * MT)));
-    const hipError_t e = launch_kernel(a.gated ? kern::fp4_kernel<X8, NT, MT, WK, true> : kern::fp4_kernel<X8, NT, MT, WK, false>,
-                                       grid, dim3(64 * WK), s, b);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+template <int KIND, int NT, int MT, int WK, int D>
+hipError_t launch_form(const Fp4Args& a, hipStream_t s) {
+  const int tiles = (a.N + 15) / 16, per = a.gated ? NT / 2 : NT;
+  const dim3 grid((unsigned)((tiles + per - 1) / per), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
+  if constexpr (NT % 2 == 0)
+    if (a.gated) return launch_kernel(kern::fp4_kernel<KIND, NT, MT, WK, D, true>, grid, dim3(64 * WK), s, a);
+  return launch_kernel(kern::fp4_kernel<KIND, NT, MT, WK, D, false>, grid, dim3(64 * WK), s, a);
 }
 
-template <bool X8>
-hipError_t launch_x(const Fp4Args& a, hipStream_t s) {
-  if (a.M <= 16) return launch_form<X8, 2, 1, 8>(a, s);
-  if (a.M <= 32) return launch_form<X8, 2, 2, 8>(a, s);
-  return launch_form<X8, 4, 4, 8>(a, s);
+// Tiles of W rows a workgroup (gated: of gate and up rows together).  A CU's time is W's 1 KiB a tile
+// and block of 128 k, and X's 4 KiB a token tile, each read by every workgroup, which costs about
+// FP4_X_COST tiles of W (nothing for up to four tokens); the CU that has most workgroups ends last.  (20480 x 20480 gated
+// by 16 tokens: 640 pairs of tiles, 3 workgroups of 1 on a CU 62 us, 2 of 2 58, 1 of 3 the least.)
+constexpr int FP4_X_COST = 3;
+int fp4_tiles(const Fp4Args& a, int mt, int most) {
+  const int tiles = (a.N + 15) / 16, step = a.gated ? 2 : 1;
+  int best = step;
+  int64_t least = INT64_MAX;
+  for (int nt = step; nt <= most; nt += step) {
+    const int64_t groups = (tiles + nt / step - 1) / (nt / step), busiest = (groups + 255) / 256;
+    const int64_t cost = busiest * (nt + FP4_X_COST * mt);
+    if (cost < least) {
+      least = cost;
+      best = nt;
+    }
+  }
+  return best;
+}
+
+template <int KIND, int MT, int D, int MOST>
+hipError_t launch_tiles(const Fp4Args& a, hipStream_t s) {
+  const int nt = fp4_tiles(a, a.M <= 4 ? 0 : MT, MOST);
+  switch (nt) {
+    case 1: return launch_form<KIND, 1, MT, 8, D>(a, s);
+    case 2: return launch_form<KIND, 2, MT, 8, D>(a, s);
+    case 3: return launch_form<KIND, 3, MT, 8, D>(a, s);
+    default: break;
+  }
+  if constexpr (MOST >= 5) {
+    if (nt == 5) return launch_form<KIND, 5, MT, 8, D>(a, s);
+    if (nt == 6) return launch_form<KIND, 6, MT, 8, D>(a, s);
+  }
+  return launch_form<KIND, 4, MT, 8, D>(a, s);
+}
+
+template <int KIND>
+hipError_t launch_kind(const Fp4Args& a, hipStream_t s) {
+  const int64_t tiles = (a.M + 15) / 16;
+  if (a.direct) {
+    if (tiles == 1) return launch_tiles<KIND, 1, 2, 4>(a, s);
+    if (tiles == 2) return launch_tiles<KIND, 2, 2, 4>(a, s);
+    if (tiles == 3) return launch_tiles<KIND, 3, 1, 4>(a, s);
+    return launch_tiles<KIND, 4, 1, 4>(a, s);
+  }
+  const dim3 grid((unsigned)((tiles * ((a.K + 127) / 128) + 3) / 4));
+  const hipError_t e = launch_kernel(fp4_pack_x_kernel<KIND>, grid, dim3(256), s, a);
+  if (e != hipSuccess) return e;
+  if (tiles == 1) return launch_tiles<X_PACKED, 1, 2, 6>(a, s);
+  if (tiles == 2) return launch_tiles<X_PACKED, 2, 2, 6>(a, s);
+  if (tiles == 3) return launch_tiles<X_PACKED, 3, 1, 6>(a, s);
+  return launch_tiles<X_PACKED, 4, 1, 6>(a, s);
+}
+
+hipError_t launch_part(const Fp4Args& a, hipStream_t s) {
+  switch (a.x_kind) {
+    case TPMLP_X_BF16: return launch_kind<TPMLP_X_BF16>(a, s);
+    case TPMLP_X_E4M3_ROW: return launch_kind<TPMLP_X_E4M3_ROW>(a, s);
+    default: return launch_kind<TPMLP_X_E4M3_MX>(a, s);
+  }
+}
+
+// Codes and scales into the blocks that the product reads, [tile][block of 128 k][lane] 16 bytes, then a
+// byte each, zeros times one past the rows' and K's end: a thread writes a lane's.
+__global__ void __launch_bounds__(256) fp4_pack_kernel(Fp4PackArgs a) {
+  const int tiles = (a.N + 15) / 16, blocks = (a.K + 127) / 128;
+  const int64_t total = (int64_t)(a.gated ? 2 : 1) * tiles * blocks * 64;
+  u32x4* codes = static_cast<u32x4*>(a.packed);
+  uint8_t* scales = reinterpret_cast<uint8_t*>(codes + total);
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int lane = (int)(i & 63);
+    const int64_t tile = (i >> 6) / blocks;
+    const int k32 = 4 * (int)((i >> 6) - tile * blocks) + (lane >> 4);
+    const int n = 16 * (int)(tile % tiles) + (lane & 15);
+    const int64_t at = (n + (tile >= tiles ? (int64_t)a.N : 0)) * (a.K / 32) + k32;
+    const bool in = n < a.N && k32 < a.K / 32;
+    codes[i] = in ? reinterpret_cast<const u32x4*>(a.codes)[at] : u32x4{0, 0, 0, 0};
+    scales[i] = in ? a.scales[at] : 127;
+  }
 }
 
 // Weights [K][N] in bf16 to codes and scales: a lane takes the 32 values of one column.
@@ -259,8 +378,43 @@ __global__ void __launch_bounds__(256) fp4_quantize_kernel(Fp4QuantArgs a) {
 
 }  // namespace
 
-hipError_t launch_fp4(const Fp4Args& a, bool x_bf16, hipStream_t s) {
-  return x_bf16 ? launch_x<false>(a, s) : launch_x<true>(a, s);
+int64_t fp4_packed_bytes(int64_t N, int64_t K, bool gated) {
+  const int64_t tiles = (N + 15) / 16 * (gated ? 2 : 1), blocks = (K + 127) / 128;
+  return tiles * blocks * (1024 + 64);
+}
+
+// Whether X is read where it lies.  Few tokens take few of a load's 64 accesses; more take them all, about
+// 80 ns a block of 128 k and tile of tokens on each CU, where packing costs a launch, 3.5 us.
+bool fp4_direct(int64_t M, int64_t N, int64_t K, int gated) {
+  if (M <= 4) return true;
+  const int64_t groups = ((N + 15) / 16 + (gated ? 1 : 3)) / (gated ? 2 : 4);  // workgroups of four tiles
+  return M <= 64 && (groups + 255) / 256 * ((M + 15) / 16) * ((K + 127) / 128) <= FP4_DIRECT_BLOCKS;
+}
+
+int64_t fp4_ws_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
+  return M < 1 || fp4_direct(M, N, K, gated) ? 0 : std::min<int64_t>((M + 15) / 16, FP4_LAUNCH_TILES) * ((K + 127) / 128) * 4096;
+}
+
+hipError_t launch_fp4(const Fp4Args& a, hipStream_t s) {
+  // Launches of so many tokens that their tiles fit a grid and the packed X its workspace.
+  const int64_t M = a.M, most = FP4_LAUNCH_TILES * 16;
+  const int xs = a.x_kind == TPMLP_X_BF16 ? 2 : 1, per = a.x_kind == TPMLP_X_E4M3_MX ? a.K / 32 : 4;
+  for (int64_t m = 0; m < M; m += most) {
+    Fp4Args b = a;
+    b.M = std::min(most, M - m);
+    b.direct = M <= most && fp4_direct(M, a.N, a.K, a.gated);
+    b.x = static_cast<const char*>(a.x) + m * a.ld_x * xs;
+    if (a.x_scale) b.x_scale = static_cast<const char*>(a.x_scale) + m * per;
+    b.y = static_cast<char*>(a.y) + m * a.ld_y * (a.y_bf16 ? 2 : 4);
+    const hipError_t e = launch_part(b, s);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_fp4_pack(const Fp4PackArgs& a, hipStream_t s) {
+  const int64_t threads = fp4_packed_bytes(a.N, a.K, a.gated != 0) / 17;
+  return launch_kernel(fp4_pack_kernel, dim3((unsigned)std::min<int64_t>(8192, (threads + 255) / 256)), dim3(256), s, a);
 }
 
 hipError_t launch_fp4_quantize(const Fp4QuantArgs& a, hipStream_t s) {

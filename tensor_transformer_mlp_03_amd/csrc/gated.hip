@@ -136,34 +136,65 @@ tpmlp_status fp4_quantize(const tpmlp_bf16* W, int64_t ld_w, int64_t K, int64_t 
                   "tpmlp_fp4_quantize launch");
 }
 
-tpmlp_status fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scales, const uint8_t* codes, const uint8_t* scales,
-                     void* Y, int y_type, int64_t ld_y, int act, int gated, int64_t M, int64_t N, int64_t K, void* stream) {
+Mat packed_mat(const void* p, int64_t N, int64_t K, int gated) {
+  const int64_t n = fp4_packed_bytes(N, K, gated != 0);
+  return Mat{p, 1, n, n, 1, "packed"};
+}
+
+// check_mat but for the length of a row, which may pass its limit.
+tpmlp_status check_bytes(const Mat& m) {
+  if (!m.p) return fail(TPMLP_ERR_NULL, std::string(m.name) + " is NULL");
+  if (!aligned16(m.p)) return fail(TPMLP_ERR_ALIGN, std::string(m.name) + " is not 16-byte aligned");
+  return TPMLP_OK;
+}
+
+tpmlp_status fp4_pack(const uint8_t* codes, const uint8_t* scales, void* packed, int gated, int64_t N, int64_t K, void* stream) {
+  TRY(check_fp4(N, K));
+  const int64_t rows = gated ? 2 * N : N;
+  const Mat c{codes, rows, K / 2, K / 2, 1, "codes"}, sc{scales, rows, K / 32, K / 32, 1, "scales"}, p = packed_mat(packed, N, K, gated);
+  TRY(check_mat(c));
+  TRY(check_mat(sc));
+  if (!aligned16(codes)) return fail(TPMLP_ERR_ALIGN, "codes is not 16-byte aligned");
+  TRY(check_bytes(p));
+  const Mat outs[] = {p}, ins[] = {c, sc};
+  TRY(check_overlaps(outs, ins));
+  TRY(check_device());
+  return launched(launch_fp4_pack(Fp4PackArgs{codes, scales, packed, (int)N, (int)K, gated != 0}, stream_of(stream)),
+                  "tpmlp_fp4_pack launch");
+}
+
+tpmlp_status fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scales, const void* packed, void* Y, int y_type,
+                     int64_t ld_y, int act, int gated, int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream) {
   TRY(check_fp4(N, K));
   if (M < 0 || M > MAX_TOKENS) return fail(TPMLP_ERR_SHAPE, "M outside 0 .. 2^23");
   if (x_kind < TPMLP_X_BF16 || x_kind > TPMLP_X_E4M3_MX) return fail(TPMLP_ERR_SHAPE, "x_kind must be a tpmlp_x");
   if (act < TPMLP_ACT_NONE || act > TPMLP_ACT_SIGMOID) return fail(TPMLP_ERR_SHAPE, "act must be a tpmlp_act");
   if (!type_ok(y_type)) return fail(TPMLP_ERR_SHAPE, "y_type must be a tpmlp_dtype");
   const bool bf16 = x_kind == TPMLP_X_BF16, mx = x_kind == TPMLP_X_E4M3_MX;
-  const int64_t rows = gated ? 2 * N : N;
   const Mat x{X, M, K, ld_or(ld_x, K), bf16 ? 2 : 1, "X"}, y{Y, M, N, ld_or(ld_y, N), size_of(y_type), "Y"};
-  const Mat c{codes, rows, K / 2, K / 2, 1, "codes"}, sc{scales, rows, K / 32, K / 32, 1, "scales"};
+  const Mat p = packed_mat(packed, N, K, gated);
   Mat xs{nullptr, 0, 1, 1, 1, "x_scales"};
   if (mx) xs = Mat{x_scales, M, K / 32, K / 32, 1, "x_scales"};
   else if (!bf16) xs = Mat{x_scales, M > 0 ? 1 : 0, M, M, 4, "x_scales"};
   else if (x_scales) return fail(TPMLP_ERR_SHAPE, "x_scales is given with a bf16 X");
-  if (x.ld > MAX_SIZE) return fail(TPMLP_ERR_SHAPE, "ld of X is above 2^23");
-  for (const Mat& m : {x, y, c, sc, xs}) TRY(check_mat(m));
-  if (!aligned16(codes)) return fail(TPMLP_ERR_ALIGN, "codes is not 16-byte aligned");
+  for (const Mat& m : {x, y, xs}) TRY(check_mat(m));
+  TRY(check_bytes(p));
   if (!starts_at(x, bf16 ? 8 : 16)) return fail(TPMLP_ERR_ALIGN, "the rows of X do not start at multiples of 16 bytes");
-  const Mat outs[] = {y}, ins[] = {x, xs, c, sc};
+  const int64_t need = fp4_ws_bytes(M, N, K, gated != 0);
+  const Mat w{need ? ws : nullptr, 1, need, need, 1, "ws"};
+  if (need) {
+    TRY(check_bytes(Mat{ws, 1, need, need, 1, "ws"}));
+    if (ws_bytes < (size_t)need) return fail(TPMLP_ERR_WORKSPACE, "ws_bytes below tpmlp_fp4_workspace_bytes");
+  }
+  const Mat outs[] = {y, w}, ins[] = {x, xs, p};
   TRY(check_overlaps(outs, ins));
   if (M == 0) return TPMLP_OK;
   TRY(check_device());
   Fp4Args a{};
   a.x = X;
   a.x_scale = x_scales;
-  a.w = codes;
-  a.w_scale = scales;
+  a.w = packed;
+  a.packed_x = ws;
   a.y = Y;
   a.M = M;
   a.ld_x = x.ld;
@@ -172,10 +203,10 @@ tpmlp_status fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scal
   a.K = (int)K;
   a.act = act;
   a.gated = gated != 0;
-  a.x_mx = mx;
+  a.x_kind = x_kind;
   a.y_bf16 = y_type == TPMLP_BF16;
   a.y_vec = N % 4 == 0 && starts_at(y, 4);
-  return launched(launch_fp4(a, bf16, stream_of(stream)), "tpmlp_fp4_fwd launch");
+  return launched(launch_fp4(a, stream_of(stream)), "tpmlp_fp4_fwd launch");
 }
 
 }  // namespace
@@ -210,11 +241,24 @@ tpmlp_status tpmlp_fp4_quantize(const tpmlp_bf16* W, int64_t ld_w, int64_t K, in
   return guarded([&] { return fp4_quantize(W, ld_w, K, N, codes, scales, stream); });
 }
 
-tpmlp_status tpmlp_fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scales, const uint8_t* codes,
-                           const uint8_t* scales, void* Y, int y_type, int64_t ld_y, int act, int gated, int64_t M, int64_t N,
-                           int64_t K, void* stream) {
+size_t tpmlp_fp4_packed_bytes(int64_t N, int64_t K, int gated) {
+  return N < 1 || N > MAX_SIZE || K < 32 || K > MAX_SIZE || K % 32 ? 0 : (size_t)fp4_packed_bytes(N, K, gated != 0);
+}
+
+tpmlp_status tpmlp_fp4_pack(const uint8_t* codes, const uint8_t* scales, void* packed, int gated, int64_t N, int64_t K,
+                            void* stream) {
+  return guarded([&] { return fp4_pack(codes, scales, packed, gated, N, K, stream); });
+}
+
+size_t tpmlp_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated) {
+  return M < 1 || M > MAX_TOKENS || N < 1 || N > MAX_SIZE || K < 32 || K > MAX_SIZE || K % 32 ? 0 : (size_t)fp4_ws_bytes(M, N, K, gated != 0);
+}
+
+tpmlp_status tpmlp_fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scales, const void* packed, void* Y,
+                           int y_type, int64_t ld_y, int act, int gated, int64_t M, int64_t N, int64_t K, void* ws,
+                           size_t ws_bytes, void* stream) {
   return guarded([&] {
-    return fp4_fwd(X, x_kind, ld_x, x_scales, codes, scales, Y, y_type, ld_y, act, gated, M, N, K, stream);
+    return fp4_fwd(X, x_kind, ld_x, x_scales, packed, Y, y_type, ld_y, act, gated, M, N, K, ws, ws_bytes, stream);
   });
 }
 

@@ -7,7 +7,7 @@ caller's inputs and outputs, enqueues kernels on a stream (the current one by de
 returns.  No arithmetic happens here.  A workspace is made by the first call of a size on the
 stream of that call and belongs to one stream at a time, as block.py's buffers do: a program
 that uses an object on two streams orders them itself, and two threads do not call one object
-at once.  Fp4Linear and Dropout.forward hold none.
+at once.  Dropout.forward uses none.
 """
 from __future__ import annotations
 
@@ -117,10 +117,12 @@ class Fp4Linear:
     """A product with 4-bit weights:  Y = act(X W^T), or gated  Y = act(X W_g^T) * (X W_u^T).
 
     ``codes`` [N, K / 2] uint8, two E2M1 values a byte, the lower k in the low half; ``scales``
-    [N, K / 32] bytes, 2^(e - 127) for every 32 values; gated: W_g's rows, then W_u's.
+    [N, K / 32] bytes, 2^(e - 127) for every 32 values; gated: W_g's rows, then W_u's.  They are
+    copied into the order that the kernels read, on ``stream``, and not kept.
     """
 
-    def __init__(self, codes, scales, act="none", gated=False):
+    def __init__(self, codes, scales, act="none", gated=False, stream=None):
+        import torch
         rows, k2 = codes.shape
         self.K, self.N = 2 * k2, rows // 2 if gated else rows
         if self.K % 32 or (gated and rows % 2):
@@ -129,7 +131,15 @@ class Fp4Linear:
             raise ValueError(f"scales has shape {tuple(scales.shape)}, expected {(rows, self.K // 32)}")
         if act not in L.ACTS:
             raise ValueError(f"no activation {act!r}")
-        self.codes, self.scales, self.act, self.gated = codes, scales, act, gated
+        self.act, self.gated = act, gated
+        n = L.tpmlp_fp4_packed_bytes(self.N, self.K, gated)
+        if stream is None:
+            self.packed = torch.empty(n, dtype=torch.uint8, device=codes.device)
+        else:
+            with _on(stream, codes.device):
+                self.packed = torch.empty(n, dtype=torch.uint8, device=codes.device)
+        L.tpmlp_fp4_pack(codes, scales, self.packed, gated, stream)
+        self._ws, self._sizes = _Workspace(), {}
 
     @classmethod
     def from_weight(cls, W, act="none", gated=False, stream=None):
@@ -138,9 +148,12 @@ class Fp4Linear:
         K, N = W.shape
         if K % 32:
             raise ValueError(f"a weight of {K} rows has no blocks of 32")
+        if stream is not None:
+            with _on(stream, W.device):
+                return cls.from_weight(W, act, gated)
         codes = torch.empty(N, K // 2, dtype=torch.uint8, device=W.device)
         scales = torch.empty(N, K // 32, dtype=torch.uint8, device=W.device)
-        L.tpmlp_fp4_quantize(W, codes, scales, stream)
+        L.tpmlp_fp4_quantize(W, codes, scales)
         return cls(codes, scales, act, gated)
 
     def forward(self, X, Y, x_scales=None, stream=None):
@@ -148,4 +161,9 @@ class Fp4Linear:
         ``block.Edge.forward_fp8`` writes them."""
         if X.shape[1] != self.K or Y.shape[1] != self.N:
             raise ValueError(f"X {tuple(X.shape)} and Y {tuple(Y.shape)} do not fit a weight of {self.N} by {self.K}")
-        L.tpmlp_fp4_fwd(X, x_scales, self.codes, self.scales, Y, self.act, self.gated, stream)
+        M = X.shape[0]
+        n = self._sizes.get(M)
+        if n is None:
+            n = self._sizes[M] = L.tpmlp_fp4_workspace_bytes(M, self.N, self.K, self.gated)
+        ws = self._ws.get(n, X.device, stream) if n else None
+        L.tpmlp_fp4_fwd(X, x_scales, self.packed, Y, self.act, self.gated, ws, stream)

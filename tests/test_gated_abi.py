@@ -176,8 +176,12 @@ def quantize(**kw):
 
 
 def fp4(**kw):
-    return _call("tpmlp_fp4_fwd", dict(X=_p(0), kind=0, lx=0, xs=None, c=_p(1), s=_p(2), Y=_p(3), yt=F32, ly=0, act=0, gated=0, M=5,
-                                       N=9, K=64), kw)
+    return _call("tpmlp_fp4_fwd", dict(X=_p(0), kind=0, lx=0, xs=None, p=_p(1), Y=_p(3), yt=F32, ly=0, act=0, gated=0, M=5, N=9, K=64,
+                                       ws=_p(5), n=1 << 40), kw)
+
+
+def pack(**kw):
+    return _call("tpmlp_fp4_pack", dict(c=_p(1), s=_p(2), p=_p(3), gated=0, N=9, K=64), kw)
 
 
 def test_fp4_accepts():
@@ -187,21 +191,45 @@ def test_fp4_accepts():
     assert fp4(kind=1, xs=_p(4))[0] in PASSED and fp4(kind=2, xs=_p(4, 1))[0] in PASSED
     assert fp4(lx=72, ly=11, Y=_p(3, 4), yt=BF16)[0] in PASSED and fp4(M=1 << 23)[0] in PASSED
     assert fp4(M=0, X=None, Y=None)[0] == OK and fp4(M=0, X=None, Y=None, kind=1)[0] == OK
+    assert pack()[0] in PASSED and pack(gated=1, s=_p(2, 1))[0] in PASSED
+    assert fp4(M=1, ws=None, n=0)[0] in PASSED  # a token's X is read where it lies
+    assert fp4(lx=1 << 30)[0] in PASSED
+
+
+def test_fp4_sizes():
+    packed, ws = L.lib().tpmlp_fp4_packed_bytes, L.lib().tpmlp_fp4_workspace_bytes
+    for bad in ((0, 64), (9, 0), (9, 48), ((1 << 23) + 1, 64), (9, (1 << 23) + 32)):
+        assert packed(*bad, 0) == 0
+    assert packed(9, 64, 0) == 1024 + 64 and packed(9, 64, 1) == 2 * packed(9, 64, 0)
+    assert packed(17, 544, 0) == 2 * 5 * (1024 + 64)
+    assert packed(1 << 23, 1 << 23, 1) > 1 << 45
+    for bad in ((0, 9, 64), (-1, 9, 64), ((1 << 23) + 1, 9, 64), (5, 9, 63), (5, 0, 64)):
+        assert ws(*bad, 0) == 0
+    assert ws(4, 20480, 20480, 1) == 0 and ws(5, 20480, 20480, 1) == 160 * 4096 and ws(17, 40000, 2080, 0) == 2 * 17 * 4096
+    assert ws(37, 1367, 1056, 0) == 0 and ws(65, 16, 32, 0) == 5 * 4096
 
 
 def test_fp4_refuses():
-    for call in (quantize, fp4):
+    for call in (quantize, fp4, pack):
         _refused(call, [(dict(N=0), SHAPE, "N outside"), (dict(N=(1 << 23) + 1), SHAPE, "N outside"), (dict(K=0), SHAPE, "K"),
-                        (dict(K=48), SHAPE, "K"), (dict(K=(1 << 23) + 32), SHAPE, "K"), (dict(c=None), NULL, "codes"),
-                        (dict(s=None), NULL, "scales"), (dict(c=_p(1, 8)), ALIGN, "codes")])
+                        (dict(K=48), SHAPE, "K"), (dict(K=(1 << 23) + 32), SHAPE, "K")])
+    for call in (quantize, pack):
+        _refused(call, [(dict(c=None), NULL, "codes"), (dict(s=None), NULL, "scales"), (dict(c=_p(1, 8)), ALIGN, "codes")])
+    for call in (fp4, pack):
+        _refused(call, [(dict(p=None), NULL, "packed"), (dict(p=_p(1, 8)), ALIGN, "packed")])
+    _refused(pack, [(dict(p=_p(1)), ALIAS, "packed overlaps codes"), (dict(p=_p(2, -1072)), ALIAS, "packed overlaps scales"),
+                    (dict(p=_p(2, -2160), gated=1), ALIAS, "packed overlaps scales")])
     _refused(quantize, [(dict(W=None), NULL, "W"), (dict(ld=8), SHAPE, "ld of W"), (dict(c=_p(0, 16)), ALIAS, "codes overlaps W"),
                         (dict(s=_p(1, 16)), ALIAS, "codes overlaps scales")])
     _refused(fp4, [(dict(M=-1), SHAPE, "M outside"), (dict(M=(1 << 23) + 1), SHAPE, "M outside"), (dict(kind=3), SHAPE, "x_kind"),
                    (dict(act=5), SHAPE, "act"), (dict(yt=2), SHAPE, "y_type"), (dict(X=None), NULL, "X"), (dict(Y=None), NULL, "Y"),
                    (dict(kind=1), NULL, "x_scales"), (dict(xs=_p(4)), SHAPE, "x_scales"), (dict(X=_p(0, 2)), ALIGN, "X"),
-                   (dict(lx=68), ALIGN, "X"), (dict(lx=(1 << 23) + 8), SHAPE, "ld of X"), (dict(kind=1, xs=_p(4, 2)), ALIGN, "x_scales"),
-                   (dict(lx=56), SHAPE, "ld of X"), (dict(Y=_p(0)), ALIAS, "Y overlaps X"), (dict(Y=_p(2)), ALIAS, "Y overlaps scales"),
+                   (dict(lx=68), ALIGN, "X"), (dict(lx=(1 << 31) + 8), SHAPE, "ld of X"), (dict(kind=1, xs=_p(4, 2)), ALIGN, "x_scales"),
+                   (dict(lx=56), SHAPE, "ld of X"), (dict(Y=_p(0)), ALIAS, "Y overlaps X"), (dict(Y=_p(1)), ALIAS, "Y overlaps packed"),
                    (dict(kind=1, xs=_p(3)), ALIAS, "Y overlaps x_scales"), (dict(ly=8), SHAPE, "ld of Y")])
+    big = lambda **kw: fp4(**{**dict(M=65), **kw})  # noqa: E731
+    _refused(big, [(dict(ws=None), NULL, "ws"), (dict(ws=_p(5, 8)), ALIGN, "ws"), (dict(n=5 * 4096 - 1), WS, "tpmlp_fp4_workspace_bytes"),
+                   (dict(ws=_p(0)), ALIAS, "ws overlaps X"), (dict(ws=_p(3)), ALIAS, "Y overlaps ws")])
 
 
 # --- the binding ----------------------------------------------------------------------------------------
@@ -249,7 +277,11 @@ def test_binding_refuses():
         gated.Fp4Linear(z(9, 32, dtype=u8), z(9, 2, dtype=u8), gated=True)
     with pytest.raises(ValueError, match="blocks of 32"):
         gated.Fp4Linear.from_weight(z(40, 9))
-    q = gated.Fp4Linear(z(9, 32, dtype=u8), z(9, 2, dtype=u8))
+    with pytest.raises(ValueError, match="packed holds"):
+        L.tpmlp_fp4_pack(z(9, 32, dtype=u8), z(9, 2, dtype=u8), z(1087, dtype=u8))
+    q = object.__new__(gated.Fp4Linear)  # without the packing, which needs a GPU
+    q.K, q.N, q.act, q.gated, q.packed, q._ws = 64, 9, "none", False, z(1088, dtype=u8), gated._Workspace()
+    q._sizes = {}
     with pytest.raises(ValueError, match="do not fit"):
         q.forward(z(5, 32), z(5, 9))
     with pytest.raises(ValueError, match="needs x_scales"):
@@ -260,6 +292,8 @@ def test_binding_refuses():
         q.forward(z(5, 64, dtype=u8), z(5, 9), torch.zeros(4))
     with pytest.raises(TypeError, match="one-byte"):
         q.forward(z(5, 64, dtype=u8), z(5, 9), torch.zeros(5, 2, dtype=bf))
+    with pytest.raises(ValueError, match="packed holds"):
+        L.tpmlp_fp4_fwd(z(5, 64), None, z(1087, dtype=u8), z(5, 9))
     e = Edge(64, pre="rms", w_pre=z(64))
     with pytest.raises(TypeError, match="codes must hold one-byte"):
         e.forward_fp8(None, z(5, 64), None, z(5, 64), torch.zeros(5))

@@ -591,6 +591,20 @@ def test_fp4_inner_sizes(K, x, M):
     check_fp4(M, 33, K, x)
 
 
+@pytest.mark.parametrize("M", [4, 5, 16, 17, 33, 49, 64, 65])
+@pytest.mark.parametrize("N,gated", [(17, False), (100, True), (20, True)])
+@pytest.mark.parametrize("x", ["bf16", "row", "mx"])
+def test_fp4_packed_tokens(M, N, gated, x):
+    """A K long enough that X is packed from five tokens on, and not a whole number of blocks."""
+    check_fp4(M, N, 5408, x, "silu" if gated else "none", gated, BF16, x_pad=16)
+
+
+@pytest.mark.parametrize("M,N,gated", [(16, 20480, True), (3, 12291, False), (40, 20490, False), (64, 4100, True), (20, 6160, True)])
+def test_fp4_tiles_a_workgroup(M, N, gated):
+    """Numbers of rows that ask for each of the tiles a workgroup, the last one short."""
+    check_fp4(M, N, 96, "mx" if M % 2 else "bf16", "gelu", gated, BF16)
+
+
 @pytest.mark.parametrize("act", ["none", "silu", "gelu", "relu", "sigmoid"])
 @pytest.mark.parametrize("gated", [False, True])
 @pytest.mark.parametrize("y", ["f32", "bf16"])
