@@ -30,6 +30,24 @@ struct DGluSplitArgs {
   uint16_t* ht;        // [F][ldt], columns M .. roundup8(M) - 1 zero
 };
 
+// A few tokens' products (glu_tokens.hip): out = slices along K of x w, [slice][M][N].
+constexpr int GLU_TOKENS_LDS = 8192;  // floats of x that a workgroup holds
+struct GluTokensArgs {
+  const uint16_t* x;     // [M][K] bf16, or
+  const float* slices;   // n_slices of P [M][2 K]: x = act(P_g) * P_u
+  uint16_t* p_save;      // with slices: their sum in bf16, or null
+  const uint16_t* w;     // [K][N] bf16
+  float* out;
+  int64_t M, N, K;
+  int n_slices, act, rows;
+};
+struct GluTokensPlan {
+  int rows, slices;  // rows of K a wave, slices of K
+};
+bool glu_tokens(int64_t M, int64_t H, int64_t F);  // whether M tokens take these kernels
+GluTokensPlan plan_glu_tokens(int64_t M, int64_t N, int64_t K);
+hipError_t launch_glu_tokens(const GluTokensArgs& a, const GluTokensPlan& p, hipStream_t s);
+
 // ---------------------------------------------------------------------------
 // Dropout with a bias, added to the residual stream (drop.hip)
 // ---------------------------------------------------------------------------

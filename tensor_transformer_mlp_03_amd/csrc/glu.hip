@@ -136,13 +136,23 @@ hipError_t launch_act(int act, int64_t blocks, const A& a, hipStream_t s, K1 sil
 // Plans: functions of the sizes alone
 // ---------------------------------------------------------------------------
 struct GluFwdPlan {
+  bool tokens;  // a few tokens' kernels, with the slices of P at off_h and of Z at off_part
+  GluTokensPlan t1, t2;
   GemmPlan g1, g2;
   bool wt;  // the products read A^T and B^T from the workspace
   size_t off_h, off_At, off_Bt, off_part, total;
 };
 
 GluFwdPlan plan_glu_fwd(int64_t M, int64_t H, int64_t F) {
-  GluFwdPlan p;
+  GluFwdPlan p{};
+  p.tokens = glu_tokens(M, H, F);
+  if (p.tokens) {
+    p.t1 = plan_glu_tokens(M, 2 * F, H);
+    p.t2 = plan_glu_tokens(M, H, F);
+    p.off_part = align_up(size_t(p.t1.slices) * M * F * 8);
+    p.total = p.off_part + align_up(size_t(p.t2.slices) * M * H * 4);
+    return p;
+  }
   p.g1 = plan_gemm(M, 2 * F, H, false);
   p.g2 = plan_gemm(M, H, F);
   p.wt = transpose_weights(M, H, F);
@@ -204,6 +214,12 @@ hipError_t enqueue_glu_fwd(const uint16_t* X, const uint16_t* A, const uint16_t*
   uint16_t *h = at<uint16_t>(ws, p.off_h), *At = at<uint16_t>(ws, p.off_At), *Bt = at<uint16_t>(ws, p.off_Bt);
   float* part = at<float>(ws, p.off_part);
   hipError_t e;
+  if (p.tokens) {
+    float* P_slices = at<float>(ws, p.off_h);
+    if ((e = launch_glu_tokens({X, nullptr, nullptr, A, P_slices, M, 2 * F, H, 0, act, 0}, p.t1, s)) != hipSuccess) return e;
+    if ((e = launch_glu_tokens({nullptr, P_slices, P, B, part, M, H, F, p.t1.slices, act, 0}, p.t2, s)) != hipSuccess) return e;
+    return launch_splitk_epilogue(z_epi, part, p.t2.slices, M, H, Z, nullptr, nullptr, H, M, s);
+  }
   if (p.wt) {
     if ((e = launch_transpose(A, H, 2 * F, 2 * F, At, s)) != hipSuccess) return e;
     if ((e = launch_transpose(B, F, H, H, Bt, s)) != hipSuccess) return e;
