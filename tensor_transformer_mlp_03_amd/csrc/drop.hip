@@ -12,6 +12,10 @@
 // random numbers: as easy as 1, 2, 3, SC 2011), key = the seed's halves, counter = (column /
 // 8, row, site, step).  Its four words are the numbers of eight columns, low half first:
 // 16 bits an element, which round p to 1 / 65536, instead of 32 halve the arithmetic.
+//
+// Bound by bandwidth: 2048 x 20480 with a float32 y and a bf16 stream 59.5 us, 5.6 TB/s; with
+// one round of Philox instead of ten 59 (its multiplications run below the loads).  dy and
+// db of 4096 x 1024 9.9 us, 25 MB in two launches.
 
 #include "block_dev.h"
 #include "gated.h"
@@ -40,7 +44,8 @@ __device__ __forceinline__ u32x4 philox(uint32_t g, uint32_t row, uint32_t site,
 
 __device__ __forceinline__ uint32_t number(u32x4 w, int e) { return e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xFFFFu; }
 
-// Eight elements of a row from column c on: FULL rows by vectors, others one by one.
+// Eight elements of a row from column c on: FULL rows by aligned vectors, others by vectors at any
+// element, but for the row's last few.
 template <class T, bool FULL, bool NT>
 __device__ __forceinline__ void load8(const void* base, int64_t at, int c, int n, float (&v)[8]) {
   const typename T::elem* p = static_cast<const typename T::elem*>(base) + at + c;
@@ -57,20 +62,28 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int c, int n
       for (int e = 0; e < 8; ++e)
         v[e] = __builtin_bit_cast(float, e & 1 ? a[e >> 1] & 0xFFFF0000u : a[e >> 1] << 16);
     }
+  } else if (c + 8 <= n) {  // at any element
+    const typename T::vec* q = reinterpret_cast<const typename T::vec*>(p);
+    const f32x4 a = widen(q[0]), b = widen(q[1]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < 4 ? a[e & 3] : b[e & 3];
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = c + e < n ? widen(p[e]) : 0.0f;
   }
 }
 
-template <class T, bool FULL, bool NT>
+// NT32: float32 non-temporal, whose stores write every other 16 bytes: a lane's rows in turn
+// (drop_bias_kernel) gain by it, dy of 2048 x 20480 64 -> 48.6 us, neighbouring items
+// lose, 48 -> 54.
+template <class T, bool FULL, bool NT, bool NT32>
 __device__ __forceinline__ void store8(void* base, int64_t at, int c, int n, const float (&v)[8]) {
   typename T::elem* p = static_cast<typename T::elem*>(base) + at + c;
   if constexpr (FULL) {
     if constexpr (sizeof(typename T::elem) == 4) {
       f32x4* q = reinterpret_cast<f32x4*>(p);
       const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-      if (NT) {
+      if (NT32) {
         __builtin_nontemporal_store(a, q);
         __builtin_nontemporal_store(b, q + 1);
       } else {
@@ -85,6 +98,9 @@ __device__ __forceinline__ void store8(void* base, int64_t at, int c, int n, con
       if (NT) __builtin_nontemporal_store(a, q);
       else *q = a;
     }
+  } else if (c + 8 <= n) {
+    put(p, f32x4{v[0], v[1], v[2], v[3]});
+    put(p + 4, f32x4{v[4], v[5], v[6], v[7]});
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -119,8 +135,8 @@ __global__ void __launch_bounds__(256) drop_kernel(DropArgs a) {
     const u32x4 w = philox((uint32_t)c[u] / 8, (uint32_t)(a.first_row + row[u]), a.site, step, seed);
     if (a.bias) {
       float b[8];
-      if (a.bias_bf16) load8<BF16, false, false>(a.bias, 0, c[u], a.H, b);
-      else load8<F32, false, false>(a.bias, 0, c[u], a.H, b);
+      if (a.bias_bf16) load8<BF16, FULL, false>(a.bias, 0, c[u], a.H, b);
+      else load8<F32, FULL, false>(a.bias, 0, c[u], a.H, b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[u][e] += b[e];
     }
@@ -130,13 +146,16 @@ __global__ void __launch_bounds__(256) drop_kernel(DropArgs a) {
       const float kept = number(w, e) >= a.drop ? y[u][e] * a.scale : 0.0f;
       o[e] = a.r ? r[u][e] + kept : kept;
     }
-    store8<RT, FULL, NT>(a.out, row[u] * a.ld_out, c[u], a.H, o);
+    store8<RT, FULL, NT, false>(a.out, row[u] * a.ld_out, c[u], a.H, o);
   }
 }
 
 // The backward with the bias's gradient: four waves share a stripe of 64 groups of columns
-// (fewer, and several rows a wave, where a row has fewer) over chunk_rows rows; the sums of
-// their unrounded dy meet in LDS.
+// (fewer, and several rows a wave, where a row has fewer) over chunk_rows rows, DROP_ROWS of
+// a lane's rows loaded at a time; the sums of their unrounded dy meet in LDS.  The gradient is
+// read without the non-temporal mark: 2048 x 20480 in bf16 43.5 us with it, 29.7 without.
+constexpr int DROP_ROWS = 4;
+
 template <class GT, class YT, bool FULL, bool NT>
 __global__ void __launch_bounds__(256) drop_bias_kernel(DropArgs a) {
   __shared__ float sums[256][9];
@@ -149,16 +168,22 @@ __global__ void __launch_bounds__(256) drop_bias_kernel(DropArgs a) {
   const int step_rows = 256 / width;
   float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   if (g < a.groups) {
-    for (int64_t row = blockIdx.y * a.chunk_rows + threadIdx.x / width; row < end; row += step_rows) {
-      float v[8];
-      load8<GT, FULL, NT>(a.y, row * a.ld_y, c, a.H, v);
-      const u32x4 w = philox((uint32_t)g, (uint32_t)(a.first_row + row), a.site, step, seed);
+    for (int64_t row = blockIdx.y * a.chunk_rows + threadIdx.x / width; row < end; row += DROP_ROWS * step_rows) {
+      float v[DROP_ROWS][8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        v[e] = number(w, e) >= a.drop ? v[e] * a.scale : 0.0f;
-        s[e] += v[e];
+      for (int u = 0; u < DROP_ROWS; ++u) load8<GT, FULL, false>(a.y, min(row + u * step_rows, end - 1) * a.ld_y, c, a.H, v[u]);
+#pragma unroll
+      for (int u = 0; u < DROP_ROWS; ++u) {
+        const int64_t r = row + u * step_rows;
+        if (r >= end) break;
+        const u32x4 w = philox((uint32_t)g, (uint32_t)(a.first_row + r), a.site, step, seed);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          v[u][e] = number(w, e) >= a.drop ? v[u][e] * a.scale : 0.0f;
+          s[e] += v[u][e];
+        }
+        store8<YT, FULL, NT, NT>(a.out, r * a.ld_out, c, a.H, v[u]);
       }
-      store8<YT, FULL, NT>(a.out, row * a.ld_out, c, a.H, v);
     }
   }
 #pragma unroll
@@ -172,13 +197,20 @@ __global__ void __launch_bounds__(256) drop_bias_kernel(DropArgs a) {
   }
 }
 
-// db[j] = sum over chunks of part[chunk][j]: 16 columns a workgroup, 16 runs of chunks each.
+// db[j] = sum over chunks of part[chunk][j]: 16 columns a workgroup, 16 runs of chunks each,
+// eight loads at a time.
 __global__ void __launch_bounds__(256) drop_sum_kernel(DropSumArgs a) {
   __shared__ float sums[16][17];
   const int c = threadIdx.x & 15, k = threadIdx.x >> 4, col = blockIdx.x * 16 + c;
   float s = 0.0f;
   if (col < a.H)
-    for (int64_t i = k; i < a.chunks; i += 16) s += a.part[i * a.H + col];
+    for (int64_t i = k; i < a.chunks; i += 128) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = a.part[min(i + 16 * u, a.chunks - 1) * a.H + col];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += i + 16 * u < a.chunks ? v[u] : 0.0f;
+    }
   sums[k][c] = s;
   __syncthreads();
   if (k == 0 && col < a.H) {

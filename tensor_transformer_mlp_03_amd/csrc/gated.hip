@@ -67,7 +67,7 @@ tpmlp_status dropout_fwd(const void* y, int y_type, int64_t ld_y, const void* bi
   a.H = (int)H;
   a.groups = (int)((H + 7) / 8);
   a.bias_bf16 = bias_type == TPMLP_BF16;
-  const Mat rows[] = {my, mr};
+  const Mat rows[] = {my, mr, mb};
   a.nt = past_caches(outs, rows);
   return launched(launch_drop(a, y_type, out_type, all_eights(H, outs, rows), stream_of(stream)), "tpmlp_dropout_fwd launch");
 }
