@@ -19,8 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtpmlp.so")
 SOURCES = ["gemm.hip", "reduce.hip", "ffn.hip", "fp8.hip", "tpmlp.hip", "block_edge.hip", "block_edge_bwd.hip",
-           "block_edge_bwd_layer.hip", "block_route.hip", "block_clip.hip", "block.hip", "gemm_glu.hip", "glu.hip", "glu_tokens.hip", "block_edge_fp8.hip",
-           "drop.hip", "fp4.hip", "gated.hip"]
+           "block_edge_bwd_layer.hip", "block_route.hip", "block_clip.hip", "block.hip", "gemm_glu.hip",
+           "gemm_group.hip", "glu.hip", "glu_tokens.hip", "block_edge_fp8.hip", "drop.hip", "fp4.hip", "gated.hip"]
 
 ARCH = "gfx950"
 CFLAGS = [

@@ -25,6 +25,7 @@ typedef uint16_t u16x4_t __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
 
 int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
+int64_t up64(int64_t x) { return (x + 63) / 64 * 64; }
 
 // ---------------------------------------------------------------------------
 // The gated product split along K: the slices' sum with the epilogue of EPI_GLU
@@ -164,9 +165,61 @@ GluFwdPlan plan_glu_fwd(int64_t M, int64_t H, int64_t F) {
   return p;
 }
 
+// The products behind the activation in one launch (gemm_group.hip), dX split along K or not:
+// taken when the model gives it less time than three launches.  The makespan is that of
+// workgroups handed to free CUs in their order, dX's first.  A backward of 2048 tokens by 512 x
+// 2048 67 -> 45 us, of 180 by 1104 x 800 38 -> 28; where it is not taken, one token by 4096 x 2048,
+// whose 1568 tiles have a K step each, 46 us, together 49.
+constexpr int GROUP_TILE_STEPS = 3;  // what a tile takes beside its K steps, in steps: first loads and epilogue
+
+struct GroupPlan {
+  bool on = false;
+  int splits = 1, k_split = 0;  // of dX
+};
+
+double group_steps(int64_t n0, int64_t k0, int64_t n1, int64_t k1) {
+  const int64_t q = n0 / NUM_CU, r = n0 % NUM_CU;  // r CUs take one more of the first
+  const int64_t t0 = q * k0, t1 = r ? t0 + k0 : t0;
+  if (n1 == 0) return (double)t1;
+  auto done = [&](int64_t at) {
+    return (NUM_CU - r) * std::max<int64_t>(0, (at - t0) / k1) + r * std::max<int64_t>(0, (at - t1) / k1);
+  };
+  int64_t lo = t0, hi = t1 + (n1 + NUM_CU - 1) / NUM_CU * k1;  // the first time at which all are done
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (done(mid) < n1) lo = mid + 1;
+    else hi = mid;
+  }
+  return (double)std::max(lo, t1);
+}
+
+GroupPlan plan_group(int64_t M, int64_t H, int64_t F, const GemmPlan& gdb, const GemmPlan& gda, const GemmPlan& gdx) {
+  GroupPlan p;
+  const int64_t tm = ceil_div(M, 128), th = ceil_div(H, 128), tf = ceil_div(F, 128), t2f = ceil_div(2 * F, 128);
+  const int64_t n1 = tf * th + th * t2f, k1 = ceil_div(M, TILE_BK);
+  if (tm * th + n1 > 8 * NUM_CU) return p;  // larger tiles are faster
+  const double step = 128.0 * 128 * 2 * TILE_BK / CU_RATE_128;
+  double best = gdb.seconds + gda.seconds + gdx.seconds + 2 * LAUNCH_S;
+  for (int s = 1; s <= 16; ++s) {
+    const int64_t steps = (ceil_div(2 * F, TILE_BK) + s - 1) / s;
+    if (ceil_div(2 * F, steps * TILE_BK) != s) continue;
+    if (s > 1 && steps < 8) break;
+    double t = step * group_steps(tm * th * s, steps + GROUP_TILE_STEPS, n1, k1 + GROUP_TILE_STEPS);
+    if (s > 1) t += double(s) * M * H * 4 * 2 / SPLIT_BW + LAUNCH_S;
+    if (t < best * (1 - 1e-9)) {
+      best = t;
+      p.on = true;
+      p.splits = s;
+      p.k_split = (int)(steps * TILE_BK);
+    }
+  }
+  return p;
+}
+
 struct GluBwdPlan {
   GemmPlan g0, g1, gdb, gda, gdx;
-  bool wt, tdp;  // the recomputed product reads A^T; dA reads dP^T
+  GroupPlan group;
+  bool wt, tdp, tdz;  // the recomputed product reads A^T; dA reads dP^T; dB reads dZ^T
   size_t off_Xt, off_dZt, off_At, off_P, off_ht, off_dP, off_dPt, off_part, total;
 };
 
@@ -175,23 +228,27 @@ GluBwdPlan plan_glu_bwd(int64_t M, int64_t H, int64_t F, bool recompute) {
   const int64_t M8 = up8(M);
   p.g0 = plan_gemm(M, 2 * F, H);
   p.g1 = plan_gemm(M, F, H, false);
-  p.gdb = plan_gemm(F, H, M8);
-  p.gda = plan_gemm(H, 2 * F, M8);
+  p.gdb = plan_gemm(F, H, M);
+  p.gda = plan_gemm(H, 2 * F, M);
   p.gdx = plan_gemm(M, H, 2 * F);
   p.wt = recompute && transpose_weights(M, H, F);
-  p.tdp = transpose_dp(M, H, F);
+  p.group = plan_group(M, H, F, p.gdb, p.gda, p.gdx);
+  // dZ^T pays as dP^T does, by F instead of H: 2048 tokens by 4096 x 2048 without it save 6 us of
+  // transposing and lose 4 in dB.
+  p.tdp = !p.group.on && transpose_dp(M, H, F);
+  p.tdz = !p.group.on && transpose_dp(M, F, H);
   const size_t mh = align_up(size_t(M8) * H * 2), mf = align_up(size_t(M8) * F * 2), m2f = align_up(size_t(M8) * F * 4);
   p.off_Xt = 0;
   p.off_dZt = mh;
-  p.off_At = 2 * mh;
+  p.off_At = mh + (p.tdz ? mh : 0);
   p.off_P = p.off_At + (p.wt ? align_up(size_t(H) * F * 4) : 0);
   p.off_ht = p.off_P + (recompute ? m2f : 0);
   p.off_dP = p.off_ht + mf;
   p.off_dPt = p.off_dP + m2f;
   p.off_part = p.off_dPt + (p.tdp ? m2f : 0);
-  size_t part = recompute ? part_bytes(p.g0, M, 2 * F) : 0;
-  part = std::max({part, part_bytes(p.g1, M, F), part_bytes(p.gdb, F, H), part_bytes(p.gda, H, 2 * F),
-                   part_bytes(p.gdx, M, H)});
+  size_t part = std::max(recompute ? part_bytes(p.g0, M, 2 * F) : 0, part_bytes(p.g1, M, F));
+  if (p.group.on) part = std::max(part, p.group.splits > 1 ? size_t(p.group.splits) * M * H * 4 : 0);
+  else part = std::max({part, part_bytes(p.gdb, F, H), part_bytes(p.gda, H, 2 * F), part_bytes(p.gdx, M, H)});
   p.total = p.off_part + align_up(part);
   return p;
 }
@@ -251,7 +308,7 @@ hipError_t enqueue_glu_bwd(const uint16_t* dZ, const uint16_t* X, const uint16_t
   uint16_t *Xt = at<uint16_t>(ws, p.off_Xt), *dZt = at<uint16_t>(ws, p.off_dZt), *ht = at<uint16_t>(ws, p.off_ht);
   uint16_t* dP = at<uint16_t>(ws, p.off_dP);
   float* part = at<float>(ws, p.off_part);
-  hipError_t e = launch_transpose2(X, Xt, dZ, dZt, M, H, H, s, M8);
+  hipError_t e = launch_transpose2(X, Xt, p.tdz ? dZ : nullptr, dZt, M, H, H, s, M8);
   if (e != hipSuccess) return e;
   if (!P) {
     uint16_t *Pw = at<uint16_t>(ws, p.off_P), *At = at<uint16_t>(ws, p.off_At);
@@ -276,8 +333,21 @@ hipError_t enqueue_glu_bwd(const uint16_t* dZ, const uint16_t* X, const uint16_t
     e = launch_act(act, ((M + 63) / 64) * ((F + 63) / 64), a, s, BY_ACT(dglu_split_kernel));
   }
   if (e != hipSuccess) return e;
-  // dB = h^T dZ             h^T: [F][M8], dZ^T: [H][M8]
-  e = run_gemm(-1, KC, KC, w_epi, ht, M8, dZt, M8, F, H, M8, p.gdb, dB, nullptr, nullptr, part, s);
+  if (p.group.on) {
+    const bool split = p.group.splits > 1;
+    const int m = (int)M, h = (int)H, f = (int)F;
+    const int tm = ceil_div(M, 128), th = ceil_div(H, 128);
+    const GroupItem items[GROUP_ITEMS] = {
+        {dP, A, 2 * F, 2 * F, m, h, 2 * f, p.group.k_split, split ? part : dX, tm, th},
+        {ht, dZ, M8, H, f, h, m, (int)up64(M), dB, ceil_div(F, 128), th},
+        {Xt, dP, M8, 2 * F, h, 2 * f, m, (int)up64(M), dA, th, ceil_div(2 * F, 128)}};
+    e = launch_gemm_group(items, !split && x_epi == EPI_BF16, w_epi == EPI_BF16, s);
+    if (e != hipSuccess || !split) return e;
+    return launch_splitk_epilogue(x_epi, part, p.group.splits, M, H, dX, nullptr, nullptr, H, M, s);
+  }
+  // dB = h^T dZ             h^T: [F][M8], dZ: [M][H] (rows past M masked) or dZ^T [H][M8]
+  if (p.tdz) e = run_gemm(-1, KC, KC, w_epi, ht, M8, dZt, M8, F, H, M8, p.gdb, dB, nullptr, nullptr, part, s);
+  else e = run_gemm(-1, KC, MC, w_epi, ht, M8, dZ, H, F, H, M, p.gdb, dB, nullptr, nullptr, part, s);
   if (e != hipSuccess) return e;
   // dA = X^T dP             X^T: [H][M8], dP: [M][2 F] (rows past M masked) or dP^T [2 F][M8]
   if (p.tdp) {

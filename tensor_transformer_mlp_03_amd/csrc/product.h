@@ -20,10 +20,18 @@ struct GemmPlan {
   // unsplit 256 x 256 tiles with the product's own epilogue; only the tail
   // columns [n_full, N) are split along K (splits, k_split) and reduced.
   int n_full = 0;
+  double seconds = 0;  // by the planner's model
 };
 
 // The plan of C[M,N] over K; hybrid: its columns may be cut as above.
 GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool hybrid = true);
+
+// The model's rates of one CU on a tile, its bandwidth for split-K slices and its launch.
+constexpr double CU_RATE_256 = 4.3e12;      // flop/s per CU, 256x256 tile
+constexpr double CU_RATE_256x128 = 3.8e12;  // flop/s per CU, 256x128 tile (half the MFMAs per load)
+constexpr double CU_RATE_128 = 3.3e12;      // flop/s per CU, 128x128 tile (a quarter)
+constexpr double SPLIT_BW = 4.0e12;         // bytes/s for the slices' write and re-read
+constexpr double LAUNCH_S = 5e-6;
 
 // Bytes of a plan's float32 split-K slices.
 inline size_t part_bytes(const GemmPlan& p, int64_t M, int64_t N) {
@@ -43,5 +51,18 @@ GemmArgs gemm_args(const void* a, int64_t lda, const void* b, int64_t ldb, int64
 hipError_t run_gemm(int kind, Layout la, Layout lb, Epi epi, const void* a, int64_t lda, const void* b, int64_t ldb,
                     int64_t M, int64_t N, int64_t K, const GemmPlan& p, void* out, uint16_t* out2, const uint16_t* aux,
                     float* part, hipStream_t s, int64_t ldo = 0, int64_t ldt = 0);
+
+// A bf16 product of a launch of several (gemm_group.hip), on 128 x 128 tiles: C[M,N] = A B with A
+// K-contiguous, out with rows of N.  Item 0 has B K-contiguous and may be split along K, its
+// float32 slices one after the other in out; the others have B N-contiguous.
+struct GroupItem {
+  const uint16_t *a, *b;
+  int64_t lda, ldb;
+  int M, N, K, k_split;
+  void* out;
+  int tiles_m, tiles_n;
+};
+constexpr int GROUP_ITEMS = 3;
+hipError_t launch_gemm_group(const GroupItem (&item)[GROUP_ITEMS], bool bf16_0, bool bf16_1, hipStream_t s);
 
 }  // namespace tpmlp

@@ -66,12 +66,7 @@ bool shape_ok(int64_t v) { return v > 0 && v <= MAX_DIM && (v % 8) == 0; }
 // over the chip's CUs (one block per CU: every tile takes the whole LDS); a
 // block's time is proportional to its MACs at the measured per-CU rate of its
 // tile; split-K adds a float32 round trip of the slices through memory and one
-// reduction launch.  Splits keep at least 512 of K each.
-constexpr double CU_RATE_256 = 4.3e12;      // flop/s per CU, 256x256 tile
-constexpr double CU_RATE_256x128 = 3.8e12;  // flop/s per CU, 256x128 tile (half the MFMAs per load)
-constexpr double CU_RATE_128 = 3.3e12;      // flop/s per CU, 128x128 tile (a quarter)
-constexpr double SPLIT_BW = 4.0e12;         // bytes/s for the slices' write and re-read
-constexpr double LAUNCH_S = 5e-6;
+// reduction launch (constants in product.h).  Splits keep at least 512 of K each.
 
 }  // namespace
 
@@ -93,7 +88,7 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool hybrid) {
       if (s > 1) t += double(s) * M * N * 4 * 2 / SPLIT_BW + LAUNCH_S;
       if (t < best_t * (1 - 1e-9)) {
         best_t = t;
-        best = GemmPlan{tile, s, (int)kslice};
+        best = GemmPlan{tile, s, (int)kslice, 0, t};
       }
     }
   }
@@ -116,7 +111,7 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool hybrid) {
                          double(s) * M * nt * 4 * 2 / SPLIT_BW + 2 * LAUNCH_S;
         if (t < best_t * (1 - 1e-9)) {
           best_t = t;
-          best = GemmPlan{TILE_256x256, s, (int)kslice, (int)(c * 256)};
+          best = GemmPlan{TILE_256x256, s, (int)kslice, (int)(c * 256), t};
         }
       }
     }
