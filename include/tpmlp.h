@@ -588,16 +588,13 @@ size_t tpmlp_fp4_packed_bytes(int64_t N, int64_t K, int gated);
 tpmlp_status tpmlp_fp4_pack(const uint8_t* codes, const uint8_t* scales, void* packed, int gated, int64_t N, int64_t K,
                             void* stream);
 
-/* Workspace bytes of tpmlp_fp4_fwd; 0 if none is needed or the sizes are invalid. */
-size_t tpmlp_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated);
-
 /* Y[M,N] = act(X W^T), or with `gated` act(X W_g^T) (.) (X W_u^T), from `packed` weights.  For
  * few tokens, whose time is the reading of W; any M from 0 to 2^23 is taken.  The products
  * are exact, sums float32, Y (y_type) rounded once.  Rows of X start at multiples of 16 bytes
  * (TPMLP_ERR_ALIGN). */
 tpmlp_status tpmlp_fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scales, const void* packed, void* Y,
-                           int y_type, int64_t ld_y, int act, int gated, int64_t M, int64_t N, int64_t K, void* ws,
-                           size_t ws_bytes, void* stream);
+                           int y_type, int64_t ld_y, int act, int gated, int64_t M, int64_t N, int64_t K,
+                           void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Kernel timing (measurement aid; not needed to compute anything)           */

@@ -104,8 +104,7 @@ _SIGS = {
     "tpmlp_fp4_quantize": ([_vp, _i64, _i64, _i64, _vp, _vp, _vp], _int),
     "tpmlp_fp4_packed_bytes": ([_i64, _i64, _int], _sz),
     "tpmlp_fp4_pack": ([_vp, _vp, _vp, _int, _i64, _i64, _vp], _int),
-    "tpmlp_fp4_workspace_bytes": ([_i64, _i64, _i64, _int], _sz),
-    "tpmlp_fp4_fwd": ([_vp, _int, _i64, _vp, _vp, _vp, _int, _i64, _int, _int, _i64, _i64, _i64, _vp, _sz, _vp], _int),
+    "tpmlp_fp4_fwd": ([_vp, _int, _i64, _vp, _vp, _vp, _int, _i64, _int, _int, _i64, _i64, _i64, _vp], _int),
     "tpmlp_timing_begin": ([_int], _int),
     "tpmlp_timing_begin_kinds": ([_int, ctypes.c_uint], _int),
     "tpmlp_timing_end": ([ctypes.POINTER(_int), ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_int)], _int),
@@ -976,11 +975,7 @@ def tpmlp_fp4_pack(codes, scales, packed, gated: bool = False, stream=None):
     _check(lib().tpmlp_fp4_pack(pc, ps, pp, int(bool(gated)), N, K, _stream(stream)), "tpmlp_fp4_pack")
 
 
-def tpmlp_fp4_workspace_bytes(M: int, N: int, K: int, gated: bool = False) -> int:
-    return lib().tpmlp_fp4_workspace_bytes(M, N, K, int(bool(gated)))
-
-
-def tpmlp_fp4_fwd(X, x_scales, packed, Y, act: str = "none", gated: bool = False, ws=None, stream=None):
+def tpmlp_fp4_fwd(X, x_scales, packed, Y, act: str = "none", gated: bool = False, stream=None):
     """Y[M,N] = act(X W^T), or act(X W_g^T) * (X W_u^T) with W = [W_g; W_u], from a packed weight; X[M,K]
     bf16, or E4M3 codes (one-byte values) with x_scales as tpmlp_edge_fwd_fp8 writes them; Y float32 or bf16."""
     import torch
@@ -1000,9 +995,7 @@ def tpmlp_fp4_fwd(X, x_scales, packed, Y, act: str = "none", gated: bool = False
             raise ValueError("x_scales is given with a bf16 X")
     pp = _flat(packed, tpmlp_fp4_packed_bytes(N, K, gated), torch.uint8, "packed")
     py, ly = _rows(Y, (M, N), "Y")
-    pw, nw = _ws(ws)
-    st = lib().tpmlp_fp4_fwd(px, kind, lx, ps, pp, py, _dtype(Y, "Y"), ly, ACTS[act], int(bool(gated)), M, N, K, pw, nw,
-                             _stream(stream))
+    st = lib().tpmlp_fp4_fwd(px, kind, lx, ps, pp, py, _dtype(Y, "Y"), ly, ACTS[act], int(bool(gated)), M, N, K, _stream(stream))
     if st:
         _check(st, "tpmlp_fp4_fwd")
 

@@ -7,14 +7,14 @@
 // float32 scale a token or such a power of two for every 32 values.
 //
 // Layout.  A wave multiplies 16 rows of W (several such tiles) with 16 tokens (several
-// tiles too), 128 k at a time: lane l holds 32 weights of row l % 16 from 32 (l / 16) on, 16
-// bytes.  In a row-major W the 64 lanes of such a load lie in 16 rows, 64 accesses where
+// tiles too), 128 k at a time: lane l holds 32 weights of row l % 16, eight from each 32 j + 8 (l /
+// 16) on, j < 4, in 16 bytes.  In a row-major W the 64 lanes of such a load lie in 16 rows, 64 accesses where
 // 1 KiB of neighbours takes 16: 20480 x 20480 weights by one token took 64 us, whatever
 // the tiles, the prefetch or the order of K.  So W is packed once into these blocks of 1
-// KiB, padded with zeros, and its scales into a word a lane for every four blocks; X, which
-// every wave reads whole, is packed by a small kernel before the product (unless fp4_direct
-// says that this costs more than it gives), in bf16 whatever it was: E4M3 values times a power
-// of two are exact in it.
+// KiB, padded with zeros, and its scales into a word a row for every 128 k.  X, which every
+// workgroup reads whole, is loaded along its rows and turned in LDS, a wave for itself (packed by a
+// launch before, 16 tokens by 4096 x 2048 gated took 9.7 us, so 7.1; 64 by 10240 x 20480
+// 44.6 and 40.8).  E4M3 values times a power of two are exact in bf16.
 //
 // The weights become bf16, exactly, by v_cvt_scalef32_pk_bf16_fp4 with the block's scale (one
 // instruction for two weights); four v_mfma_f32_16x16x32_bf16 follow.
@@ -34,11 +34,14 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
-constexpr int X_PACKED = 3;  // beside the tpmlp_x
+constexpr int X_MX_SHORT = 3;  // TPMLP_X_E4M3_MX with K below 128
 
-// 2^(e - 127) as a float: 2^-127 is subnormal, and 255 (not a number) is infinity here,
-// which the conversions turn into NaN.
-__device__ __forceinline__ float power(uint32_t e) { return __builtin_bit_cast(float, e ? e << 23 : 0x00400000u); }
+// 2^(e - 127) as a float, e byte j of a word: 2^-127 is subnormal, and 255 (not a number) is
+// infinity here, which the conversions turn into NaN.
+__device__ __forceinline__ float power(uint32_t word, int j) {
+  const uint32_t e = (j == 3 ? word >> 1 : word << (23 - 8 * j)) & 0x7F800000u;
+  return __builtin_bit_cast(float, max(e, 0x00400000u));
+}
 
 __device__ __forceinline__ bf16x8_t join(bf16x2_t a, bf16x2_t b, bf16x2_t c, bf16x2_t d) {
   return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
@@ -62,58 +65,26 @@ __device__ __forceinline__ bf16x8_t from_e4m3(uint32_t lo, uint32_t hi, float sc
 }
 #endif
 
-// X[m, 8 k8 .. 8 k8 + 7] as it lies, and its scale; m and k8 inside X.
-template <int KIND>
-__device__ __forceinline__ u32x4 x_raw(const Fp4Args& a, int64_t m, int k8, uint32_t& scale) {
-  if constexpr (KIND == TPMLP_X_BF16) return *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) + m * a.ld_x + 8 * k8);
-  const u32x2 c = *reinterpret_cast<const u32x2*>(static_cast<const uint8_t*>(a.x) + m * a.ld_x + 8 * k8);
-  scale = KIND == TPMLP_X_E4M3_MX ? static_cast<const uint8_t*>(a.x_scale)[m * (a.K / 32) + k8 / 4] : 127u;
-  return u32x4{c[0], c[1], 0, 0};
-}
-// The eight values in bf16, as the matrix instructions take them; zeros where it is not `in`.
-template <int KIND>
-__device__ __forceinline__ u32x4 x_values(u32x4 v, uint32_t scale, bool in) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  if constexpr (KIND != TPMLP_X_BF16) v = __builtin_bit_cast(u32x4, from_e4m3(v[0], v[1], power(scale)));
-#endif
-#pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = in ? v[e] : 0;
-  return v;
-}
-
-// X into the order in which lanes take it: [token tile][block of 128 k][j][lane] 16 bytes, lane l the
-// eight values of token l % 16 at 32 (l / 16) + 8 j.
-template <int KIND>
-__global__ void __launch_bounds__(256) fp4_pack_x_kernel(Fp4Args a) {
-  const int64_t block = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);  // [token tile][block of 128 k]
-  const int blocks = (a.K + 127) / 128;
-  const int64_t tile = block / blocks;
-  if (tile * 16 >= a.M) return;
-  const int kb = (int)(block - tile * blocks), lane = threadIdx.x & 63;
-  const int64_t m = tile * 16 + (lane & 15);
-  u32x4* out = static_cast<u32x4*>(a.packed_x) + block * 256 + lane;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int k8 = 16 * kb + 4 * (lane >> 4) + j;
-    const bool in = m < a.M && 8 * k8 < a.K;  // K is a multiple of 8
-    uint32_t scale = 127;
-    const u32x4 v = x_raw<KIND>(a, in ? m : 0, in ? k8 : 0, scale);
-    out[64 * j] = x_values<KIND>(v, scale, in);
-  }
-}
-
 }  // namespace
 
 namespace kern {
 
 // NT tiles of 16 rows of W (gated: NT / 2 of gate rows, then the same pairs' up rows) by MT
 // tiles of 16 tokens a wave; the WK waves take the blocks of 128 k in turn.  D blocks'
-// loads are in flight at a time.  KIND: a tpmlp_x, read where it lies, or X_PACKED.
+// loads are in flight at a time.  KIND: a tpmlp_x, or X_MX_SHORT.
 template <int KIND, int NT, int MT, int WK, int D, bool GATED>
 __global__ void __launch_bounds__(64 * WK) fp4_kernel(Fp4Args a) {
 #if defined(__HIP_DEVICE_COMPILE__)
   constexpr int NO = GATED ? NT / 2 : NT;  // tiles of outputs
-  __shared__ f32x4 sums[WK][NT][64];
+  constexpr bool MX = KIND == TPMLP_X_E4M3_MX || KIND == X_MX_SHORT;
+  constexpr int XV = KIND == TPMLP_X_BF16 ? 4 : 2;  // loads of 16 bytes a lane, for a tile of tokens and 128 k
+  constexpr int REGIONS = MT > 1 ? 2 : 1;           // of a wave's staged X
+  union Shared {
+    u32x4 x[WK][REGIONS][64 * XV];
+    f32x4 sums[WK][NT][64];
+  };
+  __shared__ Shared shared;
+  auto& sums = shared.sums;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tiles = (a.N + 15) / 16, t0 = blockIdx.x * NO;  // tiles of outputs: of all, first of the workgroup's
@@ -122,18 +93,14 @@ __global__ void __launch_bounds__(64 * WK) fp4_kernel(Fp4Args a) {
 
   // A tile past the last one is read as the last one and not stored.
   const u32x4* w[NT];
-  const uint8_t* ws[NT];
+  const uint32_t* ws[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     const int64_t tile = min(t0 + t % NO, tiles - 1) + (t >= NO ? (int64_t)tiles : 0);
     w[t] = static_cast<const u32x4*>(a.w) + tile * blocks * 64 + lane;
-    ws[t] = reinterpret_cast<const uint8_t*>(static_cast<const u32x4*>(a.w) + (GATED ? 2 : 1) * (int64_t)tiles * blocks * 64) +
-            tile * blocks * 64 + lane;
+    ws[t] = reinterpret_cast<const uint32_t*>(static_cast<const u32x4*>(a.w) + (GATED ? 2 : 1) * (int64_t)tiles * blocks * 64) +
+            tile * blocks * 16 + (lane & 15);
   }
-  const u32x4* x[MT];
-  if (KIND == X_PACKED)
-#pragma unroll
-    for (int m = 0; m < MT; ++m) x[m] = static_cast<const u32x4*>(a.packed_x) + min(mt0 + m, (a.M + 15) / 16 - 1) * blocks * 256 + lane;
 
   f32x4 acc[MT][NT];
 #pragma unroll
@@ -141,50 +108,87 @@ __global__ void __launch_bounds__(64 * WK) fp4_kernel(Fp4Args a) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-  u32x4 wv[D][NT], xv[D][MT][4];
-  uint32_t sv[D][NT], xs[D][MT][4];
-  constexpr bool PACKED = KIND == X_PACKED;
+  u32x4 wv[D][NT], xv[D][MT][XV];
+  uint32_t sv[D][NT], xs[D][MT];
   // Past the last block its data are read again, so that no load stands behind a branch and the
-  // compiler knows which are in flight.
+  // compiler knows which are in flight.  A token or k outside X is read as the last one's.
   auto load = [&](int d, int kb) {
     kb = min(kb, blocks - 1);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       wv[d][t] = __builtin_nontemporal_load(w[t] + (int64_t)kb * 64);
-      sv[d][t] = ws[t][(int64_t)kb * 64];
+      sv[d][t] = ws[t][(int64_t)kb * 16];
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m) {
+      const int64_t first = (mt0 + m) * 16;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (PACKED) {
-          xv[d][m][j] = x[m][(int64_t)kb * 256 + 64 * j];
-        } else {  // a token or k outside X is read as the last one's
-          const int k8 = 16 * kb + 4 * (lane >> 4) + j;
-          xv[d][m][j] = x_raw<KIND>(a, min((mt0 + m) * 16 + (lane & 15), a.M - 1), min(k8, a.K / 8 - 1), xs[d][m][j]);
+      for (int v = 0; v < XV; ++v) {
+        if constexpr (KIND == TPMLP_X_BF16) {
+          const int64_t token = min(first + (lane >> 2), a.M - 1);
+          const int k8 = min(16 * kb + 4 * v + (lane & 3), a.K / 8 - 1);
+          xv[d][m][v] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.x) + token * a.ld_x + 8 * k8);
+        } else {
+          const int64_t token = min(first + 8 * v + (lane >> 3), a.M - 1);
+          const int k16 = min(8 * kb + (lane & 7), a.K / 16 - 1);
+          xv[d][m][v] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(a.x) + token * a.ld_x + 16 * k16);
         }
       }
-  };
-  auto multiply = [&](int d, int kb) {
-    if constexpr (!PACKED) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int k8 = 16 * kb + 4 * (lane >> 4) + j;
-          xv[d][m][j] = x_values<KIND>(xv[d][m][j], xs[d][m][j], (mt0 + m) * 16 + (lane & 15) < a.M && 8 * k8 < a.K);
+      if constexpr (MX) {
+        const uint8_t* p = static_cast<const uint8_t*>(a.x_scale) + min(first + (lane & 15), a.M - 1) * (a.K / 32);
+        if constexpr (KIND == X_MX_SHORT) {
+          xs[d][m] = p[0] | p[min(1, a.K / 32 - 1)] << 8 | p[min(2, a.K / 32 - 1)] << 16;
+        } else {  // at any byte; shifted where it would pass the row's end
+          const int at = min(4 * kb, a.K / 32 - 4);
+          uint32_t word;
+          __builtin_memcpy(&word, p + at, 4);
+          xs[d][m] = word;
         }
+      }
     }
+  };
+  // X of a block and tile of tokens: from the order of loads, neighbours along a token's row, to that of
+  // the matrix instructions, through LDS; 16-byte chunks are swizzled by the token, so that neither
+  // side meets bank conflicts.
+  auto tokens = [&](int d, int m, int kb, bf16x8_t (&f)[4]) {
+    u32x4* region = shared.x[wave][m % REGIONS];
+    const int token = lane & 15, g = lane >> 4;
+    if constexpr (KIND == TPMLP_X_BF16) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float scale = power(sv[d][t]);
+      for (int v = 0; v < 4; ++v) region[64 * v + (lane & ~3) + ((lane & 3) ^ (lane >> 4))] = xv[d][m][v];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[j] = __builtin_bit_cast(bf16x8_t, region[64 * j + 4 * token + (g ^ (token >> 2))]);
+    } else {
+#pragma unroll
+      for (int v = 0; v < 2; ++v) region[64 * v + (lane & ~7) + ((lane & 7) ^ (lane >> 3))] = xv[d][m][v];
+      uint32_t scales = 0x7F7F7F7Fu;
+      if constexpr (KIND == X_MX_SHORT) scales = xs[d][m];
+      else if constexpr (MX) scales = xs[d][m] >> 8 * max(0, 4 * kb - (a.K / 32 - 4));
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        const u32x2 c = reinterpret_cast<const u32x2*>(region)[2 * (8 * token + ((2 * j + (g >> 1)) ^ (token & 7))) + (g & 1)];
+        f[j] = from_e4m3(c[0], c[1], MX ? power(scales, j) : 1.0f);
+      }
+    }
+    if (kb == blocks - 1 && a.K % 128)  // W's zeros there times infinity were no zeros
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (128 * kb + 32 * j >= a.K) f[j] = __builtin_bit_cast(bf16x8_t, u32x4{0, 0, 0, 0});
+  };
+  auto multiply = [&](int d, int kb) {
+    bf16x8_t x[MT][4];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) tokens(d, m, kb, x[m]);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float scale = power(sv[d][t], j);
         const bf16x8_t b = join(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wv[d][t][j], scale, 0), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wv[d][t][j], scale, 1),
                                 __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wv[d][t][j], scale, 2), __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(wv[d][t][j], scale, 3));
 #pragma unroll
         for (int m = 0; m < MT; ++m)
-          acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, __builtin_bit_cast(bf16x8_t, xv[d][m][j]), acc[m][t], 0, 0, 0);
+          acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, x[m][j], acc[m][t], 0, 0, 0);
       }
     }
   };
@@ -202,6 +206,8 @@ __global__ void __launch_bounds__(64 * WK) fp4_kernel(Fp4Args a) {
 #pragma unroll
   for (int d = 0; d < D - 1; ++d)
     if (kb + d * WK < blocks) multiply(d, kb + d * WK);
+
+  __syncthreads();  // the staged X and the sums share their place
 
   // Register e of a tile holds W row 4 (l / 16) + e by token l % 16.
 #pragma unroll
@@ -295,7 +301,9 @@ hipError_t launch_tiles(const Fp4Args& a, hipStream_t s) {
   }
   if constexpr (MOST >= 5) {
     if (nt == 5) return launch_form<KIND, 5, MT, 8, D>(a, s);
-    if (nt == 6) return launch_form<KIND, 6, MT, 8, D>(a, s);
+    // Six by four tiles do not fit the registers of eight waves (64 tokens by 20480 x 10240
+    // gated 112 us, with four waves and two blocks in flight 78).
+    if (nt == 6) return launch_form<KIND, 6, MT, (MT > 3 ? 4 : 8), (MT > 3 ? 2 : D)>(a, s);
   }
   return launch_form<KIND, 4, MT, 8, D>(a, s);
 }
@@ -303,22 +311,14 @@ hipError_t launch_tiles(const Fp4Args& a, hipStream_t s) {
 template <int KIND>
 hipError_t launch_kind(const Fp4Args& a, hipStream_t s) {
   const int64_t tiles = (a.M + 15) / 16;
-  if (a.direct) {
-    if (tiles == 1) return launch_tiles<KIND, 1, 2, 4>(a, s);
-    if (tiles == 2) return launch_tiles<KIND, 2, 2, 4>(a, s);
-    if (tiles == 3) return launch_tiles<KIND, 3, 1, 4>(a, s);
-    return launch_tiles<KIND, 4, 1, 4>(a, s);
-  }
-  const dim3 grid((unsigned)((tiles * ((a.K + 127) / 128) + 3) / 4));
-  const hipError_t e = launch_kernel(fp4_pack_x_kernel<KIND>, grid, dim3(256), s, a);
-  if (e != hipSuccess) return e;
-  if (tiles == 1) return launch_tiles<X_PACKED, 1, 2, 6>(a, s);
-  if (tiles == 2) return launch_tiles<X_PACKED, 2, 2, 6>(a, s);
-  if (tiles == 3) return launch_tiles<X_PACKED, 3, 1, 6>(a, s);
-  return launch_tiles<X_PACKED, 4, 1, 6>(a, s);
+  if (tiles == 1) return launch_tiles<KIND, 1, 2, 6>(a, s);
+  if (tiles == 2) return launch_tiles<KIND, 2, 2, 6>(a, s);
+  if (tiles == 3) return launch_tiles<KIND, 3, 1, 6>(a, s);
+  return launch_tiles<KIND, 4, 1, 6>(a, s);
 }
 
 hipError_t launch_part(const Fp4Args& a, hipStream_t s) {
+  if (a.x_kind == TPMLP_X_E4M3_MX && a.K < 128) return launch_form<X_MX_SHORT, 2, 1, 8, 1>(a, s);
   switch (a.x_kind) {
     case TPMLP_X_BF16: return launch_kind<TPMLP_X_BF16>(a, s);
     case TPMLP_X_E4M3_ROW: return launch_kind<TPMLP_X_E4M3_ROW>(a, s);
@@ -334,14 +334,16 @@ __global__ void __launch_bounds__(256) fp4_pack_kernel(Fp4PackArgs a) {
   u32x4* codes = static_cast<u32x4*>(a.packed);
   uint8_t* scales = reinterpret_cast<uint8_t*>(codes + total);
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int lane = (int)(i & 63);
+    const int lane = (int)(i & 63), g = lane >> 4;
     const int64_t tile = (i >> 6) / blocks;
-    const int k32 = 4 * (int)((i >> 6) - tile * blocks) + (lane >> 4);
+    const int first = 4 * (int)((i >> 6) - tile * blocks);  // block of 32
     const int n = 16 * (int)(tile % tiles) + (lane & 15);
-    const int64_t at = (n + (tile >= tiles ? (int64_t)a.N : 0)) * (a.K / 32) + k32;
-    const bool in = n < a.N && k32 < a.K / 32;
-    codes[i] = in ? reinterpret_cast<const u32x4*>(a.codes)[at] : u32x4{0, 0, 0, 0};
-    scales[i] = in ? a.scales[at] : 127;
+    const int64_t at = (n + (tile >= tiles ? (int64_t)a.N : 0)) * (a.K / 32) + first;
+    u32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = n < a.N && first + j < a.K / 32 ? reinterpret_cast<const uint32_t*>(a.codes)[(at + j) * 4 + g] : 0;
+    codes[i] = v;
+    scales[(i >> 6) * 64 + 4 * (lane & 15) + g] = n < a.N && first + g < a.K / 32 ? a.scales[at + g] : 127;
   }
 }
 
@@ -383,26 +385,13 @@ int64_t fp4_packed_bytes(int64_t N, int64_t K, bool gated) {
   return tiles * blocks * (1024 + 64);
 }
 
-// Whether X is read where it lies.  Few tokens take few of a load's 64 accesses; more take them all, about
-// 80 ns a block of 128 k and tile of tokens on each CU, where packing costs a launch, 3.5 us.
-bool fp4_direct(int64_t M, int64_t N, int64_t K, int gated) {
-  if (M <= 4) return true;
-  const int64_t groups = ((N + 15) / 16 + (gated ? 1 : 3)) / (gated ? 2 : 4);  // workgroups of four tiles
-  return M <= 64 && (groups + 255) / 256 * ((M + 15) / 16) * ((K + 127) / 128) <= FP4_DIRECT_BLOCKS;
-}
-
-int64_t fp4_ws_bytes(int64_t M, int64_t N, int64_t K, bool gated) {
-  return M < 1 || fp4_direct(M, N, K, gated) ? 0 : std::min<int64_t>((M + 15) / 16, FP4_LAUNCH_TILES) * ((K + 127) / 128) * 4096;
-}
-
 hipError_t launch_fp4(const Fp4Args& a, hipStream_t s) {
-  // Launches of so many tokens that their tiles fit a grid and the packed X its workspace.
+  // Launches of so many tokens that their tiles fit a grid.
   const int64_t M = a.M, most = FP4_LAUNCH_TILES * 16;
   const int xs = a.x_kind == TPMLP_X_BF16 ? 2 : 1, per = a.x_kind == TPMLP_X_E4M3_MX ? a.K / 32 : 4;
   for (int64_t m = 0; m < M; m += most) {
     Fp4Args b = a;
     b.M = std::min(most, M - m);
-    b.direct = M <= most && fp4_direct(M, a.N, a.K, a.gated);
     b.x = static_cast<const char*>(a.x) + m * a.ld_x * xs;
     if (a.x_scale) b.x_scale = static_cast<const char*>(a.x_scale) + m * per;
     b.y = static_cast<char*>(a.y) + m * a.ld_y * (a.y_bf16 ? 2 : 4);

@@ -80,20 +80,17 @@ hipError_t launch_drop_bias(const DropArgs& a, const DropPlan& p, float* db, int
 // ---------------------------------------------------------------------------
 // Products with 4-bit weights (fp4.hip)
 // ---------------------------------------------------------------------------
-constexpr int64_t FP4_DIRECT_BLOCKS = 40;   // most blocks of 128 k by 16 tokens a CU reads of an X that is not packed
 constexpr int64_t FP4_LAUNCH_TILES = 4096;  // tiles of 16 tokens of one launch
 
 struct Fp4Args {
   const void* x;        // [M][ld_x] bf16, or E4M3 codes
   const void* x_scale;  // float32 [M], or [M][K / 32] powers of two
   const void* w;        // packed codes and scales (fp4_pack_kernel)
-  void* packed_x;       // fp4_ws_bytes
   void* y;
   int64_t M, ld_x, ld_y;
-  int N, K, act, gated, x_kind, y_bf16, y_vec, direct;
+  int N, K, act, gated, x_kind, y_bf16, y_vec;
 };
 int64_t fp4_packed_bytes(int64_t N, int64_t K, bool gated);
-int64_t fp4_ws_bytes(int64_t M, int64_t N, int64_t K, bool gated);
 hipError_t launch_fp4(const Fp4Args& a, hipStream_t s);
 
 struct Fp4PackArgs {

@@ -164,7 +164,7 @@ tpmlp_status fp4_pack(const uint8_t* codes, const uint8_t* scales, void* packed,
 }
 
 tpmlp_status fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scales, const void* packed, void* Y, int y_type,
-                     int64_t ld_y, int act, int gated, int64_t M, int64_t N, int64_t K, void* ws, size_t ws_bytes, void* stream) {
+                     int64_t ld_y, int act, int gated, int64_t M, int64_t N, int64_t K, void* stream) {
   TRY(check_fp4(N, K));
   if (M < 0 || M > MAX_TOKENS) return fail(TPMLP_ERR_SHAPE, "M outside 0 .. 2^23");
   if (x_kind < TPMLP_X_BF16 || x_kind > TPMLP_X_E4M3_MX) return fail(TPMLP_ERR_SHAPE, "x_kind must be a tpmlp_x");
@@ -180,13 +180,7 @@ tpmlp_status fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scal
   for (const Mat& m : {x, y, xs}) TRY(check_mat(m));
   TRY(check_bytes(p));
   if (!starts_at(x, bf16 ? 8 : 16)) return fail(TPMLP_ERR_ALIGN, "the rows of X do not start at multiples of 16 bytes");
-  const int64_t need = fp4_ws_bytes(M, N, K, gated != 0);
-  const Mat w{need ? ws : nullptr, 1, need, need, 1, "ws"};
-  if (need) {
-    TRY(check_bytes(Mat{ws, 1, need, need, 1, "ws"}));
-    if (ws_bytes < (size_t)need) return fail(TPMLP_ERR_WORKSPACE, "ws_bytes below tpmlp_fp4_workspace_bytes");
-  }
-  const Mat outs[] = {y, w}, ins[] = {x, xs, p};
+  const Mat outs[] = {y}, ins[] = {x, xs, p};
   TRY(check_overlaps(outs, ins));
   if (M == 0) return TPMLP_OK;
   TRY(check_device());
@@ -194,7 +188,6 @@ tpmlp_status fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scal
   a.x = X;
   a.x_scale = x_scales;
   a.w = packed;
-  a.packed_x = ws;
   a.y = Y;
   a.M = M;
   a.ld_x = x.ld;
@@ -250,16 +243,9 @@ tpmlp_status tpmlp_fp4_pack(const uint8_t* codes, const uint8_t* scales, void* p
   return guarded([&] { return fp4_pack(codes, scales, packed, gated, N, K, stream); });
 }
 
-size_t tpmlp_fp4_workspace_bytes(int64_t M, int64_t N, int64_t K, int gated) {
-  return M < 1 || M > MAX_TOKENS || N < 1 || N > MAX_SIZE || K < 32 || K > MAX_SIZE || K % 32 ? 0 : (size_t)fp4_ws_bytes(M, N, K, gated != 0);
-}
-
 tpmlp_status tpmlp_fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scales, const void* packed, void* Y,
-                           int y_type, int64_t ld_y, int act, int gated, int64_t M, int64_t N, int64_t K, void* ws,
-                           size_t ws_bytes, void* stream) {
-  return guarded([&] {
-    return fp4_fwd(X, x_kind, ld_x, x_scales, packed, Y, y_type, ld_y, act, gated, M, N, K, ws, ws_bytes, stream);
-  });
+                           int y_type, int64_t ld_y, int act, int gated, int64_t M, int64_t N, int64_t K, void* stream) {
+  return guarded([&] { return fp4_fwd(X, x_kind, ld_x, x_scales, packed, Y, y_type, ld_y, act, gated, M, N, K, stream); });
 }
 
 }  // extern "C"

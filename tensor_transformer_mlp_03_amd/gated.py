@@ -7,7 +7,7 @@ caller's inputs and outputs, enqueues kernels on a stream (the current one by de
 returns.  No arithmetic happens here.  A workspace is made by the first call of a size on the
 stream of that call and belongs to one stream at a time, as block.py's buffers do: a program
 that uses an object on two streams orders them itself, and two threads do not call one object
-at once.  Dropout.forward uses none.
+at once.  Dropout.forward and Fp4Linear use none.
 """
 from __future__ import annotations
 
@@ -139,7 +139,6 @@ class Fp4Linear:
             with _on(stream, codes.device):
                 self.packed = torch.empty(n, dtype=torch.uint8, device=codes.device)
         L.tpmlp_fp4_pack(codes, scales, self.packed, gated, stream)
-        self._ws, self._sizes = _Workspace(), {}
 
     @classmethod
     def from_weight(cls, W, act="none", gated=False, stream=None):
@@ -161,9 +160,4 @@ class Fp4Linear:
         ``block.Edge.forward_fp8`` writes them."""
         if X.shape[1] != self.K or Y.shape[1] != self.N:
             raise ValueError(f"X {tuple(X.shape)} and Y {tuple(Y.shape)} do not fit a weight of {self.N} by {self.K}")
-        M = X.shape[0]
-        n = self._sizes.get(M)
-        if n is None:
-            n = self._sizes[M] = L.tpmlp_fp4_workspace_bytes(M, self.N, self.K, self.gated)
-        ws = self._ws.get(n, X.device, stream) if n else None
-        L.tpmlp_fp4_fwd(X, x_scales, self.packed, Y, self.act, self.gated, ws, stream)
+        L.tpmlp_fp4_fwd(X, x_scales, self.packed, Y, self.act, self.gated, stream)

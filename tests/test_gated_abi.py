@@ -176,8 +176,8 @@ def quantize(**kw):
 
 
 def fp4(**kw):
-    return _call("tpmlp_fp4_fwd", dict(X=_p(0), kind=0, lx=0, xs=None, p=_p(1), Y=_p(3), yt=F32, ly=0, act=0, gated=0, M=5, N=9, K=64,
-                                       ws=_p(5), n=1 << 40), kw)
+    return _call("tpmlp_fp4_fwd", dict(X=_p(0), kind=0, lx=0, xs=None, p=_p(1), Y=_p(3), yt=F32, ly=0, act=0, gated=0, M=5, N=9,
+                                       K=64), kw)
 
 
 def pack(**kw):
@@ -192,21 +192,16 @@ def test_fp4_accepts():
     assert fp4(lx=72, ly=11, Y=_p(3, 4), yt=BF16)[0] in PASSED and fp4(M=1 << 23)[0] in PASSED
     assert fp4(M=0, X=None, Y=None)[0] == OK and fp4(M=0, X=None, Y=None, kind=1)[0] == OK
     assert pack()[0] in PASSED and pack(gated=1, s=_p(2, 1))[0] in PASSED
-    assert fp4(M=1, ws=None, n=0)[0] in PASSED  # a token's X is read where it lies
     assert fp4(lx=1 << 30)[0] in PASSED
 
 
 def test_fp4_sizes():
-    packed, ws = L.lib().tpmlp_fp4_packed_bytes, L.lib().tpmlp_fp4_workspace_bytes
+    packed = L.lib().tpmlp_fp4_packed_bytes
     for bad in ((0, 64), (9, 0), (9, 48), ((1 << 23) + 1, 64), (9, (1 << 23) + 32)):
         assert packed(*bad, 0) == 0
     assert packed(9, 64, 0) == 1024 + 64 and packed(9, 64, 1) == 2 * packed(9, 64, 0)
     assert packed(17, 544, 0) == 2 * 5 * (1024 + 64)
     assert packed(1 << 23, 1 << 23, 1) > 1 << 45
-    for bad in ((0, 9, 64), (-1, 9, 64), ((1 << 23) + 1, 9, 64), (5, 9, 63), (5, 0, 64)):
-        assert ws(*bad, 0) == 0
-    assert ws(4, 20480, 20480, 1) == 0 and ws(5, 20480, 20480, 1) == 160 * 4096 and ws(17, 40000, 2080, 0) == 2 * 17 * 4096
-    assert ws(37, 1367, 1056, 0) == 0 and ws(65, 16, 32, 0) == 5 * 4096
 
 
 def test_fp4_refuses():
@@ -227,9 +222,6 @@ def test_fp4_refuses():
                    (dict(lx=68), ALIGN, "X"), (dict(lx=(1 << 31) + 8), SHAPE, "ld of X"), (dict(kind=1, xs=_p(4, 2)), ALIGN, "x_scales"),
                    (dict(lx=56), SHAPE, "ld of X"), (dict(Y=_p(0)), ALIAS, "Y overlaps X"), (dict(Y=_p(1)), ALIAS, "Y overlaps packed"),
                    (dict(kind=1, xs=_p(3)), ALIAS, "Y overlaps x_scales"), (dict(ly=8), SHAPE, "ld of Y")])
-    big = lambda **kw: fp4(**{**dict(M=65), **kw})  # noqa: E731
-    _refused(big, [(dict(ws=None), NULL, "ws"), (dict(ws=_p(5, 8)), ALIGN, "ws"), (dict(n=5 * 4096 - 1), WS, "tpmlp_fp4_workspace_bytes"),
-                   (dict(ws=_p(0)), ALIAS, "ws overlaps X"), (dict(ws=_p(3)), ALIAS, "Y overlaps ws")])
 
 
 # --- the binding ----------------------------------------------------------------------------------------

@@ -594,8 +594,8 @@ def test_fp4_inner_sizes(K, x, M):
 @pytest.mark.parametrize("M", [4, 5, 16, 17, 33, 49, 64, 65])
 @pytest.mark.parametrize("N,gated", [(17, False), (100, True), (20, True)])
 @pytest.mark.parametrize("x", ["bf16", "row", "mx"])
-def test_fp4_packed_tokens(M, N, gated, x):
-    """A K long enough that X is packed from five tokens on, and not a whole number of blocks."""
+def test_fp4_long_rows(M, N, gated, x):
+    """A K of many blocks for each wave, and not a whole number of them."""
     check_fp4(M, N, 5408, x, "silu" if gated else "none", gated, BF16, x_pad=16)
 
 
@@ -658,6 +658,23 @@ def test_fp4_bad_token_stays_alone(x, M):
     bad = run(bad_x)
     keep = [i for i in range(M) if i != 3]
     assert torch.equal(good[keep], bad[keep]) and torch.isnan(bad[3]).all()
+
+
+@pytest.mark.parametrize("K", [32, 96, 160, 480])
+@pytest.mark.parametrize("M", [1, 20, 50])
+def test_fp4_infinity_in_the_last_block(K, M):
+    """An infinite value of X times weights that are not zero is infinite, whatever fills the last
+    block of 128 k."""
+    from tensor_transformer_mlp_03_amd.gated import Fp4Linear
+    codes = torch.full((40, K // 2), 0x22, dtype=U8)  # ones
+    codes[1::2, K // 2 - 1] = 0xA2                    # the last one negative
+    X = torch.ones(M, K, dtype=BF16)
+    X[M // 2, K - 1] = float("inf")
+    Y = torch.empty(M, 40, device="cuda")
+    Fp4Linear(codes.cuda(), torch.full((40, K // 32), 127, dtype=U8).cuda()).forward(X.cuda(), Y)
+    want = torch.tensor([float(K), float(K - 2)]).repeat(M, 20)
+    want[M // 2] = torch.tensor([float("inf"), -float("inf")]).repeat(20)
+    assert torch.equal(Y.cpu(), want)
 
 
 @pytest.mark.parametrize("K,N,pad", [(32, 1, 0), (64, 9, 0), (96, 300, 5), (1056, 77, 0), (2048, 264, 8)])
