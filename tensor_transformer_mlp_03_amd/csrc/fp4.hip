@@ -272,8 +272,9 @@ hipError_t launch_form(const Fp4Args& a, hipStream_t s) {
 
 // Tiles of W rows a workgroup (gated: of gate and up rows together).  A CU's time is W's 1 KiB a tile
 // and block of 128 k, and X's 4 KiB a token tile, each read by every workgroup, which costs about
-// FP4_X_COST tiles of W (nothing for up to four tokens); the CU that has most workgroups ends last.  (20480 x 20480 gated
-// by 16 tokens: 640 pairs of tiles, 3 workgroups of 1 on a CU 62 us, 2 of 2 58, 1 of 3 the least.)
+// FP4_X_COST tiles of W; the CU that has most workgroups ends last.  (20480 x 20480 gated by 16
+// tokens: 640 pairs of tiles; 3 workgroups of one pair on a CU 63 us, 2 of two 61, 1 of three 44.5.
+// 64 by 10240 x 20480: 5 of two tiles 78 us, 2 of four 65, 1 of five 41, 1 of six 50.)
 constexpr int FP4_X_COST = 3;
 int fp4_tiles(const Fp4Args& a, int mt, int most) {
   const int tiles = (a.N + 15) / 16, step = a.gated ? 2 : 1;
@@ -292,7 +293,7 @@ int fp4_tiles(const Fp4Args& a, int mt, int most) {
 
 template <int KIND, int MT, int D, int MOST>
 hipError_t launch_tiles(const Fp4Args& a, hipStream_t s) {
-  const int nt = fp4_tiles(a, a.M <= 4 ? 0 : MT, MOST);
+  const int nt = fp4_tiles(a, MT, MOST);
   switch (nt) {
     case 1: return launch_form<KIND, 1, MT, 8, D>(a, s);
     case 2: return launch_form<KIND, 2, MT, 8, D>(a, s);
