@@ -179,6 +179,42 @@ def test_glu_large(M, H, F):
         assert big <= 0.1, (name, big)  # no element is wrong, whatever the norm says
 
 
+def test_glu_offsets_past_32_bits():
+    """P and dP of more than 2^32 bytes.  P of the first and last rows has the bits that the rows alone get
+    (one K step); Z and dX are float32 sums of F and 2 F terms in another order, dA and dB the sums of two halves'."""
+    from tensor_transformer_mlp_03_amd.gated import GatedMLP
+    M, H, F = 70000, 64, 16384
+    gen = torch.Generator("cuda").manual_seed(5)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=gen)  # noqa: E731
+    X, dZ = n(M, H).bfloat16(), n(M, H).bfloat16()
+    mlp = GatedMLP((n(H, 2 * F) / 8).bfloat16(), (n(F, H) / 128).bfloat16())
+    e = lambda *s, dtype=F32: torch.full(s, float("nan"), dtype=dtype, device="cuda")  # noqa: E731
+
+    def run(lo, hi):
+        Z, P, dX, dA, dB = e(hi - lo, H), e(hi - lo, 2 * F, dtype=BF16), e(hi - lo, H), e(H, 2 * F), e(F, H)
+        mlp.forward(X[lo:hi], Z, P)
+        mlp.backward(dZ[lo:hi], X[lo:hi], P, dX, dA, dB)
+        return Z, P, dX, dA, dB
+
+    Z, P, dX, dA, dB = run(0, M)
+    for lo, hi in ((0, 128), (M - 200, M)):
+        z, p, dx, _, _ = run(lo, hi)
+        assert torch.equal(p, P[lo:hi])
+        g, u = p[:, :F].float(), p[:, F:].float()
+        h, dh = torch.nn.functional.silu(g) * u, dZ[lo:hi].float() @ mlp.B.float().t()
+        s = torch.sigmoid(g)
+        dp = torch.cat((dh * u * s * (1 + g * (1 - s)), dh * g * s), 1)
+        assert ((z - Z[lo:hi]).abs() <= 2.1 * F * U * (h.abs() @ mlp.B.float().abs())).all()
+        assert ((dx - dX[lo:hi]).abs() <= 2.1 * 2 * F * U * (dp.abs() @ mlp.A.float().abs().t())).all()
+    del P
+    halves = [run(0, M // 2)[3:], run(M // 2, M)[3:]]
+    # Of M additions each is off by at most 2^-24 of a partial sum, whose norm over the elements grows with its
+    # terms (random ones): on either side at most M 2^-24 of the sums' norm.
+    for i, got in enumerate((dA, dB)):
+        want = halves[0][i].double() + halves[1][i].double()
+        assert float((got - want).norm() / want.norm()) <= 2 * M * U, i
+
+
 def test_glu_gradient_is_a_difference():
     """<dZ, Z(x + h d) - Z(x - h d)> / 2h against <gradient, d> with float32 outputs.  The step moves values by
     1/8 of themselves, so that the difference stands out of the bf16 roundings in Z: these are off by at most 2^-8 of h's
