@@ -136,6 +136,11 @@ hipError_t launch_act(int act, int64_t blocks, const A& a, hipStream_t s, K1 sil
 // ---------------------------------------------------------------------------
 // Plans: functions of the sizes alone
 // ---------------------------------------------------------------------------
+// The forward's products in slices of 256 of K or more: 5 tokens by 1104 x 800 19.2 us with 512, 16.7
+// so, 100 by 2048 x 1024 22.2 and 21.2, 64 by 4096 x 2048 28.1 and 29.1.  (The
+// backward's lose by it: 64 by 4096 x 2048 50.7 and 54.6.)
+constexpr int64_t FWD_SLICE = 256;
+
 struct GluFwdPlan {
   bool tokens;  // a few tokens' kernels, with the slices of P at off_h and of Z at off_part
   GluTokensPlan t1, t2;
@@ -154,8 +159,8 @@ GluFwdPlan plan_glu_fwd(int64_t M, int64_t H, int64_t F) {
     p.total = p.off_part + align_up(size_t(p.t2.slices) * M * H * 4);
     return p;
   }
-  p.g1 = plan_gemm(M, 2 * F, H, false);
-  p.g2 = plan_gemm(M, H, F);
+  p.g1 = plan_gemm(M, 2 * F, H, false, FWD_SLICE);
+  p.g2 = plan_gemm(M, H, F, true, FWD_SLICE);
   p.wt = transpose_weights(M, H, F);
   p.off_h = 0;
   p.off_At = align_up(size_t(M) * F * 2);

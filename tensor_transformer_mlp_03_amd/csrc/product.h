@@ -23,15 +23,16 @@ struct GemmPlan {
   double seconds = 0;  // by the planner's model
 };
 
-// The plan of C[M,N] over K; hybrid: its columns may be cut as above.
-GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool hybrid = true);
-
 // The model's rates of one CU on a tile, its bandwidth for split-K slices and its launch.
 constexpr double CU_RATE_256 = 4.3e12;      // flop/s per CU, 256x256 tile
 constexpr double CU_RATE_256x128 = 3.8e12;  // flop/s per CU, 256x128 tile (half the MFMAs per load)
 constexpr double CU_RATE_128 = 3.3e12;      // flop/s per CU, 128x128 tile (a quarter)
 constexpr double SPLIT_BW = 4.0e12;         // bytes/s for the slices' write and re-read
 constexpr double LAUNCH_S = 5e-6;
+
+// The plan of C[M,N] over K; hybrid: its columns may be cut as above.  Slices along K hold at
+// least min_slice of it.
+GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool hybrid = true, int64_t min_slice = 512);
 
 // Bytes of a plan's float32 split-K slices.
 inline size_t part_bytes(const GemmPlan& p, int64_t M, int64_t N) {

@@ -66,11 +66,11 @@ bool shape_ok(int64_t v) { return v > 0 && v <= MAX_DIM && (v % 8) == 0; }
 // over the chip's CUs (one block per CU: every tile takes the whole LDS); a
 // block's time is proportional to its MACs at the measured per-CU rate of its
 // tile; split-K adds a float32 round trip of the slices through memory and one
-// reduction launch (constants in product.h).  Splits keep at least 512 of K each.
+// reduction launch (constants in product.h).  Splits keep at least 512 of K each unless the caller asks for less.
 
 }  // namespace
 
-GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool hybrid) {
+GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool hybrid, int64_t min_slice) {
   GemmPlan best{TILE_256x256, 1, (int)((K + TILE_BK - 1) / TILE_BK * TILE_BK)};
   double best_t = 1e30;
   for (TileCfg tile : {TILE_256x256, TILE_256x128, TILE_128x128}) {
@@ -80,7 +80,7 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, bool hybrid) {
       const int64_t kslice = ((K + s - 1) / s + TILE_BK - 1) / TILE_BK * TILE_BK;
       const int splits = ceil_div(K, kslice);
       if (splits != s) continue;
-      if (s > 1 && kslice < 512) break;
+      if (s > 1 && kslice < min_slice) break;
       const double flops = double(bm * bn * 2 * kslice);
       const int64_t blocks = tiles * s;
       const double rate = tile == TILE_256x256 ? CU_RATE_256 : tile == TILE_256x128 ? CU_RATE_256x128 : CU_RATE_128;
