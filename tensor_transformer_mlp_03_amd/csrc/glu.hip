@@ -170,16 +170,19 @@ GluFwdPlan plan_glu_fwd(int64_t M, int64_t H, int64_t F) {
   return p;
 }
 
-// The products behind the activation in one launch (gemm_group.hip), dX split along K or not:
-// taken when the model gives it less time than three launches.  The makespan is that of
-// workgroups handed to free CUs in their order, dX's first.  A backward of 2048 tokens by 512 x
-// 2048 67 -> 45 us, of 180 by 1104 x 800 38 -> 28; where it is not taken, one token by 4096 x 2048,
-// whose 1568 tiles have a K step each, 46 us, together 49.
+// The products behind the activation in one launch (gemm_group.hip), each split along K or not, and one
+// launch that adds the slices up: taken when the model gives it less time than three
+// products.  The makespan is that of workgroups handed to free CUs in their order, the longest
+// first.  A backward of 2048 tokens by 512 x 2048 67 -> 45 us, of 180 by 1104 x 800 38 -> 28, of
+// 4305 by 64 x 408, where dB and dA are split, 44 -> 23; where it is not taken, one token by 4096
+// x 2048, whose 1568 tiles have a K step each, 46 us, together 49.
 constexpr int GROUP_TILE_STEPS = 3;  // what a tile takes beside its K steps, in steps: first loads and epilogue
+constexpr int GROUP_MIN_STEPS = 8;   // of a slice
 
 struct GroupPlan {
   bool on = false;
-  int splits = 1, k_split = 0;  // of dX
+  int s_dx = 1, s_dw = 1;  // slices along K of dX, of dB and dA each
+  int k_dx = 0, k_dw = 0;  // a slice's K
 };
 
 double group_steps(int64_t n0, int64_t k0, int64_t n1, int64_t k1) {
@@ -201,21 +204,23 @@ double group_steps(int64_t n0, int64_t k0, int64_t n1, int64_t k1) {
 GroupPlan plan_group(int64_t M, int64_t H, int64_t F, const GemmPlan& gdb, const GemmPlan& gda, const GemmPlan& gdx) {
   GroupPlan p;
   const int64_t tm = ceil_div(M, 128), th = ceil_div(H, 128), tf = ceil_div(F, 128), t2f = ceil_div(2 * F, 128);
-  const int64_t n1 = tf * th + th * t2f, k1 = ceil_div(M, TILE_BK);
-  if (tm * th + n1 > 8 * NUM_CU) return p;  // larger tiles are faster
+  const int64_t n0 = tm * th, n1 = tf * th + th * t2f, k0 = ceil_div(2 * F, TILE_BK), k1 = ceil_div(M, TILE_BK);
+  if (n0 + n1 > 8 * NUM_CU) return p;  // larger tiles are faster
   const double step = 128.0 * 128 * 2 * TILE_BK / CU_RATE_128;
   double best = gdb.seconds + gda.seconds + gdx.seconds + 2 * LAUNCH_S;
-  for (int s = 1; s <= 16; ++s) {
-    const int64_t steps = (ceil_div(2 * F, TILE_BK) + s - 1) / s;
-    if (ceil_div(2 * F, steps * TILE_BK) != s) continue;
-    if (s > 1 && steps < 8) break;
-    double t = step * group_steps(tm * th * s, steps + GROUP_TILE_STEPS, n1, k1 + GROUP_TILE_STEPS);
-    if (s > 1) t += double(s) * M * H * 4 * 2 / SPLIT_BW + LAUNCH_S;
-    if (t < best * (1 - 1e-9)) {
-      best = t;
-      p.on = true;
-      p.splits = s;
-      p.k_split = (int)(steps * TILE_BK);
+  for (int sx : {1, 2, 3, 4, 6, 8, 12, 16}) {
+    const int64_t kx = (k0 + sx - 1) / sx;
+    if ((sx > 1 && kx < GROUP_MIN_STEPS) || ceil_div(k0, kx) != sx) continue;
+    for (int sw : {1, 2, 4, 8, 16}) {
+      const int64_t kw = (k1 + sw - 1) / sw;
+      if ((sw > 1 && kw < GROUP_MIN_STEPS) || ceil_div(k1, kw) != sw) continue;
+      double t = step * (kx >= kw ? group_steps(n0 * sx, kx + GROUP_TILE_STEPS, n1 * sw, kw + GROUP_TILE_STEPS)
+                                  : group_steps(n1 * sw, kw + GROUP_TILE_STEPS, n0 * sx, kx + GROUP_TILE_STEPS));
+      if (sx > 1 || sw > 1) t += ((sx > 1 ? double(sx) * M * H : 0) + (sw > 1 ? double(sw) * 3 * H * F : 0)) * 4 * 2 / SPLIT_BW + LAUNCH_S;
+      if (t < best * (1 - 1e-9)) {
+        best = t;
+        p = GroupPlan{true, sx, sw, (int)(kx * TILE_BK), (int)(kw * TILE_BK)};
+      }
     }
   }
   return p;
@@ -257,7 +262,8 @@ GluBwdPlan plan_glu_bwd(int64_t M, int64_t H, int64_t F, bool recompute) {
   p.off_dPt = p.off_dP + m2f;
   p.off_part = p.off_dPt + (p.tdp ? m2f : 0);
   size_t part = std::max(recompute ? part_bytes(p.g0, M, 2 * F) : 0, part_bytes(p.g1, M, F));
-  if (p.group.on) part = std::max(part, p.group.splits > 1 ? size_t(p.group.splits) * M * H * 4 : 0);
+  if (p.group.on)
+    part = std::max(part, (p.group.s_dx > 1 ? size_t(p.group.s_dx) * M * H * 4 : 0) + (p.group.s_dw > 1 ? size_t(p.group.s_dw) * 3 * H * F * 4 : 0));
   else part = std::max({part, part_bytes(p.gdb, F, H), part_bytes(p.gda, H, 2 * F), part_bytes(p.gdx, M, H)});
   p.total = p.off_part + align_up(part);
   return p;
@@ -276,8 +282,7 @@ T* at(void* ws, size_t off) {
 // The launches
 // ---------------------------------------------------------------------------
 hipError_t enqueue_glu_fwd(const uint16_t* X, const uint16_t* A, const uint16_t* B, void* Z, Epi z_epi, uint16_t* P, int act,
-                           int64_t M, int64_t H, int64_t F, void* ws, hipStream_t s) {
-  const GluFwdPlan p = plan_glu_fwd(M, H, F);
+                           int64_t M, int64_t H, int64_t F, const GluFwdPlan& p, void* ws, hipStream_t s) {
   uint16_t *h = at<uint16_t>(ws, p.off_h), *At = at<uint16_t>(ws, p.off_At), *Bt = at<uint16_t>(ws, p.off_Bt);
   float* part = at<float>(ws, p.off_part);
   hipError_t e;
@@ -311,9 +316,8 @@ hipError_t enqueue_glu_fwd(const uint16_t* X, const uint16_t* A, const uint16_t*
 }
 
 hipError_t enqueue_glu_bwd(const uint16_t* dZ, const uint16_t* X, const uint16_t* A, const uint16_t* B, const uint16_t* P, void* dX,
-                           Epi x_epi, void* dA, void* dB, Epi w_epi, int act, int64_t M, int64_t H, int64_t F, void* ws,
-                           hipStream_t s) {
-  const GluBwdPlan p = plan_glu_bwd(M, H, F, P == nullptr);
+                           Epi x_epi, void* dA, void* dB, Epi w_epi, int act, int64_t M, int64_t H, int64_t F,
+                           const GluBwdPlan& p, void* ws, hipStream_t s) {
   const int64_t M8 = up8(M);
   uint16_t *Xt = at<uint16_t>(ws, p.off_Xt), *dZt = at<uint16_t>(ws, p.off_dZt), *ht = at<uint16_t>(ws, p.off_ht);
   uint16_t* dP = at<uint16_t>(ws, p.off_dP);
@@ -345,16 +349,19 @@ hipError_t enqueue_glu_bwd(const uint16_t* dZ, const uint16_t* X, const uint16_t
   }
   if (e != hipSuccess) return e;
   if (p.group.on) {
-    const bool split = p.group.splits > 1;
+    const GroupPlan& q = p.group;
     const int m = (int)M, h = (int)H, f = (int)F;
     const int tm = ceil_div(M, 128), th = ceil_div(H, 128);
+    float* part_dw = part + (q.s_dx > 1 ? q.s_dx * M * H : 0);
+    const bool xs = q.s_dx > 1, ws_ = q.s_dw > 1;
     const GroupItem items[GROUP_ITEMS] = {
-        {dP, A, 2 * F, 2 * F, m, h, 2 * f, p.group.k_split, split ? part : dX, tm, th},
-        {ht, dZ, M8, H, f, h, m, (int)up64(M), dB, ceil_div(F, 128), th},
-        {Xt, dP, M8, 2 * F, h, 2 * f, m, (int)up64(M), dA, th, ceil_div(2 * F, 128)}};
-    e = launch_gemm_group(items, !split && x_epi == EPI_BF16, w_epi == EPI_BF16, s);
-    if (e != hipSuccess || !split) return e;
-    return launch_splitk_epilogue(x_epi, part, p.group.splits, M, H, dX, nullptr, nullptr, H, M, s);
+        {dP, A, 2 * F, 2 * F, m, h, 2 * f, q.k_dx, xs ? part : dX, tm, th},
+        {ht, dZ, M8, H, f, h, m, q.k_dw, ws_ ? part_dw : dB, ceil_div(F, 128), th},
+        {Xt, dP, M8, 2 * F, h, 2 * f, m, q.k_dw, ws_ ? part_dw + q.s_dw * F * H : dA, th, ceil_div(2 * F, 128)}};
+    e = launch_gemm_group(items, !xs && x_epi == EPI_BF16, !ws_ && w_epi == EPI_BF16, s);
+    if (e != hipSuccess || !(xs || ws_)) return e;
+    void* const outs[GROUP_ITEMS] = {xs ? dX : nullptr, ws_ ? dB : nullptr, ws_ ? dA : nullptr};
+    return launch_group_sum(items, outs, x_epi == EPI_BF16, w_epi == EPI_BF16, s);
   }
   // dB = h^T dZ             h^T: [F][M8], dZ: [M][H] (rows past M masked) or dZ^T [H][M8]
   if (p.tdz) e = run_gemm(-1, KC, KC, w_epi, ht, M8, dZt, M8, F, H, M8, p.gdb, dB, nullptr, nullptr, part, s);
@@ -410,12 +417,13 @@ tpmlp_status tpmlp_glu_fwd(const tpmlp_bf16* X, const tpmlp_bf16* A, const tpmlp
     if (M == 0) return TPMLP_OK;
     TRY(check_ptrs({{X, "X"}, {A, "A"}, {B, "B"}, {Z, "Z"}}));
     if (P_save && !aligned16(P_save)) return fail(TPMLP_ERR_ALIGN, "P_save is not 16-byte aligned");
-    const size_t need = plan_glu_fwd(M, H, F).total, mh = size_t(M) * H, mf = size_t(M) * F, hf = size_t(H) * F;
+    const GluFwdPlan plan = plan_glu_fwd(M, H, F);
+    const size_t need = plan.total, mh = size_t(M) * H, mf = size_t(M) * F, hf = size_t(H) * F;
     TRY(check_ws(ws, ws_bytes, need, "tpmlp_glu_fwd_workspace_bytes"));
     TRY(check_alias({{Z, mh * size_of(z_type), "Z"}, {P_save, mf * 4, "P_save"}, {ws, need, "ws"}},
                     {{X, mh * 2, "X"}, {A, hf * 4, "A"}, {B, hf * 2, "B"}}));
     TRY(check_device());
-    return launched(enqueue_glu_fwd(X, A, B, Z, z_type == TPMLP_BF16 ? EPI_BF16 : EPI_F32, P_save, act, M, H, F, ws,
+    return launched(enqueue_glu_fwd(X, A, B, Z, z_type == TPMLP_BF16 ? EPI_BF16 : EPI_F32, P_save, act, M, H, F, plan, ws,
                                     stream_of(stream)),
                     "tpmlp_glu_fwd launch");
   });
@@ -430,11 +438,13 @@ tpmlp_status tpmlp_glu_bwd(const tpmlp_bf16* dZ, const tpmlp_bf16* X, const tpml
     const size_t mh = size_t(M) * H, mf = size_t(M) * F, hf = size_t(H) * F;
     const size_t xs = size_of(dx_type), wsz = size_of(dw_type);
     TRY(check_ptrs({{dA, "dA"}, {dB, "dB"}}));
+    GluBwdPlan plan;
     size_t need = 0;
     if (M > 0) {
       TRY(check_ptrs({{dZ, "dZ"}, {X, "X"}, {A, "A"}, {B, "B"}, {dX, "dX"}}));
       if (P_saved && !aligned16(P_saved)) return fail(TPMLP_ERR_ALIGN, "P_saved is not 16-byte aligned");
-      need = plan_glu_bwd(M, H, F, P_saved == nullptr).total;
+      plan = plan_glu_bwd(M, H, F, P_saved == nullptr);
+      need = plan.total;
       TRY(check_ws(ws, ws_bytes, need, "tpmlp_glu_bwd_workspace_bytes"));
     }
     TRY(check_alias({{dX, mh * xs, "dX"}, {dA, hf * 2 * wsz, "dA"}, {dB, hf * wsz, "dB"}, {ws, need, "ws"}},
@@ -446,7 +456,7 @@ tpmlp_status tpmlp_glu_bwd(const tpmlp_bf16* dZ, const tpmlp_bf16* X, const tpml
       return launched(zero(dB, (int64_t)(hf * wsz), s), "tpmlp_glu_bwd launch");
     }
     return launched(enqueue_glu_bwd(dZ, X, A, B, P_saved, dX, dx_type == TPMLP_BF16 ? EPI_BF16 : EPI_F32, dA, dB,
-                                    dw_type == TPMLP_BF16 ? EPI_BF16 : EPI_F32, act, M, H, F, ws, s),
+                                    dw_type == TPMLP_BF16 ? EPI_BF16 : EPI_F32, act, M, H, F, plan, ws, s),
                     "tpmlp_glu_bwd launch");
   });
 }

@@ -54,8 +54,9 @@ hipError_t run_gemm(int kind, Layout la, Layout lb, Epi epi, const void* a, int6
                     float* part, hipStream_t s, int64_t ldo = 0, int64_t ldt = 0);
 
 // A bf16 product of a launch of several (gemm_group.hip), on 128 x 128 tiles: C[M,N] = A B with A
-// K-contiguous, out with rows of N.  Item 0 has B K-contiguous and may be split along K, its
-// float32 slices one after the other in out; the others have B N-contiguous.
+// K-contiguous, out with rows of N.  Item 0 has B K-contiguous, the others N-contiguous.  Split along K
+// (k_split below K; float32), an item's slices lie one after the other in out, and
+// launch_group_sum adds them up into outs[i] (null: item i was not split).
 struct GroupItem {
   const uint16_t *a, *b;
   int64_t lda, ldb;
@@ -70,5 +71,7 @@ hipError_t launch_gemm_transpose(const GemmArgs& g, int splits, int act, const u
                                  int64_t ld_out, hipStream_t s);
 
 hipError_t launch_gemm_group(const GroupItem (&item)[GROUP_ITEMS], bool bf16_0, bool bf16_1, hipStream_t s);
+hipError_t launch_group_sum(const GroupItem (&item)[GROUP_ITEMS], void* const (&outs)[GROUP_ITEMS], bool bf16_0, bool bf16_1,
+                            hipStream_t s);
 
 }  // namespace tpmlp

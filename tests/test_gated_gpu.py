@@ -153,6 +153,13 @@ def test_glu_several_tiles(M, H, F):
     check_glu(M, H, F, "silu", z=F32, x=F32, w=BF16, keep=M != 513)
 
 
+@pytest.mark.parametrize("M,H,F", [(2100, 72, 40), (3000, 136, 24), (4305, 64, 408), (1999, 24, 1032)])
+@pytest.mark.parametrize("x,w", [("f32", "bf16"), ("bf16", "f32")])
+def test_glu_many_tokens(M, H, F, x, w):
+    """Small weights: their gradients' products are split along the tokens, the tokens' along F or not."""
+    check_glu(M, H, F, "silu", x=NAMES[x], w=NAMES[w], keep=x == "f32")
+
+
 @pytest.mark.parametrize("M,H,F", [(1001, 1000, 1368), (40, 4096, 2048), (2, 4104, 2056), (9, 8200, 520), (2056, 1032, 2048),
                                    (6400, 264, 520)])
 def test_glu_large(M, H, F):
