@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(256) glu_split_kernel(GluSplitArgs a) {
     const int64_t row = (uint64_t)j / f4, col = 4 * ((uint64_t)j % f4);
     const float* pg = a.part + row * 2 * a.F + col;
     f32x4_t g = *reinterpret_cast<const f32x4_t*>(pg), u = *reinterpret_cast<const f32x4_t*>(pg + a.F);
+#pragma unroll 4
     for (int i = 1; i < a.splits; ++i) {
       g += *reinterpret_cast<const f32x4_t*>(pg + i * plane);
       u += *reinterpret_cast<const f32x4_t*>(pg + i * plane + a.F);
@@ -79,6 +80,7 @@ __global__ void __launch_bounds__(256) dglu_split_kernel(DGluSplitArgs a) {
     if (row < a.M && col < a.F) {  // F % 8 == 0: eight columns in or out together
       const float* x = a.part + row * a.F + col;
       f32x4_t s0 = *reinterpret_cast<const f32x4_t*>(x), s1 = *reinterpret_cast<const f32x4_t*>(x + 4);
+#pragma unroll 4  // loads in flight together: 16 slices 7.2 us without
       for (int i = 1; i < a.splits; ++i) {
         s0 += *reinterpret_cast<const f32x4_t*>(x + i * plane);
         s1 += *reinterpret_cast<const f32x4_t*>(x + i * plane + 4);
@@ -245,9 +247,11 @@ GluBwdPlan plan_glu_bwd(int64_t M, int64_t H, int64_t F, bool recompute) {
   p.wt = recompute && transpose_weights(M, H, F);
   p.group = plan_group(M, H, F, p.gdb, p.gda, p.gdx);
   // dZ^T pays as dP^T does, by F instead of H: 2048 tokens by 4096 x 2048 without it save 6 us of
-  // transposing and lose 4 in dB.
-  p.tdp = !p.group.on && transpose_dp(M, H, F);
-  p.tdz = !p.group.on && transpose_dp(M, F, H);
+  // transposing and lose 4 in dB.  Either is a launch as well, which few tokens' products do not earn
+  // (4.4e-17 s a multiply-add of dB, twice that of dA).
+  const bool large = double(M) * H * F * 4.4e-17 * 2 > LAUNCH_S;
+  p.tdp = !p.group.on && large && transpose_dp(M, H, F);
+  p.tdz = !p.group.on && large && transpose_dp(M, F, H);
   // Where the workgroups of both fit the chip at once, the transpose is hidden: 300 tokens by 520 x
   // 264 20.7 us after it, 18.0 beside it; 1001 by 1000 x 1368 with P made again 62.6 and 59.3.
   const int64_t tiles = (int64_t)ceil_div(M, 128) * ceil_div(F, 128) * p.g1.splits;
