@@ -25,7 +25,6 @@ typedef uint16_t u16x4_t __attribute__((ext_vector_type(4)));
 typedef uint16_t u16x8_t __attribute__((ext_vector_type(8)));
 
 int64_t up8(int64_t x) { return (x + 7) / 8 * 8; }
-int64_t up64(int64_t x) { return (x + 63) / 64 * 64; }
 
 // ---------------------------------------------------------------------------
 // The gated product split along K: the slices' sum with the epilogue of EPI_GLU
