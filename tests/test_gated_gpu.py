@@ -743,6 +743,26 @@ def test_fp4_quantize(K, N, pad):
         assert (OG.e2m1_values(got)[np.repeat(diff, 2, 1)] == OG.e2m1_values(want_c)[np.repeat(diff, 2, 1)]).all()
 
 
+@pytest.mark.parametrize("x", ["bf16", "row", "mx"])
+@pytest.mark.parametrize("K", [64, 160])
+def test_fp4_more_tokens_than_a_launch_takes(x, K):
+    """The first and last rows equal those of the rows alone, across the launches' border too."""
+    from tensor_transformer_mlp_03_amd.gated import Fp4Linear
+    gen = torch.Generator().manual_seed(K)
+    M, N = 16 * 4096 + 37, 24
+    codes, scales = fp4_weight(gen, N, K)
+    X, xs, _ = fp4_x(gen, M, K, x)
+    X, xs = X.cuda(), None if xs is None else xs.cuda()
+    lin = Fp4Linear(codes.cuda(), scales.cuda(), "gelu")
+    Y = torch.full((M, N), float("nan"), device="cuda")
+    lin.forward(X, Y, xs)
+    assert torch.isfinite(Y).all()
+    for lo, hi in ((0, 50), (16 * 4096 - 20, 16 * 4096 + 20), (M - 30, M)):
+        part = torch.empty(hi - lo, N, device="cuda")
+        lin.forward(X[lo:hi], part, None if xs is None else xs[lo:hi])
+        assert torch.equal(part, Y[lo:hi]), lo
+
+
 def test_fp4_offsets_past_32_bits():
     """Codes of more than 2^31 bytes: the last rows' products equal those of the rows alone."""
     from tensor_transformer_mlp_03_amd.gated import Fp4Linear
