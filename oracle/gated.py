@@ -27,7 +27,7 @@ def act(x, kind):
     if kind == "none":
         return x, np.ones_like(x)
     if kind == "relu":
-        return np.where(x > 0, x, 0 * x), (x > 0).astype(np.float64)
+        return np.where(x < 0, 0.0, x), (x > 0).astype(np.float64)
     if kind == "gelu":
         cdf = 0.5 * (1 + _erf(x / math.sqrt(2))) if x.size else x
         return x * cdf, cdf + x * np.exp(-x * x / 2) / math.sqrt(2 * math.pi)

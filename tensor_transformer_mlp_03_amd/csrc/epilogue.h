@@ -123,7 +123,7 @@ template <int ACT>
 __device__ __forceinline__ float act_f32(float x) {
   if constexpr (ACT == 1) return x * sigmoid_f32(x);
   else if constexpr (ACT == 2) return gelu_f32(x);
-  else if constexpr (ACT == 3) return x > 0.0f ? x : x * 0.0f;  // NaN stays NaN
+  else if constexpr (ACT == 3) return x < 0.0f ? 0.0f : x;  // NaN stays NaN
   else if constexpr (ACT == 4) return sigmoid_f32(x);
   else return x;
 }
@@ -141,7 +141,7 @@ __device__ __forceinline__ void act_grad_f32(float x, float& a, float& da) {
     a = x * cdf;
     da = __builtin_fmaf(x, n.f, cdf);
   } else if constexpr (ACT == 3) {
-    a = x > 0.0f ? x : x * 0.0f;
+    a = x < 0.0f ? 0.0f : x;
     da = x > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == 4) {
     a = sigmoid_f32(x);

@@ -1,0 +1,101 @@
+"""The gated block's kernels at the ends of their arguments: infinite pre-activations, derivatives far
+out, scales at the ends of their range.  What is wanted is exact or follows from the definition; where
+it is neither, the tolerance stands beside it."""
+import sys
+
+import numpy as np
+import pytest
+
+from oracle import gated as OG
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+F32, BF16, U8 = torch.float32, torch.bfloat16, torch.uint8
+U = OG.U
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from tensor_transformer_mlp_03_amd import _lib as L
+    L.lib()
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    print(f"[case] {request.node.name}", flush=True)
+    sys.stdout.flush()
+
+
+def filled(*shape, dtype=F32):
+    return torch.full(shape, float("nan"), dtype=dtype, device="cuda")
+
+
+def infinite_gates(M, H, F, row, value, seed=0):
+    """X, A, B, dZ whose gates in `row` are value * 2^100 plus the other terms, which are far below it and
+    as they are in all rows; value 2^100 makes them infinite.  The up projections do not see it."""
+    gen = torch.Generator().manual_seed(seed + M + H + F)
+    n = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    X, A, B, dZ = n(M, H), n(H, 2 * F) * H ** -0.5, n(F, H) * F ** -0.5, n(M, H)
+    X[:, 0] = 0
+    X[row, 0] = value
+    A[0, :F], A[0, F:] = 2.0 ** 100, 0
+    return [t.bfloat16().cuda() for t in (X, A, B, dZ)]
+
+
+# The forward's kernels: a few tokens', split along K, and fused.
+SIZES = [(1, 520, 72), (3, 136, 72), (40, 4096, 256), (300, 136, 264), (1500, 1032, 1032)]
+
+
+@pytest.mark.parametrize("M,H,F", SIZES)
+def test_relu_of_minus_infinity_is_zero(M, H, F):
+    """max(-inf, 0) = 0, as for any negative gate: equal bits with the gates at -2^110, forward and, with P kept
+    and made again, backward."""
+    from tensor_transformer_mlp_03_amd.gated import GatedMLP
+    row, got = M // 2, []
+    for value in (-2.0 ** 100, -2.0 ** 10):
+        X, A, B, dZ = infinite_gates(M, H, F, row, value)
+        mlp = GatedMLP(A, B, "relu")
+        Z, P = filled(M, H), filled(M, 2 * F, dtype=BF16)
+        mlp.forward(X, Z, P)
+        assert (P[row, :F] == (-float("inf") if value < -2.0 ** 50 else -2.0 ** 110)).all()
+        out = [Z]
+        for kept in (P, None):
+            dX, dA, dB = filled(M, H), filled(H, 2 * F), filled(F, H)
+            mlp.backward(dZ, X, kept, dX, dA, dB)
+            out += [dX, dA, dB]
+        assert (Z[row] == 0).all() and all(torch.isfinite(t).all() for t in out)
+        got.append(out)
+    for i, (a, b) in enumerate(zip(*got)):
+        assert torch.equal(a, b), i
+
+
+@pytest.mark.parametrize("M", [1, 40, 70])
+@pytest.mark.parametrize("gated", [False, True])
+def test_relu_of_a_4_bit_product_of_minus_infinity(M, gated):
+    from tensor_transformer_mlp_03_amd.gated import Fp4Linear
+    N, K = 40, 160
+    codes = torch.full((2 * N if gated else N, K // 2), 0x22, dtype=U8)  # ones
+    scales = torch.full((codes.shape[0], K // 32), 127, dtype=U8)
+    codes[:N, 0] = 0x2A       # the gates' first weight is -2^100
+    codes[N:, 0] = 0x20       # the ups' is 0
+    scales[:N, 0] = 227
+    X = torch.zeros(M, K, dtype=BF16)
+    X[:, 40] = 3.0
+    X[M // 2, 0] = 2.0 ** 100
+    Y = filled(M, N)
+    Fp4Linear(codes.cuda(), scales.cuda(), "relu", gated).forward(X.cuda(), Y)
+    want = torch.full((M, N), 9.0 if gated else 3.0)
+    want[M // 2] = 0
+    assert torch.equal(Y.cpu(), want)
+
+
+def test_relu_keeps_nan():
+    from tensor_transformer_mlp_03_amd.gated import GatedMLP
+    for M in (1, 40, 300):
+        X, A, B, dZ = infinite_gates(M, 136, 72, 0, float("nan"))
+        Z = torch.zeros(M, 136, device="cuda")
+        GatedMLP(A, B, "relu").forward(X, Z)
+        assert torch.isnan(Z[0]).all() and torch.isfinite(Z[1:]).all()
