@@ -122,7 +122,7 @@ __device__ __forceinline__ float sigmoid_f32(float x) {
 template <int ACT>
 __device__ __forceinline__ float act_f32(float x) {
   if constexpr (ACT == 1) return x * sigmoid_f32(x);
-  else if constexpr (ACT == 2) return gelu_f32(x);
+  else if constexpr (ACT == 2) return x > 3.402823466e38f ? x : gelu_f32(x);  // infinity, whose |x| Phi(-|x|) were NaN
   else if constexpr (ACT == 3) return x < 0.0f ? 0.0f : x;  // NaN stays NaN
   else if constexpr (ACT == 4) return sigmoid_f32(x);
   else return x;
