@@ -144,8 +144,10 @@ __device__ __forceinline__ void act_grad_f32(float x, float& a, float& da) {
     a = x < 0.0f ? 0.0f : x;
     da = x > 0.0f ? 1.0f : 0.0f;
   } else if constexpr (ACT == 4) {
-    a = sigmoid_f32(x);
-    da = a * (1.0f - a);
+    // e / (1 + e)^2 with e = exp(-|x|): a (1 - a) would lose its bits where a is next to 1
+    const float e = __builtin_amdgcn_exp2f(fabsf(x) * -1.4426950408889634f), r = __builtin_amdgcn_rcpf(1.0f + e);
+    a = x < 0.0f ? e * r : r;
+    da = e * r * r;
   } else {
     a = x;
     da = 1.0f;

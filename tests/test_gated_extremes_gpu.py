@@ -132,3 +132,26 @@ def test_gelu_of_a_4_bit_product_of_infinity():
         Y = filled(5, 24)
         Fp4Linear(codes.cuda(), torch.full((24, 1), 200, dtype=U8).cuda(), act).forward(X.cuda(), Y)
         assert (Y == float("inf")).all(), act
+
+
+@pytest.mark.parametrize("M", [3, 40, 200])
+@pytest.mark.parametrize("split", [False, True])
+def test_sigmoid_derivative_far_out(M, split):
+    """sigmoid' = s(g) s(-g) keeps its bits where s is next to 1: dX = dP_g with A_g the unit matrix, A_u zero, h and dh
+    chosen 1.  dP_g is rounded to bf16 (2^-8 of the value, as it counts half a step) behind an exponential, a
+    reciprocal, and products: |g| 2^-24 log2(e) for the exponent's rounding and 16 more of 2^-24."""
+    from tensor_transformer_mlp_03_amd.gated import GatedMLP
+    H = 1024 if split else 64
+    F = H
+    g = torch.linspace(-40, 40, M * F).view(M, F).bfloat16()
+    A = torch.zeros(H, 2 * F)
+    A[:, :F] = torch.eye(H)
+    X, B = torch.zeros(M, H), torch.eye(F, H)
+    P = torch.cat((g, torch.ones(M, F).bfloat16()), 1)
+    dX, dA, dB = filled(M, H), filled(H, 2 * F), filled(F, H)
+    GatedMLP(A.bfloat16().cuda(), B.bfloat16().cuda(), "sigmoid").backward(
+        torch.ones(M, H, dtype=BF16).cuda(), X.bfloat16().cuda(), P.cuda(), dX, dA, dB)
+    x = np.abs(g.double().numpy())
+    want = np.exp(-x) / (1 + np.exp(-x)) ** 2
+    off = np.abs(dX.cpu().double().numpy() - want) / want
+    assert (off <= 2.0 ** -8 + (2 * x + 16) * U).all(), (float(off.max()), float(x.ravel()[off.argmax()]))
