@@ -907,10 +907,18 @@ def tpmlp_dropout_bwd(dout, dy, db, p: float, state, site: int = 0, first_row: i
         _check(st, "tpmlp_dropout_bwd")
 
 
-def _bytes(t, shape, name):
-    """(pointer, row stride) of a [rows, columns] tensor of one-byte values with contiguous columns."""
-    if t.element_size() != 1:
-        raise TypeError(f"{name} must hold one-byte values, got {t.dtype}")
+_BYTE_TYPES = {}  # torch's types of each kind of one-byte values, beside raw bytes
+
+
+def _bytes(t, shape, name, kind):
+    """(pointer, row stride) of a [rows, columns] tensor with contiguous columns of one-byte values of a
+    kind: "E4M3", "E8M0" or "E2M1" (two a byte), as torch's type of that format or as uint8."""
+    if not _BYTE_TYPES:
+        import torch
+        for k, n in (("E4M3", "float8_e4m3fn"), ("E8M0", "float8_e8m0fnu"), ("E2M1", "float4_e2m1fn_x2")):
+            _BYTE_TYPES[k] = (torch.uint8, getattr(torch, n, torch.uint8))
+    if t.dtype not in _BYTE_TYPES[kind]:
+        raise TypeError(f"{name} must hold one-byte values, {kind} or uint8, got {t.dtype}")
     return _rows(t, shape, name)
 
 
@@ -919,13 +927,13 @@ def _scales(t, M, blocks, name):
     import torch
     if t.dtype == torch.float32:
         return _flat(t, M, torch.float32, name), 0, SCALE_ROW
-    p, ld = _bytes(t, (M, blocks), name)
+    p, ld = _bytes(t, (M, blocks), name, "E8M0")
     return p, ld, SCALE_MX
 
 
 def tpmlp_edge_fwd_fp8(d: EdgeDesc, y, r, r_out, codes, scales, stream=None):
-    """tpmlp_edge_fwd with x as E4M3 codes [M,H] (one-byte values) and scales: float32 [M], or a byte
-    for every 32 values, [M, H / 32]."""
+    """tpmlp_edge_fwd with x as E4M3 codes [M,H] (float8_e4m3fn or uint8) and scales: float32 [M], or a
+    byte for every 32 values, [M, H / 32] (float8_e8m0fnu or uint8)."""
     M, H = r.shape[0], d.H
     if d.gate_tokens is not None:
         _check_gate(d, M)
@@ -937,7 +945,7 @@ def tpmlp_edge_fwd_fp8(d: EdgeDesc, y, r, r_out, codes, scales, stream=None):
         c.y_type = _dtype(y, "y")
         py, ly = _rows(y, (M, H), "y")
     po, lo = _rows(r_out, (M, H), "r_out", c.r_type)
-    pc, lc = _bytes(codes, (M, H), "codes")
+    pc, lc = _bytes(codes, (M, H), "codes", "E4M3")
     ps, ls, kind = _scales(scales, M, H // 32, "scales")
     st = lib().tpmlp_edge_fwd_fp8(ctypes.byref(c), py, ly or 0, pr, lr, po, lo, pc, lc, ps, ls, kind, _stream(stream))
     if st:
@@ -945,11 +953,12 @@ def tpmlp_edge_fwd_fp8(d: EdgeDesc, y, r, r_out, codes, scales, stream=None):
 
 
 def tpmlp_fp4_quantize(W, codes, scales, stream=None):
-    """E2M1 codes [N, K/2] and scales [N, K/32] (one-byte values) of bf16 weights W[K,N]."""
+    """E2M1 codes [N, K/2] (float4_e2m1fn_x2 or uint8) and scales [N, K/32] (float8_e8m0fnu or uint8) of
+    bf16 weights W[K,N]."""
     K, N = W.shape
     pw, lw = _rows(W, (K, N), "W", BF16)
-    pc, lc = _bytes(codes, (N, K // 2), "codes")
-    ps, ls = _bytes(scales, (N, K // 32), "scales")
+    pc, lc = _bytes(codes, (N, K // 2), "codes", "E2M1")
+    ps, ls = _bytes(scales, (N, K // 32), "scales", "E8M0")
     if lc or ls:
         raise ValueError("codes and scales must be contiguous")
     _check(lib().tpmlp_fp4_quantize(pw, lw, K, N, pc, ps, _stream(stream)), "tpmlp_fp4_quantize")
@@ -967,8 +976,8 @@ def tpmlp_fp4_pack(codes, scales, packed, gated: bool = False, stream=None):
     if gated and rows % 2:
         raise ValueError(f"a gated weight has an even number of rows, not {rows}")
     N = rows // 2 if gated else rows
-    pc, lc = _bytes(codes, (rows, K // 2), "codes")
-    ps, ls = _bytes(scales, (rows, K // 32), "scales")
+    pc, lc = _bytes(codes, (rows, K // 2), "codes", "E2M1")
+    ps, ls = _bytes(scales, (rows, K // 32), "scales", "E8M0")
     if lc or ls:
         raise ValueError("codes and scales must be contiguous")
     pp = _flat(packed, tpmlp_fp4_packed_bytes(N, K, gated), torch.uint8, "packed")
@@ -977,14 +986,14 @@ def tpmlp_fp4_pack(codes, scales, packed, gated: bool = False, stream=None):
 
 def tpmlp_fp4_fwd(X, x_scales, packed, Y, act: str = "none", gated: bool = False, stream=None):
     """Y[M,N] = act(X W^T), or act(X W_g^T) * (X W_u^T) with W = [W_g; W_u], from a packed weight; X[M,K]
-    bf16, or E4M3 codes (one-byte values) with x_scales as tpmlp_edge_fwd_fp8 writes them; Y float32 or bf16."""
+    bf16, or E4M3 codes (float8_e4m3fn or uint8) with x_scales as tpmlp_edge_fwd_fp8 writes them; Y float32 or bf16."""
     import torch
     (M, K), N = X.shape, Y.shape[1]
     ps, kind = None, X_BF16
     if X.element_size() == 1:
         if x_scales is None:
             raise ValueError("X in E4M3 needs x_scales")
-        px, lx = _rows(X, (M, K), "X")
+        px, lx = _bytes(X, (M, K), "X", "E4M3")
         ps, ls, scale = _scales(x_scales, M, K // 32, "x_scales")
         if ls:
             raise ValueError("x_scales must be contiguous")
