@@ -822,6 +822,13 @@ def _dense(t, shape, name, kind=None):
     return t.data_ptr()
 
 
+def _act(act: str) -> int:
+    kind = ACTS.get(act)
+    if kind is None:
+        raise ValueError(f"no activation {act!r}")
+    return kind
+
+
 def _glu_sizes(A, B):
     (F, H), (h, f2) = B.shape, A.shape
     if h != H or f2 != 2 * F:
@@ -843,7 +850,7 @@ def tpmlp_glu_fwd(X, A, B, Z, P_save, act: str, ws, stream=None):
     M = X.shape[0]
     pw, nw = _ws(ws)
     st = lib().tpmlp_glu_fwd(_dense(X, (M, H), "X", BF16), _dense(A, (H, 2 * F), "A", BF16), _dense(B, (F, H), "B", BF16),
-                             _dense(Z, (M, H), "Z"), _dtype(Z, "Z"), _dense(P_save, (M, 2 * F), "P_save", BF16), ACTS[act], M,
+                             _dense(Z, (M, H), "Z"), _dtype(Z, "Z"), _dense(P_save, (M, 2 * F), "P_save", BF16), _act(act), M,
                              H, F, pw, nw, _stream(stream))
     if st:
         _check(st, "tpmlp_glu_fwd")
@@ -858,7 +865,7 @@ def tpmlp_glu_bwd(dZ, X, A, B, P_saved, dX, dA, dB, act: str, ws, stream=None):
     st = lib().tpmlp_glu_bwd(_dense(dZ, (M, H), "dZ", BF16), _dense(X, (M, H), "X", BF16), _dense(A, (H, 2 * F), "A", BF16),
                              _dense(B, (F, H), "B", BF16), _dense(P_saved, (M, 2 * F), "P_saved", BF16),
                              _dense(dX, (M, H), "dX"), _dtype(dX, "dX"), _dense(dA, (H, 2 * F), "dA"),
-                             _dense(dB, (F, H), "dB", kind), kind, ACTS[act], M, H, F, pw, nw, _stream(stream))
+                             _dense(dB, (F, H), "dB", kind), kind, _act(act), M, H, F, pw, nw, _stream(stream))
     if st:
         _check(st, "tpmlp_glu_bwd")
 
@@ -1004,7 +1011,7 @@ def tpmlp_fp4_fwd(X, x_scales, packed, Y, act: str = "none", gated: bool = False
             raise ValueError("x_scales is given with a bf16 X")
     pp = _flat(packed, tpmlp_fp4_packed_bytes(N, K, gated), torch.uint8, "packed")
     py, ly = _rows(Y, (M, N), "Y")
-    st = lib().tpmlp_fp4_fwd(px, kind, lx, ps, pp, py, _dtype(Y, "Y"), ly, ACTS[act], int(bool(gated)), M, N, K, _stream(stream))
+    st = lib().tpmlp_fp4_fwd(px, kind, lx, ps, pp, py, _dtype(Y, "Y"), ly, _act(act), int(bool(gated)), M, N, K, _stream(stream))
     if st:
         _check(st, "tpmlp_fp4_fwd")
 

@@ -75,3 +75,15 @@ def test_the_formats_own_types_are_taken():
                 L.tpmlp_fp4_pack(c, s, z(1088, dtype=U8), stream=0)
             with pytest.raises(L.TpmlpError):
                 L.tpmlp_fp4_quantize(z(64, 9), c, s, stream=0)
+
+
+def test_unknown_activations_are_named():
+    """By the calls themselves, as by the objects."""
+    X, A, B, P = z(5, 64), z(64, 80), z(40, 64), z(5, 80)
+    for act in ("tanh", None):
+        with pytest.raises(ValueError, match="no activation"):
+            L.tpmlp_glu_fwd(X, A, B, z(5, 64), P, act, None)
+        with pytest.raises(ValueError, match="no activation"):
+            L.tpmlp_glu_bwd(X, X, A, B, P, z(5, 64), z(64, 80), z(40, 64), act, None)
+        with pytest.raises(ValueError, match="no activation"):
+            L.tpmlp_fp4_fwd(X, None, z(1088, dtype=U8), z(5, 9), act)
