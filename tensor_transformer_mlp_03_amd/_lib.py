@@ -886,14 +886,14 @@ def tpmlp_dropout_fwd(y, bias, r, out, p: float, state, site: int = 0, first_row
     pr, lr = _rows(r, (M, H), "r", kind)
     st = lib().tpmlp_dropout_fwd(py, _dtype(y, "y"), ly, _flat(bias, H, bias.dtype, "bias") if bias is not None else None,
                                  _dtype(bias, "bias") if bias is not None else F32, pr, lr, po, kind, lo, M, H, p,
-                                 _state(state), _u32(site, "site"), first_row, _stream(stream))
+                                 _state(state), _u32(site, "site"), _u32(first_row, "first_row", 1), _stream(stream))
     if st:
         _check(st, "tpmlp_dropout_fwd")
 
 
-def _u32(v: int, name: str) -> int:
-    if not 0 <= v < 1 << 32:  # ctypes would take its low bits
-        raise ValueError(f"{name} must be from 0 to 2^32 - 1")
+def _u32(v: int, name: str, past: int = 0) -> int:
+    if not 0 <= v < (1 << 32) + past:  # ctypes would take its low bits
+        raise ValueError(f"{name} must be from 0 to 2^32" + (" - 1" if not past else ""))
     return v
 
 
@@ -909,7 +909,7 @@ def tpmlp_dropout_bwd(dout, dy, db, p: float, state, site: int = 0, first_row: i
     py, ly = _rows(dy, (M, H), "dy")
     pw, nw = _ws(ws)
     st = lib().tpmlp_dropout_bwd(pg, _dtype(dout, "dout"), lg, py, _dtype(dy, "dy"), ly, _flat(db, H, torch.float32, "db"), M, H,
-                                 p, _state(state), _u32(site, "site"), first_row, pw, nw, _stream(stream))
+                                 p, _state(state), _u32(site, "site"), _u32(first_row, "first_row", 1), pw, nw, _stream(stream))
     if st:
         _check(st, "tpmlp_dropout_bwd")
 

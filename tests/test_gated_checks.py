@@ -87,3 +87,15 @@ def test_unknown_activations_are_named():
             L.tpmlp_glu_bwd(X, X, A, B, P, z(5, 64), z(64, 80), z(40, 64), act, None)
         with pytest.raises(ValueError, match="no activation"):
             L.tpmlp_fp4_fwd(X, None, z(1088, dtype=U8), z(5, 9), act)
+
+
+def test_first_rows_past_64_bits_are_refused():
+    """They would reach the library as their low bits."""
+    y, state = z(5, 64), torch.zeros(2, dtype=torch.int64)
+    for first in (1 << 64, (1 << 64) + 8, -(1 << 64), -1, (1 << 32) + 1):
+        with pytest.raises(ValueError, match="first_row"):
+            L.tpmlp_dropout_fwd(y, None, None, z(5, 64), 0.1, state, first_row=first, stream=0)
+        with pytest.raises(ValueError, match="first_row"):
+            L.tpmlp_dropout_bwd(y, z(5, 64), None, 0.1, state, first_row=first, stream=0)
+    with pytest.raises(L.TpmlpError, match="first_row"):  # the library counts the rows behind it
+        L.tpmlp_dropout_fwd(y, None, None, z(5, 64), 0.1, state, first_row=1 << 32, stream=0)
