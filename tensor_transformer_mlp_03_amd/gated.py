@@ -43,6 +43,15 @@ class _Workspace:
         return self._ws
 
 
+def _used(stream, *tensors):
+    """Marks tensors as used on the stream that a call was given: one that is freed goes back to the
+    stream that it was made on when what the other does by now is done."""
+    import torch
+    with _on(stream, tensors[0].device):
+        for t in (t for t in tensors if t.is_cuda):
+            t.record_stream(torch.cuda.current_stream())
+
+
 class GatedMLP:
     """One rank's gated MLP:  [P_g | P_u] = X A,  Z = (act(P_g) * P_u) B.
 
@@ -116,9 +125,10 @@ class Dropout:
 class Fp4Linear:
     """A product with 4-bit weights:  Y = act(X W^T), or gated  Y = act(X W_g^T) * (X W_u^T).
 
-    ``codes`` [N, K / 2] uint8, two E2M1 values a byte, the lower k in the low half; ``scales``
-    [N, K / 32] bytes, 2^(e - 127) for every 32 values; gated: W_g's rows, then W_u's.  They are
-    copied into the order that the kernels read, on ``stream``, and not kept.
+    ``codes`` [N, K / 2] uint8 (or float4_e2m1fn_x2), two E2M1 values a byte, the lower k in the low half;
+    ``scales`` [N, K / 32] uint8 (or float8_e8m0fnu), 2^(e - 127) for every 32 values; gated: W_g's rows,
+    then W_u's.  They are copied into the order that the kernels read, on ``stream``, and not kept: their
+    memory is not used anew before that is done.
     """
 
     def __init__(self, codes, scales, act="none", gated=False, stream=None):
@@ -139,6 +149,13 @@ class Fp4Linear:
             with _on(stream, codes.device):
                 self.packed = torch.empty(n, dtype=torch.uint8, device=codes.device)
         L.tpmlp_fp4_pack(codes, scales, self.packed, gated, stream)
+        if self.packed.is_cuda:
+            self._made = L._stream(stream)
+            self._pinned = None if scales.is_cuda else scales  # in host memory that no stream keeps
+            if stream is not None:
+                _used(stream, codes, scales)
+
+    _made = None  # the stream that ``packed`` was made on
 
     @classmethod
     def from_weight(cls, W, act="none", gated=False, stream=None):
@@ -149,7 +166,10 @@ class Fp4Linear:
             raise ValueError(f"a weight of {K} rows has no blocks of 32")
         if stream is not None:
             with _on(stream, W.device):
-                return cls.from_weight(W, act, gated)
+                self = cls.from_weight(W, act, gated)
+            if W.is_cuda:
+                _used(stream, W)
+            return self
         codes = torch.empty(N, K // 2, dtype=torch.uint8, device=W.device)
         scales = torch.empty(N, K // 32, dtype=torch.uint8, device=W.device)
         L.tpmlp_fp4_quantize(W, codes, scales)
@@ -161,3 +181,6 @@ class Fp4Linear:
         if X.shape[1] != self.K or Y.shape[1] != self.N:
             raise ValueError(f"X {tuple(X.shape)} and Y {tuple(Y.shape)} do not fit a weight of {self.N} by {self.K}")
         L.tpmlp_fp4_fwd(X, x_scales, self.packed, Y, self.act, self.gated, stream)
+        if self.packed.is_cuda and L._stream(stream) != self._made:
+            import torch
+            _used(torch.cuda.current_stream() if stream is None else stream, self.packed)

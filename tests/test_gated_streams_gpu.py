@@ -1,0 +1,117 @@
+"""Who may free what while another stream still works: 4-bit weights that are made from temporaries,
+and ones that are dropped behind a call."""
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+U8 = torch.uint8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from tensor_transformer_mlp_03_amd import _lib as L
+    L.lib()
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    print(f"[case] {request.node.name}", flush=True)
+    sys.stdout.flush()
+
+
+class Case:
+    """A weight of 4096 x 4096, its product on the current stream, and another stream with some milliseconds
+    of work before it."""
+
+    def __init__(self):
+        from tensor_transformer_mlp_03_amd.gated import Fp4Linear
+        gen = torch.Generator("cuda").manual_seed(6)
+        self.W = torch.randn(4096, 4096, device="cuda", generator=gen).bfloat16()
+        self.codes = torch.randint(0, 256, (4096, 2048), dtype=U8, device="cuda", generator=gen)
+        self.scales = torch.randint(120, 130, (4096, 128), dtype=U8, device="cuda", generator=gen)
+        self.X = torch.randn(3, 4096, device="cuda", generator=gen).bfloat16()
+        self.want, self.from_w, self.Y = (torch.empty(3, 4096, device="cuda") for _ in range(3))
+        Fp4Linear(self.codes, self.scales).forward(self.X, self.want)
+        Fp4Linear.from_weight(self.W).forward(self.X, self.from_w)
+        self.busy = [torch.randn(8192, 8192, device="cuda", generator=gen).bfloat16() for _ in range(2)]
+        self.stream = torch.cuda.Stream()
+        torch.mm(*self.busy)
+        torch.cuda.synchronize()
+
+    def work(self):
+        self.stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(self.stream):
+            out = torch.empty_like(self.busy[0])
+            for _ in range(60):
+                torch.mm(*self.busy, out=out)
+
+    def overwrite(self):
+        """Tensors of every size in play, which would lie where freed ones were."""
+        n = [self.codes.numel(), self.scales.numel(), 2 * self.W.numel(), 4096 * 32 * 68]
+        fill = [torch.full((k,), 0x91, dtype=U8, device="cuda") for k in n for _ in range(3)]
+        torch.cuda.current_stream().synchronize()
+        assert not self.stream.query()  # still held back: what it reads it has not read yet
+        return fill
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_fp4_weight_from_temporaries(handle):
+    from tensor_transformer_mlp_03_amd.gated import Fp4Linear
+    c = Case()
+    codes, scales = c.codes.clone(), c.scales.clone()
+    c.work()
+    s = c.stream.cuda_stream if handle else c.stream
+    lin = Fp4Linear(codes, scales, stream=s)
+    del codes, scales
+    fill = c.overwrite()
+    lin.forward(c.X, c.Y, stream=s)
+    c.stream.synchronize()
+    assert torch.equal(c.Y, c.want) and fill
+
+
+def test_fp4_weight_from_a_temporary_bf16_weight():
+    from tensor_transformer_mlp_03_amd.gated import Fp4Linear
+    c = Case()
+    W = c.W.clone()
+    c.work()
+    lin = Fp4Linear.from_weight(W, stream=c.stream)
+    del W
+    fill = c.overwrite()
+    lin.forward(c.X, c.Y, stream=c.stream)
+    c.stream.synchronize()
+    assert torch.equal(c.Y, c.from_w) and fill
+
+
+@pytest.mark.parametrize("current", [False, True])
+def test_fp4_weight_dropped_behind_a_call(current):
+    from tensor_transformer_mlp_03_amd.gated import Fp4Linear
+    c = Case()
+    lin = Fp4Linear(c.codes, c.scales)
+    c.work()
+    if current:
+        with torch.cuda.stream(c.stream):
+            lin.forward(c.X, c.Y)
+    else:
+        lin.forward(c.X, c.Y, stream=c.stream)
+    del lin
+    fill = c.overwrite()
+    c.stream.synchronize()
+    assert torch.equal(c.Y, c.want) and fill
+
+
+def test_fp4_weight_with_pinned_scales():
+    from tensor_transformer_mlp_03_amd.gated import Fp4Linear
+    c = Case()
+    codes, scales = c.codes.clone(), c.scales.cpu().pin_memory()
+    c.work()
+    lin = Fp4Linear(codes, scales, stream=c.stream)
+    del codes, scales
+    fill = [torch.full((4096, 128), 0x91, dtype=U8).pin_memory() for _ in range(4)], c.overwrite()
+    lin.forward(c.X, c.Y, stream=c.stream)
+    c.stream.synchronize()
+    assert torch.equal(c.Y, c.want) and fill
