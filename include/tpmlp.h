@@ -589,9 +589,12 @@ tpmlp_status tpmlp_fp4_pack(const uint8_t* codes, const uint8_t* scales, void* p
                             void* stream);
 
 /* Y[M,N] = act(X W^T), or with `gated` act(X W_g^T) (.) (X W_u^T), from `packed` weights.  For
- * few tokens, whose time is the reading of W; any M from 0 to 2^23 is taken.  The products
- * are exact, sums float32, Y (y_type) rounded once.  Rows of X start at multiples of 16 bytes
- * (TPMLP_ERR_ALIGN). */
+ * few tokens, whose time is the reading of W; any M from 0 to 2^23 is taken.  Values (a code
+ * times its power of two) enter the products as bf16, exactly but at the ends: X's below 2^-133
+ * (scale bytes 0 to 2 only) are rounded to a multiple of it, and values of 2^128 or more (X's from
+ * byte 247 on, W's from 253 on) are infinite.  Products are exact, sums float32; a row's float32
+ * scale multiplies its sums; Y (y_type) is rounded once.  Rows of X start at multiples of 16
+ * bytes (TPMLP_ERR_ALIGN). */
 tpmlp_status tpmlp_fp4_fwd(const void* X, int x_kind, int64_t ld_x, const void* x_scales, const void* packed, void* Y,
                            int y_type, int64_t ld_y, int act, int gated, int64_t M, int64_t N, int64_t K,
                            void* stream);

@@ -14,10 +14,12 @@
 // KiB, padded with zeros, and its scales into a word a row for every 128 k.  X, which every
 // workgroup reads whole, is loaded along its rows and turned in LDS, a wave for itself (packed by a
 // launch before, 16 tokens by 4096 x 2048 gated took 9.7 us, so 7.1; 64 by 10240 x 20480
-// 44.6 and 40.8).  E4M3 values times a power of two are exact in bf16.
+// 44.6 and 40.8).  E4M3 values times a power of two are exact in bf16 from 2^-124 to 2^119 (bytes
+// 3 to 246): of four significant bits, from bf16's least value 2^-133 to below 2^128.  Smaller ones
+// round to multiples of 2^-133, larger ones are infinite.
 //
-// The weights become bf16, exactly, by v_cvt_scalef32_pk_bf16_fp4 with the block's scale (one
-// instruction for two weights); four v_mfma_f32_16x16x32_bf16 follow.
+// The weights become bf16 by v_cvt_scalef32_pk_bf16_fp4 with the block's scale (one
+// instruction for two weights), exactly up to 2^125 (byte 252; 6 times 2^126 is past bf16); four v_mfma_f32_16x16x32_bf16 follow.
 // (v_mfma_scale_f32_16x16x128_f8f6f4 takes the codes and scales as they are, but aligns its
 // products to the largest with too few bits for a float32 sum: on codes of the whole E4M3
 // range it was off by 2^-15 of the magnitude.)  The waves of a workgroup share its rows and

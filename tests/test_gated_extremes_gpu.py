@@ -155,3 +155,49 @@ def test_sigmoid_derivative_far_out(M, split):
     want = np.exp(-x) / (1 + np.exp(-x)) ** 2
     off = np.abs(dX.cpu().double().numpy() - want) / want
     assert (off <= 2.0 ** -8 + (2 * x + 16) * U).all(), (float(off.max()), float(x.ravel()[off.argmax()]))
+
+
+@pytest.mark.parametrize("w", [7, 67, 127, 187, 247])
+def test_fp4_every_code_and_scale_of_x(w):
+    """Every E4M3 code with every power of two, times a weight 2^(w - 127): exactly the product of the value in
+    bf16, which is the value for bytes 3 to 246.  Below, it is rounded to a multiple of 2^-133; from 2^128 on it is
+    infinite.  A product below float32's normal range is rounded to a multiple of 2^-149."""
+    from tensor_transformer_mlp_03_amd.gated import Fp4Linear
+    X, xs = torch.zeros(256 * 256, 32, dtype=U8), torch.zeros(256 * 256, 1, dtype=U8)
+    X[:, 5] = torch.arange(256).repeat(256).to(U8)
+    xs[:, 0] = torch.arange(256).repeat_interleave(256).to(U8)
+    codes = torch.zeros(1, 16, dtype=U8)
+    codes[0, 2] = 0x20  # a 1 at k = 5
+    Y = filled(X.shape[0], 1)
+    Fp4Linear(codes.cuda(), torch.full((1, 1), w, dtype=U8).cuda()).forward(X.cuda(), Y, xs.cuda())
+    x = OG.e4m3_values(X.numpy())[:, 5] * OG.mx_values(xs.numpy())[:, 5]
+    byte = xs[:, 0].numpy().astype(int)
+    inside = np.isfinite(x) & (byte >= 3) & (byte <= 246)
+    as_bf16 = np.where(np.abs(x) >= 2.0 ** 128, np.copysign(np.inf, x), x)
+    small = np.abs(as_bf16) < 2.0 ** -126
+    as_bf16 = np.where(small, np.rint(np.where(small, as_bf16, 0) * 2.0 ** 133) * 2.0 ** -133, as_bf16)
+    assert np.array_equal(as_bf16[inside], x[inside])
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy(as_bf16 * 2.0 ** (w - 127)).float()  # rounded to float32
+    assert torch.equal(torch.nan_to_num(Y[:, 0].cpu(), 7e7, float("inf"), -float("inf")),
+                       torch.nan_to_num(want, 7e7, float("inf"), -float("inf")))
+
+
+@pytest.mark.parametrize("k", [-60, 0, 60])
+def test_fp4_every_code_and_scale_of_w(k):
+    """The same for the weights, times an X of 2^k: exact for bytes up to 252, and beyond it where a value is below 2^128."""
+    from tensor_transformer_mlp_03_amd.gated import Fp4Linear
+    N = 16 * 256
+    codes = torch.zeros(N, 16, dtype=U8)
+    codes[:, 0] = torch.arange(N) % 16
+    scales = (torch.arange(N) // 16).to(U8).view(N, 1)
+    X, Y = torch.zeros(1, 32, dtype=BF16), filled(1, N)
+    X[0, 0] = 2.0 ** k
+    Fp4Linear(codes.cuda(), scales.cuda()).forward(X.cuda(), Y)
+    v = OG.e2m1_values(codes.numpy())[:, 0] * OG.mx_values(scales.numpy())[:, 0]
+    assert (np.abs(v[:16 * 253]) < 2.0 ** 128).all()
+    v = np.where(np.abs(v) >= 2.0 ** 128, np.copysign(np.inf, v), v)
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy(v * 2.0 ** k).float()
+    nan = torch.isnan(want)
+    assert torch.equal(torch.isnan(Y[0].cpu()), nan) and torch.equal(Y[0].cpu()[~nan], want[~nan])
