@@ -1,0 +1,85 @@
+"""The gated MLP on every kernel that its planner chooses among (glu_plans.PLANS), against float64 products
+on the GPU.
+
+What ends a sum weighs most, so that losing it, or reading past it, shows: the last token's dZ is as large as all
+others' together, and the last eight columns of X and rows of B are four times the others.
+
+On the way to an output lie at most three roundings to bf16 (P, and h or dP, and the output's), each off by at most 2^-8 of the
+value, and act' and act'' are below 1.2: within 4 * 2^-8 of the output in the norm over all of it, and over its last
+rows and columns."""
+import math
+import sys
+
+import pytest
+
+import glu_plans as G
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from tensor_transformer_mlp_03_amd import _lib as L
+    L.lib()
+
+
+@pytest.fixture(autouse=True)
+def _announce(request):
+    print(f"[case] {request.node.name}", flush=True)
+    sys.stdout.flush()
+
+
+def check(name, got, want):
+    assert torch.isfinite(got).all(), name
+    off = got.double() - want
+    for part in (slice(None), slice(-8, None)):
+        for o, w in ((off[part], want[part]), (off[:, part], want[:, part])):
+            ratio = float(o.norm() / w.norm())
+            assert ratio <= 4 * 2.0 ** -8, (name, part, ratio)
+    # No element is wrong, whatever the norms say.  An output's row (or column) is linear in the row of dZ or X (or the
+    # column of A or B) that is larger than others, and so are its errors: they go by its own root mean square.
+    rms = torch.maximum(want.square().mean(1, keepdim=True), want.square().mean(0, keepdim=True)).sqrt()
+    big = float((off.abs() / (want.abs() + rms)).max())
+    assert big <= 0.1, (name, big)
+
+
+ACTS = {"silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu, "sigmoid": torch.sigmoid}
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,H,F", G.LARGE)
+def test_glu_plan(M, H, F, act):
+    from tensor_transformer_mlp_03_amd.gated import GatedMLP
+    print(sorted(G.taken(M, H, F)), flush=True)
+    gen = torch.Generator("cuda").manual_seed(M + H + F)
+    n = lambda *s, scale=1.0: torch.randn(*s, device="cuda", generator=gen) * scale  # noqa: E731
+    X, A, B, dZ = n(M, H), n(H, 2 * F, scale=H ** -0.5), n(F, H, scale=F ** -0.5), n(M, H, scale=0.1)
+    X[:, -8:] *= 4
+    B[-8:] *= 4
+    dZ[-1] *= 2.0 ** round(math.log2(M) / 2)
+    X, A, B, dZ = (t.to(BF16) for t in (X, A, B, dZ))
+    e = lambda *s: torch.full(s, float("nan"), dtype=BF16, device="cuda")  # noqa: E731
+    mlp = GatedMLP(A, B, act)
+    Z, P, got = e(M, H), e(M, 2 * F), []
+    mlp.forward(X, Z, P)
+    for kept in (P, None):
+        got.append((e(M, H), e(H, 2 * F), e(F, H)))
+        mlp.backward(dZ, X, kept, *got[-1])
+    X, A, B, dZ = (t.double() for t in (X, A, B, dZ))
+    Pd = (X @ A).requires_grad_()
+    h = ACTS[act](Pd[:, :F]) * Pd[:, F:]
+    check("P", P, Pd.detach())
+    check("Z", Z, (h @ B).detach())
+    dB = (h.t() @ dZ).detach()
+    h.backward(dZ @ B.t())
+    dP = Pd.grad
+    dX, dA = dP @ A.t(), X.t() @ dP
+    for how, (x, a, b) in zip(("kept", "again"), got):
+        check("dX " + how, x, dX)
+        check("dA " + how, a, dA)
+        check("dB " + how, b, dB)
