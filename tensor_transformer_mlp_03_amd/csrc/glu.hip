@@ -7,8 +7,10 @@
 //             dh = dZ B^T      with dP_g = dh u act'(g), dP_u = dh act(g), h^T
 //             dB = h^T dZ,  dA = X^T dP,  dX = dP A^T          12 M H F
 //
-// with g = P_g, u = P_u.  h, P and dP are bf16 between the products, as the plain MLP's G
-// and dP are; every sum is float32.  Tokens need not be a multiple of 8: X^T and h^T, whose
+// with g = P_g, u = P_u.  h, P and dP are bf16 between the products, which is what the matrix
+// instructions take and half of float32's bytes, as the plain MLP's G and dP are (P also where the
+// backward makes it again, so that a kept one gives the same gradients); every sum is float32.  A few
+// tokens' forward (glu_tokens.hip), which multiplies without those instructions, keeps h in float32.  Tokens need not be a multiple of 8: X^T and h^T, whose
 // rows are the tokens, are padded with zeros, and rows past the last token are masked in
 // the loads of the other operands.
 

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(64 * WAVES) glu_tokens_kernel(GluTokensArgs a)
             u += s0 + s < a.n_slices ? us[s] : 0.0f;
           }
         }
-        v = bf16_to_f32(f32_to_bf16(act_of(g, a.act) * u));
+        v = act_of(g, a.act) * u;  // h stays float32 here
         if (a.p_save && blockIdx.x == 0) {
           a.p_save[(int64_t)m * 2 * a.K + k0 + r] = f32_to_bf16(g);
           a.p_save[(int64_t)m * 2 * a.K + a.K + k0 + r] = f32_to_bf16(u);
