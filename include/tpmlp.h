@@ -557,7 +557,8 @@ typedef enum {
 /* tpmlp_edge_fwd with x as E4M3 codes[M,H] and scales, x = code * scale: [M] float32 (a
  * row's largest magnitude / 448; 1 for a row of zeros, at least 2^-126), or [M, H / 32] bytes
  * (the smallest power of two with a block's largest magnitude at most 448 times it; 1 for
- * zeros; H a multiple of 32).  The codes are x / scale rounded to nearest even, from float32.
+ * zeros; H a multiple of 32).  The codes are x times 1 / scale (both in float32) rounded to nearest
+ * even.
  * NaN is NaN's code and counts for no scale. */
 tpmlp_status tpmlp_edge_fwd_fp8(const tpmlp_edge* e, const void* y, int64_t ld_y, const void* r, int64_t ld_r,
                                 void* r_out, int64_t ld_r_out, uint8_t* codes, int64_t ld_codes, void* scales,

@@ -43,7 +43,9 @@ __device__ __forceinline__ void row_stats(const f32x4 (&v)[NV], int kind, int la
 // The row's x as E4M3 codes and scales, from its float32 values: one scale a row, amax /
 // 448 (float32, 1 for a row of zeros, at least 2^-126 so that its reciprocal is finite),
 // or one power of two for every 32 values, the smallest with amax <= 448 times it.  The
-// largest value is so at most 448 codes high and nothing saturates.  NaN keeps its code.
+// largest value is so at most 448 codes high and nothing saturates.  Codes are those of x
+// times the scale's reciprocal: exact for powers of two, a float32 rounding more for a row's, less
+// than a division costs.  NaN keeps its code.
 __device__ __forceinline__ uint32_t e4m3x4(f32x4 v) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {  // comparisons: a NaN passes
