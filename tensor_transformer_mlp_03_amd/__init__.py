@@ -24,7 +24,6 @@ from ._lib import (  # noqa: F401
     tpmlp_fp4_pack,
     tpmlp_fp4_packed_bytes,
     tpmlp_fp4_quantize,
-   
     tpmlp_fwd,
     tpmlp_fwd_workspace_bytes,
     tpmlp_glu_bwd,

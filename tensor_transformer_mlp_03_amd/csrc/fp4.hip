@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(64 * WK) fp4_kernel(Fp4Args a) {
     }
   };
   // X of a block and tile of tokens: from the order of loads, neighbours along a token's row, to that of
-  // the matrix instructions, through LDS; 16-byte chunks are swizzled by the token, so that neither
-  // side meets bank conflicts.
+  // the matrix instructions, through LDS; 16-byte chunks are swizzled by the token against bank
+  // conflicts, of which some are left: 0.59 of the LDS's active cycles at 16 tokens of bf16, 0.42 at 64 of E4M3.
   auto tokens = [&](int d, int m, int kb, bf16x8_t (&f)[4]) {
     u32x4* region = shared.x[wave][m % REGIONS];
     const int token = lane & 15, g = lane >> 4;

@@ -13,7 +13,7 @@ typedef uint32_t transpose_u32x4 __attribute__((ext_vector_type(4)));
 // tile (8 loads of 16 bytes: one instruction reads 8 rows x 128 bytes), turns
 // it around in registers with v_perm_b32 and writes rows 8*cb .. +7 of the
 // output tile, columns 8*rb .. +7 (one instruction writes 8 rows x 128 bytes).
-// R and C are multiples of 8, so a block is entirely inside or outside.
+// C is a multiple of 8 and, without PAD, R too, so a block is entirely inside or outside.
 // The four waves of a workgroup take four consecutive row tiles of one column
 // tile, and consecutive workgroups continue along the rows, so that the output
 // rows (R * 2 bytes apart, often a power of two) are written in long runs
