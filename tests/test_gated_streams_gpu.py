@@ -25,8 +25,8 @@ def _announce(request):
 
 
 class Case:
-    """A weight of 4096 x 4096, its product on the current stream, and another stream with some milliseconds
-    of work before it."""
+    """A weight of 4096 x 4096, its product on the current stream, and another stream with some tenths of a
+    second of work before it."""
 
     def __init__(self):
         from tensor_transformer_mlp_03_amd.gated import Fp4Linear
@@ -39,15 +39,21 @@ class Case:
         Fp4Linear(self.codes, self.scales).forward(self.X, self.want)
         Fp4Linear.from_weight(self.W).forward(self.X, self.from_w)
         self.busy = [torch.randn(8192, 8192, device="cuda", generator=gen).bfloat16() for _ in range(2)]
-        self.stream = torch.cuda.Stream()
         torch.mm(*self.busy)
+        for _ in range(8):  # one that does not share a hardware queue with the current stream, which would wait for it
+            self.stream = torch.cuda.Stream()
+            self.work(40)
+            self.X.add_(0)
+            torch.cuda.current_stream().synchronize()
+            if not self.stream.query():
+                break
         torch.cuda.synchronize()
 
-    def work(self):
+    def work(self, n=100):
         self.stream.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(self.stream):
             out = torch.empty_like(self.busy[0])
-            for _ in range(60):
+            for _ in range(n):
                 torch.mm(*self.busy, out=out)
 
     def overwrite(self):
@@ -55,8 +61,14 @@ class Case:
         n = [self.codes.numel(), self.scales.numel(), 2 * self.W.numel(), 4096 * 32 * 68]
         fill = [torch.full((k,), 0x91, dtype=U8, device="cuda") for k in n for _ in range(3)]
         torch.cuda.current_stream().synchronize()
-        assert not self.stream.query()  # still held back: what it reads it has not read yet
+        self.held = not self.stream.query()  # what it reads it has not read yet
         return fill
+
+    def holds(self, want):
+        self.stream.synchronize()
+        assert torch.equal(self.Y, want)
+        if not self.held:
+            pytest.skip("the other stream was done before the memory was written to")
 
 
 @pytest.mark.parametrize("handle", [False, True])
@@ -70,8 +82,8 @@ def test_fp4_weight_from_temporaries(handle):
     del codes, scales
     fill = c.overwrite()
     lin.forward(c.X, c.Y, stream=s)
-    c.stream.synchronize()
-    assert torch.equal(c.Y, c.want) and fill
+    c.holds(c.want)
+    del fill
 
 
 def test_fp4_weight_from_a_temporary_bf16_weight():
@@ -83,8 +95,8 @@ def test_fp4_weight_from_a_temporary_bf16_weight():
     del W
     fill = c.overwrite()
     lin.forward(c.X, c.Y, stream=c.stream)
-    c.stream.synchronize()
-    assert torch.equal(c.Y, c.from_w) and fill
+    c.holds(c.from_w)
+    del fill
 
 
 @pytest.mark.parametrize("current", [False, True])
@@ -100,8 +112,8 @@ def test_fp4_weight_dropped_behind_a_call(current):
         lin.forward(c.X, c.Y, stream=c.stream)
     del lin
     fill = c.overwrite()
-    c.stream.synchronize()
-    assert torch.equal(c.Y, c.want) and fill
+    c.holds(c.want)
+    del fill
 
 
 def test_fp4_weight_with_pinned_scales():
@@ -113,5 +125,5 @@ def test_fp4_weight_with_pinned_scales():
     del codes, scales
     fill = [torch.full((4096, 128), 0x91, dtype=U8).pin_memory() for _ in range(4)], c.overwrite()
     lin.forward(c.X, c.Y, stream=c.stream)
-    c.stream.synchronize()
-    assert torch.equal(c.Y, c.want) and fill
+    c.holds(c.want)
+    del fill
