@@ -501,9 +501,9 @@ tpmlp_status tpmlp_clip_grad_norm(const void* const* grads, void* const* outs, c
  * with A[H, 2 F] = [A_g | A_u] (a rank's column blocks of the gate and the up weight side by
  * side) and B[F, H].  The conventions at the top hold (contiguous, 16-byte aligned), but M
  * is any number from 0 to 2^23; H and F are positive multiples of 8 up to 2^23 and 2^22;
- * act is a tpmlp_act other than TPMLP_ACT_NONE.  h, P (kept, or made again by the gradients) and
- * the gradients of P pass through bf16 between the products (h in a forward of up to 2 tokens, or 4
- * with H F up to 2^24, does not), sums are float32. */
+ * act is a tpmlp_act other than TPMLP_ACT_NONE.  h, a kept P and the gradients of P pass through
+ * bf16 between the products (h in a forward of up to 2 tokens, or 4 with H F up to 2^24, and a P that
+ * the gradients make again do not), sums are float32. */
 size_t tpmlp_glu_fwd_workspace_bytes(int64_t M, int64_t H, int64_t F);
 
 /* Z[M,H] in z_type (tpmlp_dtype).  P_save (nullable) receives P[M, 2 F] in bf16 for a

@@ -49,12 +49,12 @@ def glu_forward(X, A, B, kind):
     return {"P": P, "P_tol": eP, "Z": Z, "Z_tol": eh @ np.abs(B) + (F + 4) * U * ((np.abs(h) + eh) @ np.abs(B))}
 
 
-def glu_backward(dZ, X, A, B, P, kind):
-    """{"dX", "dA", "dB"} and tolerances; P None: made again, and rounded to bf16."""
+def glu_backward(dZ, X, A, B, P, kind, again=BF):
+    """{"dX", "dA", "dB"} and tolerances; P None: made again, and rounded by half a step of `again`."""
     (M, H), F = X.shape, B.shape[0]
     if P is None:
         P = X @ A
-        eP = BF * np.abs(P) + 1.01 * (H + 4) * U * (np.abs(X) @ np.abs(A))
+        eP = again * np.abs(P) + 1.01 * (H + 4) * U * (np.abs(X) @ np.abs(A))
     else:
         eP = np.zeros_like(P)
     g, u, eg, eu = P[:, :F], P[:, F:], eP[:, :F], eP[:, F:]

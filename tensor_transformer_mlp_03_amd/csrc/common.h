@@ -42,7 +42,8 @@ enum Layout : int { KC = 0, MC = 1 };
 
 // What the epilogue does with the float32 accumulator of C[m,n].
 enum Epi : int {
-  EPI_F32 = 0,      // out_f32[m,n] = acc (split-K: slice z writes its own partial)
+  EPI_F32 = 0,      // out_f32[m,n] = acc (split-K: slice z writes its own partial); stored past
+                    //   the caches unless aux is set, to any address: the next launch reads it
   EPI_GELU = 1,     // out_bf16[m,n] = GeLU(acc); out2_bf16[m,n] = acc if out2 != null
   EPI_BF16 = 2,     // out_bf16[m,n] = acc
   EPI_DGELU = 3,    // p = aux_bf16[m,n]; out_bf16[m,n] = acc * GeLU'(p); transposed:
@@ -64,9 +65,12 @@ enum Epi : int {
   //   out_bf16[m,n] = acc u act'(g), out_bf16[m,N+n] = acc act(g); transposed:
   //   out2_bf16[n,m] = act(g) u, zeros for the rows m that pad M to a multiple of 8
   EPI_DGLU = 32,
+  EPI_DGLU32 = 48,  // the same with aux in float32
 };
 constexpr bool is_glu(int epi) { return epi >= EPI_GLU && epi < EPI_DGLU; }
 constexpr bool is_dglu(int epi) { return epi >= EPI_DGLU; }
+constexpr bool is_dglu32(int epi) { return epi >= EPI_DGLU32; }
+constexpr int act_of_epi(int epi) { return epi & 15; }  // of the gated epilogues
 
 // Largest output row stride of an EPI_F32_ACC product (its loads of the running
 // sum take 32-bit byte offsets within a 64-row band).
@@ -83,7 +87,7 @@ struct GemmArgs {
   int k_split;        // K elements per split-K slice (multiple of the K tile); K if none
   void* out;          // float* (EPI_F32) or uint16_t* (bf16 epilogues)
   uint16_t* out2;     // second bf16 output or null
-  const uint16_t* aux;  // EPI_DGELU's pre-activation input
+  const uint16_t* aux;  // EPI_DGELU's pre-activation input (EPI_DGLU32: a const float*)
   int64_t ldo;        // leading dimension of out, aux and (EPI_GELU) out2
   int64_t ldt;        // leading dimension of EPI_DGELU's transposed outputs
   int64_t split_stride;  // elements between split-K partial outputs
@@ -121,9 +125,9 @@ enum TileCfg : int {
 hipError_t launch_gemm(TileCfg tile, Layout la, Layout lb, Epi epi, const GemmArgs& args,
                        int splits, hipStream_t stream);
 
-// The gated MLP's products (EPI_GLU or EPI_DGLU without the activation; dglu takes B
+// The gated MLP's products (base: EPI_GLU, or EPI_DGLU or EPI_DGLU32, which take B
 // K-contiguous), unsplit.  act: a tpmlp_act other than TPMLP_ACT_NONE.
-hipError_t launch_gemm_glu(TileCfg tile, Layout lb, bool dglu, int act, const GemmArgs& args, hipStream_t stream);
+hipError_t launch_gemm_glu(TileCfg tile, Layout lb, Epi base, int act, const GemmArgs& args, hipStream_t stream);
 
 // out[j] = sum over i < n_parts of parts[i][j], left to right, j < n (n % 4 == 0).
 hipError_t launch_sum(const float* const* parts, int n_parts, float* out, int64_t n,

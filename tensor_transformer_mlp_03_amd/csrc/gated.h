@@ -25,7 +25,7 @@ struct DGluSplitArgs {
   const float* part;   // splits slices of [M][F]
   int splits, act;
   int64_t M, F, ldt;
-  const uint16_t* p;   // [M][2 F]
+  const void* p;       // [M][2 F] bf16, or float32
   uint16_t* dp;        // [M][2 F]
   uint16_t* ht;        // [F][ldt], columns M .. roundup8(M) - 1 zero
 };

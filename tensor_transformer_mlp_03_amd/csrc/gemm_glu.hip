@@ -2,6 +2,7 @@
 //
 //   forward   [P_g | P_u] = X [A_g | A_u],  h = act(P_g) * P_u     EPI_GLU
 //   backward  dh = dZ B^T, dP_g = dh u act'(g), dP_u = dh act(g)    EPI_DGLU, with h^T for dB
+//             the same from a P in float32, made again              EPI_DGLU32
 //
 // One launch makes both projections, the activation and the product of its two sides: a
 // tile takes gate and up columns in blocks of 32, so the pair meets in one wave's
@@ -30,19 +31,21 @@ hipError_t with_act(int act, const GemmArgs& a, hipStream_t s) {
 }
 
 template <int BM, int BN>
-hipError_t with_layout(Layout lb, bool dglu, int act, const GemmArgs& a, hipStream_t s) {
-  if (dglu) return lb == KC ? with_act<BM, BN, KC, EPI_DGLU>(act, a, s) : hipErrorInvalidValue;
+hipError_t with_layout(Layout lb, Epi base, int act, const GemmArgs& a, hipStream_t s) {
+  if (base == EPI_DGLU) return lb == KC ? with_act<BM, BN, KC, EPI_DGLU>(act, a, s) : hipErrorInvalidValue;
+  if (base == EPI_DGLU32) return lb == KC ? with_act<BM, BN, KC, EPI_DGLU32>(act, a, s) : hipErrorInvalidValue;
+  if (base != EPI_GLU) return hipErrorInvalidValue;
   return lb == KC ? with_act<BM, BN, KC, EPI_GLU>(act, a, s) : with_act<BM, BN, MC, EPI_GLU>(act, a, s);
 }
 
 }  // namespace
 
-hipError_t launch_gemm_glu(TileCfg tile, Layout lb, bool dglu, int act, const GemmArgs& args, hipStream_t stream) {
+hipError_t launch_gemm_glu(TileCfg tile, Layout lb, Epi base, int act, const GemmArgs& args, hipStream_t stream) {
   if (args.batch > 1 || args.k_split < args.K) return hipErrorInvalidValue;
   switch (tile) {
-    case TILE_256x256: return with_layout<256, 256>(lb, dglu, act, args, stream);
-    case TILE_128x128: return with_layout<128, 128>(lb, dglu, act, args, stream);
-    case TILE_256x128: return with_layout<256, 128>(lb, dglu, act, args, stream);
+    case TILE_256x256: return with_layout<256, 256>(lb, base, act, args, stream);
+    case TILE_128x128: return with_layout<128, 128>(lb, base, act, args, stream);
+    case TILE_256x128: return with_layout<256, 128>(lb, base, act, args, stream);
     default: return hipErrorInvalidValue;
   }
 }

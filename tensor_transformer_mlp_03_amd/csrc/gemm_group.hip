@@ -128,23 +128,26 @@ __global__ void __launch_bounds__(256) gemm_transpose_kernel(WithTransposeArgs a
 #endif
 }
 
+template <int BASE>
+auto with_act(int act) -> void (*)(WithTransposeArgs) {
+  switch (act) {
+    case TPMLP_ACT_SILU: return gemm_transpose_kernel<BASE + TPMLP_ACT_SILU>;
+    case TPMLP_ACT_GELU: return gemm_transpose_kernel<BASE + TPMLP_ACT_GELU>;
+    case TPMLP_ACT_RELU: return gemm_transpose_kernel<BASE + TPMLP_ACT_RELU>;
+    default: return gemm_transpose_kernel<BASE + TPMLP_ACT_SIGMOID>;
+  }
+}
+
 }  // namespace
 
-hipError_t launch_gemm_transpose(const GemmArgs& g, int splits, int act, const uint16_t* in, uint16_t* out, int64_t R, int64_t C,
+hipError_t launch_gemm_transpose(const GemmArgs& g, int splits, Epi base, int act, const uint16_t* in, uint16_t* out, int64_t R, int64_t C,
                                  int64_t ld_out, hipStream_t s) {
   WithTransposeArgs a;
   a.g = g;
   a.tiles = g.tiles_m * g.tiles_n * splits;
   const int blocks = plan_transpose(a.t, in, out, nullptr, nullptr, R, C, C, ld_out);
   if (blocks == 0 || g.batch > 1) return hipErrorInvalidValue;
-  void (*k)(WithTransposeArgs) = nullptr;
-  switch (act) {
-    case TPMLP_ACT_NONE: k = gemm_transpose_kernel<EPI_F32>; break;
-    case TPMLP_ACT_SILU: k = gemm_transpose_kernel<EPI_DGLU + TPMLP_ACT_SILU>; break;
-    case TPMLP_ACT_GELU: k = gemm_transpose_kernel<EPI_DGLU + TPMLP_ACT_GELU>; break;
-    case TPMLP_ACT_RELU: k = gemm_transpose_kernel<EPI_DGLU + TPMLP_ACT_RELU>; break;
-    default: k = gemm_transpose_kernel<EPI_DGLU + TPMLP_ACT_SIGMOID>; break;
-  }
+  void (*k)(WithTransposeArgs) = base == EPI_DGLU ? with_act<EPI_DGLU>(act) : base == EPI_DGLU32 ? with_act<EPI_DGLU32>(act) : gemm_transpose_kernel<EPI_F32>;
   return launch_kernel(k, dim3(a.tiles + blocks), dim3(256), s, a);
 }
 

@@ -299,6 +299,23 @@ __device__ __forceinline__ void store_staged(StageChunk&& stage_chunk, ScaleFn&&
       }
     }
   };
+  // EPI_DGLU32: all of them, eight float32 values of either in a lane's row.
+  f32x4_t wide[2][is_dglu32(EPI) ? 16 : 1];
+  auto load_wide_pairs = [&](int c) {
+    const int r0 = row0(c), c0 = col0(c);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const __amdgpu_buffer_rsrc_t rs =
+          make_rsrc(reinterpret_cast<const float*>(args.aux) + (int64_t)r0 * args.ldo + (half ? args.N : 0) + c0);
+#pragma unroll
+      for (int u = 0; u < (is_dglu32(EPI) ? 16 : 1); ++u) {
+        const int q = (u >> 1) * 64 + lane, r = q >> 3, cp = q & 7;
+        const bool ok = r0 + r < args.M && c0 + 8 * cp < args.N;
+        const uint32_t off = (uint32_t)(((int64_t)r * args.ldo + 8 * cp + 4 * (u & 1)) * 4);
+        wide[half][u] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, ok ? off : OOB, 0, 0));
+      }
+    }
+  };
   auto load_pre = [&](int c) {
     const int r0 = row0(c), c0 = col0(c);
     const __amdgpu_buffer_rsrc_t rs = make_rsrc(args.aux + (int64_t)r0 * args.ldo + c0);
@@ -334,7 +351,8 @@ __device__ __forceinline__ void store_staged(StageChunk&& stage_chunk, ScaleFn&&
       __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (is_dglu(EPI)) {
-      load_pairs(ch);
+      if constexpr (is_dglu32(EPI)) load_wide_pairs(ch);
+      else load_pairs(ch);
       __builtin_amdgcn_sched_barrier(0);
     }
     stage_chunk(ch, sc);
@@ -363,7 +381,7 @@ __device__ __forceinline__ void store_staged(StageChunk&& stage_chunk, ScaleFn&&
         const bool ok = row + r < args.M && col_c + 8 * cp < args.N;  // N % 8 == 0
         u16x8_t v;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = f32_to_bf16(act_f32<EPI - EPI_GLU>(x[it][e >> 2][e & 3]) * x[it][2 + (e >> 2)][e & 3]);
+        for (int e = 0; e < 8; ++e) v[e] = f32_to_bf16(act_f32<act_of_epi(EPI)>(x[it][e >> 2][e & 3]) * x[it][2 + (e >> 2)][e & 3]);
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rh,
                                                ok ? (uint32_t)(((int64_t)r * args.ldo + 8 * cp) * 2) : OOB, 0, 0);
       }
@@ -384,7 +402,7 @@ __device__ __forceinline__ void store_staged(StageChunk&& stage_chunk, ScaleFn&&
         }
       }
     } else if (EPI == EPI_F32 || ACC || PAIR) {
-      const bool final_out = args.k_split >= args.K;  // not a split-K slice
+      const bool final_out = args.k_split >= args.K && !args.aux;  // not a split-K slice
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<float*>(args.out) +
                                                   (int64_t)split * args.split_stride +
                                                   (int64_t)(row_w + 64 * h) * args.ldo + col_c);
@@ -416,19 +434,24 @@ __device__ __forceinline__ void store_staged(StageChunk&& stage_chunk, ScaleFn&&
     } else {
       const int64_t base = (int64_t)(row_w + 64 * h) * args.ldo + col_c;
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<uint16_t*>(args.out) + base);
-      f32x4_t x0s[8], x1s[8];
+      // EPI_DGLU32's pairs leave registers for half of the chunk's values at a time: rows 0 .. 31, whose
+      // h (below) takes the bytes of rows 0 .. 15, then rows 32 .. 63.
+      constexpr int BATCH = is_dglu32(EPI) ? 4 : 8;
 #pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const int q = it * 64 + lane, r = q >> 3, cp = q & 7;
-        x0s[it] = *reinterpret_cast<const f32x4_t*>(stage + r * ROW_B + (((2 * cp) ^ (r & 15)) << 4));
-        x1s[it] = *reinterpret_cast<const f32x4_t*>(stage + r * ROW_B + (((2 * cp + 1) ^ (r & 15)) << 4));
+      for (int b = 0; b < 8; b += BATCH) {
+      f32x4_t x0s[BATCH], x1s[BATCH];
+#pragma unroll
+      for (int u = 0; u < BATCH; ++u) {
+        const int q = (b + u) * 64 + lane, r = q >> 3, cp = q & 7;
+        x0s[u] = *reinterpret_cast<const f32x4_t*>(stage + r * ROW_B + (((2 * cp) ^ (r & 15)) << 4));
+        x1s[u] = *reinterpret_cast<const f32x4_t*>(stage + r * ROW_B + (((2 * cp + 1) ^ (r & 15)) << 4));
       }
       __builtin_amdgcn_sched_barrier(0);  // the reads stay one batch
 #pragma unroll
-      for (int it = 0; it < 8; ++it) {
-        const int q = it * 64 + lane, r = q >> 3, cp = q & 7;
-        const float x[8] = {x0s[it][0], x0s[it][1], x0s[it][2], x0s[it][3],
-                            x1s[it][0], x1s[it][1], x1s[it][2], x1s[it][3]};
+      for (int u = 0; u < BATCH; ++u) {
+        const int it = b + u, q = it * 64 + lane, r = q >> 3, cp = q & 7;
+        const float x[8] = {x0s[u][0], x0s[u][1], x0s[u][2], x0s[u][3],
+                            x1s[u][0], x1s[u][1], x1s[u][2], x1s[u][3]};
         const bool ok = row_w + 64 * h + r < args.M && col_c + 8 * cp < args.N;  // N % 8 == 0
         const uint32_t off = ok ? (uint32_t)(((int64_t)r * args.ldo + 8 * cp) * 2) : OOB;
         auto store = [&](const __amdgpu_buffer_rsrc_t& rd, const u16x8_t& v) {
@@ -455,12 +478,18 @@ __device__ __forceinline__ void store_staged(StageChunk&& stage_chunk, ScaleFn&&
           u16x8_t v3;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float g = bf16_to_f32(pre[0][it][e]), u = bf16_to_f32(pre[1][it][e]);
-            float a, da;
-            act_grad_f32<EPI - EPI_DGLU>(g, a, da);
-            v1[e] = f32_to_bf16(x[e] * u * da);
+            float g, up, a, da;
+            if constexpr (is_dglu32(EPI)) {
+              g = wide[0][2 * it + (e >> 2)][e & 3];
+              up = wide[1][2 * it + (e >> 2)][e & 3];
+            } else {
+              g = bf16_to_f32(pre[0][it][e]);
+              up = bf16_to_f32(pre[1][it][e]);
+            }
+            act_grad_f32<act_of_epi(EPI)>(g, a, da);
+            v1[e] = f32_to_bf16(x[e] * up * da);
             v3[e] = f32_to_bf16(x[e] * a);
-            v2[e] = f32_to_bf16(a * u);
+            v2[e] = f32_to_bf16(a * up);
           }
           store(rs, v1);
           store(make_rsrc(reinterpret_cast<uint16_t*>(args.out) + base + args.N), v3);
@@ -491,6 +520,7 @@ __device__ __forceinline__ void store_staged(StageChunk&& stage_chunk, ScaleFn&&
           // transposed store below reads.
           *reinterpret_cast<u16x8_t*>(stage + r * G_ROW_B + ((cp ^ gt_swz(r)) << 4)) = v2;
         }
+      }
       }
       if ((EPI == EPI_DGELU && !FP8) || is_dglu(EPI)) {
         // Transposed store of G in whole 128-byte lines.  ds_read_b64_tr_b16

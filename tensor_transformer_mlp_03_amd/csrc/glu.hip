@@ -7,10 +7,11 @@
 //             dh = dZ B^T      with dP_g = dh u act'(g), dP_u = dh act(g), h^T
 //             dB = h^T dZ,  dA = X^T dP,  dX = dP A^T          12 M H F
 //
-// with g = P_g, u = P_u.  h, P and dP are bf16 between the products, which is what the matrix
-// instructions take and half of float32's bytes, as the plain MLP's G and dP are (P also where the
-// backward makes it again, so that a kept one gives the same gradients); every sum is float32.  A few
-// tokens' forward (glu_tokens.hip), which multiplies without those instructions, keeps h in float32.  Tokens need not be a multiple of 8: X^T and h^T, whose
+// with g = P_g, u = P_u.  h and dP are bf16 between the products, which is what the matrix
+// instructions take, as the plain MLP's G and dP are, and so is a kept P, for its bytes; every sum
+// is float32.  A P that the backward makes again stays float32: in bf16 it would double the gradients'
+// error.  A few tokens' forward (glu_tokens.hip), which multiplies without those instructions, keeps h
+// in float32.  Tokens need not be a multiple of 8: X^T and h^T, whose
 // rows are the tokens, are padded with zeros, and rows past the last token are masked in
 // the loads of the other operands.
 
@@ -59,12 +60,24 @@ __global__ void __launch_bounds__(256) glu_split_kernel(GluSplitArgs a) {
   }
 }
 
+// Eight values of P.
+__device__ __forceinline__ void eight(const uint16_t* p, float (&v)[8]) {
+  const u16x8_t b = *reinterpret_cast<const u16x8_t*>(p);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = bf16_to_f32(b[e]);
+}
+__device__ __forceinline__ void eight(const float* p, float (&v)[8]) {
+  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p), b = *reinterpret_cast<const f32x4_t*>(p + 4);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < 4 ? a[e & 3] : b[e & 3];
+}
+
 // ---------------------------------------------------------------------------
 // dh split along K: the slices' sum with the epilogue of EPI_DGLU.  One 64 x 64 tile a
 // workgroup: a thread finishes eight columns of two rows, then, through LDS, 16 rows of
 // one column of h^T.
 // ---------------------------------------------------------------------------
-template <int ACT>
+template <int ACT, class PT>
 __global__ void __launch_bounds__(256) dglu_split_kernel(DGluSplitArgs a) {
   __shared__ uint16_t s_h[64][72];  // 8 elements of padding a row
   const int64_t tiles_n = (a.F + 63) / 64;
@@ -87,16 +100,18 @@ __global__ void __launch_bounds__(256) dglu_split_kernel(DGluSplitArgs a) {
         s1 += *reinterpret_cast<const f32x4_t*>(x + i * plane + 4);
       }
       const int64_t o = row * 2 * a.F + col;
-      const u16x8_t gb = *reinterpret_cast<const u16x8_t*>(a.p + o), ub = *reinterpret_cast<const u16x8_t*>(a.p + o + a.F);
+      float gs[8], us[8];
+      eight(static_cast<const PT*>(a.p) + o, gs);
+      eight(static_cast<const PT*>(a.p) + o + a.F, us);
       u16x8_t dg, du;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float dh = e < 4 ? s0[e & 3] : s1[e & 3], u = bf16_to_f32(ub[e]);
+        const float dh = e < 4 ? s0[e & 3] : s1[e & 3];
         float f, df;
-        act_grad_f32<ACT>(bf16_to_f32(gb[e]), f, df);
-        dg[e] = f32_to_bf16(dh * u * df);
+        act_grad_f32<ACT>(gs[e], f, df);
+        dg[e] = f32_to_bf16(dh * us[e] * df);
         du[e] = f32_to_bf16(dh * f);
-        h[e] = f32_to_bf16(f * u);
+        h[e] = f32_to_bf16(f * us[e]);
       }
       *reinterpret_cast<u16x8_t*>(a.dp + o) = dg;
       *reinterpret_cast<u16x8_t*>(a.dp + o + a.F) = du;
@@ -134,7 +149,8 @@ hipError_t launch_act(int act, int64_t blocks, const A& a, hipStream_t s, K1 sil
   void (*k)(A) = act == TPMLP_ACT_SILU ? silu : act == TPMLP_ACT_GELU ? gelu : act == TPMLP_ACT_RELU ? relu : sigmoid;
   return launch_kernel(k, dim3((unsigned)blocks), dim3(256), s, a);
 }
-#define BY_ACT(kernel) kernel<TPMLP_ACT_SILU>, kernel<TPMLP_ACT_GELU>, kernel<TPMLP_ACT_RELU>, kernel<TPMLP_ACT_SIGMOID>
+#define BY_ACT(kernel, ...) \
+  kernel<TPMLP_ACT_SILU __VA_ARGS__>, kernel<TPMLP_ACT_GELU __VA_ARGS__>, kernel<TPMLP_ACT_RELU __VA_ARGS__>, kernel<TPMLP_ACT_SIGMOID __VA_ARGS__>
 
 // ---------------------------------------------------------------------------
 // Plans: functions of the sizes alone
@@ -262,7 +278,7 @@ GluBwdPlan plan_glu_bwd(int64_t M, int64_t H, int64_t F, bool recompute) {
   p.off_dZt = mh;
   p.off_At = mh + (p.tdz ? mh : 0);
   p.off_P = p.off_At + (p.wt ? align_up(size_t(H) * F * 4) : 0);
-  p.off_ht = p.off_P + (recompute ? m2f : 0);
+  p.off_ht = p.off_P + (recompute ? 2 * m2f : 0);  // in float32
   p.off_dP = p.off_ht + mf;
   p.off_dPt = p.off_dP + m2f;
   p.off_part = p.off_dPt + (p.tdp ? m2f : 0);
@@ -307,7 +323,7 @@ hipError_t enqueue_glu_fwd(const uint16_t* X, const uint16_t* A, const uint16_t*
     g.tiles_n = ceil_div(F, tile_bn(p.g1.tile) / 2);
     g.out2 = P;
     g.ldt = 2 * F;
-    e = launch_gemm_glu(p.g1.tile, p.wt ? KC : MC, false, act, g, s);
+    e = launch_gemm_glu(p.g1.tile, p.wt ? KC : MC, EPI_GLU, act, g, s);
   } else {
     GemmArgs g = gemm_args(X, H, p.wt ? At : A, p.wt ? H : 2 * F, M, 2 * F, H, p.g1, part, 2 * F);
     e = launch_gemm(p.g1.tile, KC, p.wt ? KC : MC, EPI_F32, g, p.g1.splits, s);
@@ -329,28 +345,34 @@ hipError_t enqueue_glu_bwd(const uint16_t* dZ, const uint16_t* X, const uint16_t
   float* part = at<float>(ws, p.off_part);
   hipError_t e = hipSuccess;
   if (!p.xt_beside && (e = launch_transpose2(X, Xt, p.tdz ? dZ : nullptr, dZt, M, H, H, s, M8)) != hipSuccess) return e;
-  if (!P) {
-    uint16_t *Pw = at<uint16_t>(ws, p.off_P), *At = at<uint16_t>(ws, p.off_At);
+  const bool again = !P;
+  const void* p_in = P;
+  if (again) {
+    float* Pw = at<float>(ws, p.off_P);
+    uint16_t* At = at<uint16_t>(ws, p.off_At);
     if (p.wt && (e = launch_transpose(A, H, 2 * F, 2 * F, At, s)) != hipSuccess) return e;
-    e = run_gemm(-1, KC, p.wt ? KC : MC, EPI_BF16, X, H, p.wt ? At : A, p.wt ? H : 2 * F, M, 2 * F, H, p.g0, Pw, nullptr, nullptr,
+    // X as aux: P is read by the next launch (2048 x 4096, F 4096 480 us without, 464 so)
+    e = run_gemm(-1, KC, p.wt ? KC : MC, EPI_F32, X, H, p.wt ? At : A, p.wt ? H : 2 * F, M, 2 * F, H, p.g0, Pw, nullptr, X,
                  part, s);
     if (e != hipSuccess) return e;
-    P = Pw;
+    p_in = Pw;
   }
   // dh = dZ B^T -> dP [M][2 F], h^T [F][M8]       dZ: [M][H], B: [F][H] = [N][K]
   if (p.g1.splits == 1) {
     GemmArgs g = gemm_args(dZ, H, B, H, M, F, H, p.g1, dP, 2 * F);
     g.out2 = ht;
-    g.aux = P;
+    g.aux = static_cast<const uint16_t*>(p_in);
     g.ldt = M8;
-    e = p.xt_beside ? launch_gemm_transpose(g, 1, act, X, Xt, M, H, M8, s) : launch_gemm_glu(p.g1.tile, KC, true, act, g, s);
+    const Epi base = again ? EPI_DGLU32 : EPI_DGLU;
+    e = p.xt_beside ? launch_gemm_transpose(g, 1, base, act, X, Xt, M, H, M8, s) : launch_gemm_glu(p.g1.tile, KC, base, act, g, s);
   } else {
     GemmArgs g = gemm_args(dZ, H, B, H, M, F, H, p.g1, part, F);
-    e = p.xt_beside ? launch_gemm_transpose(g, p.g1.splits, TPMLP_ACT_NONE, X, Xt, M, H, M8, s)
+    e = p.xt_beside ? launch_gemm_transpose(g, p.g1.splits, EPI_F32, TPMLP_ACT_NONE, X, Xt, M, H, M8, s)
                     : launch_gemm(p.g1.tile, KC, KC, EPI_F32, g, p.g1.splits, s);
     if (e != hipSuccess) return e;
-    const DGluSplitArgs a{part, p.g1.splits, act, M, F, M8, P, dP, ht};
-    e = launch_act(act, ((M + 63) / 64) * ((F + 63) / 64), a, s, BY_ACT(dglu_split_kernel));
+    const DGluSplitArgs a{part, p.g1.splits, act, M, F, M8, p_in, dP, ht};
+    const int64_t blocks = ((M + 63) / 64) * ((F + 63) / 64);
+    e = again ? launch_act(act, blocks, a, s, BY_ACT(dglu_split_kernel, , float)) : launch_act(act, blocks, a, s, BY_ACT(dglu_split_kernel, , uint16_t));
   }
   if (e != hipSuccess) return e;
   if (p.group.on) {

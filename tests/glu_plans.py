@@ -138,7 +138,7 @@ def backward(M, H, F, recompute):
     tiles = ceil(M, 128) * ceil(F, 128) * p["dh"].splits
     p["beside"] = not p["tdz"] and p["dh"].tile == (128, 128) and tiles + ceil(M, 256) * ceil(H, 64) <= CU
     mh, mf, m2f = up(M8 * H * 2), up(M8 * F * 2), up(M8 * F * 4)
-    n = mh * (2 if p["tdz"] else 1) + (up(H * F * 4) if p["wt"] else 0) + (m2f if recompute else 0) + mf + m2f + (m2f if p["tdp"] else 0)
+    n = mh * (2 if p["tdz"] else 1) + (up(H * F * 4) if p["wt"] else 0) + (2 * m2f if recompute else 0) + mf + m2f + (m2f if p["tdp"] else 0)
     slices = [part(p["P"], M, 2 * F) if recompute else 0, part(p["dh"], M, F)]
     if g:
         slices.append((g[0] * M * H * 4 if g[0] > 1 else 0) + (g[1] * 3 * H * F * 4 if g[1] > 1 else 0))

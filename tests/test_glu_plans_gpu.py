@@ -79,7 +79,11 @@ def test_glu_plan(M, H, F, act):
     h.backward(dZ @ B.t())
     dP = Pd.grad
     dX, dA = dP @ A.t(), X.t() @ dP
-    for how, (x, a, b) in zip(("kept", "again"), got):
-        check("dX " + how, x, dX)
-        check("dA " + how, a, dA)
-        check("dB " + how, b, dB)
+    for how, grads in zip(("kept", "again"), got):
+        for name, g, want in zip(("dX", "dA", "dB"), grads, (dX, dA, dB)):
+            check(f"{name} {how}", g, want)
+            # A P made again is float32: on the way lie the rounding of dP or h and the output's.  Each is off by an
+            # even spread over a step of at most 2^-7, 2^-7 / sqrt(12) in the mean square, where enough values are rounded.
+            if how == "again" and F >= 256:
+                off = float((g.double() - want).norm() / want.norm())
+                assert off <= 1.02 * 2.0 ** -7 / math.sqrt(6), (name, off)
