@@ -402,7 +402,8 @@ __device__ __forceinline__ void store_staged(StageChunk&& stage_chunk, ScaleFn&&
         }
       }
     } else if (EPI == EPI_F32 || ACC || PAIR) {
-      const bool final_out = args.k_split >= args.K && !args.aux;  // not a split-K slice
+      const bool keep = EPI == EPI_F32 && !FP8 && args.aux;        // the next launch reads it
+      const bool final_out = args.k_split >= args.K && !keep;      // nor a split-K slice
       const __amdgpu_buffer_rsrc_t rs = make_rsrc(reinterpret_cast<float*>(args.out) +
                                                   (int64_t)split * args.split_stride +
                                                   (int64_t)(row_w + 64 * h) * args.ldo + col_c);
