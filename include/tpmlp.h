@@ -517,8 +517,8 @@ size_t tpmlp_glu_bwd_workspace_bytes(int64_t M, int64_t H, int64_t F, int recomp
 
 /* From dZ[M,H] (bf16), with g = P_g, u = P_u and dh = dZ B^T:
  *   dP = [dh u act'(g) | dh act(g)],  dB = h^T dZ,  dA = X^T dP,  dX = dP A^T
- * dX[M,H] in dx_type, dA[H, 2 F] and dB[F, H] in dw_type.  P_saved NULL recomputes P.
- * With M = 0, dA and dB are zero. */
+ * dX[M,H] in dx_type, dA[H, 2 F] and dB[F, H] in dw_type.  P_saved NULL recomputes P,
+ * in float32.  With M = 0, dA and dB are zero. */
 tpmlp_status tpmlp_glu_bwd(const tpmlp_bf16* dZ, const tpmlp_bf16* X, const tpmlp_bf16* A, const tpmlp_bf16* B,
                            const tpmlp_bf16* P_saved, void* dX, int dx_type, void* dA, void* dB, int dw_type, int act,
                            int64_t M, int64_t H, int64_t F, void* ws, size_t ws_bytes, void* stream);

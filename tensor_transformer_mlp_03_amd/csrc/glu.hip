@@ -270,7 +270,7 @@ GluBwdPlan plan_glu_bwd(int64_t M, int64_t H, int64_t F, bool recompute) {
   p.tdp = !p.group.on && large && transpose_dp(M, H, F);
   p.tdz = !p.group.on && large && transpose_dp(M, F, H);
   // Where the workgroups of both fit the chip at once, the transpose is hidden: 300 tokens by 520 x
-  // 264 20.7 us after it, 18.0 beside it; 1001 by 1000 x 1368 with P made again 62.6 and 59.3.
+  // 264 20.7 us after it, 18.0 beside it; 1001 by 1000 x 1368 with P made again (bf16 then) 62.6 and 59.3.
   const int64_t tiles = (int64_t)ceil_div(M, 128) * ceil_div(F, 128) * p.g1.splits;
   p.xt_beside = !p.tdz && p.g1.tile == TILE_128x128 && tiles + (int64_t)ceil_div(M, 256) * ceil_div(H, 64) <= NUM_CU;
   const size_t mh = align_up(size_t(M8) * H * 2), mf = align_up(size_t(M8) * F * 2), m2f = align_up(size_t(M8) * F * 4);

@@ -76,7 +76,7 @@ class GatedMLP:
 
     def backward(self, dZ, X, P, dX, dA, dB, stream=None):
         """dX [M,H] and the weights' gradients dA, dB (each float32 or bf16) from dZ [M,H] bf16; P
-        as the forward left it, or None to make it again."""
+        as the forward left it, or None to make it again, in float32."""
         M = X.shape[0]
         ws = self._ws.get(self._bytes(M, P is None), X.device, stream)
         L.tpmlp_glu_bwd(dZ, X, self.A, self.B, P, dX, dA, dB, self.act, ws, stream)
