@@ -19,7 +19,8 @@
 // round to multiples of 2^-133, larger ones are infinite.
 //
 // The weights become bf16 by v_cvt_scalef32_pk_bf16_fp4 with the block's scale (one
-// instruction for two weights), exactly up to 2^125 (byte 252; 6 times 2^126 is past bf16); four v_mfma_f32_16x16x32_bf16 follow.
+// instruction for two weights), exactly up to 2^125 (byte 252; 6 times 2^126 is past bf16); four
+// v_mfma_f32_16x16x32_bf16 follow.
 // (v_mfma_scale_f32_16x16x128_f8f6f4 takes the codes and scales as they are, but aligns its
 // products to the largest with too few bits for a float32 sum: on codes of the whole E4M3
 // range it was off by 2^-15 of the magnitude.)  The waves of a workgroup share its rows and

@@ -140,14 +140,16 @@ auto with_act(int act) -> void (*)(WithTransposeArgs) {
 
 }  // namespace
 
-hipError_t launch_gemm_transpose(const GemmArgs& g, int splits, Epi base, int act, const uint16_t* in, uint16_t* out, int64_t R, int64_t C,
-                                 int64_t ld_out, hipStream_t s) {
+hipError_t launch_gemm_transpose(const GemmArgs& g, int splits, Epi base, int act, const uint16_t* in, uint16_t* out, int64_t R,
+                                 int64_t C, int64_t ld_out, hipStream_t s) {
   WithTransposeArgs a;
   a.g = g;
   a.tiles = g.tiles_m * g.tiles_n * splits;
   const int blocks = plan_transpose(a.t, in, out, nullptr, nullptr, R, C, C, ld_out);
   if (blocks == 0 || g.batch > 1) return hipErrorInvalidValue;
-  void (*k)(WithTransposeArgs) = base == EPI_DGLU ? with_act<EPI_DGLU>(act) : base == EPI_DGLU32 ? with_act<EPI_DGLU32>(act) : gemm_transpose_kernel<EPI_F32>;
+  void (*k)(WithTransposeArgs) = base == EPI_DGLU     ? with_act<EPI_DGLU>(act)
+                                 : base == EPI_DGLU32 ? with_act<EPI_DGLU32>(act)
+                                                      : gemm_transpose_kernel<EPI_F32>;
   return launch_kernel(k, dim3(a.tiles + blocks), dim3(256), s, a);
 }
 

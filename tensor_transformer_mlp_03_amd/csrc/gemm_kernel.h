@@ -440,88 +440,88 @@ __device__ __forceinline__ void store_staged(StageChunk&& stage_chunk, ScaleFn&&
       constexpr int BATCH = is_dglu32(EPI) ? 4 : 8;
 #pragma unroll
       for (int b = 0; b < 8; b += BATCH) {
-      f32x4_t x0s[BATCH], x1s[BATCH];
+        f32x4_t x0s[BATCH], x1s[BATCH];
 #pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        const int q = (b + u) * 64 + lane, r = q >> 3, cp = q & 7;
-        x0s[u] = *reinterpret_cast<const f32x4_t*>(stage + r * ROW_B + (((2 * cp) ^ (r & 15)) << 4));
-        x1s[u] = *reinterpret_cast<const f32x4_t*>(stage + r * ROW_B + (((2 * cp + 1) ^ (r & 15)) << 4));
-      }
-      __builtin_amdgcn_sched_barrier(0);  // the reads stay one batch
-#pragma unroll
-      for (int u = 0; u < BATCH; ++u) {
-        const int it = b + u, q = it * 64 + lane, r = q >> 3, cp = q & 7;
-        const float x[8] = {x0s[u][0], x0s[u][1], x0s[u][2], x0s[u][3],
-                            x1s[u][0], x1s[u][1], x1s[u][2], x1s[u][3]};
-        const bool ok = row_w + 64 * h + r < args.M && col_c + 8 * cp < args.N;  // N % 8 == 0
-        const uint32_t off = ok ? (uint32_t)(((int64_t)r * args.ldo + 8 * cp) * 2) : OOB;
-        auto store = [&](const __amdgpu_buffer_rsrc_t& rd, const u16x8_t& v) {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rd, off, 0, 0);
-        };
-        u16x8_t v1, v2;
-        if (EPI == EPI_GELU) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v1[e] = epi_gelu(x[e]);
-            v2[e] = f32_to_bf16(x[e]);
-          }
-          store(rs, v1);
-          if (args.out2) store(make_rsrc(args.out2 + base), v2);
-        } else if (EPI == EPI_BF16) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v1[e] = f32_to_bf16(x[e]);
-          store(rs, v1);
-          if (FP8) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) am.add(ok ? bf16_to_f32(v1[e]) : 0.0f);
-          }
-        } else if constexpr (is_dglu(EPI)) {
-          u16x8_t v3;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float g, up, a, da;
-            if constexpr (is_dglu32(EPI)) {
-              g = wide[0][2 * it + (e >> 2)][e & 3];
-              up = wide[1][2 * it + (e >> 2)][e & 3];
-            } else {
-              g = bf16_to_f32(pre[0][it][e]);
-              up = bf16_to_f32(pre[1][it][e]);
-            }
-            act_grad_f32<act_of_epi(EPI)>(g, a, da);
-            v1[e] = f32_to_bf16(x[e] * up * da);
-            v3[e] = f32_to_bf16(x[e] * a);
-            v2[e] = f32_to_bf16(a * up);
-          }
-          store(rs, v1);
-          store(make_rsrc(reinterpret_cast<uint16_t*>(args.out) + base + args.N), v3);
-          // G of this row over the chunk's float32 values, as for EPI_DGELU below
-          *reinterpret_cast<u16x8_t*>(stage + r * G_ROW_B + ((cp ^ gt_swz(r)) << 4)) = v2;
-        } else if (FP8) {  // EPI_DGELU of an FP8 product: dP and its amax
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v1[e] = f32_to_bf16(dgelu_f32(x[e], pre[ch & 1][it][e]));
-          store(rs, v1);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float v = ok ? bf16_to_f32(v1[e]) : 0.0f;
-            am.v_max = fmaxf(am.v_max, v);
-            am.v_min = fminf(am.v_min, v);
-          }
-        } else {  // EPI_DGELU
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const DGelu d = epi_dgelu(x[e], pre[ch & 1][it][e]);
-            v1[e] = d.dp;
-            v2[e] = d.g;
-          }
-          store(rs, v1);
-          // Keep G of this row in LDS, over the chunk's float32 values (the
-          // wave has read all of them above, and its LDS accesses complete in
-          // order), at G_ROW_B pitch, 16-byte chunks swizzled by the row
-          // (gt_swz).  Rows and columns outside the output hold values that no
-          // transposed store below reads.
-          *reinterpret_cast<u16x8_t*>(stage + r * G_ROW_B + ((cp ^ gt_swz(r)) << 4)) = v2;
+        for (int u = 0; u < BATCH; ++u) {
+          const int q = (b + u) * 64 + lane, r = q >> 3, cp = q & 7;
+          x0s[u] = *reinterpret_cast<const f32x4_t*>(stage + r * ROW_B + (((2 * cp) ^ (r & 15)) << 4));
+          x1s[u] = *reinterpret_cast<const f32x4_t*>(stage + r * ROW_B + (((2 * cp + 1) ^ (r & 15)) << 4));
         }
-      }
+        __builtin_amdgcn_sched_barrier(0);  // the reads stay one batch
+#pragma unroll
+        for (int u = 0; u < BATCH; ++u) {
+          const int it = b + u, q = it * 64 + lane, r = q >> 3, cp = q & 7;
+          const float x[8] = {x0s[u][0], x0s[u][1], x0s[u][2], x0s[u][3],
+                              x1s[u][0], x1s[u][1], x1s[u][2], x1s[u][3]};
+          const bool ok = row_w + 64 * h + r < args.M && col_c + 8 * cp < args.N;  // N % 8 == 0
+          const uint32_t off = ok ? (uint32_t)(((int64_t)r * args.ldo + 8 * cp) * 2) : OOB;
+          auto store = [&](const __amdgpu_buffer_rsrc_t& rd, const u16x8_t& v) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), rd, off, 0, 0);
+          };
+          u16x8_t v1, v2;
+          if (EPI == EPI_GELU) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              v1[e] = epi_gelu(x[e]);
+              v2[e] = f32_to_bf16(x[e]);
+            }
+            store(rs, v1);
+            if (args.out2) store(make_rsrc(args.out2 + base), v2);
+          } else if (EPI == EPI_BF16) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v1[e] = f32_to_bf16(x[e]);
+            store(rs, v1);
+            if (FP8) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) am.add(ok ? bf16_to_f32(v1[e]) : 0.0f);
+            }
+          } else if constexpr (is_dglu(EPI)) {
+            u16x8_t v3;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float g, up, a, da;
+              if constexpr (is_dglu32(EPI)) {
+                g = wide[0][2 * it + (e >> 2)][e & 3];
+                up = wide[1][2 * it + (e >> 2)][e & 3];
+              } else {
+                g = bf16_to_f32(pre[0][it][e]);
+                up = bf16_to_f32(pre[1][it][e]);
+              }
+              act_grad_f32<act_of_epi(EPI)>(g, a, da);
+              v1[e] = f32_to_bf16(x[e] * up * da);
+              v3[e] = f32_to_bf16(x[e] * a);
+              v2[e] = f32_to_bf16(a * up);
+            }
+            store(rs, v1);
+            store(make_rsrc(reinterpret_cast<uint16_t*>(args.out) + base + args.N), v3);
+            // G of this row over the chunk's float32 values, as for EPI_DGELU below
+            *reinterpret_cast<u16x8_t*>(stage + r * G_ROW_B + ((cp ^ gt_swz(r)) << 4)) = v2;
+          } else if (FP8) {  // EPI_DGELU of an FP8 product: dP and its amax
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v1[e] = f32_to_bf16(dgelu_f32(x[e], pre[ch & 1][it][e]));
+            store(rs, v1);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float v = ok ? bf16_to_f32(v1[e]) : 0.0f;
+              am.v_max = fmaxf(am.v_max, v);
+              am.v_min = fminf(am.v_min, v);
+            }
+          } else {  // EPI_DGELU
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const DGelu d = epi_dgelu(x[e], pre[ch & 1][it][e]);
+              v1[e] = d.dp;
+              v2[e] = d.g;
+            }
+            store(rs, v1);
+            // Keep G of this row in LDS, over the chunk's float32 values (the
+            // wave has read all of them above, and its LDS accesses complete in
+            // order), at G_ROW_B pitch, 16-byte chunks swizzled by the row
+            // (gt_swz).  Rows and columns outside the output hold values that no
+            // transposed store below reads.
+            *reinterpret_cast<u16x8_t*>(stage + r * G_ROW_B + ((cp ^ gt_swz(r)) << 4)) = v2;
+          }
+        }
       }
       if ((EPI == EPI_DGELU && !FP8) || is_dglu(EPI)) {
         // Transposed store of G in whole 128-byte lines.  ds_read_b64_tr_b16

@@ -149,8 +149,9 @@ hipError_t launch_act(int act, int64_t blocks, const A& a, hipStream_t s, K1 sil
   void (*k)(A) = act == TPMLP_ACT_SILU ? silu : act == TPMLP_ACT_GELU ? gelu : act == TPMLP_ACT_RELU ? relu : sigmoid;
   return launch_kernel(k, dim3((unsigned)blocks), dim3(256), s, a);
 }
-#define BY_ACT(kernel, ...) \
-  kernel<TPMLP_ACT_SILU __VA_ARGS__>, kernel<TPMLP_ACT_GELU __VA_ARGS__>, kernel<TPMLP_ACT_RELU __VA_ARGS__>, kernel<TPMLP_ACT_SIGMOID __VA_ARGS__>
+#define BY_ACT(kernel, ...)                                                     \
+  kernel<TPMLP_ACT_SILU __VA_ARGS__>, kernel<TPMLP_ACT_GELU __VA_ARGS__>, \
+      kernel<TPMLP_ACT_RELU __VA_ARGS__>, kernel<TPMLP_ACT_SIGMOID __VA_ARGS__>
 
 // ---------------------------------------------------------------------------
 // Plans: functions of the sizes alone
@@ -372,7 +373,8 @@ hipError_t enqueue_glu_bwd(const uint16_t* dZ, const uint16_t* X, const uint16_t
     if (e != hipSuccess) return e;
     const DGluSplitArgs a{part, p.g1.splits, act, M, F, M8, p_in, dP, ht};
     const int64_t blocks = ((M + 63) / 64) * ((F + 63) / 64);
-    e = again ? launch_act(act, blocks, a, s, BY_ACT(dglu_split_kernel, , float)) : launch_act(act, blocks, a, s, BY_ACT(dglu_split_kernel, , uint16_t));
+    e = again ? launch_act(act, blocks, a, s, BY_ACT(dglu_split_kernel, , float))
+              : launch_act(act, blocks, a, s, BY_ACT(dglu_split_kernel, , uint16_t));
   }
   if (e != hipSuccess) return e;
   if (p.group.on) {

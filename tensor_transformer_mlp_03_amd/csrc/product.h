@@ -67,8 +67,8 @@ struct GroupItem {
 constexpr int GROUP_ITEMS = 3;
 // A product with both operands K-contiguous on 128 x 128 tiles, EPI_F32, or EPI_DGLU or EPI_DGLU32 with act, and
 // the transpose out[C][ld_out] of in[R][C] (zeros past R) in one launch.
-hipError_t launch_gemm_transpose(const GemmArgs& g, int splits, Epi base, int act, const uint16_t* in, uint16_t* out, int64_t R, int64_t C,
-                                 int64_t ld_out, hipStream_t s);
+hipError_t launch_gemm_transpose(const GemmArgs& g, int splits, Epi base, int act, const uint16_t* in, uint16_t* out, int64_t R,
+                                 int64_t C, int64_t ld_out, hipStream_t s);
 
 hipError_t launch_gemm_group(const GroupItem (&item)[GROUP_ITEMS], bool bf16_0, bool bf16_1, hipStream_t s);
 hipError_t launch_group_sum(const GroupItem (&item)[GROUP_ITEMS], void* const (&outs)[GROUP_ITEMS], bool bf16_0, bool bf16_1,

@@ -166,10 +166,10 @@ class Fp4Linear:
             raise ValueError(f"a weight of {K} rows has no blocks of 32")
         if stream is not None:
             with _on(stream, W.device):
-                self = cls.from_weight(W, act, gated)
+                made = cls.from_weight(W, act, gated)
             if W.is_cuda:
                 _used(stream, W)
-            return self
+            return made
         codes = torch.empty(N, K // 2, dtype=torch.uint8, device=W.device)
         scales = torch.empty(N, K // 32, dtype=torch.uint8, device=W.device)
         L.tpmlp_fp4_quantize(W, codes, scales)

@@ -47,6 +47,7 @@ class Case:
             torch.cuda.current_stream().synchronize()
             if not self.stream.query():
                 break
+        self.fill(2)
         torch.cuda.synchronize()
 
     def work(self, n=100):
@@ -56,19 +57,17 @@ class Case:
             for _ in range(n):
                 torch.mm(*self.busy, out=out)
 
-    def overwrite(self):
-        """Tensors of every size in play, which would lie where freed ones were."""
-        n = [self.codes.numel(), self.scales.numel(), 2 * self.W.numel(), 4096 * 32 * 68]
-        fill = [torch.full((k,), 0x91, dtype=U8, device="cuda") for k in n for _ in range(3)]
-        torch.cuda.current_stream().synchronize()
-        self.held = not self.stream.query()  # what it reads it has not read yet
-        return fill
+    def fill(self, n):
+        """n tensors of every size in play, which would lie where freed ones were."""
+        sizes = [self.codes.numel(), self.scales.numel(), 2 * self.W.numel(), 4096 * 32 * 68]
+        return [torch.full((k,), 0x91, dtype=U8, device="cuda") for k in sizes for _ in range(n)]
 
     def holds(self, want):
+        """After the call: fills the memory that is free, and compares what the other stream makes."""
+        fill = self.fill(3)  # two of each size are there already: a third is what was freed, or new
+        torch.cuda.current_stream().synchronize()
         self.stream.synchronize()
-        assert torch.equal(self.Y, want)
-        if not self.held:
-            pytest.skip("the other stream was done before the memory was written to")
+        assert torch.equal(self.Y, want) and fill
 
 
 @pytest.mark.parametrize("handle", [False, True])
@@ -80,10 +79,8 @@ def test_fp4_weight_from_temporaries(handle):
     s = c.stream.cuda_stream if handle else c.stream
     lin = Fp4Linear(codes, scales, stream=s)
     del codes, scales
-    fill = c.overwrite()
     lin.forward(c.X, c.Y, stream=s)
     c.holds(c.want)
-    del fill
 
 
 def test_fp4_weight_from_a_temporary_bf16_weight():
@@ -93,10 +90,8 @@ def test_fp4_weight_from_a_temporary_bf16_weight():
     c.work()
     lin = Fp4Linear.from_weight(W, stream=c.stream)
     del W
-    fill = c.overwrite()
     lin.forward(c.X, c.Y, stream=c.stream)
     c.holds(c.from_w)
-    del fill
 
 
 @pytest.mark.parametrize("current", [False, True])
@@ -111,9 +106,7 @@ def test_fp4_weight_dropped_behind_a_call(current):
     else:
         lin.forward(c.X, c.Y, stream=c.stream)
     del lin
-    fill = c.overwrite()
     c.holds(c.want)
-    del fill
 
 
 def test_fp4_weight_with_pinned_scales():
@@ -123,7 +116,7 @@ def test_fp4_weight_with_pinned_scales():
     c.work()
     lin = Fp4Linear(codes, scales, stream=c.stream)
     del codes, scales
-    fill = [torch.full((4096, 128), 0x91, dtype=U8).pin_memory() for _ in range(4)], c.overwrite()
     lin.forward(c.X, c.Y, stream=c.stream)
+    pinned = [torch.full((4096, 128), 0x91, dtype=U8).pin_memory() for _ in range(4)]
     c.holds(c.want)
-    del fill
+    del pinned
